@@ -255,7 +255,7 @@ def _scan_train(s):
     before[first] = h0
     c = torch.cat([a[1:], a[:1]])
     c[last] = 0
-    gy = s["grad_y"].float()
+    gy = s["grad_y"].to(torch.float32, copy=True)
     gy[last] += s["grad_slots"]
     g = _linear_scan(c.flip(0), gy.flip(0), s["longest"]).flip(0)
     dloga = g * (a * before - torch.where(m > 0, a * a / m, 0.0) * i * x)
