@@ -416,6 +416,159 @@ int ssm_conv1d(const float *x, const float *weight, const float *bias,
                int n_seqs, int n_tokens, int channels, int kernel_size,
                float *snapshots, void *stream);
 
+/* Element types of the layer operators below. */
+typedef enum {
+    SSM_F32 = 0,
+    SSM_BF16 = 1,
+    SSM_F16 = 2
+} ssm_dtype;
+
+/*
+ * The layer operators around the scan: a gated linear recurrence per channel
+ * (forward, backward), the RMS norm with the residual's addition (forward,
+ * 8-bit output, backward), a row quantiser and the 8-bit integer matrix product
+ * that reads the codes.  Ownership, stream and error rules are those of
+ * ssm_scan: caller-owned device memory, nothing allocated, nothing
+ * synchronised, host-checkable faults return before any launch.  Rows are
+ * contiguous and `..._stride` is the distance of two rows in elements (at least
+ * the row's length), so x and the gates may be slices of one projection.
+ * Sums, states, norms and statistics are held in fp32 or exact integers; a
+ * result is rounded to its type once.
+ */
+
+/*
+ * Gated linear recurrence.  For token t of a sequence and channel c:
+ *     r = sigmoid(gate_a[t,c]),  i = sigmoid(gate_x[t,c])
+ *     log a = -decay_scale * softplus(lam[c]) * r,  a = exp(log a)
+ *     h_t = a h_{t-1} + sqrt(1 - a^2) i x[t,c],  y[t,c] = h_t
+ * h is the fp32 state of the sequence's slot; packed tokens, seq_starts,
+ * seq_lens and resume_flags as for ssm_scan (a fresh sequence never reads its
+ * slot; a zero-length one leaves zeros if fresh and its slot if resuming).  A
+ * sequence whose range is not inside [0, n_tokens) counts as empty; ranges that
+ * overlap are not supported (SSM_SCAN_CHECK=1 reports both).
+ *   state_slots  [n_seqs][channels] fp32, in/out
+ *   x, gate_a, gate_x, y   [n_tokens][channels] of `dtype` (ssm_dtype)
+ *   lam          [channels] fp32;  decay_scale > 0 and finite
+ *   chunk_states NULL, or (training) fp32 [ssm_gated_scan_chunks(...)][channels],
+ *                out: the state entering each time chunk, which the backward
+ *                pass reads
+ *   workspace    256-byte aligned, at least ssm_gated_scan_workspace_bytes(...)
+ *                (training 1 with chunk_states); scratch, not shared by calls
+ *                that overlap on the GPU
+ * Where n_tokens == n_seqs and chunk_states is NULL (one token a sequence) the
+ * call steps every sequence token by token, needs no workspace and is one
+ * launch; otherwise sequences are cut into time chunks that run in parallel and
+ * pass their states on.  That wait is bounded: on giving up y and the slots
+ * behind it become NaN and, under SSM_SCAN_CHECK=1, the call returns
+ * SSM_ERR_TIMEOUT.  y must not overlap an input.
+ * Errors: SSM_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, strides
+ * below channels, workspace), SSM_ERR_UNSUPPORTED (more than 2^31 (chunk,
+ * 32 channels) pairs), SSM_ERR_CUDA.
+ */
+int ssm_gated_scan(float *state_slots, const void *x, const void *gate_a, const void *gate_x, const float *lam,
+                   float decay_scale, void *y, const int32_t *seq_starts, const int32_t *seq_lens,
+                   const int32_t *resume_flags, int n_seqs, int n_tokens, int channels, int dtype,
+                   long long x_stride, long long gate_a_stride, long long gate_x_stride, long long y_stride,
+                   float *chunk_states, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Rows of chunk_states for these sizes; 0 for invalid or unsupported ones. */
+long long ssm_gated_scan_chunks(int n_seqs, int n_tokens, int channels);
+
+/* Workspace of ssm_gated_scan (training 0, or 1 with chunk_states) and of
+ * ssm_gated_scan_backward (training 1). */
+size_t ssm_gated_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, int training);
+
+/*
+ * Gradients of ssm_gated_scan.  Takes the forward call's inputs, metadata and
+ * chunk_states, the gradient of y (grad_y) and optionally of the slots after
+ * the call (grad_state [n_seqs][channels] fp32 or NULL), and writes
+ *   grad_x, grad_gate_a, grad_gate_x   [n_tokens][channels] of dtype (tokens
+ *                owned by no sequence are not written)
+ *   grad_lam     [channels] fp32, summed in a fixed order (the same bits every
+ *                time; zeros when n_seqs is 0)
+ *   grad_initial_state  [n_seqs][channels] fp32 or NULL: gradient of the slots
+ *                before the call (zeros for fresh sequences)
+ * h is recomputed in fp32 from chunk_states.  workspace: at least
+ * ssm_gated_scan_workspace_bytes(n_seqs, n_tokens, channels, 1).
+ */
+int ssm_gated_scan_backward(const void *grad_y, const float *grad_state, const void *x, const void *gate_a,
+                            const void *gate_x, const float *lam, float decay_scale, const float *chunk_states,
+                            const int32_t *seq_starts, const int32_t *seq_lens, const int32_t *resume_flags,
+                            int n_seqs, int n_tokens, int channels, int dtype, long long x_stride,
+                            long long gate_a_stride, long long gate_x_stride, long long grad_y_stride,
+                            void *grad_x, void *grad_gate_a, void *grad_gate_x, long long grad_x_stride,
+                            long long grad_gate_a_stride, long long grad_gate_x_stride, float *grad_lam,
+                            float *grad_initial_state, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * RMS norm with the residual's addition, per row of `width` elements:
+ *     h = x + residual, rounded to residual_dtype (written to residual_out)
+ *     inv = 1 / sqrt(mean(h^2) + eps),  y = h * inv * weight
+ * or, with codes and scales instead of y, in 8 bits:
+ *     v = h * weight,  f = min(127 / max|v|, FLT_MAX),  both in fp32
+ *     codes = rint(v * f) (half to even),  scales = inv / f
+ * so codes * scales is y to half a step of its row's largest value / 127.  The
+ * codes do not depend on inv, nor on any order of summation.  A row of zeros
+ * has codes 0; a row with a NaN or an infinity (in h or in v) has scale NaN.
+ *   x, y          [rows][width] of dtype;  weight [width] fp32
+ *   residual      [rows][width] of residual_dtype (dtype or SSM_F32), or NULL:
+ *                 h = x
+ *   residual_out  as residual, or NULL: not written; may be residual itself
+ *                 (same stride), else it must not overlap an input
+ *   y or codes (int8) with scales [rows] fp32: exactly one of the two outputs;
+ *                 out_stride is y's or codes'
+ * eps >= 0; width at most 16384 (SSM_ERR_UNSUPPORTED above).
+ */
+int ssm_add_norm(const void *x, const void *residual, const float *weight, float eps, void *residual_out, void *y,
+                 int8_t *codes, float *scales, int rows, int width, int dtype, int residual_dtype,
+                 long long x_stride, long long residual_stride, long long residual_out_stride, long long out_stride,
+                 void *stream);
+
+/*
+ * Gradient of ssm_add_norm's y and residual_out.  With n = h * inv:
+ *     grad_in = grad_h + inv * (weight * grad_y - n * mean(n * weight * grad_y))
+ *     grad_weight = sum over rows of grad_y * n
+ * grad_in (residual_dtype) is the gradient of x and of residual alike.
+ *   grad_y [rows][width] of dtype; h as written by the forward call; grad_h as
+ *   h: the gradient that reaches residual_out from elsewhere, or NULL
+ *   grad_weight [width] fp32, summed in a fixed order
+ *   grad_in may be grad_h itself (same stride)
+ * workspace: 256-byte aligned, ssm_add_norm_backward_workspace_bytes(...).
+ */
+int ssm_add_norm_backward(const void *grad_y, const void *h, const float *weight, float eps, const void *grad_h,
+                          void *grad_in, float *grad_weight, int rows, int width, int dtype, int residual_dtype,
+                          long long grad_y_stride, long long h_stride, long long grad_h_stride,
+                          long long grad_in_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+size_t ssm_add_norm_backward_workspace_bytes(int rows, int width);
+
+/*
+ * Rows in 8 bits with a scale each (activations in front of a projection,
+ * weights once when they are loaded): f = min(127 / max|x|, FLT_MAX),
+ * codes = rint(x * f), scales = 1 / f; zeros, NaN and infinities as above.
+ */
+int ssm_quantize_rows(const void *x, int8_t *codes, float *scales, int rows, int width, int dtype,
+                      long long x_stride, long long codes_stride, void *stream);
+
+/*
+ * 8-bit integer matrix product with a scale for each token and each output
+ * channel:
+ *     out[t][n] = (sum_k x[t][k] * w[n][k]) * x_scales[t] * w_scales[n] + bias[n]
+ *   x  [rows][inner] int8, w [out_features][inner] int8 (any value, -128 too)
+ *   x_scales [rows], w_scales [out_features], bias [out_features] or NULL: fp32
+ *   out [rows][out_features] of out_dtype
+ * The sum is the exact integer, rounded once to fp32 (inner at most 131071;
+ * SSM_ERR_UNSUPPORTED above); the scales and the bias are applied in fp32.
+ * workspace: 256-byte aligned, at least ssm_int8_matmul_workspace_bytes(...)
+ * (which may be 0: then none is needed); scratch, not shared by calls that
+ * overlap on the GPU.
+ */
+int ssm_int8_matmul(const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales, const float *bias,
+                    void *out, int rows, int out_features, int inner, int out_dtype, long long x_stride,
+                    long long w_stride, long long out_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+size_t ssm_int8_matmul_workspace_bytes(int rows, int out_features, int inner);
+
 /* Text for a status code (static storage; never NULL). */
 const char *ssm_status_string(int status);
 

@@ -88,6 +88,21 @@ def load():
             lib.ssm_scan_ssd_workspace_bytes.argtypes = [_I] * 7
             lib.ssm_conv1d.restype = _I
             lib.ssm_conv1d.argtypes = [_P] * 8 + [_I] * 4 + [_P, _P]
+            L, F, S = ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+            for name, res, args in (
+                    ("ssm_gated_scan", _I, [_P] * 5 + [F] + [_P] * 4 + [_I] * 4 + [L] * 4 + [_P, _P, S, _P]),
+                    ("ssm_gated_scan_chunks", L, [_I] * 3),
+                    ("ssm_gated_scan_workspace_bytes", S, [_I] * 4),
+                    ("ssm_gated_scan_backward", _I, [_P] * 6 + [F] + [_P] * 4 + [_I] * 4 + [L] * 4 + [_P] * 3 +
+                     [L] * 3 + [_P, _P, _P, S, _P]),
+                    ("ssm_add_norm", _I, [_P] * 3 + [F] + [_P] * 4 + [_I] * 4 + [L] * 4 + [_P]),
+                    ("ssm_add_norm_backward", _I, [_P] * 3 + [F] + [_P] * 3 + [_I] * 4 + [L] * 4 + [_P, S, _P]),
+                    ("ssm_add_norm_backward_workspace_bytes", S, [_I] * 2),
+                    ("ssm_quantize_rows", _I, [_P] * 3 + [_I] * 3 + [L] * 2 + [_P]),
+                    ("ssm_int8_matmul", _I, [_P] * 6 + [_I] * 4 + [L] * 3 + [_P, S, _P]),
+                    ("ssm_int8_matmul_workspace_bytes", S, [_I] * 3)):
+                getattr(lib, name).restype = res
+                getattr(lib, name).argtypes = args
             lib.ssm_status_string.restype = ctypes.c_char_p
             lib.ssm_status_string.argtypes = [_I]
             _lib = lib

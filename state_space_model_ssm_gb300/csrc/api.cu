@@ -797,6 +797,22 @@ int ssd_impl(float *state, const float *x, const float *dt, const float *A, cons
 
 }  // namespace
 
+namespace ssm {
+
+bool debug_checks() { return check_env(); }
+
+int debug_check_sequences(const int32_t *seq_starts, const int32_t *seq_lens, int n_seqs, int n_tokens,
+                          cudaStream_t stream)
+{
+    ScanArgs m{};
+    m.seq_starts = seq_starts; m.seq_lens = seq_lens; m.n_seqs = n_seqs; m.n_tokens = n_tokens;
+    return check_metadata(m, stream);
+}
+
+int debug_read_status(const int *status, cudaStream_t stream) { return read_status(status, stream); }
+
+}  // namespace ssm
+
 extern "C" {
 
 int ssm_scan(float *state_slots, const float *x, const float *dt, const float *A, const float *B,
