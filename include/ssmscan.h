@@ -560,14 +560,18 @@ int ssm_quantize_rows(const void *x, int8_t *codes, float *scales, int rows, int
  * The sum is the exact integer, rounded once to fp32 (inner at most 131071;
  * SSM_ERR_UNSUPPORTED above); the scales and the bias are applied in fp32.
  * workspace: 256-byte aligned, at least ssm_int8_matmul_workspace_bytes(...)
- * (which may be 0: then none is needed); scratch, not shared by calls that
- * overlap on the GPU.
+ * of the same operands, sizes and strides (0: none is needed); scratch, not
+ * shared by calls that overlap on the GPU.  It holds the tokens as fp16 when
+ * there are more than 64 or their rows are not 16-byte aligned, and the weights
+ * when theirs are not: keep weights in rows that are a multiple of 16 bytes apart.
+ * The kernel's waits are bounded; a block that gives up writes NaN.
  */
 int ssm_int8_matmul(const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales, const float *bias,
                     void *out, int rows, int out_features, int inner, int out_dtype, long long x_stride,
                     long long w_stride, long long out_stride, void *workspace, size_t workspace_bytes, void *stream);
 
-size_t ssm_int8_matmul_workspace_bytes(int rows, int out_features, int inner);
+size_t ssm_int8_matmul_workspace_bytes(const int8_t *x, const int8_t *w, int rows, int out_features, int inner,
+                                       long long x_stride, long long w_stride);
 
 /* Text for a status code (static storage; never NULL). */
 const char *ssm_status_string(int status);

@@ -100,7 +100,7 @@ def load():
                     ("ssm_add_norm_backward_workspace_bytes", S, [_I] * 2),
                     ("ssm_quantize_rows", _I, [_P] * 3 + [_I] * 3 + [L] * 2 + [_P]),
                     ("ssm_int8_matmul", _I, [_P] * 6 + [_I] * 4 + [L] * 3 + [_P, S, _P]),
-                    ("ssm_int8_matmul_workspace_bytes", S, [_I] * 3)):
+                    ("ssm_int8_matmul_workspace_bytes", S, [_P] * 2 + [_I] * 3 + [L] * 2)):
                 getattr(lib, name).restype = res
                 getattr(lib, name).argtypes = args
             lib.ssm_status_string.restype = ctypes.c_char_p

@@ -801,6 +801,8 @@ namespace ssm {
 
 bool debug_checks() { return check_env(); }
 
+bool debug_fail_waits() { return fail_waits_env(); }
+
 int debug_check_sequences(const int32_t *seq_starts, const int32_t *seq_lens, int n_seqs, int n_tokens,
                           cudaStream_t stream)
 {

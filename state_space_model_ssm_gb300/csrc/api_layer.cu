@@ -31,6 +31,16 @@ int gated_sizes(int n_seqs, int n_tokens, int channels)
     return SSM_OK;
 }
 
+int int8_sizes(int rows, int out_features, int inner)
+{
+    if (rows < 0 || out_features <= 0 || inner <= 0)
+        return SSM_ERR_INVALID_ARG;
+    // blocks of the smallest tiles, and of the repacking kernel
+    const long long tiles = (rows / 16 + 1LL) * (out_features / 128 + 1LL) * 8;
+    const long long cells = ((long long)rows + out_features) * (inner / 16 + 1LL) / 256 + 2;
+    return inner > kMaxInner || tiles > INT_MAX || cells > INT_MAX ? SSM_ERR_UNSUPPORTED : SSM_OK;
+}
+
 int gated_debug_check(const int32_t *starts, const int32_t *lens, int n_seqs, int n_tokens, cudaStream_t stream)
 {
     return ssm::debug_checks() ? ssm::debug_check_sequences(starts, lens, n_seqs, n_tokens, stream) : SSM_OK;
@@ -248,28 +258,29 @@ int ssm_add_norm_backward(const void *grad_y, const void *h, const float *weight
                                                    grad_in_stride, stream));
 }
 
-size_t ssm_int8_matmul_workspace_bytes(int rows, int out_features, int inner)
+size_t ssm_int8_matmul_workspace_bytes(const int8_t *x, const int8_t *w, int rows, int out_features, int inner,
+                                       long long x_stride, long long w_stride)
 {
-    if (rows <= 0 || out_features <= 0 || inner <= 0 || inner > kMaxInner)
+    if (rows <= 0 || int8_sizes(rows, out_features, inner) != SSM_OK || x_stride < inner || w_stride < inner)
         return 0;
-    return ssm::int8_matmul_workspace_bytes(rows, out_features, inner);
+    return ssm::int8_matmul_workspace_bytes(x, w, rows, out_features, inner, x_stride, w_stride);
 }
 
 int ssm_int8_matmul(const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales, const float *bias,
                     void *out, int rows, int out_features, int inner, int out_dtype, long long x_stride,
                     long long w_stride, long long out_stride, void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (rows < 0 || out_features <= 0 || inner <= 0 || !known_dtype(out_dtype) || x_stride < inner ||
-        w_stride < inner || out_stride < out_features)
+    if (!known_dtype(out_dtype) || (inner > 0 && (x_stride < inner || w_stride < inner)) || out_stride < out_features)
         return SSM_ERR_INVALID_ARG;
-    if (inner > kMaxInner)
-        return SSM_ERR_UNSUPPORTED;
+    const int rc = int8_sizes(rows, out_features, inner);
+    if (rc != SSM_OK)
+        return rc;
     if (rows == 0)
         return SSM_OK;
     if (!x || !x_scales || !w || !w_scales || !out || !is_aligned(x_scales, 4) || !is_aligned(w_scales, 4) ||
         !is_aligned(bias, 4) || !is_aligned(out, ssm::dtype_size(out_dtype)))
         return SSM_ERR_INVALID_ARG;
-    const size_t need = ssm::int8_matmul_workspace_bytes(rows, out_features, inner);
+    const size_t need = ssm::int8_matmul_workspace_bytes(x, w, rows, out_features, inner, x_stride, w_stride);
     if (need > 0 && (!workspace || !is_aligned(workspace, 256) || workspace_bytes < need))
         return SSM_ERR_INVALID_ARG;
     return status_of(ssm::launch_int8_matmul(x, x_scales, w, w_scales, bias, out, rows, out_features, inner, out_dtype,

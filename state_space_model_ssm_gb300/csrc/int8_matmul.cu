@@ -1,90 +1,622 @@
 // 8-bit integer matrix product with a scale for each token and each output
 // channel (sm_103a):
 //
-//   out[t][n] = (sum_k xq[t][k] wq[n][k]) xs[t] ws[n] + bias[n]
+//   out[t][n] = (sum_k x[t][k] w[n][k]) xs[t] ws[n] + bias[n]
 //
-// The sum is an exact integer (inner <= 131071 keeps it inside 32 bits).
+// On sm_103a the tensor cores have no fast path for 8-bit integers, but fp16 holds
+// every 8-bit integer exactly and a product of two is an integer of at most 2^14,
+// so the fp16 tensor cores with their fp32 accumulator give the exact integer as
+// long as the partial sums stay within 2^24: for 1024 terms.  Every kFold stages
+// (1024 terms) the accumulator is moved to 32-bit integers in registers and
+// starts again from zero, so the sum is the exact integer for every input.
+//
+// A block owns 128 output channels and NT tokens, M = 128 channels x N = NT tokens
+// x K: the weights are the A operand, which the tensor core reads from tensor
+// memory.  They cross HBM, L2 and shared memory as bytes and become fp16 on their
+// way from shared to tensor memory: 8 warps turn each byte b into the fp16
+// number 1024 + (b ^ 0x80) by placing it under the constant's exponent, and
+// subtract 1152 (5 instructions for 4 values).  So a weight costs one byte of
+// bandwidth in every place that is short of it.  The tokens are the B operand, K-major in
+// shared memory with the 128-byte swizzle: for few tokens (NT <= 64) they arrive
+// as bytes too and the same warps convert them; for many, a kernel in front has
+// written them as fp16 once, since every block of a column of tiles reads them.
+// Rows that TMA cannot describe (an address or a stride that is no multiple of
+// 16) are repacked by that kernel.
+//
+// Roles: one warp loads weights (and 8-bit tokens) by TMA, one fp16 tokens, one
+// issues the MMAs, 8 convert and afterwards write the result (thread: one output
+// channel, NT / 2 tokens).  They hand stages of 64 terms to each other through
+// mbarriers.  With few tiles the terms are split over the blocks of a cluster, whose
+// integer sums meet in the first block's shared memory: no workspace, and the
+// same bits as without a split.
+//
+// Every wait is bounded; a block that gave up drains its copies and products,
+// frees its tensor memory and writes NaN.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "layer_common.cuh"
+#include "tc_common.cuh"
 
 namespace ssm {
 
 namespace {
 
+using namespace tc;
+
+constexpr int kRows = 128;                    // output channels of a block
+constexpr int kTerms = 64;                    // terms of a stage
+constexpr int kFold = 16;                     // stages whose sum is exact in fp32: 16 x 64 x 2^14 = 2^24
+constexpr int kWStages = 6;                   // weight stages (8 KB each)
+constexpr int kABufs = 4;                     // converted weight stages in tensor memory (32 columns each)
+constexpr int kConvWarps = 8;
+constexpr int kWarpW = 8, kWarpMma = 9, kWarpX = 10;
+constexpr int kThreads = 352;
+
 struct I8Args {
-    const int8_t *x, *w;
     const float *xs, *ws, *bias;
     void *out;
     int M, N, K;
-    long long sx, sw, so;
+    long long so;
+    int tiles_m, tiles_n, split;              // token tiles, channel tiles, blocks of a cluster
+    int fail_waits;
 };
 
-constexpr int kTile = 64, kStep = 64;
+// Shared memory (bytes; tiles 1024-aligned).
+template <int NT, bool XCONV>
+struct I8Layout {
+    static constexpr int kXStages = XCONV ? kABufs : 4;
+    static constexpr int kXTile = NT * 128;                 // 64 fp16 terms of NT tokens
+    static constexpr int kW = 0;
+    static constexpr int kX = kW + kWStages * kRows * kTerms;
+    static constexpr int kXi = kX + kXStages * kXTile;      // 8-bit tokens of a weight stage
+    static constexpr int kRed = kXi + (XCONV ? kWStages * NT * kTerms : 0);
+    static int red_bytes(int split) { return (split - 1) * NT * kRows * 4; }
+    // mbarriers (after the split's sums, whose size the launch knows)
+    static constexpr int kBars = 2 * kWStages + 2 * 4 + 2 * kABufs + 4;
+    static int total(int split) { return kRed + red_bytes(split) + kBars * 8 + 32; }
+    static constexpr int kTmem = NT + 32 * kABufs <= 256 ? 256 : 512;
+};
 
-// 64 x 64 outputs a block, 4 x 4 a thread, packed 4-term integer products.
-template <class T>
-__global__ void __launch_bounds__(256)
-int8_matmul_kernel(const I8Args a)
+// Shared-memory descriptor of a K-major tile of 128-byte rows with the 128-byte
+// swizzle (8-row groups 1024 bytes apart).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
 {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+// kind::f16, A and B fp16 (K-major), D fp32, M x N.
+__device__ __forceinline__ uint32_t idesc_f16(int m, int n)
+{
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+                 ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const void *map, int c0, int c1, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];\n"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)) : "memory");
+}
+
+// Four signed bytes as fp16: lo = bytes 0, 1 and hi = bytes 2, 3.
+__device__ __forceinline__ void bytes_to_half(uint32_t b, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = b ^ 0x80808080u;
+    const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+    const uint32_t off = 0xE480E480u;                       // -1152 twice
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(l), "r"(off));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(h), "r"(off));
+}
+
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                   "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(float (&v)[8], uint32_t taddr)
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
+// A shared-memory address of this block as seen in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v)
+{
+    asm volatile("st.shared::cluster.s32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+
+template <class T, int NT, bool XCONV>
+__global__ void __launch_bounds__(kThreads, NT <= 64 ? 2 : 1)
+int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
+{
+    using L = I8Layout<NT, XCONV>;
     griddep_entry();
-    __shared__ int xt[kTile][kStep / 4 + 1], wt[kTile][kStep / 4 + 1];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const long long m0 = (long long)blockIdx.x * kTile, n0 = (long long)blockIdx.y * kTile;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += kStep) {
-        for (int i = tid; i < kTile * kStep / 4; i += 256) {
-            const int r = i / (kStep / 4), c = i % (kStep / 4);
-            unsigned xv = 0, wv = 0;
-            for (int b = 0; b < 4; ++b) {
-                const int k = k0 + 4 * c + b;
-                if (k < a.K) {
-                    if (m0 + r < a.M)
-                        xv |= (unsigned)(uint8_t)a.x[(m0 + r) * a.sx + k] << (8 * b);
-                    if (n0 + r < a.N)
-                        wv |= (unsigned)(uint8_t)a.w[(n0 + r) * a.sw + k] << (8 * b);
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t base = smem_u32(sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x % a.split, tile = blockIdx.x / a.split;
+    // Tiles in groups of 8 token tiles: the blocks that run together share weights and tokens in L2.
+    const int group = tile / (8 * a.tiles_n), in_group = tile - group * 8 * a.tiles_n;
+    const int gm = min(8, a.tiles_m - 8 * group);
+    const int m0 = (8 * group + in_group % gm) * NT, n0 = in_group / gm * kRows;
+    const int nk = (a.K + kTerms - 1) / kTerms;
+    const int k0 = (int)((long long)nk * rank / a.split), n = (int)((long long)nk * (rank + 1) / a.split) - k0;
+    const int red = L::kRed + (a.split - 1) * NT * kRows * 4;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + red);
+    uint64_t *wfull = bars, *wempty = wfull + kWStages, *xfull = wempty + kWStages, *xempty = xfull + 4;
+    uint64_t *afull = xempty + 4, *aempty = afull + kABufs, *accfull = aempty + kABufs, *accempty = accfull + 1;
+    uint64_t *drain = accempty + 1;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
+    volatile int *fail = reinterpret_cast<volatile int *>(slot + 1);
+    const long cap = a.fail_waits ? 0 : kSpinLimit;
+
+    if (warp == kWarpMma)
+        tmem_alloc(slot, L::kTmem);
+    if (tid == 0) {
+        for (int i = 0; i < kWStages; ++i) {
+            mbar_init(wfull + i, 1);
+            mbar_init(wempty + i, kConvWarps);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(xfull + i, 1);
+            mbar_init(xempty + i, 1);
+        }
+        for (int i = 0; i < kABufs; ++i) {
+            mbar_init(afull + i, kConvWarps);
+            mbar_init(aempty + i, 1);
+        }
+        mbar_init(accfull, 1);
+        mbar_init(accempty, kConvWarps);
+        mbar_init(drain, 1);
+        mbar_init_fence();
+        *fail = 0;
+    }
+    fence_before();
+    __syncthreads();
+    if (a.split > 1)
+        cluster_arrive();                                   // every block of the cluster runs
+    fence_after();
+    const uint32_t tmem = *slot, tmem_a = tmem + NT;
+
+    if (warp == kWarpW) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < n; ++i) {
+                const int s = i % kWStages;
+                if (i >= kWStages && !mbar_wait(wempty + s, (i / kWStages - 1) & 1, cap)) {
+                    *fail = 1;
+                    break;
+                }
+                mbar_expect_tx(wfull + s, kRows * kTerms + (XCONV ? NT * kTerms : 0));
+                tma_2d(base + L::kW + s * kRows * kTerms, &wmap, (k0 + i) * kTerms, n0, wfull + s);
+                if (XCONV)
+                    tma_2d(base + L::kXi + s * NT * kTerms, &xmap, (k0 + i) * kTerms, m0, wfull + s);
+            }
+            for (int j = max(0, i - kWStages); j < i; ++j)  // no copy lands after the block has gone
+                mbar_wait(wfull + j % kWStages, (j / kWStages) & 1);
+        }
+    } else if (warp == kWarpX) {
+        if (!XCONV && lane == 0) {
+            int i = 0;
+            for (; i < n; ++i) {
+                const int s = i % L::kXStages;
+                if (i >= L::kXStages && !mbar_wait(xempty + s, (i / L::kXStages - 1) & 1, cap)) {
+                    *fail = 1;
+                    break;
+                }
+                mbar_expect_tx(xfull + s, L::kXTile);
+                tma_2d(base + L::kX + s * L::kXTile, &xmap, (k0 + i) * kTerms, m0, xfull + s);
+            }
+            for (int j = max(0, i - L::kXStages); j < i; ++j)
+                mbar_wait(xfull + j % L::kXStages, (j / L::kXStages) & 1);
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            const uint32_t id = idesc_f16(kRows, NT);
+            for (int i = 0; i < n; ++i) {
+                const int b = i % kABufs, s = i % L::kXStages;
+                bool ok = mbar_wait(afull + b, (i / kABufs) & 1, cap);
+                if (!XCONV)
+                    ok = ok && mbar_wait(xfull + s, (i / L::kXStages) & 1, cap);
+                if (i > 0 && i % kFold == 0)
+                    ok = ok && mbar_wait(accempty, (i / kFold - 1) & 1, cap);
+                if (!ok) {
+                    *fail = 1;
+                    break;
+                }
+                fence_after();
+                const uint64_t bd = desc_sw128(base + L::kX + s * L::kXTile);
+#pragma unroll
+                for (int kk = 0; kk < kTerms / 16; ++kk)
+                    mma_f16_ts(tmem, tmem_a + 32 * b + 8 * kk, bd + 2 * kk, id, (i % kFold) != 0 || kk > 0);
+                commit(aempty + b);
+                if (!XCONV)
+                    commit(xempty + s);
+                if (i % kFold == kFold - 1 || i == n - 1)
+                    commit(accfull);
+            }
+            commit(drain);                                  // every product issued is done before TMEM is freed
+            mbar_wait(drain, 0);
+        }
+    } else {
+        const int q = warp & 3, half = warp >> 2;           // TMEM lanes 32 q .., half of the terms / of the tokens
+        const int row = 32 * q + lane;
+        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        constexpr int HT = NT / 2;                          // tokens of this thread
+        int acc[HT];
+        const int chunks = (n + kFold - 1) / kFold;
+        const bool ints = chunks > 1 || a.split > 1;
+        if (ints)
+#pragma unroll
+            for (int j = 0; j < HT; ++j)
+                acc[j] = 0;
+        int folded = 0;
+        bool ok = true;
+        // the accumulator into the integers
+        auto fold = [&]() {
+            ok = ok && mbar_wait(accfull, folded & 1, cap);
+            if (__all_sync(kFullMask, ok)) {
+                fence_after();
+#pragma unroll
+                for (int j = 0; j < HT; j += 8) {
+                    float v[8];
+                    tmem_ld8(v, tmem + lanes + half * HT + j);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        acc[j + e] += __float2int_rn(v[e]);
+                }
+                fence_before();
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(accempty);
+            ++folded;
+        };
+        for (int i = 0; i < n; ++i) {
+            if (i % kFold == 2 && i > kFold)                // two stages of the next sum are ready
+                fold();
+            const int s = i % kWStages, b = i % kABufs;
+            ok = ok && mbar_wait(wfull + s, (i / kWStages) & 1, cap);
+            if (!__all_sync(kFullMask, ok)) {
+                ok = false;
+                break;
+            }
+            // 32 bytes of this thread's weight row: 16-byte chunks 2 half, 2 half + 1 of the 64-byte swizzle
+            const unsigned char *wr = sm + L::kW + s * kRows * kTerms + row * kTerms;
+            const int sw = (row >> 1) & 3;
+            const uint4 c0 = *reinterpret_cast<const uint4 *>(wr + (((2 * half) ^ sw) << 4));
+            const uint4 c1 = *reinterpret_cast<const uint4 *>(wr + (((2 * half + 1) ^ sw) << 4));
+            constexpr int XW = XCONV ? NT / 16 : 1;
+            uint32_t xw[XW];
+            if (XCONV)
+#pragma unroll
+                for (int j = 0; j < XW; ++j)
+                    xw[j] = *reinterpret_cast<const uint32_t *>(sm + L::kXi + s * NT * kTerms + (tid + 256 * j) * 4);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(wempty + s);
+            uint32_t h[16];
+            bytes_to_half(c0.x, h[0], h[1]);
+            bytes_to_half(c0.y, h[2], h[3]);
+            bytes_to_half(c0.z, h[4], h[5]);
+            bytes_to_half(c0.w, h[6], h[7]);
+            bytes_to_half(c1.x, h[8], h[9]);
+            bytes_to_half(c1.y, h[10], h[11]);
+            bytes_to_half(c1.z, h[12], h[13]);
+            bytes_to_half(c1.w, h[14], h[15]);
+            if (i >= kABufs) {
+                ok = mbar_wait(aempty + b, (i / kABufs - 1) & 1, cap);
+                if (!__all_sync(kFullMask, ok)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+            }
+            tmem_st16u(tmem_a + lanes + 32 * b + 16 * half, h);
+            if (XCONV) {
+#pragma unroll
+                for (int j = 0; j < XW; ++j) {
+                    const int e = tid + 256 * j, t = e >> 4, w = e & 15;
+                    uint2 v;
+                    bytes_to_half(xw[j], v.x, v.y);
+                    *reinterpret_cast<uint2 *>(sm + L::kX + b * L::kXTile + t * 128 + (((w >> 1) ^ (t & 7)) << 4) +
+                                               (w & 1) * 8) = v;
+                }
+                fence_async_smem();
+            }
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(afull + b);
+        }
+        if (ok)
+            while (folded < chunks - 1)
+                fold();
+        if (n > 0)
+            ok = ok && mbar_wait(accfull, (chunks - 1) & 1, cap);
+        ok = __all_sync(kFullMask, ok);
+        fence_after();
+        if (!ok && lane == 0)
+            *fail = 1;
+        if (rank > 0) {
+            // this block's sums to the first block: [rank - 1][token][channel]
+            cluster_wait();
+            const uint32_t to = in_block(base + L::kRed + (rank - 1) * NT * kRows * 4, 0);
+#pragma unroll
+            for (int j = 0; j < HT; j += 8) {
+                float v[8];
+                if (ok && n > 0)
+                    tmem_ld8(v, tmem + lanes + half * HT + j);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    st_cluster(to + ((half * HT + j + e) * kRows + row) * 4,
+                               acc[j + e] + (n > 0 ? __float2int_rn(v[e]) : 0));
+            }
+            if (!ok && lane == 0)
+                st_cluster(in_block(smem_u32(const_cast<int *>(fail)), 0), 1);
+            cluster_arrive();
+        } else {
+            if (a.split > 1) {
+                cluster_wait();
+                cluster_arrive();
+                cluster_wait();                             // the other blocks' sums are here
+            }
+            const int c = n0 + row;
+            const bool in = c < a.N;
+            const float ws = in ? __ldg(a.ws + c) : 0.f, bias = in && a.bias ? __ldg(a.bias + c) : 0.f;
+            const bool bad = a.split > 1 ? (!ok || *fail != 0) : !ok;
+#pragma unroll
+            for (int j = 0; j < HT; j += 8) {
+                float v[8];
+                if (ok)
+                    tmem_ld8(v, tmem + lanes + half * HT + j);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int col = half * HT + j + e, t = m0 + col;
+                    float sum = v[e];
+                    if (ints) {
+                        int tot = acc[j + e] + __float2int_rn(v[e]);
+                        for (int r = 1; r < a.split; ++r)
+                            tot += *reinterpret_cast<const int *>(sm + L::kRed + (((r - 1) * NT + col) * kRows + row) * 4);
+                        sum = __int2float_rn(tot);
+                    }
+                    if (t < a.M && in) {
+                        float o = fmaf(sum * __ldg(a.xs + t), ws, bias);
+                        if (bad)
+                            o = __int_as_float(0x7fc00000);
+                        static_cast<T *>(a.out)[t * a.so + c] = from_float<T>(o);
+                    }
                 }
             }
-            xt[r][c] = (int)xv;
-            wt[r][c] = (int)wv;
         }
-        __syncthreads();
-        for (int c = 0; c < kStep / 4; ++c) {
-            int xv[4], wv[4];
-            for (int i = 0; i < 4; ++i) {
-                xv[i] = xt[ty + 16 * i][c];
-                wv[i] = wt[tx + 16 * i][c];
-            }
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __dp4a(xv[i], wv[j], acc[i][j]);
-        }
-        __syncthreads();
+        fence_before();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < a.M && n < a.N) {
-                float v = (float)acc[i][j] * a.xs[m] * a.ws[n];
-                if (a.bias)
-                    v += a.bias[n];
-                static_cast<T *>(a.out)[m * a.so + n] = from_float<T>(v);
-            }
-        }
+    __syncwarp();
+    // the other warps' share of the cluster's barriers
+    if (a.split > 1 && warp >= kConvWarps) {
+        cluster_wait();
+        cluster_arrive();
+        if (rank == 0)
+            cluster_wait();
+    }
+    __syncthreads();
+    if (a.split > 1 && rank > 0)
+        cluster_wait();
+    if (warp == kWarpMma) {
+        fence_after();
+        tmem_dealloc(tmem, L::kTmem);
+    }
 }
+
+// Tokens as fp16 rows of `kp` elements (blocks below `xblocks`), weights as rows
+// of `kp` bytes (the others); 16 values a thread.
+struct PackArgs {
+    const int8_t *x, *w;
+    __half *x16;
+    int8_t *wp;
+    int M, N, K, kp;
+    long long sx, sw;
+    unsigned xblocks;
+};
+
+__global__ void __launch_bounds__(256)
+int8_pack_kernel(const PackArgs a)
+{
+    griddep_entry();
+    const bool tokens = blockIdx.x < a.xblocks;
+    const long long i = (long long)(blockIdx.x - (tokens ? 0 : a.xblocks)) * 256 + threadIdx.x;
+    const int per_row = a.kp / 16, rows = tokens ? a.M : a.N;
+    const long long r = i / per_row;
+    const int k = (int)(i - r * per_row) * 16;
+    if (r >= rows)
+        return;
+    const int8_t *src = (tokens ? a.x + r * a.sx : a.w + r * a.sw) + k;
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (k + 16 <= a.K && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(src);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (k + e < a.K)
+                v[e >> 2] |= (uint32_t)(uint8_t)src[e] << (8 * (e & 3));
+    }
+    if (tokens) {
+        uint4 o[2];
+        bytes_to_half(v[0], o[0].x, o[0].y);
+        bytes_to_half(v[1], o[0].z, o[0].w);
+        bytes_to_half(v[2], o[1].x, o[1].y);
+        bytes_to_half(v[3], o[1].z, o[1].w);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.x16 + r * a.kp + k);
+        dst[0] = o[0];
+        dst[1] = o[1];
+    } else {
+        *reinterpret_cast<uint4 *>(a.wp + r * a.kp + k) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// [rows][width] of bytes or fp16 in boxes of kTerms x box_rows; zeros outside.
+bool encode_rows(CUtensorMap *map, const void *p, bool half, int width, int rows, long long stride_bytes, int box_rows,
+                 CUtensorMapSwizzle swizzle)
+{
+    const auto fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride_bytes};
+    const cuuint32_t box[2] = {kTerms, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p),
+              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tma_rows(const void *p, long long stride) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride) & 15) == 0; }
+
+// Tokens of a tile, blocks of a cluster, and whether tokens stay bytes.
+struct Shape {
+    int nt, split;
+    bool xconv;
+};
+
+Shape pick_shape(int M, int N, int K, bool x_tma)
+{
+    const long long tn = (N + kRows - 1) / kRows;
+    Shape s{256, 1, false};
+    for (int nt : {16, 32, 64, 128, 256})
+        if (M <= nt || nt == 256) {
+            s.nt = nt;
+            break;
+        }
+    while (s.nt > 64 && tn * ((M + s.nt - 1) / s.nt) < 152)
+        s.nt /= 2;
+    if (s.nt <= 64) {
+        const int stages = (K + kTerms - 1) / kTerms, most = s.nt == 16 ? 6 : s.nt == 32 ? 4 : 2;
+        const long long tiles = tn * ((M + s.nt - 1) / s.nt);
+        while (s.split < most && tiles * (s.split + 1) <= 304 && stages / (s.split + 1) >= 4)
+            ++s.split;
+    }
+    s.xconv = s.nt <= 64 && x_tma;
+    return s;
+}
+
+template <class T, int NT, bool XCONV>
+cudaError_t launch_tile(const I8Args &a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t st)
+{
+    const int smem = I8Layout<NT, XCONV>::total(a.split);
+    const auto kernel = int8_matmul_kernel<T, NT, XCONV>;
+    cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.tiles_m * a.tiles_n * a.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.split > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a, wmap, xmap);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_type(const I8Args &a, const Shape &s, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t st)
+{
+    switch (s.nt) {
+    case 16: return s.xconv ? launch_tile<T, 16, true>(a, wmap, xmap, st) : launch_tile<T, 16, false>(a, wmap, xmap, st);
+    case 32: return s.xconv ? launch_tile<T, 32, true>(a, wmap, xmap, st) : launch_tile<T, 32, false>(a, wmap, xmap, st);
+    case 64: return s.xconv ? launch_tile<T, 64, true>(a, wmap, xmap, st) : launch_tile<T, 64, false>(a, wmap, xmap, st);
+    case 128: return launch_tile<T, 128, false>(a, wmap, xmap, st);
+    default: return launch_tile<T, 256, false>(a, wmap, xmap, st);
+    }
+}
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t int8_matmul_workspace_bytes(int, int, int) { return 0; }
+size_t int8_matmul_workspace_bytes(const void *x, const void *w, int M, int N, int K, long long sx, long long sw)
+{
+    const Shape s = pick_shape(M, N, K, tma_rows(x, sx));
+    const size_t kp = ((size_t)K + 15) / 16 * 16;
+    return (s.xconv ? 0 : up256((size_t)M * kp * 2)) + (tma_rows(w, sw) ? 0 : up256((size_t)N * kp));
+}
 
 cudaError_t launch_int8_matmul(const int8_t *x, const float *xs, const int8_t *w, const float *ws, const float *bias,
                                void *out, int M, int N, int K, int dtype, long long sx, long long sw, long long so,
-                               void *, cudaStream_t st)
+                               void *workspace, cudaStream_t st)
 {
-    const I8Args a{x, w, xs, ws, bias, out, M, N, K, sx, sw, so};
-    const dim3 grid((unsigned)((M + kTile - 1) / kTile), (unsigned)((N + kTile - 1) / kTile));
+    const Shape s = pick_shape(M, N, K, tma_rows(x, sx));
+    const bool pack_w = !tma_rows(w, sw);
+    const int kp = (K + 15) / 16 * 16;
+    PackArgs p{};
+    p.x = x; p.w = w; p.M = M; p.N = N; p.K = K; p.kp = kp; p.sx = sx; p.sw = sw;
+    p.x16 = static_cast<__half *>(workspace);
+    p.wp = static_cast<int8_t *>(workspace) + (s.xconv ? 0 : up256((size_t)M * kp * 2));
+    const long long xb = s.xconv ? 0 : ((long long)M * (kp / 16) + 255) / 256;
+    const long long wb = pack_w ? ((long long)N * (kp / 16) + 255) / 256 : 0;
+    p.xblocks = (unsigned)xb;
+    CUtensorMap wmap, xmap;
+    if (!encode_rows(&wmap, pack_w ? p.wp : w, false, K, N, pack_w ? kp : sw, kRows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !(s.xconv ? encode_rows(&xmap, x, false, K, M, sx, s.nt, CU_TENSOR_MAP_SWIZZLE_NONE)
+                  : encode_rows(&xmap, p.x16, true, K, M, (long long)kp * 2, s.nt, CU_TENSOR_MAP_SWIZZLE_128B)))
+        return cudaErrorInvalidValue;
+    if (xb + wb > 0) {
+        const cudaError_t e = launch_pdl(int8_pack_kernel, dim3((unsigned)(xb + wb)), dim3(256), 0, st, p);
+        if (e != cudaSuccess)
+            return e;
+    }
+    I8Args a{xs, ws, bias, out, M, N, K, so, (M + s.nt - 1) / s.nt, (N + kRows - 1) / kRows, s.split, debug_fail_waits() ? 1 : 0};
     switch (dtype) {
-    case kF32: return launch_pdl(int8_matmul_kernel<float>, grid, dim3(256), 0, st, a);
-    case kBF16: return launch_pdl(int8_matmul_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, a);
-    case kF16: return launch_pdl(int8_matmul_kernel<__half>, grid, dim3(256), 0, st, a);
+    case kF32: return launch_type<float>(a, s, wmap, xmap, st);
+    case kBF16: return launch_type<__nv_bfloat16>(a, s, wmap, xmap, st);
+    case kF16: return launch_type<__half>(a, s, wmap, xmap, st);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -64,6 +64,7 @@ __device__ __forceinline__ void st_release(int *p, int v)
 // checked on the host, and a kernel's status word read back.  The last two
 // synchronise and return an ssm_status.
 bool debug_checks();
+bool debug_fail_waits();                  // SSM_SCAN_TEST_FAIL_WAITS=1: bounded waits give up at once
 int debug_check_sequences(const int32_t *seq_starts, const int32_t *seq_lens, int n_seqs, int n_tokens,
                           cudaStream_t stream);
 int debug_read_status(const int *status, cudaStream_t stream);
@@ -78,7 +79,7 @@ cudaError_t launch_add_norm_backward(const void *gy, const void *h, const void *
                                      long long sgy, long long sh, long long sgh, long long sgi, cudaStream_t st);
 
 // int8_matmul.cu
-size_t int8_matmul_workspace_bytes(int M, int N, int K);
+size_t int8_matmul_workspace_bytes(const void *x, const void *w, int M, int N, int K, long long sx, long long sw);
 cudaError_t launch_int8_matmul(const int8_t *x, const float *xs, const int8_t *w, const float *ws, const float *bias,
                                void *out, int M, int N, int K, int dtype, long long sx, long long sw, long long so,
                                void *workspace, cudaStream_t st);

@@ -330,7 +330,7 @@ def ssm_int8_matmul(x, x_scales, w, w_scales, *, bias=None, out=None, out_dtype=
         if out is None:
             out = torch.empty((T, N), dtype=out_dtype, device=dev)
         po, so = _rows(out, "out", out_dtype, dev, (T, N))
-        ws, nb, workspace = _workspace(workspace, lib.ssm_int8_matmul_workspace_bytes(T, N, K), dev)
+        ws, nb, workspace = _workspace(workspace, lib.ssm_int8_matmul_workspace_bytes(px, pw, T, N, K, sx, sw), dev)
         rc = lib.ssm_int8_matmul(px, pxs, pw, pws, pb, po, T, N, K, code, sx, sw, so, ws, nb, handle)
     if rc != SSM_OK:
         raise SsmScanError(rc, "ssm_int8_matmul")
