@@ -49,7 +49,9 @@ constexpr int kTerms = 64;                    // terms of a stage
 constexpr int kFold = 16;                     // stages whose sum is exact in fp32: 16 x 64 x 2^14 = 2^24
 constexpr int kWStages = 6;                   // weight stages (8 KB each)
 constexpr int kABufs = 4;                     // converted weight stages in tensor memory (32 columns each)
-constexpr int kConvWarps = 8;
+constexpr int kXRing = 5;                     // fp16 token stages
+constexpr int kConvWarps = 8;                 // two groups of four: a group converts every other stage
+constexpr int kGroupWarps = 4;
 constexpr int kWarpW = 8, kWarpMma = 9, kWarpX = 10;
 constexpr int kThreads = 352;
 
@@ -65,7 +67,7 @@ struct I8Args {
 // Shared memory (bytes; tiles 1024-aligned).
 template <int NT, bool XCONV>
 struct I8Layout {
-    static constexpr int kXStages = XCONV ? kABufs : 4;
+    static constexpr int kXStages = XCONV ? kABufs : kXRing;
     static constexpr int kXTile = NT * 128;                 // 64 fp16 terms of NT tokens
     static constexpr int kW = 0;
     static constexpr int kX = kW + kWStages * kRows * kTerms;
@@ -73,8 +75,8 @@ struct I8Layout {
     static constexpr int kRed = kXi + (XCONV ? kWStages * NT * kTerms : 0);
     static int red_bytes(int split) { return (split - 1) * NT * kRows * 4; }
     // mbarriers (after the split's sums, whose size the launch knows)
-    static constexpr int kBars = 2 * kWStages + 2 * 4 + 2 * kABufs + 4;
-    static int total(int split) { return kRed + red_bytes(split) + kBars * 8 + 32; }
+    static constexpr int kBars = 2 * kWStages + 2 * kXRing + 2 * kABufs + 4;
+    static int total(int split) { return kRed + red_bytes(split) + kBars * 8 + 16 + NT * 4; }
     static constexpr int kTmem = NT + 32 * kABufs <= 256 ? 256 : 512;
 };
 
@@ -87,7 +89,7 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
 }
 
 // kind::f16, A and B fp16 (K-major), D fp32, M x N.
-__device__ __forceinline__ uint32_t idesc_f16(int m, int n)
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n)
 {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
@@ -124,16 +126,76 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(float (&v)[8], uint32_t taddr)
+// C consecutive fp32 TMEM columns of this thread's lane (C = 8 or 32).
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[C], uint32_t taddr)
 {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr) : "memory");
+    static_assert(C == 8 || C == 32, "columns");
+    if constexpr (C == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr) : "memory");
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                       "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                       "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                       "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                     : "r"(taddr) : "memory");
+    }
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = __uint_as_float(r[i]);
+}
+
+// Place in a ring of N stages and the parity of its current round: a full
+// barrier is waited for with `phase`, an empty one with `phase ^ 1` (which a fresh
+// barrier passes).
+template <int N>
+struct Ring {
+    uint32_t s = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == N) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Poll an mbarrier phase (shared-memory address); false after `cap` polls.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int cap)
+{
+    for (int it = 0; it < cap; ++it) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}\n"
+                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done)
+            return true;
+    }
+    return false;
+}
+
+__device__ __forceinline__ void arrive_bar(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void commit_bar(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
+// One lane of a converged warp.  The tensor-core warp runs its loop with all lanes
+// (so its addresses stay in uniform registers) and issues from this one: with the
+// whole loop inside `lane == 0` a stage took 1100 cycles to issue, twice what
+// its products take.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
 }
 
 // A shared-memory address of this block as seen in block `rank` of the cluster.
@@ -170,26 +232,30 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
     const int k0 = (int)((long long)nk * rank / a.split), n = (int)((long long)nk * (rank + 1) / a.split) - k0;
     const int red = L::kRed + (a.split - 1) * NT * kRows * 4;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + red);
-    uint64_t *wfull = bars, *wempty = wfull + kWStages, *xfull = wempty + kWStages, *xempty = xfull + 4;
-    uint64_t *afull = xempty + 4, *aempty = afull + kABufs, *accfull = aempty + kABufs, *accempty = accfull + 1;
+    uint64_t *wfull = bars, *wempty = wfull + kWStages, *xfull = wempty + kWStages, *xempty = xfull + kXRing;
+    uint64_t *afull = xempty + kXRing, *aempty = afull + kABufs, *accfull = aempty + kABufs, *accempty = accfull + 1;
     uint64_t *drain = accempty + 1;
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
     volatile int *fail = reinterpret_cast<volatile int *>(slot + 1);
-    const long cap = a.fail_waits ? 0 : kSpinLimit;
+    float *xsc = reinterpret_cast<float *>(slot + 4);       // the tokens' scales
+    const int cap = a.fail_waits ? 0 : (int)kSpinLimit;
+    const uint32_t b_wfull = smem_u32(wfull), b_wempty = smem_u32(wempty), b_xfull = smem_u32(xfull);
+    const uint32_t b_xempty = smem_u32(xempty), b_afull = smem_u32(afull), b_aempty = smem_u32(aempty);
+    const uint32_t b_accfull = smem_u32(accfull), b_accempty = smem_u32(accempty);
 
     if (warp == kWarpMma)
         tmem_alloc(slot, L::kTmem);
     if (tid == 0) {
         for (int i = 0; i < kWStages; ++i) {
             mbar_init(wfull + i, 1);
-            mbar_init(wempty + i, kConvWarps);
+            mbar_init(wempty + i, kGroupWarps);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kXRing; ++i) {
             mbar_init(xfull + i, 1);
             mbar_init(xempty + i, 1);
         }
         for (int i = 0; i < kABufs; ++i) {
-            mbar_init(afull + i, kConvWarps);
+            mbar_init(afull + i, kGroupWarps);
             mbar_init(aempty + i, 1);
         }
         mbar_init(accfull, 1);
@@ -198,6 +264,8 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
         mbar_init_fence();
         *fail = 0;
     }
+    for (int i = tid; i < NT; i += kThreads)
+        xsc[i] = m0 + i < a.M ? __ldg(a.xs + m0 + i) : 0.f;
     fence_before();
     __syncthreads();
     if (a.split > 1)
@@ -206,67 +274,85 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
     const uint32_t tmem = *slot, tmem_a = tmem + NT;
 
     if (warp == kWarpW) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % kWStages;
-                if (i >= kWStages && !mbar_wait(wempty + s, (i / kWStages - 1) & 1, cap)) {
-                    *fail = 1;
-                    break;
-                }
-                mbar_expect_tx(wfull + s, kRows * kTerms + (XCONV ? NT * kTerms : 0));
-                tma_2d(base + L::kW + s * kRows * kTerms, &wmap, (k0 + i) * kTerms, n0, wfull + s);
-                if (XCONV)
-                    tma_2d(base + L::kXi + s * NT * kTerms, &xmap, (k0 + i) * kTerms, m0, wfull + s);
+        Ring<kWStages> w;
+        int i = 0;
+        for (; i < n; ++i) {
+            if (!__all_sync(kFullMask, wait_bar(b_wempty + 8 * w.s, w.phase ^ 1, cap))) {
+                *fail = 1;
+                break;
             }
-            for (int j = max(0, i - kWStages); j < i; ++j)  // no copy lands after the block has gone
-                mbar_wait(wfull + j % kWStages, (j / kWStages) & 1);
+            if (elect_one()) {
+                mbar_expect_tx(wfull + w.s, kRows * kTerms + (XCONV ? NT * kTerms : 0));
+                tma_2d(base + L::kW + w.s * kRows * kTerms, &wmap, (k0 + i) * kTerms, n0, wfull + w.s);
+                if (XCONV)
+                    tma_2d(base + L::kXi + w.s * NT * kTerms, &xmap, (k0 + i) * kTerms, m0, wfull + w.s);
+            }
+            w.next();
         }
+        for (int j = max(0, i - kWStages); j < i; ++j)      // no copy lands after the block has gone
+            wait_bar(b_wfull + 8 * (j % kWStages), (j / kWStages) & 1, (int)kSpinLimit);
     } else if (warp == kWarpX) {
-        if (!XCONV && lane == 0) {
+        if (!XCONV) {
+            Ring<L::kXStages> x;
             int i = 0;
             for (; i < n; ++i) {
-                const int s = i % L::kXStages;
-                if (i >= L::kXStages && !mbar_wait(xempty + s, (i / L::kXStages - 1) & 1, cap)) {
+                if (!__all_sync(kFullMask, wait_bar(b_xempty + 8 * x.s, x.phase ^ 1, cap))) {
                     *fail = 1;
                     break;
                 }
-                mbar_expect_tx(xfull + s, L::kXTile);
-                tma_2d(base + L::kX + s * L::kXTile, &xmap, (k0 + i) * kTerms, m0, xfull + s);
+                if (elect_one()) {
+                    mbar_expect_tx(xfull + x.s, L::kXTile);
+                    tma_2d(base + L::kX + x.s * L::kXTile, &xmap, (k0 + i) * kTerms, m0, xfull + x.s);
+                }
+                x.next();
             }
             for (int j = max(0, i - L::kXStages); j < i; ++j)
-                mbar_wait(xfull + j % L::kXStages, (j / L::kXStages) & 1);
+                wait_bar(b_xfull + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            const uint32_t id = idesc_f16(kRows, NT);
-            for (int i = 0; i < n; ++i) {
-                const int b = i % kABufs, s = i % L::kXStages;
-                bool ok = mbar_wait(afull + b, (i / kABufs) & 1, cap);
-                if (!XCONV)
-                    ok = ok && mbar_wait(xfull + s, (i / L::kXStages) & 1, cap);
-                if (i > 0 && i % kFold == 0)
-                    ok = ok && mbar_wait(accempty, (i / kFold - 1) & 1, cap);
-                if (!ok) {
-                    *fail = 1;
-                    break;
-                }
-                fence_after();
-                const uint64_t bd = desc_sw128(base + L::kX + s * L::kXTile);
+        constexpr uint32_t id = idesc_f16(kRows, NT);
+        Ring<kABufs> ab;
+        Ring<L::kXStages> x;                                // XCONV: as many token tiles as weight buffers
+        const uint64_t bd0 = desc_sw128(base + L::kX);
+        uint32_t chunk = 0;
+        int left = kFold;                                   // stages until the accumulator is moved
+        for (int i = 0; i < n; ++i) {
+            bool ok = wait_bar(b_afull + 8 * ab.s, ab.phase, cap);
+            if (!XCONV)
+                ok = ok && wait_bar(b_xfull + 8 * x.s, x.phase, cap);
+            if (left == kFold)
+                ok = ok && wait_bar(b_accempty, (chunk & 1) ^ 1, cap);
+            if (!__all_sync(kFullMask, ok)) {
+                *fail = 1;
+                break;
+            }
+            fence_after();
+            if (elect_one()) {
+                const uint64_t bd = bd0 + x.s * (L::kXTile >> 4);
+                const uint32_t at = tmem_a + 32 * ab.s;
 #pragma unroll
                 for (int kk = 0; kk < kTerms / 16; ++kk)
-                    mma_f16_ts(tmem, tmem_a + 32 * b + 8 * kk, bd + 2 * kk, id, (i % kFold) != 0 || kk > 0);
-                commit(aempty + b);
+                    mma_f16_ts(tmem, at + 8 * kk, bd + 2 * kk, id, left != kFold || kk > 0);
+                commit_bar(b_aempty + 8 * ab.s);
                 if (!XCONV)
-                    commit(xempty + s);
-                if (i % kFold == kFold - 1 || i == n - 1)
-                    commit(accfull);
+                    commit_bar(b_xempty + 8 * x.s);
+                if (left == 1 || i == n - 1)
+                    commit_bar(b_accfull);
             }
-            commit(drain);                                  // every product issued is done before TMEM is freed
-            mbar_wait(drain, 0);
+            __syncwarp();
+            if (--left == 0) {
+                left = kFold;
+                ++chunk;
+            }
+            ab.next();
+            x.next();
         }
+        if (elect_one())
+            commit_bar(smem_u32(drain));                    // every product issued is done before TMEM is freed
+        __syncwarp();
+        wait_bar(smem_u32(drain), 0, (int)kSpinLimit);
     } else {
-        const int q = warp & 3, half = warp >> 2;           // TMEM lanes 32 q .., half of the terms / of the tokens
+        const int q = warp & 3, half = warp >> 2;           // TMEM lanes 32 q ..; group, and half of the tokens
         const int row = 32 * q + lane;
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         constexpr int HT = NT / 2;                          // tokens of this thread
@@ -280,70 +366,81 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
         int folded = 0;
         bool ok = true;
         // the accumulator into the integers
+        constexpr int LC = HT < 32 ? 8 : 32;                // columns of a TMEM load
         auto fold = [&]() {
-            ok = ok && mbar_wait(accfull, folded & 1, cap);
+            ok = ok && wait_bar(b_accfull, folded & 1, cap);
             if (__all_sync(kFullMask, ok)) {
                 fence_after();
 #pragma unroll
-                for (int j = 0; j < HT; j += 8) {
-                    float v[8];
-                    tmem_ld8(v, tmem + lanes + half * HT + j);
+                for (int j = 0; j < HT; j += LC) {
+                    uint32_t v[LC];
+                    tmem_ld<LC>(v, tmem + lanes + half * HT + j);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[j + e] += __float2int_rn(v[e]);
+                    for (int e = 0; e < LC; ++e)
+                        acc[j + e] += __float2int_rn(__uint_as_float(v[e]));
                 }
                 fence_before();
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(accempty);
+                arrive_bar(b_accempty);
             ++folded;
         };
-        for (int i = 0; i < n; ++i) {
-            if (i % kFold == 2 && i > kFold)                // two stages of the next sum are ready
+        int fold_at = kFold + 2 + half;                     // a stage of each group of the next sum is ready then
+        Ring<kWStages> w;
+        Ring<kABufs> ab;
+        if (half) {
+            w.next();
+            ab.next();
+        }
+        for (int i = half; i < n; i += 2) {
+            if (i == fold_at) {
                 fold();
-            const int s = i % kWStages, b = i % kABufs;
-            ok = ok && mbar_wait(wfull + s, (i / kWStages) & 1, cap);
+                fold_at += kFold;
+            }
+            const uint32_t s = w.s, b = ab.s;
+            ok = ok && wait_bar(b_wfull + 8 * s, w.phase, cap);
             if (!__all_sync(kFullMask, ok)) {
                 ok = false;
                 break;
             }
-            // 32 bytes of this thread's weight row: 16-byte chunks 2 half, 2 half + 1 of the 64-byte swizzle
+            // this thread's weight row, 16-byte chunks of the 64-byte swizzle
             const unsigned char *wr = sm + L::kW + s * kRows * kTerms + row * kTerms;
             const int sw = (row >> 1) & 3;
-            const uint4 c0 = *reinterpret_cast<const uint4 *>(wr + (((2 * half) ^ sw) << 4));
-            const uint4 c1 = *reinterpret_cast<const uint4 *>(wr + (((2 * half + 1) ^ sw) << 4));
-            constexpr int XW = XCONV ? NT / 16 : 1;
+            uint4 c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                c[j] = *reinterpret_cast<const uint4 *>(wr + ((j ^ sw) << 4));
+            constexpr int XW = XCONV ? NT / 8 : 1;
             uint32_t xw[XW];
             if (XCONV)
 #pragma unroll
                 for (int j = 0; j < XW; ++j)
-                    xw[j] = *reinterpret_cast<const uint32_t *>(sm + L::kXi + s * NT * kTerms + (tid + 256 * j) * 4);
+                    xw[j] = *reinterpret_cast<const uint32_t *>(sm + L::kXi + s * NT * kTerms + (row + 128 * j) * 4);
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(wempty + s);
-            uint32_t h[16];
-            bytes_to_half(c0.x, h[0], h[1]);
-            bytes_to_half(c0.y, h[2], h[3]);
-            bytes_to_half(c0.z, h[4], h[5]);
-            bytes_to_half(c0.w, h[6], h[7]);
-            bytes_to_half(c1.x, h[8], h[9]);
-            bytes_to_half(c1.y, h[10], h[11]);
-            bytes_to_half(c1.z, h[12], h[13]);
-            bytes_to_half(c1.w, h[14], h[15]);
-            if (i >= kABufs) {
-                ok = mbar_wait(aempty + b, (i / kABufs - 1) & 1, cap);
-                if (!__all_sync(kFullMask, ok)) {
-                    ok = false;
-                    break;
-                }
-                fence_after();
+                arrive_bar(b_wempty + 8 * s);
+            uint32_t h[2][16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t *o = h[j >> 1] + 8 * (j & 1);
+                bytes_to_half(c[j].x, o[0], o[1]);
+                bytes_to_half(c[j].y, o[2], o[3]);
+                bytes_to_half(c[j].z, o[4], o[5]);
+                bytes_to_half(c[j].w, o[6], o[7]);
             }
-            tmem_st16u(tmem_a + lanes + 32 * b + 16 * half, h);
+            ok = wait_bar(b_aempty + 8 * b, ab.phase ^ 1, cap);
+            if (!__all_sync(kFullMask, ok)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            tmem_st16u(tmem_a + lanes + 32 * b, h[0]);
+            tmem_st16u(tmem_a + lanes + 32 * b + 16, h[1]);
             if (XCONV) {
 #pragma unroll
                 for (int j = 0; j < XW; ++j) {
-                    const int e = tid + 256 * j, t = e >> 4, w = e & 15;
+                    const int e = row + 128 * j, t = e >> 4, w = e & 15;
                     uint2 v;
                     bytes_to_half(xw[j], v.x, v.y);
                     *reinterpret_cast<uint2 *>(sm + L::kX + b * L::kXTile + t * 128 + (((w >> 1) ^ (t & 7)) << 4) +
@@ -355,13 +452,16 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
             fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(afull + b);
+                arrive_bar(b_afull + 8 * b);
+            w.next();
+            w.next();
+            ab.next();
+            ab.next();
         }
         if (ok)
             while (folded < chunks - 1)
                 fold();
-        if (n > 0)
-            ok = ok && mbar_wait(accfull, (chunks - 1) & 1, cap);
+        ok = ok && wait_bar(b_accfull, (chunks - 1) & 1, cap);
         ok = __all_sync(kFullMask, ok);
         fence_after();
         if (!ok && lane == 0)
@@ -371,14 +471,13 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
             cluster_wait();
             const uint32_t to = in_block(base + L::kRed + (rank - 1) * NT * kRows * 4, 0);
 #pragma unroll
-            for (int j = 0; j < HT; j += 8) {
-                float v[8];
-                if (ok && n > 0)
-                    tmem_ld8(v, tmem + lanes + half * HT + j);
+            for (int j = 0; j < HT; j += LC) {
+                uint32_t v[LC];
+                tmem_ld<LC>(v, tmem + lanes + half * HT + j);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < LC; ++e)
                     st_cluster(to + ((half * HT + j + e) * kRows + row) * 4,
-                               acc[j + e] + (n > 0 ? __float2int_rn(v[e]) : 0));
+                               acc[j + e] + __float2int_rn(__uint_as_float(v[e])));
             }
             if (!ok && lane == 0)
                 st_cluster(in_block(smem_u32(const_cast<int *>(fail)), 0), 1);
@@ -393,27 +492,26 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
             const bool in = c < a.N;
             const float ws = in ? __ldg(a.ws + c) : 0.f, bias = in && a.bias ? __ldg(a.bias + c) : 0.f;
             const bool bad = a.split > 1 ? (!ok || *fail != 0) : !ok;
+            T *out = static_cast<T *>(a.out) + (long long)(m0 + half * HT) * a.so + c;
+            const int left = in ? a.M - m0 - half * HT : 0; // tokens of this thread that exist
 #pragma unroll
-            for (int j = 0; j < HT; j += 8) {
-                float v[8];
-                if (ok)
-                    tmem_ld8(v, tmem + lanes + half * HT + j);
+            for (int j = 0; j < HT; j += LC) {
+                uint32_t v[LC];
+                tmem_ld<LC>(v, tmem + lanes + half * HT + j);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int col = half * HT + j + e, t = m0 + col;
-                    float sum = v[e];
+                for (int e = 0; e < LC; ++e) {
+                    const int col = half * HT + j + e;
+                    float sum = __uint_as_float(v[e]);
                     if (ints) {
-                        int tot = acc[j + e] + __float2int_rn(v[e]);
+                        int tot = acc[j + e] + __float2int_rn(sum);
                         for (int r = 1; r < a.split; ++r)
                             tot += *reinterpret_cast<const int *>(sm + L::kRed + (((r - 1) * NT + col) * kRows + row) * 4);
                         sum = __int2float_rn(tot);
                     }
-                    if (t < a.M && in) {
-                        float o = fmaf(sum * __ldg(a.xs + t), ws, bias);
-                        if (bad)
-                            o = __int_as_float(0x7fc00000);
-                        static_cast<T *>(a.out)[t * a.so + c] = from_float<T>(o);
-                    }
+                    const float o = bad ? __int_as_float(0x7fc00000) : fmaf(sum * xsc[col], ws, bias);
+                    if (j + e < left)
+                        *out = from_float<T>(o);
+                    out += a.so;
                 }
             }
         }
