@@ -452,31 +452,24 @@ typedef enum {
  *   chunk_states NULL, or (training) fp32 [ssm_gated_scan_chunks(...)][channels],
  *                out: the state entering each time chunk, which the backward
  *                pass reads
- *   workspace    256-byte aligned, at least ssm_gated_scan_workspace_bytes(...)
- *                (training 1 with chunk_states); scratch, not shared by calls
- *                that overlap on the GPU
  * Where n_tokens == n_seqs and chunk_states is NULL (one token a sequence) the
- * call steps every sequence token by token, needs no workspace and is one
- * launch; otherwise sequences are cut into time chunks that run in parallel and
- * pass their states on.  That wait is bounded: on giving up y and the slots
- * behind it become NaN and, under SSM_SCAN_CHECK=1, the call returns
- * SSM_ERR_TIMEOUT.  y must not overlap an input.
+ * call steps every sequence token by token; otherwise blocks walk the sequences'
+ * time chunks, with the time of a sequence shared by a cluster of blocks where
+ * there are few sequences and channels.  One launch, no workspace, the same bits
+ * every time.  The cluster's waits are bounded: on giving up y and the slots
+ * behind it become NaN.  y must not overlap an input.
  * Errors: SSM_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, strides
- * below channels, workspace), SSM_ERR_UNSUPPORTED (more than 2^31 (chunk,
- * 32 channels) pairs), SSM_ERR_CUDA.
+ * below channels), SSM_ERR_UNSUPPORTED (more than 2^28 (sequence, 64 channels)
+ * pairs), SSM_ERR_CUDA.
  */
 int ssm_gated_scan(float *state_slots, const void *x, const void *gate_a, const void *gate_x, const float *lam,
                    float decay_scale, void *y, const int32_t *seq_starts, const int32_t *seq_lens,
                    const int32_t *resume_flags, int n_seqs, int n_tokens, int channels, int dtype,
                    long long x_stride, long long gate_a_stride, long long gate_x_stride, long long y_stride,
-                   float *chunk_states, void *workspace, size_t workspace_bytes, void *stream);
+                   float *chunk_states, void *stream);
 
 /* Rows of chunk_states for these sizes; 0 for invalid or unsupported ones. */
 long long ssm_gated_scan_chunks(int n_seqs, int n_tokens, int channels);
-
-/* Workspace of ssm_gated_scan (training 0, or 1 with chunk_states) and of
- * ssm_gated_scan_backward (training 1). */
-size_t ssm_gated_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, int training);
 
 /*
  * Gradients of ssm_gated_scan.  Takes the forward call's inputs, metadata and
@@ -488,8 +481,9 @@ size_t ssm_gated_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, in
  *                time; zeros when n_seqs is 0)
  *   grad_initial_state  [n_seqs][channels] fp32 or NULL: gradient of the slots
  *                before the call (zeros for fresh sequences)
- * h is recomputed in fp32 from chunk_states.  workspace: at least
- * ssm_gated_scan_workspace_bytes(n_seqs, n_tokens, channels, 1).
+ * h is recomputed in fp32 from chunk_states.  workspace: 256-byte aligned, at
+ * least ssm_gated_scan_backward_workspace_bytes(...); scratch, not shared by
+ * calls that overlap on the GPU.
  */
 int ssm_gated_scan_backward(const void *grad_y, const float *grad_state, const void *x, const void *gate_a,
                             const void *gate_x, const float *lam, float decay_scale, const float *chunk_states,
@@ -499,6 +493,8 @@ int ssm_gated_scan_backward(const void *grad_y, const float *grad_state, const v
                             void *grad_x, void *grad_gate_a, void *grad_gate_x, long long grad_x_stride,
                             long long grad_gate_a_stride, long long grad_gate_x_stride, float *grad_lam,
                             float *grad_initial_state, void *workspace, size_t workspace_bytes, void *stream);
+
+size_t ssm_gated_scan_backward_workspace_bytes(int n_seqs, int n_tokens, int channels);
 
 /*
  * RMS norm with the residual's addition, per row of `width` elements:

@@ -90,9 +90,9 @@ def load():
             lib.ssm_conv1d.argtypes = [_P] * 8 + [_I] * 4 + [_P, _P]
             L, F, S = ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
             for name, res, args in (
-                    ("ssm_gated_scan", _I, [_P] * 5 + [F] + [_P] * 4 + [_I] * 4 + [L] * 4 + [_P, _P, S, _P]),
+                    ("ssm_gated_scan", _I, [_P] * 5 + [F] + [_P] * 4 + [_I] * 4 + [L] * 4 + [_P, _P]),
                     ("ssm_gated_scan_chunks", L, [_I] * 3),
-                    ("ssm_gated_scan_workspace_bytes", S, [_I] * 4),
+                    ("ssm_gated_scan_backward_workspace_bytes", S, [_I] * 3),
                     ("ssm_gated_scan_backward", _I, [_P] * 6 + [F] + [_P] * 4 + [_I] * 4 + [L] * 4 + [_P] * 3 +
                      [L] * 3 + [_P, _P, _P, S, _P]),
                     ("ssm_add_norm", _I, [_P] * 3 + [F] + [_P] * 4 + [_I] * 4 + [L] * 4 + [_P]),

@@ -25,10 +25,8 @@ int gated_sizes(int n_seqs, int n_tokens, int channels)
 {
     if (n_seqs < 0 || n_tokens < 0 || channels <= 0)
         return SSM_ERR_INVALID_ARG;
-    const long long units = ssm::gated_max_units(n_seqs, n_tokens);
-    if (units * ((channels + 31LL) / 32) > INT_MAX)
-        return SSM_ERR_UNSUPPORTED;
-    return SSM_OK;
+    const long long blocks = (long long)n_seqs * ((channels + ssm::kGatedCh - 1LL) / ssm::kGatedCh) * ssm::kGatedMaxCluster;
+    return blocks > INT_MAX ? SSM_ERR_UNSUPPORTED : SSM_OK;
 }
 
 int int8_sizes(int rows, int out_features, int inner)
@@ -46,36 +44,27 @@ int gated_debug_check(const int32_t *starts, const int32_t *lens, int n_seqs, in
     return ssm::debug_checks() ? ssm::debug_check_sequences(starts, lens, n_seqs, n_tokens, stream) : SSM_OK;
 }
 
-// Debug mode: SSM_ERR_TIMEOUT when a bounded wait gave up.
-int gated_debug_status(const ssm::GatedArgs &a, bool chunked, cudaStream_t stream)
-{
-    return ssm::debug_checks() && chunked ? ssm::debug_read_status(a.control + 2, stream) : SSM_OK;
-}
-
 }  // namespace
 
 extern "C" {
 
 long long ssm_gated_scan_chunks(int n_seqs, int n_tokens, int channels)
 {
-    return gated_sizes(n_seqs, n_tokens, channels) == SSM_OK ? ssm::gated_max_units(n_seqs, n_tokens) : 0;
+    return gated_sizes(n_seqs, n_tokens, channels) == SSM_OK ? ssm::gated_chunk_rows(n_seqs, n_tokens) : 0;
 }
 
-size_t ssm_gated_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, int training)
+size_t ssm_gated_scan_backward_workspace_bytes(int n_seqs, int n_tokens, int channels)
 {
     if (n_seqs <= 0 || gated_sizes(n_seqs, n_tokens, channels) != SSM_OK)
         return 0;
-    if (!training)
-        return n_tokens == n_seqs ? 0 : ssm::gated_workspace_bytes(n_seqs, n_tokens, channels);
-    return ssm::gated_workspace_bytes(n_seqs, n_tokens, channels) +
-           (size_t)ssm::gated_max_units(n_seqs, n_tokens) * channels * sizeof(float);
+    return (size_t)n_seqs * ssm::gated_cluster(n_seqs, n_tokens, channels) * channels * sizeof(float);
 }
 
 int ssm_gated_scan(float *state_slots, const void *x, const void *gate_a, const void *gate_x, const float *lam,
                    float decay_scale, void *y, const int32_t *seq_starts, const int32_t *seq_lens,
                    const int32_t *resume_flags, int n_seqs, int n_tokens, int channels, int dtype,
                    long long x_stride, long long gate_a_stride, long long gate_x_stride, long long y_stride,
-                   float *chunk_states, void *workspace, size_t workspace_bytes, void *stream_v)
+                   float *chunk_states, void *stream_v)
 {
     int rc = gated_sizes(n_seqs, n_tokens, channels);
     if (rc != SSM_OK)
@@ -95,10 +84,6 @@ int ssm_gated_scan(float *state_slots, const void *x, const void *gate_a, const 
         !is_aligned(resume_flags, 4) || !is_aligned(chunk_states, 4) || !is_aligned(x, e) || !is_aligned(gate_a, e) ||
         !is_aligned(gate_x, e) || !is_aligned(y, e))
         return SSM_ERR_INVALID_ARG;
-    const bool chunked = n_tokens != n_seqs || chunk_states;
-    if (chunked && (!workspace || !is_aligned(workspace, 256) ||
-                    workspace_bytes < ssm::gated_workspace_bytes(n_seqs, n_tokens, channels)))
-        return SSM_ERR_INVALID_ARG;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_v);
     rc = gated_debug_check(seq_starts, seq_lens, n_seqs, n_tokens, stream);
     if (rc != SSM_OK)
@@ -109,12 +94,7 @@ int ssm_gated_scan(float *state_slots, const void *x, const void *gate_a, const 
     a.n_seqs = n_seqs; a.n_tokens = n_tokens; a.C = channels;
     a.sx = x_stride; a.sga = gate_a_stride; a.sgx = gate_x_stride; a.sy = y_stride;
     a.chunk_states = chunk_states;
-    rc = status_of(ssm::launch_gated_scan(a, dtype, workspace, stream));
-    if (rc == SSM_OK && chunked) {
-        a.control = static_cast<int *>(workspace);
-        rc = gated_debug_status(a, true, stream);
-    }
-    return rc;
+    return status_of(ssm::launch_gated_scan(a, dtype, stream));
 }
 
 int ssm_gated_scan_backward(const void *grad_y, const float *grad_state, const void *x, const void *gate_a,
@@ -136,8 +116,6 @@ int ssm_gated_scan_backward(const void *grad_y, const float *grad_state, const v
         return SSM_ERR_INVALID_ARG;
     if (!lam || !grad_lam || !is_aligned(lam, 4) || !is_aligned(grad_lam, 4))
         return SSM_ERR_INVALID_ARG;
-    if (!workspace || !is_aligned(workspace, 256) || workspace_bytes < 256)
-        return SSM_ERR_INVALID_ARG;
     if (n_seqs > 0 && (!chunk_states || !seq_starts || !seq_lens || !resume_flags))
         return SSM_ERR_INVALID_ARG;
     if (n_seqs > 0 && n_tokens > 0 && (!grad_y || !x || !gate_a || !gate_x || !grad_x || !grad_gate_a || !grad_gate_x))
@@ -151,7 +129,8 @@ int ssm_gated_scan_backward(const void *grad_y, const float *grad_state, const v
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_v);
     if (n_seqs == 0)                                       // no token: the parameter's gradient is zero
         return status_of(cudaMemsetAsync(grad_lam, 0, (size_t)channels * sizeof(float), stream));
-    if (workspace_bytes < ssm_gated_scan_workspace_bytes(n_seqs, n_tokens, channels, 1))
+    if (!workspace || !is_aligned(workspace, 256) ||
+        workspace_bytes < ssm_gated_scan_backward_workspace_bytes(n_seqs, n_tokens, channels))
         return SSM_ERR_INVALID_ARG;
     rc = gated_debug_check(seq_starts, seq_lens, n_seqs, n_tokens, stream);
     if (rc != SSM_OK)
@@ -166,12 +145,8 @@ int ssm_gated_scan_backward(const void *grad_y, const float *grad_state, const v
     a.grad_x = grad_x; a.grad_ga = grad_gate_a; a.grad_gx = grad_gate_x;
     a.gsx = grad_x_stride; a.gsga = grad_gate_a_stride; a.gsgx = grad_gate_x_stride;
     a.grad_lam = grad_lam; a.grad_state0 = grad_initial_state;
-    rc = status_of(ssm::launch_gated_scan_backward(a, dtype, workspace, stream));
-    if (rc == SSM_OK) {
-        a.control = static_cast<int *>(workspace);
-        rc = gated_debug_status(a, true, stream);
-    }
-    return rc;
+    a.lam_part = static_cast<float *>(workspace);
+    return status_of(ssm::launch_gated_scan_backward(a, dtype, stream));
 }
 
 int ssm_add_norm(const void *x, const void *residual, const float *weight, float eps, void *residual_out, void *y,

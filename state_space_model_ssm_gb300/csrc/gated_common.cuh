@@ -7,24 +7,34 @@
 //   log a = -decay_scale softplus(lam[c]) r,  a = exp(log a),  m = sqrt(1 - a^2)
 //   h_t = a_t h_{t-1} + b_t,  b_t = m_t i_t x_t,  y_t = h_t
 //
-// Time chunks.  The map of a run of tokens on the state is h -> P h + H, P the
-// product of its a_t and H the state it leaves from zero, and two such maps
-// compose: (P2, H2) after (P1, H1) is (P1 P2, P2 H1 + H2).  So a sequence is cut
-// into chunks of kGatedChunk tokens, a block scans one chunk of some channels
-// from zero, publishes (P, H), and obtains the state that enters its chunk from
-// the chunks before it: from the nearest one whose outgoing state is already
-// known and the (P, H) of those between.  Every input is read once.  Blocks
-// take their chunk from a counter in time order (tickets), so a chunk that a
-// block waits for is always in the hands of a block that runs already.
+// Time.  The map of a run of tokens on the state is h -> P h + H, P the product of
+// its a_t and H the state it leaves from zero, and two such maps compose: (P2, H2)
+// after (P1, H1) is (P1 P2, P2 H1 + H2).  A block owns 64 channels of one sequence and
+// walks its time chunks of 64 tokens with the state carried in registers; inside a
+// chunk its 8 warps take 8 tokens each from zero and put their maps together
+// through shared memory.  Where that leaves too few blocks, a cluster of R blocks
+// shares the sequence: in a round its blocks take R consecutive chunks, send each
+// other their chunk's map (16 bytes a channel pair, by asynchronous stores into the
+// peers' shared memory), and each composes the maps before its own.  Every input
+// is read once, there is one launch, no workspace and no word in global memory
+// that anybody waits for; the order of every operation is fixed, so the bits are too.
+//
+// A first version cut time into chunks for independent blocks that passed their
+// states on through global memory (look-back with flags): its fences and polls
+// cost 13 us a chunk, 7 times the arithmetic.
 #pragma once
 
 #include "layer_common.cuh"
+#include "tc_common.cuh"
 
 namespace ssm {
 
 constexpr int kGatedLen = 8;                               // tokens a thread holds in registers
 constexpr int kGatedWarps = 8;                             // runs of kGatedLen tokens per block
 constexpr int kGatedChunk = kGatedLen * kGatedWarps;       // tokens of a time chunk
+constexpr int kGatedCh = 64;                               // channels of a block: two a lane
+constexpr int kGatedTile = kGatedChunk * kGatedCh;
+constexpr int kGatedMaxCluster = 8;
 
 struct GatedArgs {
     float *state;                       // [n][C], in/out (forward)
@@ -35,7 +45,7 @@ struct GatedArgs {
     const int32_t *seq_starts, *seq_lens, *resume;
     int n_seqs, n_tokens, C;
     long long sx, sga, sgx, sy;         // token strides (elements)
-    float *chunk_states;                // [units][C]: the state entering each chunk (forward: out, may be null)
+    float *chunk_states;                // the state entering each chunk (gated_chunk_row; forward: out, may be null)
     // backward
     const void *grad_y;                 // [T][C], token stride sy
     const float *grad_state;            // [n][C] gradient of the slots after the call, or null
@@ -43,111 +53,268 @@ struct GatedArgs {
     long long gsx, gsga, gsgx;
     float *grad_lam;                    // [C]
     float *grad_state0;                 // [n][C] gradient of the slots before the call, or null
-    // workspace
-    int max_units;
-    int cblocks;                        // channel blocks of the launch (the stride of flags)
-    int2 *units;                        // (sequence, chunk) of each unit, sequences in order
-    int *unit_base;                     // [n + 1] first unit of each sequence
-    int *control;                       // [0] units, [1] ticket, [2] status
-    int *flags;                         // [units][cblocks]: 0 nothing, 1 (P, H), 2 the outgoing state
-    float *agg_p, *agg_h;               // [units][C]
-    float *out_state;                   // [units][C]
-    float *lam_part;                    // [units][C] (backward)
+    float *lam_part;                    // [n * cluster][C] workspace
+    int cblocks;                        // blocks of kGatedCh channels
+    int cluster;                        // blocks that share a sequence's time
+    int fail_waits;                     // test hook: bounded waits give up at once
 };
+
+// Row of chunk_states for chunk j of a sequence that starts at token t0: the first
+// chunk's by the sequence, the others' by their position (two chunks that begin in
+// the same 64 rows would overlap before them).  n_seqs + n_tokens / 64 + 1 rows.
+__host__ __device__ __forceinline__ long long gated_chunk_row(int n_seqs, int seq, long long t0, int j)
+{
+    return j == 0 ? seq : n_seqs + t0 / kGatedChunk + j;
+}
 
 // A sequence's token range; one that is not inside the packed rows counts as empty.
 __device__ __forceinline__ int gated_seq_len(const GatedArgs &a, int seq, long long &t0)
 {
     t0 = a.seq_starts[seq];
     const long long len = a.seq_lens[seq];
-    return t0 >= 0 && len > 0 && t0 + len <= a.n_tokens ? (int)len : 0;
+    if (t0 >= 0 && len > 0 && t0 + len <= a.n_tokens)
+        return (int)len;
+    t0 = 0;
+    return 0;
 }
 
 __device__ __forceinline__ float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
-// 1 / (1 + e^-v) from the hardware exponential and an approximate division
-// (a few 1e-7 relative; 0 and 1 at the infinities, NaN stays).
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// Two channels at a time: sm_103a's packed fp32 operations.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// One token's decay.  d = 1 - a with v = -log a >= 0: for v < 1/4 the Taylor
-// series of 1 - e^-v to v^7 (the next term is below 2e-9 relative), else 1 - e^-v.
-// A long memory multiplies hundreds of decays close to 1, where the hardware
-// exponential's error (2^-22) would add up; 1 - d is rounded once (2^-25).  And
-// m^2 = 1 - a^2 = d (1 + a) keeps its digits where a is close to 1.
-struct Decay {
-    float a, m, im;                     // a, sqrt(1 - a^2) and its inverse
-};
-
-__device__ __forceinline__ Decay decay_of(float v)
+__device__ __forceinline__ float ex2(float v)
 {
-    float s = fmaf(v, -1.f / 7.f, 1.f);
-    s = fmaf(v * (-1.f / 6.f), s, 1.f);
-    s = fmaf(v * (-1.f / 5.f), s, 1.f);
-    s = fmaf(v * (-1.f / 4.f), s, 1.f);
-    s = fmaf(v * (-1.f / 3.f), s, 1.f);
-    s = fmaf(v * (-1.f / 2.f), s, 1.f);
-    s *= v;
-    const float e = __expf(-v);
-    Decay r;
-    r.a = v < 0.25f ? 1.f - s : e;
-    const float m2 = (v < 0.25f ? s : 1.f - e) * (1.f + r.a);
-    // m2 = 0 (a closed gate) gives m ~ 1e-19, whose products with the gate's
-    // vanishing derivative are zero, and not 0 / 0
-    r.im = rsqrtf(fmaxf(m2, 1e-38f));
-    r.m = m2 * r.im;
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
 
-// State (or its gradient) arriving at unit u from the units on its side `dir`
-// (-1: earlier chunks, +1: later ones) down to `last`, the sequence's end on
-// that side.  Called by one warp; lane's channels c0 .. c0 + V - 1 (V values in
-// s).  It waits until one of the nearest 32 units has its outgoing state and
-// every unit between has its (P, H), and applies those from the far one to the
-// near one: s -> P s + H, the very operation each of those units does for its own
-// outgoing state, so the bits do not depend on which unit was found.  Returns
-// false when the bounded wait gave up.
-template <int V>
-__device__ __forceinline__ bool gated_gather(const GatedArgs &a, int u, int dir, int last, int cb, int c0, int lane,
-                                             float (&s)[V])
+__device__ __forceinline__ float rcp(float v)
 {
-    const int idx = u + dir * (lane + 1);
-    const bool valid = dir < 0 ? idx >= last : idx <= last;
-    const int *flag = a.flags + (long long)idx * a.cblocks + cb;
-    for (int spin = 0; spin < (1 << 22); ++spin) {
-        const int f = valid ? ld_acquire(flag) : 0;
-        const unsigned known = __ballot_sync(kFullMask, f == 2), none = __ballot_sync(kFullMask, f == 0);
-        if (known && (none == 0 || __ffs(known) < __ffs(none))) {
-            __syncwarp();                                  // the lanes' acquires order every lane's reads below
-            if (c0 < a.C) {
-                int k = __ffs(known);
-                const long long step = (long long)dir * a.C;
-                const float *p = a.agg_p + (long long)u * a.C + c0, *h = a.agg_h + (long long)u * a.C + c0;
-                const float *o = a.out_state + (long long)u * a.C + c0 + k * step;
-#pragma unroll
-                for (int q = 0; q < V; ++q)
-                    s[q] = __ldcg(o + q);
-#pragma unroll 4
-                for (--k; k > 0; --k)
-#pragma unroll
-                    for (int q = 0; q < V; ++q)
-                        s[q] = fmaf(__ldcg(p + k * step + q), s[q], __ldcg(h + k * step + q));
-            }
-            return true;
-        }
-        if (spin > 8)
-            __nanosleep(32);
-    }
-    return false;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// Host side.  Chunks of a batch: at most one begun chunk a sequence beside the full ones.
-long long gated_max_units(long long n_seqs, long long n_tokens);
-size_t gated_workspace_bytes(int n_seqs, int n_tokens, int C);
-cudaError_t launch_gated_scan(GatedArgs a, int dtype, void *workspace, cudaStream_t stream);
-cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, void *workspace, cudaStream_t stream);
-// Two channels a thread where every row starts on a pair.
-bool gated_pairs(const GatedArgs &a, int dtype, bool backward);
-void gated_carve(GatedArgs &a, void *workspace);
-cudaError_t launch_gated_plan(const GatedArgs &a, cudaStream_t stream);
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^-v) from the hardware exponential and reciprocal (a few 1e-7
+// relative; 0 and 1 at the infinities, NaN stays).
+__device__ __forceinline__ float2 sigmoid2(float2 v)
+{
+    const float2 t = mul2(v, both(-kLog2e));
+    const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
+}
+
+__device__ __forceinline__ float sigmoid_f(float v) { return rcp(1.f + ex2(v * -kLog2e)); }
+
+// One token's decay of two channels.  d = 1 - a with v = -log a >= 0: for v < 1/4
+// the Taylor series of 1 - e^-v to v^7 (the next term is below 2e-9 relative),
+// else 1 - e^-v.  A long memory multiplies hundreds of decays close to 1, where
+// the hardware exponential's error (2^-22) would add up; 1 - d is rounded once
+// (2^-25).  And m^2 = 1 - a^2 = d (1 + a) keeps its digits where a is close to 1.
+struct Decay {
+    float2 a, m, im;                    // a, sqrt(1 - a^2) and its inverse
+};
+
+__device__ __forceinline__ Decay decay_of(float2 v)
+{
+    float2 s = fma2(v, both(1.f / 5040.f), both(-1.f / 720.f));
+    s = fma2(s, v, both(1.f / 120.f));
+    s = fma2(s, v, both(-1.f / 24.f));
+    s = fma2(s, v, both(1.f / 6.f));
+    s = fma2(s, v, both(-0.5f));
+    s = fma2(s, v, both(1.f));
+    s = mul2(s, v);
+    const float2 t = mul2(v, both(-kLog2e));
+    const float2 e = make_float2(ex2(t.x), ex2(t.y));
+    const bool nx = v.x < 0.25f, ny = v.y < 0.25f;
+    const float2 d = make_float2(nx ? s.x : 1.f - e.x, ny ? s.y : 1.f - e.y);
+    Decay r;
+    r.a = make_float2(nx ? 1.f - s.x : e.x, ny ? 1.f - s.y : e.y);
+    const float2 m2 = fma2(d, r.a, d);
+    // m2 = 0 (a closed gate) gives m ~ 1e-19, whose products with the gate's
+    // vanishing derivative are zero, and not 0 / 0
+    r.im = make_float2(rsqrtf(fmaxf(m2.x, 1e-38f)), rsqrtf(fmaxf(m2.y, 1e-38f)));
+    r.m = mul2(m2, r.im);
+    return r;
+}
+
+__device__ __forceinline__ float2 pair(float2 v) { return v; }
+__device__ __forceinline__ float2 pair(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ float2 pair(__half2 v) { return __half22float2(v); }
+
+// Two neighbouring elements in shared memory as floats.
+__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) { return pair(*reinterpret_cast<const __nv_bfloat162 *>(p)); }
+__device__ __forceinline__ float2 load_pair(const __half *p) { return pair(*reinterpret_cast<const __half2 *>(p)); }
+
+// v to p and p + 1: one store where the rows allow it (`pairs`: every row starts
+// on a pair), the second element only inside the row (`two`).
+template <class T>
+__device__ __forceinline__ void store_pair(T *p, float2 v, bool pairs, bool two)
+{
+    Vec<T, 2> o;
+    o.v[0] = from_float<T>(v.x);
+    o.v[1] = from_float<T>(v.y);
+    if (pairs && two) {
+        store_vec<T, 2>(p, o);
+    } else {
+        p[0] = o.v[0];
+        if (two)
+            p[1] = o.v[1];
+    }
+}
+
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
+// Tokens t .. of one tensor (the chunk's, `n` of them) x the block's channels into
+// shared memory [kGatedChunk][kGatedCh] for rows that TMA cannot describe: 4 bytes a
+// copy where pairs of 16-bit elements (or fp32) lie on 4 bytes, else plain loads.
+// Channels and tokens outside are zero.
+template <class T>
+__device__ __forceinline__ void gated_copy(T *dst, const void *src, long long stride, long long t, int n, int c, int C,
+                                           bool words)
+{
+    const T *p = static_cast<const T *>(src) + t * stride + c;
+    constexpr int E = 4 / sizeof(T);
+    if (words) {
+        for (int i = threadIdx.x; i < kGatedTile / E; i += 32 * kGatedWarps) {
+            const int row = i / (kGatedCh / E), col = i % (kGatedCh / E) * E;
+            if (row < n && c + col < C)                     // (pairs: C is even)
+                cp_async4(dst + i * E, p + row * stride + col);
+            else
+                *reinterpret_cast<uint32_t *>(dst + i * E) = 0;
+        }
+        return;
+    }
+    for (int i = threadIdx.x; i < kGatedTile; i += 32 * kGatedWarps) {
+        const int row = i / kGatedCh, col = i % kGatedCh;
+        dst[i] = row < n && c + col < C ? p[row * stride + col] : from_float<T>(0.f);
+    }
+}
+
+// One chunk's map of two channels, as the blocks of a cluster exchange it.
+struct alignas(16) GatedMsg {
+    float2 p, h;
+};
+
+// 16 bytes into block `rank` of the cluster, counted on its mbarrier (both given as
+// addresses of this block).
+__device__ __forceinline__ void send_map(uint32_t dst, uint32_t bar, uint32_t rank, const GatedMsg &m)
+{
+    asm volatile("{\n\t.reg .b32 d, b;\n\t"
+                 "mapa.shared::cluster.u32 d, %0, %2;\n\tmapa.shared::cluster.u32 b, %1, %2;\n\t"
+                 "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [d], {%3, %4, %5, %6}, [b];\n\t}\n"
+                 ::"r"(dst), "r"(bar), "r"(rank), "f"(m.p.x), "f"(m.p.y), "f"(m.h.x), "f"(m.h.y) : "memory");
+}
+
+// Shared memory of the exchange: maps by round parity and sender.
+struct GatedExchange {
+    GatedMsg msg[2][kGatedMaxCluster][32];
+    uint64_t bar[2];
+};
+
+// Once at the kernel's start (thread 0), before gated_cluster_start.
+__device__ __forceinline__ void exchange_init(GatedExchange &x)
+{
+    tc::mbar_init(&x.bar[0], 1);
+    tc::mbar_init(&x.bar[1], 1);
+}
+
+// Every block of the cluster runs and has its barriers (all threads).
+__device__ __forceinline__ void gated_cluster_start(int cluster)
+{
+    if (cluster > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+}
+
+// No block leaves while a peer may still send to it (all threads).
+__device__ __forceinline__ void gated_cluster_end(int cluster)
+{
+    __syncwarp();
+    if (cluster > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    }
+}
+
+// Round k's map of this block (rank) to the others (one whole warp).
+__device__ __forceinline__ void exchange_send(GatedExchange &x, int k, int rank, int cluster, int lane, const GatedMsg &m)
+{
+    const int b = k & 1;
+    x.msg[b][rank][lane] = m;
+    __syncwarp();                                           // before the arrival that publishes it
+    if (lane == 0)
+        tc::mbar_expect_tx(&x.bar[b], (cluster - 1) * 32 * sizeof(GatedMsg));
+    __syncwarp();
+    for (int r = 0; r < cluster; ++r)
+        if (r != rank)
+            send_map(tc::smem_u32(&x.msg[b][rank][lane]), tc::smem_u32(&x.bar[b]), r, m);
+}
+
+// A tensor map of [T][C] rows in boxes of kGatedChunk x kGatedCh.
+struct alignas(64) GatedMap {
+    unsigned char image[128];
+};
+
+// The first 128-byte boundary of the dynamic shared memory (TMA's destination).
+__device__ __forceinline__ unsigned char *align128(unsigned char *p) { return p + (-tc::smem_u32(p) & 127u); }
+
+// TMA: the box at channel c, token t into shared memory (zeros outside the tensor).
+__device__ __forceinline__ void tma_rows(void *dst, const GatedMap *map, int c, int t, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];\n"
+                 ::"r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+
+// Host side.
+long long gated_chunk_rows(long long n_seqs, long long n_tokens);
+// Blocks of a cluster for these sizes (gated_scan.cu).
+int gated_cluster(int n_seqs, int n_tokens, int C);
+// False where TMA cannot describe the rows (address or stride no multiple of 16 bytes).
+bool gated_map(GatedMap *map, const void *p, int dtype, int n_tokens, int C, long long stride);
+// Whether 4-byte copies of a tensor's rows are aligned (its pairs, for 16-bit types).
+bool gated_words(const void *p, int dtype, int C, long long stride);
+cudaError_t launch_gated_scan(GatedArgs a, int dtype, cudaStream_t stream);
+cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, cudaStream_t stream);
+
+// `kernel` over n_seqs x cblocks clusters.
+template <class... KArgs, class... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), const GatedArgs &a, size_t smem, cudaStream_t stream, Args &&...args)
+{
+    cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.n_seqs * a.cblocks * a.cluster));
+    cfg.blockDim = dim3(32 * kGatedWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 }  // namespace ssm

@@ -1,5 +1,8 @@
 // Forward kernels of the gated linear recurrence (sm_103a); the mathematics and
-// the passing of state between time chunks are in gated_common.cuh.
+// the walk over time are in gated_common.cuh.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "gated_common.cuh"
 
 namespace ssm {
@@ -7,338 +10,298 @@ namespace ssm {
 namespace {
 
 // ---- one token a sequence (decode), or any lengths token by token ----
-// A thread owns V channels of one sequence and steps through its tokens.
-template <class T, int V>
+// A thread owns two channels of one sequence and steps through its tokens: one
+// token is a handful of loads in flight at once and one launch.
+template <class T>
 __global__ void __launch_bounds__(128)
-gated_step_kernel(const GatedArgs a)
+gated_step_kernel(const GatedArgs a, int pairs)
 {
     griddep_entry();
-    const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * V;
+    const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * 2;
     if (c0 >= a.C)
         return;
-    float rate[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q)
-        rate[q] = a.decay_scale * softplus_f(__ldg(a.lam + c0 + q));
+    const bool two = c0 + 1 < a.C;
+    const float2 lam = make_float2(__ldg(a.lam + c0), two ? __ldg(a.lam + c0 + 1) : 0.f);
+    auto load = [&](const void *base, long long at) {
+        const T *p = static_cast<const T *>(base) + at + c0;
+        if (pairs) {
+            const Vec<T, 2> v = load_vec<T, 2>(p);
+            return make_float2(to_float(v.v[0]), to_float(v.v[1]));
+        }
+        return make_float2(to_float(p[0]), two ? to_float(p[1]) : 0.f);
+    };
     for (int seq = blockIdx.y; seq < a.n_seqs; seq += gridDim.y) {
         long long t0;
         const int len = gated_seq_len(a, seq, t0);
         float *slot = a.state + (long long)seq * a.C + c0;
-        float h[V];
-        const bool resume = a.resume[seq] != 0;
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-            h[q] = resume ? slot[q] : 0.f;
+        float2 h = both(0.f);
+        if (a.resume[seq] != 0)
+            h = make_float2(slot[0], two ? slot[1] : 0.f);
+        float2 rate;
         for (int t = 0; t < len; ++t) {
-            const Vec<T, V> x = load_vec<T, V>(static_cast<const T *>(a.x) + (t0 + t) * a.sx + c0);
-            const Vec<T, V> ga = load_vec<T, V>(static_cast<const T *>(a.gate_a) + (t0 + t) * a.sga + c0);
-            const Vec<T, V> gx = load_vec<T, V>(static_cast<const T *>(a.gate_x) + (t0 + t) * a.sgx + c0);
-            Vec<T, V> y;
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const Decay d = decay_of(rate[q] * sigmoid_f(to_float(ga.v[q])));
-                h[q] = fmaf(d.a, h[q], d.m * sigmoid_f(to_float(gx.v[q])) * to_float(x.v[q]));
-                y.v[q] = from_float<T>(h[q]);
-            }
-            store_vec<T, V>(static_cast<T *>(a.y) + (t0 + t) * a.sy + c0, y);
+            const float2 x = load(a.x, (t0 + t) * a.sx), ga = load(a.gate_a, (t0 + t) * a.sga);
+            const float2 gx = load(a.gate_x, (t0 + t) * a.sgx);
+            if (t == 0)
+                rate = make_float2(a.decay_scale * softplus_f(lam.x), a.decay_scale * softplus_f(lam.y));
+            const Decay d = decay_of(mul2(rate, sigmoid2(ga)));
+            h = fma2(d.a, h, mul2(mul2(d.m, sigmoid2(gx)), x));
+            store_pair(static_cast<T *>(a.y) + (t0 + t) * a.sy + c0, h, pairs, two);
         }
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-            slot[q] = h[q];
+        slot[0] = h.x;
+        if (two)
+            slot[1] = h.y;
     }
 }
 
-// ---- plan: the units of the batch, cleared flags ----
-// Block 0 lists the (sequence, chunk) units; the others clear the flags.
-__global__ void __launch_bounds__(1024)
-gated_plan_kernel(const GatedArgs a)
-{
-    griddep_entry();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    if (blockIdx.x > 0) {
-        const long long n = (long long)a.max_units * a.cblocks;
-        for (long long i = (long long)(blockIdx.x - 1) * blockDim.x + tid; i < n; i += (long long)(gridDim.x - 1) * blockDim.x)
-            a.flags[i] = 0;
-        return;
-    }
-    __shared__ int warp_tot[32];
-    __shared__ int carry;
-    if (tid == 0)
-        carry = 0;
-    __syncthreads();
-    for (int base = 0; base < a.n_seqs; base += blockDim.x) {
-        const int i = base + tid;
-        int cnt = 0;
-        if (i < a.n_seqs) {
-            long long t0;
-            cnt = max(1, (gated_seq_len(a, i, t0) + kGatedChunk - 1) / kGatedChunk);   // an empty sequence keeps its slot's rule
-        }
-        int incl = cnt;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(kFullMask, incl, off);
-            if (lane >= off)
-                incl += v;
-        }
-        if (lane == 31)
-            warp_tot[warp] = incl;
-        __syncthreads();
-        if (warp == 0) {
-            int wt = lane < nw ? warp_tot[lane] : 0;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int v = __shfl_up_sync(kFullMask, wt, off);
-                if (lane >= off)
-                    wt += v;
-            }
-            if (lane < nw)
-                warp_tot[lane] = wt;
-        }
-        __syncthreads();
-        const int first = carry + (warp ? warp_tot[warp - 1] : 0) + incl - cnt;
-        const int total = warp_tot[nw - 1];
-        if (i < a.n_seqs)
-            a.unit_base[i] = min(first, a.max_units);
-        // the units of this round's sequences, a warp's 32 sequences one after another, its lanes over the chunks
-        for (int k = 0; k < 32; ++k) {
-            const int f = __shfl_sync(kFullMask, first, k), n = __shfl_sync(kFullMask, cnt, k);
-            for (int j = lane; j < n; j += 32)
-                if (f + j < a.max_units)
-                    a.units[f + j] = make_int2(base + warp * 32 + k, j);
-        }
-        __syncthreads();
-        if (tid == 0)
-            carry += total;
-        __syncthreads();
-    }
-    if (tid == 0) {
-        a.unit_base[a.n_seqs] = min(carry, a.max_units);
-        a.control[0] = min(carry, a.max_units);
-        a.control[1] = 0;
-        a.control[2] = 0;
-    }
-}
+// ---- walk over time ----
+// Block: 64 channels of one sequence (of one rank of the cluster), 8 warps; a lane
+// owns two channels, a warp 8 tokens of the chunk.  Per chunk: decays and inputs from
+// shared memory, the warp's run from zero in registers, the runs' maps through
+// shared memory (one barrier), then every warp composes the maps before its own
+// onto the carried state and stores y.  TMA fills the rows of later chunks into
+// the stages meanwhile.
+template <class T, bool TMA>
+struct GatedForward {
+    static constexpr int kStages = TMA && sizeof(T) == 2 ? 3 : 2;      // 24 KB a stage (48 KB fp32)
+    static constexpr size_t kSmem = 128 + kStages * 3 * kGatedTile * sizeof(T);
+};
 
-// ---- chunked kernel ----
-// Block: kGatedWarps warps; warp w holds tokens w L .. w L + L - 1 of the chunk
-// for the block's 32 V channels (lane: V channels).
-template <class T, int V>
-__global__ void __launch_bounds__(32 * kGatedWarps)
-gated_scan_kernel(const GatedArgs a)
+template <class T, bool TMA>
+__global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 ? 3 : 2)
+gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
+                  const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx)
 {
     griddep_entry();
-    constexpr int L = kGatedLen, W = kGatedWarps;
-    __shared__ float tot_p[W][32 * V], tot_h[W][32 * V], enter[32 * V];
-    __shared__ int ticket;
+    constexpr int L = kGatedLen, W = kGatedWarps, S = GatedForward<T, TMA>::kStages;
+    extern __shared__ __align__(128) unsigned char raw[];
+    T *buf = reinterpret_cast<T *>(align128(raw));
+    __shared__ float2 tot_p[2][W][32], tot_h[2][W][32];
+    __shared__ GatedExchange ex;
+    __shared__ uint64_t full[S];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0)
-        ticket = atomicAdd(a.control + 1, 1);
-    __syncthreads();
-    const int u = ticket / a.cblocks, cb = ticket - u * a.cblocks;
-    if (u >= a.control[0])
-        return;
-    const int2 unit = a.units[u];
-    const int seq = unit.x, first = a.unit_base[seq];
+    const int R = a.cluster, rank = blockIdx.x % R, job = blockIdx.x / R;
+    const int seq = job / a.cblocks, cb = job - seq * a.cblocks;
+    const int cap = a.fail_waits ? 0 : (int)tc::kSpinLimit;
     long long t0;
     const int len = gated_seq_len(a, seq, t0);
-    const int c0 = (cb * 32 + lane) * V;
-    const bool inside = c0 < a.C;
-    const int tw = unit.y * kGatedChunk + warp * L;        // this warp's first token of the sequence
-    const int cnt = min(L, len - tw);                      // its tokens (may be <= 0)
-    float rate[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q)
-        rate[q] = inside ? a.decay_scale * softplus_f(__ldg(a.lam + c0 + q)) : 0.f;
-
-    // every load first
-    Vec<T, V> x[L], ga[L], gx[L];
-#pragma unroll
-    for (int k = 0; k < L; ++k)
-        if (inside && k < cnt) {
-            const long long t = t0 + tw + k;
-            x[k] = load_vec<T, V>(static_cast<const T *>(a.x) + t * a.sx + c0);
-            ga[k] = load_vec<T, V>(static_cast<const T *>(a.gate_a) + t * a.sga + c0);
-            gx[k] = load_vec<T, V>(static_cast<const T *>(a.gate_x) + t * a.sgx + c0);
-        }
-    // the run from zero: h[k] and the product of decays p[k] up to token k
-    float h[L][V], p[L][V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        float hh = 0.f, pp = 1.f;
-#pragma unroll
-        for (int k = 0; k < L; ++k) {
-            if (inside && k < cnt) {
-                const Decay d = decay_of(rate[q] * sigmoid_f(to_float(ga[k].v[q])));
-                hh = fmaf(d.a, hh, d.m * sigmoid_f(to_float(gx[k].v[q])) * to_float(x[k].v[q]));
-                pp *= d.a;
-            }
-            h[k][q] = hh;
-            p[k][q] = pp;
-        }
-        tot_p[warp][lane * V + q] = pp;
-        tot_h[warp][lane * V + q] = hh;
+    if (tid == 0) {
+        exchange_init(ex);
+        for (int i = 0; i < S; ++i)
+            tc::mbar_init(&full[i], 1);
+        tc::mbar_init_fence();
     }
-    __syncthreads();
-    if (warp == 0) {
-        float P[V], H[V], s[V];
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            P[q] = 1.f;
-            H[q] = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                H[q] = fmaf(tot_p[w][lane * V + q], H[q], tot_h[w][lane * V + q]);
-                P[q] *= tot_p[w][lane * V + q];
+    gated_cluster_start(R);
+    const int rounds = (len + kGatedChunk * R - 1) / (kGatedChunk * R);
+    auto fetch = [&](int k) {                               // round k's rows into its stage
+        const int j = k * R + rank, t = (int)t0 + j * kGatedChunk, n = min(kGatedChunk, len - j * kGatedChunk);
+        T *to = buf + k % S * 3 * kGatedTile;
+        if (TMA) {
+            if (tid == 0 && n > 0) {
+                uint64_t *bar = &full[k % S];
+                tc::mbar_expect_tx(bar, 3 * kGatedTile * sizeof(T));
+                tma_rows(to, &mx, cb * kGatedCh, t, bar);
+                tma_rows(to + kGatedTile, &mga, cb * kGatedCh, t, bar);
+                tma_rows(to + 2 * kGatedTile, &mgx, cb * kGatedCh, t, bar);
             }
-            s[q] = 0.f;
+        } else if (n > 0) {
+            gated_copy<T>(to, a.x, a.sx, t, n, cb * kGatedCh, a.C, words);
+            gated_copy<T>(to + kGatedTile, a.gate_a, a.sga, t, n, cb * kGatedCh, a.C, words);
+            gated_copy<T>(to + 2 * kGatedTile, a.gate_x, a.sgx, t, n, cb * kGatedCh, a.C, words);
         }
-        const long long at = (long long)u * a.C + c0;
-        int *flag = a.flags + (long long)u * a.cblocks + cb;
-        bool ok = true;
-        if (u == first) {
-            if (inside && a.resume[seq] != 0)
-#pragma unroll
-                for (int q = 0; q < V; ++q)
-                    s[q] = a.state[(long long)seq * a.C + c0 + q];
+        if (!TMA)
+            cp_async_commit();
+    };
+    for (int k = 0; k < S; ++k)
+        if (k < rounds)
+            fetch(k);
+    const int c0 = cb * kGatedCh + 2 * lane;
+    const bool inside = c0 < a.C, two = c0 + 1 < a.C;
+    float2 rate = both(0.f), s = both(0.f);                 // s: the state entering the round
+    if (inside) {
+        rate = make_float2(a.decay_scale * softplus_f(__ldg(a.lam + c0)),
+                           two ? a.decay_scale * softplus_f(__ldg(a.lam + c0 + 1)) : 0.f);
+        if (a.resume[seq] != 0) {
+            const float *slot = a.state + (long long)seq * a.C + c0;
+            s = make_float2(slot[0], two ? slot[1] : 0.f);
+        }
+    }
+    bool ok = true;
+    for (int k = 0; k < rounds; ++k) {
+        const int j = k * R + rank;                         // this block's chunk
+        const int cnt = min(L, len - j * kGatedChunk - warp * L);
+        const T *bx = buf + k % S * 3 * kGatedTile, *bga = bx + kGatedTile, *bgx = bga + kGatedTile;
+        if (TMA) {
+            if (len > j * kGatedChunk)
+                ok = ok && tc::mbar_wait(&full[k % S], (k / S) & 1, cap);
         } else {
-            if (inside)
+            if (k + S - 1 < rounds)
+                cp_async_wait<S - 1>();
+            else
+                cp_async_wait<0>();
+            __syncthreads();
+        }
+        // the run from zero: h[i] and the product of decays p[i] up to token i
+        float2 h[L], p[L], hh = both(0.f), pp = both(1.f);
+        auto run = [&](auto whole) {
 #pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    __stcg(a.agg_p + at + q, P[q]);
-                    __stcg(a.agg_h + at + q, H[q]);
+            for (int i = 0; i < L; ++i) {
+                if (whole.value || i < cnt) {
+                    const int at = (warp * L + i) * kGatedCh + 2 * lane;
+                    const Decay d = decay_of(mul2(rate, sigmoid2(load_pair(bga + at))));
+                    hh = fma2(d.a, hh, mul2(mul2(d.m, sigmoid2(load_pair(bgx + at))), load_pair(bx + at)));
+                    pp = mul2(pp, d.a);
                 }
-            __threadfence();
-            __syncwarp();
-            if (lane == 0)
-                st_release(flag, 1);
-            ok = gated_gather<V>(a, u, -1, first, cb, c0, lane, s);
-            if (!ok) {
-                a.control[2] = 1;
+                h[i] = hh;
+                p[i] = pp;
+            }
+        };
+        if (cnt >= L)
+            run(Flag<true>());
+        else
+            run(Flag<false>());
+        float2 (*tp)[32] = tot_p[k & 1], (*th)[32] = tot_h[k & 1];
+        tp[warp][lane] = pp;
+        th[warp][lane] = hh;
+        __syncthreads();                                    // the runs' maps are there, the stage is read
+        if (k + S < rounds)
+            fetch(k + S);
+        if (R > 1) {
+            if (warp == 0) {
+                GatedMsg m{both(1.f), both(0.f)};
 #pragma unroll
-                for (int q = 0; q < V; ++q)
-                    s[q] = __int_as_float(0x7fc00000);
+                for (int w = 0; w < W; ++w) {
+                    m.h = fma2(tp[w][lane], m.h, th[w][lane]);
+                    m.p = mul2(m.p, tp[w][lane]);
+                }
+                exchange_send(ex, k, rank, R, lane, m);
+            }
+            ok = ok && tc::mbar_wait(&ex.bar[k & 1], (k >> 1) & 1, cap);
+            __syncwarp();
+        }
+        if (!ok)
+            s = both(__int_as_float(0x7fc00000));           // a wait gave up: seen in y and in the slot
+        // the states entering this block's chunk, this warp's run, and the next round
+        float2 mine = s, next = s;
+        if (R > 1) {
+            for (int r = 0; r < R; ++r) {
+                if (r == rank)
+                    mine = next;
+                next = fma2(ex.msg[k & 1][r][lane].p, next, ex.msg[k & 1][r][lane].h);
             }
         }
-        const bool last = u + 1 == a.unit_base[seq + 1];
-        if (inside)
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float o = fmaf(P[q], s[q], H[q]);
-                if (last)
-                    a.state[(long long)seq * a.C + c0 + q] = o;
-                else
-                    __stcg(a.out_state + at + q, o);
-                if (a.chunk_states)
-                    a.chunk_states[at + q] = s[q];
-            }
-        if (!last) {
-            __threadfence();
-            __syncwarp();
-            if (lane == 0)
-                st_release(flag, 2);
+        if (a.chunk_states && warp == 0 && inside && len > j * kGatedChunk) {
+            float *cs = a.chunk_states + gated_chunk_row(a.n_seqs, seq, t0, j) * a.C + c0;
+            cs[0] = mine.x;
+            if (two)
+                cs[1] = mine.y;
         }
+        float2 run_s = mine;
 #pragma unroll
-        for (int q = 0; q < V; ++q)
-            enter[lane * V + q] = s[q];
-    }
-    __syncthreads();
-    float s[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        s[q] = enter[lane * V + q];
-        for (int w = 0; w < warp; ++w)
-            s[q] = fmaf(tot_p[w][lane * V + q], s[q], tot_h[w][lane * V + q]);
-    }
-#pragma unroll
-    for (int k = 0; k < L; ++k)
-        if (inside && k < cnt) {
-            Vec<T, V> y;
-#pragma unroll
-            for (int q = 0; q < V; ++q)
-                y.v[q] = from_float<T>(fmaf(p[k][q], s[q], h[k][q]));
-            store_vec<T, V>(static_cast<T *>(a.y) + (t0 + tw + k) * a.sy + c0, y);
+        for (int w = 0; w < W; ++w) {
+            if (w == warp)
+                run_s = mine;
+            mine = fma2(tp[w][lane], mine, th[w][lane]);
         }
+        s = R > 1 ? next : mine;
+        if (inside) {
+            T *y = static_cast<T *>(a.y) + (t0 + j * (long long)kGatedChunk + warp * L) * a.sy + c0;
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (i < cnt)
+                    store_pair(y + i * a.sy, fma2(p[i], run_s, h[i]), pairs, two);
+        }
+    }
+    if (rank == 0 && warp == 0 && inside) {                 // (an empty sequence: what it began with)
+        float *slot = a.state + (long long)seq * a.C + c0;
+        slot[0] = s.x;
+        if (two)
+            slot[1] = s.y;
+    }
+    gated_cluster_end(R);
 }
 
-template <class T, int V>
-cudaError_t launch_forward(const GatedArgs &a, cudaStream_t stream)
+template <class T>
+cudaError_t launch_forward(GatedArgs a, bool pairs, int dtype, cudaStream_t stream)
 {
     if (a.n_tokens == a.n_seqs && !a.chunk_states) {
-        const dim3 grid((unsigned)((a.C + 128 * V - 1) / (128 * V)), (unsigned)(a.n_seqs < 65535 ? a.n_seqs : 65535));
-        return launch_pdl(gated_step_kernel<T, V>, grid, dim3(128), 0, stream, a);
+        const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)(a.n_seqs < 65535 ? a.n_seqs : 65535));
+        return launch_pdl(gated_step_kernel<T>, grid, dim3(128), 0, stream, a, pairs ? 1 : 0);
     }
-    cudaError_t e = launch_gated_plan(a, stream);
-    if (e != cudaSuccess)
-        return e;
-    return launch_pdl(gated_scan_kernel<T, V>, dim3((unsigned)((long long)a.max_units * a.cblocks)),
-                      dim3(32 * kGatedWarps), 0, stream, a);
+    GatedMap mx, mga, mgx;
+    if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
+        gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx))
+        return launch_clusters(gated_scan_kernel<T, true>, a, GatedForward<T, true>::kSmem, stream, a, pairs ? 1 : 0, 0,
+                               mx, mga, mgx);
+    const bool words = gated_words(a.x, dtype, a.C, a.sx) && gated_words(a.gate_a, dtype, a.C, a.sga) &&
+                       gated_words(a.gate_x, dtype, a.C, a.sgx);
+    return launch_clusters(gated_scan_kernel<T, false>, a, GatedForward<T, false>::kSmem, stream, a, pairs ? 1 : 0,
+                           words ? 1 : 0, mx, mga, mgx);
 }
 
-size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
 
 }  // namespace
 
-long long gated_max_units(long long n_seqs, long long n_tokens) { return n_seqs + n_tokens / kGatedChunk; }
+long long gated_chunk_rows(long long n_seqs, long long n_tokens) { return n_seqs + n_tokens / kGatedChunk + 1; }
 
-// Workspace: control, unit table, flags (for blocks of 32 channels), and three
-// fp32 rows of C a unit.
-size_t gated_workspace_bytes(int n_seqs, int n_tokens, int C)
+// Enough blocks that one sequence alone fills the device (two blocks an SM), but no
+// more blocks a sequence than it has chunks on average.
+int gated_cluster(int n_seqs, int n_tokens, int C)
 {
-    const size_t u = (size_t)gated_max_units(n_seqs, n_tokens), cb = ((size_t)C + 31) / 32;
-    return 256 + up256(u * sizeof(int2)) + up256(((size_t)n_seqs + 1) * 4) + up256(u * cb * 4) +
-           3 * up256(u * (size_t)C * 4);
+    const long long cb = (C + kGatedCh - 1) / kGatedCh, chunks = (long long)n_tokens / n_seqs / kGatedChunk;
+    int r = 1;
+    while (r < kGatedMaxCluster && cb * r < 300 && 2 * r <= chunks)
+        r *= 2;
+    return r;
 }
 
-void gated_carve(GatedArgs &a, void *workspace)
+bool gated_map(GatedMap *map, const void *p, int dtype, int n_tokens, int C, long long stride)
 {
-    const size_t u = (size_t)a.max_units, cb = ((size_t)a.C + 31) / 32;
-    char *w = static_cast<char *>(workspace);
-    auto take = [&](size_t bytes) {
-        char *p = w;
-        w += up256(bytes);
-        return p;
-    };
-    a.control = reinterpret_cast<int *>(take(256));
-    a.units = reinterpret_cast<int2 *>(take(u * sizeof(int2)));
-    a.unit_base = reinterpret_cast<int *>(take(((size_t)a.n_seqs + 1) * 4));
-    a.flags = reinterpret_cast<int *>(take(u * cb * 4));
-    a.agg_p = reinterpret_cast<float *>(take(u * (size_t)a.C * 4));
-    a.agg_h = reinterpret_cast<float *>(take(u * (size_t)a.C * 4));
-    a.out_state = reinterpret_cast<float *>(take(u * (size_t)a.C * 4));
-    a.lam_part = nullptr;
+    const auto fn = encode_fn();
+    const long long bytes = stride * dtype_size(dtype);
+    static_assert(sizeof(CUtensorMap) == sizeof(map->image), "tensor map size");
+    if (!fn || n_tokens <= 0 || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) & 15) != 0 || bytes >= 1LL << 40)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)n_tokens};
+    const cuuint64_t strides[1] = {(cuuint64_t)bytes};
+    const cuuint32_t box[2] = {kGatedCh, kGatedChunk}, step[2] = {1, 1};
+    const CUtensorMapDataType type = dtype == kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(reinterpret_cast<CUtensorMap *>(map->image), type, 2, const_cast<void *>(p), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool gated_pairs(const GatedArgs &a, int dtype, bool backward)
+bool gated_words(const void *p, int dtype, int C, long long stride)
 {
-    const uintptr_t pair = 2 * dtype_size(dtype);
-    long long odd = a.C | a.sx | a.sga | a.sgx | a.sy;
-    uintptr_t p = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate_a) |
-                  reinterpret_cast<uintptr_t>(a.gate_x) | reinterpret_cast<uintptr_t>(backward ? a.grad_y : a.y);
-    if (backward) {
-        odd |= a.gsx | a.gsga | a.gsgx;
-        p |= reinterpret_cast<uintptr_t>(a.grad_x) | reinterpret_cast<uintptr_t>(a.grad_ga) |
-             reinterpret_cast<uintptr_t>(a.grad_gx);
-    }
-    return (odd & 1) == 0 && p % pair == 0;
+    return dtype == kF32 || (((C | stride) & 1) == 0 && (reinterpret_cast<uintptr_t>(p) & 3) == 0);
 }
 
-cudaError_t launch_gated_plan(const GatedArgs &a, cudaStream_t stream)
+cudaError_t launch_gated_scan(GatedArgs a, int dtype, cudaStream_t stream)
 {
-    const long long words = (long long)a.max_units * a.cblocks;
-    const long long extra = (words + 8 * 1024 - 1) / (8 * 1024);
-    return launch_pdl(gated_plan_kernel, dim3(1 + (unsigned)(extra < 128 ? extra : 128)), dim3(1024), 0, stream, a);
-}
-
-cudaError_t launch_gated_scan(GatedArgs a, int dtype, void *workspace, cudaStream_t stream)
-{
-    const bool pairs = gated_pairs(a, dtype, false);
-    a.max_units = (int)gated_max_units(a.n_seqs, a.n_tokens);
-    a.cblocks = (a.C + (pairs ? 63 : 31)) / (pairs ? 64 : 32);
-    gated_carve(a, workspace);
+    a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
+    a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C);
+    a.fail_waits = debug_fail_waits() ? 1 : 0;
+    bool pairs = ((a.C | a.sy) & 1) == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * dtype_size(dtype)) == 0;
+    if (a.n_tokens == a.n_seqs && !a.chunk_states)          // the step kernel loads pairs too
+        pairs = pairs && ((a.sx | a.sga | a.sgx) & 1) == 0 &&
+                ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate_a) |
+                  reinterpret_cast<uintptr_t>(a.gate_x)) % (2 * dtype_size(dtype))) == 0;
     switch (dtype) {
-    case kF32: return pairs ? launch_forward<float, 2>(a, stream) : launch_forward<float, 1>(a, stream);
-    case kBF16: return pairs ? launch_forward<__nv_bfloat16, 2>(a, stream) : launch_forward<__nv_bfloat16, 1>(a, stream);
-    case kF16: return pairs ? launch_forward<__half, 2>(a, stream) : launch_forward<__half, 1>(a, stream);
+    case kF32: return launch_forward<float>(a, pairs, dtype, stream);
+    case kBF16: return launch_forward<__nv_bfloat16>(a, pairs, dtype, stream);
+    case kF16: return launch_forward<__half>(a, pairs, dtype, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -1,5 +1,5 @@
 // Backward kernel of the gated linear recurrence (sm_103a); the mathematics of
-// the forward pass and the time chunks are in gated_common.cuh.
+// the forward pass and the walk over time are in gated_common.cuh.
 //
 // With g_t the gradient of h_t through y_t and everything after it, and
 // E_t = a_t g_t what token t passes to the token before:
@@ -12,208 +12,242 @@
 // E of a run of tokens is an affine map of the E arriving from after it, with the
 // same product of decays P as the forward map: E_first = P E_in + sum_t p_t dy_t,
 // p_t the product of the decays up to and including t.  So one pass over a
-// thread's tokens gives P, H and E, a block needs the state entering its chunk
-// (saved by the forward pass, fp32: h is recomputed in registers instead of
-// read back rounded) and the E leaving the chunk after it, which it obtains as
-// the forward kernel obtains its state, from the last chunk to the first.
+// thread's tokens gives P, H and E.  The state entering a chunk was saved by the
+// forward pass (fp32: h is recomputed in registers instead of read back rounded);
+// E is carried from the last chunk to the first as the forward kernel carries h.
 #include "gated_common.cuh"
 
 namespace ssm {
 
 namespace {
 
-template <class T, int V>
-__global__ void __launch_bounds__(32 * kGatedWarps)
-gated_scan_backward_kernel(const GatedArgs a)
+// The chunk's rows stay in shared memory for both passes over them (the gates are
+// computed twice: their registers would cost half the resident blocks).  Two stages
+// of 32 KB for 16-bit types; fp32 rows take 64 KB, there one stage at three
+// blocks per SM, whose other blocks cover the wait.
+template <class T>
+struct GatedBackward {
+    static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+    static constexpr size_t kSmem = 128 + kStages * 4 * kGatedTile * sizeof(T);
+};
+
+template <class T, bool TMA>
+__global__ void __launch_bounds__(32 * kGatedWarps, 3)
+gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
+                           const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx,
+                           const __grid_constant__ GatedMap mdy)
 {
     griddep_entry();
-    constexpr int L = kGatedLen, W = kGatedWarps;
-    __shared__ float tot_p[W][32 * V], tot_h[W][32 * V], tot_e[W][32 * V], arrive[32 * V];
-    __shared__ int ticket;
+    constexpr int L = kGatedLen, W = kGatedWarps, S = GatedBackward<T>::kStages;
+    extern __shared__ __align__(128) unsigned char raw[];
+    T *buf = reinterpret_cast<T *>(align128(raw));
+    __shared__ float2 tot_p[2][W][32], tot_h[2][W][32], tot_e[2][W][32];
+    __shared__ GatedExchange ex;
+    __shared__ uint64_t full[S];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0)
-        ticket = atomicAdd(a.control + 1, 1);
-    __syncthreads();
-    const int back = ticket / a.cblocks, cb = ticket - back * a.cblocks;
-    const int u = a.control[0] - 1 - back;                 // the last chunks first
-    if (u < 0)
-        return;
-    const int2 unit = a.units[u];
-    const int seq = unit.x, first = a.unit_base[seq], last = a.unit_base[seq + 1] - 1;
+    const int R = a.cluster, rank = blockIdx.x % R, job = blockIdx.x / R;
+    const int seq = job / a.cblocks, cb = job - seq * a.cblocks;
+    const int cap = a.fail_waits ? 0 : (int)tc::kSpinLimit;
     long long t0;
     const int len = gated_seq_len(a, seq, t0);
-    const int c0 = (cb * 32 + lane) * V;
-    const bool inside = c0 < a.C;
-    const int tw = unit.y * kGatedChunk + warp * L;
-    const int cnt = min(L, len - tw);
-    const long long at = (long long)u * a.C + c0;
-    float rate[V], hin[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        rate[q] = inside ? a.decay_scale * softplus_f(__ldg(a.lam + c0 + q)) : 0.f;
-        hin[q] = inside ? __ldg(a.chunk_states + at + q) : 0.f;
+    if (tid == 0) {
+        exchange_init(ex);
+        for (int i = 0; i < S; ++i)
+            tc::mbar_init(&full[i], 1);
+        tc::mbar_init_fence();
     }
-    Vec<T, V> x[L], ga[L], gx[L], dy[L];
-#pragma unroll
-    for (int k = 0; k < L; ++k)
-        if (inside && k < cnt) {
-            const long long t = t0 + tw + k;
-            x[k] = load_vec<T, V>(static_cast<const T *>(a.x) + t * a.sx + c0);
-            ga[k] = load_vec<T, V>(static_cast<const T *>(a.gate_a) + t * a.sga + c0);
-            gx[k] = load_vec<T, V>(static_cast<const T *>(a.gate_x) + t * a.sgx + c0);
-            dy[k] = load_vec<T, V>(static_cast<const T *>(a.grad_y) + t * a.sy + c0);
-        }
-    // decays a[k] and inputs b[k] of the run; its maps of h and of E
-    float dec[L][V], hb[L][V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        float hh = 0.f, pp = 1.f, ee = 0.f;
-#pragma unroll
-        for (int k = 0; k < L; ++k) {
-            dec[k][q] = 1.f;
-            hb[k][q] = 0.f;
-            if (inside && k < cnt) {
-                const Decay d = decay_of(rate[q] * sigmoid_f(to_float(ga[k].v[q])));
-                const float b = d.m * sigmoid_f(to_float(gx[k].v[q])) * to_float(x[k].v[q]);
-                hh = fmaf(d.a, hh, b);
-                pp *= d.a;
-                ee = fmaf(pp, to_float(dy[k].v[q]), ee);
-                dec[k][q] = d.a;
-                hb[k][q] = b;
+    gated_cluster_start(R);
+    const int rounds = (len + kGatedChunk * R - 1) / (kGatedChunk * R);
+    // the chunk of this block's n-th round, the last tokens first (it may lie past the end: no tokens)
+    auto chunk_of = [&](int n) { return (rounds - 1 - n) * R + rank; };
+    uint32_t phases = 0;                                    // parity of each stage's next fill
+    auto fetch = [&](int k) {
+        const int j = chunk_of(k), t = (int)t0 + j * kGatedChunk, n = min(kGatedChunk, len - j * kGatedChunk);
+        T *to = buf + k % S * 4 * kGatedTile;
+        if (TMA) {
+            if (tid == 0 && n > 0) {
+                uint64_t *bar = &full[k % S];
+                tc::mbar_expect_tx(bar, 4 * kGatedTile * sizeof(T));
+                tma_rows(to, &mx, cb * kGatedCh, t, bar);
+                tma_rows(to + kGatedTile, &mga, cb * kGatedCh, t, bar);
+                tma_rows(to + 2 * kGatedTile, &mgx, cb * kGatedCh, t, bar);
+                tma_rows(to + 3 * kGatedTile, &mdy, cb * kGatedCh, t, bar);
             }
-        }
-        tot_p[warp][lane * V + q] = pp;
-        tot_h[warp][lane * V + q] = hh;
-        tot_e[warp][lane * V + q] = ee;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        float P[V], E[V], s[V];
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            P[q] = 1.f;
-            E[q] = 0.f;
-#pragma unroll
-            for (int w = W - 1; w >= 0; --w) {
-                E[q] = fmaf(tot_p[w][lane * V + q], E[q], tot_e[w][lane * V + q]);
-                P[q] *= tot_p[w][lane * V + q];
-            }
-            s[q] = 0.f;
-        }
-        int *flag = a.flags + (long long)u * a.cblocks + cb;
-        if (u == last) {
-            if (inside && a.grad_state)
-#pragma unroll
-                for (int q = 0; q < V; ++q)
-                    s[q] = a.grad_state[(long long)seq * a.C + c0 + q];
         } else {
-            if (inside)
+            if (n > 0) {
+                gated_copy<T>(to, a.x, a.sx, t, n, cb * kGatedCh, a.C, words);
+                gated_copy<T>(to + kGatedTile, a.gate_a, a.sga, t, n, cb * kGatedCh, a.C, words);
+                gated_copy<T>(to + 2 * kGatedTile, a.gate_x, a.sgx, t, n, cb * kGatedCh, a.C, words);
+                gated_copy<T>(to + 3 * kGatedTile, a.grad_y, a.sy, t, n, cb * kGatedCh, a.C, words);
+            }
+            cp_async_commit();
+        }
+    };
+    if (rounds > 0)
+        fetch(0);
+    const int c0 = cb * kGatedCh + 2 * lane;
+    const bool inside = c0 < a.C, two = c0 + 1 < a.C;
+    float2 rate = both(0.f), s = both(0.f), part = both(0.f);   // s: the E arriving at the round; part: dlam's sum
+    if (inside) {
+        rate = make_float2(a.decay_scale * softplus_f(__ldg(a.lam + c0)),
+                           two ? a.decay_scale * softplus_f(__ldg(a.lam + c0 + 1)) : 0.f);
+        if (a.grad_state) {
+            const float *g = a.grad_state + (long long)seq * a.C + c0;
+            s = make_float2(g[0], two ? g[1] : 0.f);
+        }
+    }
+    bool ok = true;
+    for (int k = 0; k < rounds; ++k) {
+        const int j = chunk_of(k), half = k & 1;
+        const bool some = len > j * kGatedChunk;            // this block's chunk has tokens
+        const int cnt = min(L, len - j * kGatedChunk - warp * L);
+        const T *bx = buf + k % S * 4 * kGatedTile, *bga = bx + kGatedTile, *bgx = bga + kGatedTile,
+                *bdy = bgx + kGatedTile;
+        float2 h = both(0.f);                               // the state entering the chunk
+        if (inside && some) {
+            const float *cs = a.chunk_states + gated_chunk_row(a.n_seqs, seq, t0, j) * a.C + c0;
+            h = make_float2(__ldg(cs), two ? __ldg(cs + 1) : 0.f);
+        }
+        if (TMA) {
+            if (some) {
+                ok = ok && tc::mbar_wait(&full[k % S], (phases >> (k % S)) & 1, cap);
+                phases ^= 1u << (k % S);
+            }
+        } else {
+            cp_async_wait<0>();
+            __syncthreads();
+        }
+        // decays dec[i] and inputs hb[i] of the run; its maps of h and of E
+        float2 dec[L], hb[L], hh = both(0.f), pp = both(1.f), ee = both(0.f);
+        auto run = [&](auto whole) {
 #pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    __stcg(a.agg_p + at + q, P[q]);
-                    __stcg(a.agg_h + at + q, E[q]);
+            for (int i = 0; i < L; ++i) {
+                dec[i] = both(1.f);
+                hb[i] = both(0.f);
+                if (whole.value || i < cnt) {
+                    const int at = (warp * L + i) * kGatedCh + 2 * lane;
+                    const Decay d = decay_of(mul2(rate, sigmoid2(load_pair(bga + at))));
+                    hb[i] = mul2(mul2(d.m, sigmoid2(load_pair(bgx + at))), load_pair(bx + at));
+                    dec[i] = d.a;
+                    hh = fma2(d.a, hh, hb[i]);
+                    pp = mul2(pp, d.a);
+                    ee = fma2(pp, load_pair(bdy + at), ee);
                 }
-            __threadfence();
-            __syncwarp();
-            if (lane == 0)
-                st_release(flag, 1);
-            if (!gated_gather<V>(a, u, 1, last, cb, c0, lane, s)) {
-                a.control[2] = 1;
+            }
+        };
+        if (cnt >= L)
+            run(Flag<true>());
+        else
+            run(Flag<false>());
+        float2 (*tp)[32] = tot_p[half], (*th)[32] = tot_h[half], (*te)[32] = tot_e[half];
+        tp[warp][lane] = pp;
+        th[warp][lane] = hh;
+        te[warp][lane] = ee;
+        __syncthreads();                                    // the runs' maps are there, the round before is done
+        if (S == 2 && k + 1 < rounds)
+            fetch(k + 1);
+        if (R > 1) {
+            if (warp == 0) {
+                GatedMsg m{both(1.f), both(0.f)};
 #pragma unroll
-                for (int q = 0; q < V; ++q)
-                    s[q] = __int_as_float(0x7fc00000);
+                for (int w = W - 1; w >= 0; --w) {
+                    m.h = fma2(tp[w][lane], m.h, te[w][lane]);
+                    m.p = mul2(m.p, tp[w][lane]);
+                }
+                exchange_send(ex, k, rank, R, lane, m);
+            }
+            ok = ok && tc::mbar_wait(&ex.bar[half], (k >> 1) & 1, cap);
+            __syncwarp();
+        }
+        if (!ok)
+            s = both(__int_as_float(0x7fc00000));
+        // the E arriving at this block's chunk, at this warp's run, and at the next round
+        float2 mine = s, next = s;
+        if (R > 1) {
+            for (int r = R - 1; r >= 0; --r) {
+                if (r == rank)
+                    mine = next;
+                next = fma2(ex.msg[half][r][lane].p, next, ex.msg[half][r][lane].h);
             }
         }
-        if (u == first) {
-            if (inside && a.grad_state0)
+        float2 E = mine;
 #pragma unroll
-                for (int q = 0; q < V; ++q)
-                    a.grad_state0[(long long)seq * a.C + c0 + q] =
-                        a.resume[seq] != 0 ? fmaf(P[q], s[q], E[q]) : 0.f;
-        } else {
-            if (inside)
-#pragma unroll
-                for (int q = 0; q < V; ++q)
-                    __stcg(a.out_state + at + q, fmaf(P[q], s[q], E[q]));
-            __threadfence();
-            __syncwarp();
-            if (lane == 0)
-                st_release(flag, 2);
+        for (int w = W - 1; w >= 0; --w) {
+            if (w == warp)
+                E = mine;
+            mine = fma2(tp[w][lane], mine, te[w][lane]);
         }
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-            arrive[lane * V + q] = s[q];
-    }
-    __syncthreads();
-    float E[V], part[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        float h = hin[q];
+        s = R > 1 ? next : mine;
         for (int w = 0; w < warp; ++w)
-            h = fmaf(tot_p[w][lane * V + q], h, tot_h[w][lane * V + q]);
+            h = fma2(tp[w][lane], h, th[w][lane]);
 #pragma unroll
-        for (int k = 0; k < L; ++k) {                      // hb[k]: b_k -> h_{k-1}
-            const float before = h;
-            h = fmaf(dec[k][q], h, hb[k][q]);
-            hb[k][q] = before;
+        for (int i = 0; i < L; ++i) {                       // hb[i]: b_i -> h_{i-1}
+            const float2 before = h;
+            h = fma2(dec[i], h, hb[i]);
+            hb[i] = before;
         }
-        E[q] = arrive[lane * V + q];
-        for (int w = W - 1; w > warp; --w)
-            E[q] = fmaf(tot_p[w][lane * V + q], E[q], tot_e[w][lane * V + q]);
-        part[q] = 0.f;
-    }
+        const long long t = t0 + j * (long long)kGatedChunk + warp * L;
+        T *ox = static_cast<T *>(a.grad_x) + t * a.gsx + c0;
+        T *oa = static_cast<T *>(a.grad_ga) + t * a.gsga + c0;
+        T *og = static_cast<T *>(a.grad_gx) + t * a.gsgx + c0;
 #pragma unroll
-    for (int k = L - 1; k >= 0; --k)
-        if (inside && k < cnt) {
-            Vec<T, V> ox, oa, og;
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float g = to_float(dy[k].v[q]) + E[q];
-                const float e = dec[k][q];
-                E[q] = e * g;
-                const float r = sigmoid_f(to_float(ga[k].v[q])), i = sigmoid_f(to_float(gx[k].v[q]));
-                const float v = rate[q] * r;
+        for (int i = L - 1; i >= 0; --i)
+            if (inside && i < cnt) {
+                const int at = (warp * L + i) * kGatedCh + 2 * lane;
+                const float2 g = add2(load_pair(bdy + at), E);
+                E = mul2(dec[i], g);
+                const float2 r = sigmoid2(load_pair(bga + at)), gi = sigmoid2(load_pair(bgx + at));
+                const float2 v = mul2(rate, r);
                 const Decay d = decay_of(v);
-                const float ix = i * to_float(x[k].v[q]);
-                const float dla = g * (e * hb[k][q] - e * e * d.im * ix);
-                part[q] = fmaf(dla, r, part[q]);
-                ox.v[q] = from_float<T>(g * d.m * i);
-                og.v[q] = from_float<T>(g * d.m * ix * (1.f - i));
-                oa.v[q] = from_float<T>(-dla * v * (1.f - r));
+                const float2 ix = mul2(gi, load_pair(bx + at)), gm = mul2(g, d.m);
+                // d log a = g (a h - a^2 ix / m)
+                const float2 dla = mul2(mul2(g, d.a), fma2(mul2(d.a, d.im), make_float2(-ix.x, -ix.y), hb[i]));
+                part = fma2(dla, r, part);
+                store_pair(ox + i * a.gsx, mul2(gm, gi), pairs, two);
+                store_pair(og + i * a.gsgx, mul2(mul2(gm, ix), make_float2(1.f - gi.x, 1.f - gi.y)), pairs, two);
+                store_pair(oa + i * a.gsga, mul2(mul2(dla, v), make_float2(r.x - 1.f, r.y - 1.f)), pairs, two);
             }
-            const long long t = t0 + tw + k;
-            store_vec<T, V>(static_cast<T *>(a.grad_x) + t * a.gsx + c0, ox);
-            store_vec<T, V>(static_cast<T *>(a.grad_ga) + t * a.gsga + c0, oa);
-            store_vec<T, V>(static_cast<T *>(a.grad_gx) + t * a.gsgx + c0, og);
+        if (S == 1 && k + 1 < rounds) {
+            __syncthreads();                                // the stage is read
+            fetch(k + 1);
         }
-    __syncthreads();                                       // tot_p is read no more
-#pragma unroll
-    for (int q = 0; q < V; ++q)
-        tot_p[warp][lane * V + q] = part[q];
+    }
+    if (rank == 0 && warp == 0 && inside && a.grad_state0) {
+        const bool resume = a.resume[seq] != 0;
+        float *g = a.grad_state0 + (long long)seq * a.C + c0;
+        g[0] = resume ? s.x : 0.f;
+        if (two)
+            g[1] = resume ? s.y : 0.f;
+    }
     __syncthreads();
-    if (warp == 0 && inside)
+    tot_p[0][warp][lane] = part;
+    __syncthreads();
+    if (warp == 0 && inside) {
+        float2 sum = both(0.f);
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                s += tot_p[w][lane * V + q];
-            a.lam_part[at + q] = s;
-        }
+        for (int w = 0; w < W; ++w)
+            sum = add2(sum, tot_p[0][w][lane]);
+        float *to = a.lam_part + ((long long)seq * R + rank) * a.C + c0;
+        to[0] = sum.x;
+        if (two)
+            to[1] = sum.y;
+    }
+    gated_cluster_end(R);
 }
 
-// dlam from the units' sums, in a fixed order: a block of 8 warps owns 32
-// channels, warp w adds units w, w + 8, ...
+// dlam from the blocks' sums, in a fixed order: a block of 8 warps owns 32
+// channels, warp w adds rows w, w + 8, ...
 __global__ void __launch_bounds__(256)
 gated_lam_kernel(const GatedArgs a)
 {
     griddep_entry();
     __shared__ float part[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    const int units = a.control[0];
+    const int rows = a.n_seqs * a.cluster;
     float s = 0.f;
     if (c < a.C)
-        for (int u = warp; u < units; u += 8)
+#pragma unroll 4
+        for (int u = warp; u < rows; u += 8)
             s += a.lam_part[(long long)u * a.C + c];
     part[warp][lane] = s;
     __syncthreads();
@@ -226,32 +260,40 @@ gated_lam_kernel(const GatedArgs a)
     }
 }
 
-template <class T, int V>
-cudaError_t launch_backward(const GatedArgs &a, cudaStream_t stream)
+template <class T>
+cudaError_t launch_backward(const GatedArgs &a, bool pairs, int dtype, cudaStream_t stream)
 {
-    cudaError_t e = launch_gated_plan(a, stream);
-    if (e == cudaSuccess)
-        e = launch_pdl(gated_scan_backward_kernel<T, V>, dim3((unsigned)((long long)a.max_units * a.cblocks)),
-                       dim3(32 * kGatedWarps), 0, stream, a);
-    if (e == cudaSuccess)
-        e = launch_pdl(gated_lam_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, stream, a);
-    return e;
+    GatedMap mx, mga, mgx, mdy;
+    cudaError_t e;
+    constexpr size_t smem = GatedBackward<T>::kSmem;
+    if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
+        gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx) &&
+        gated_map(&mdy, a.grad_y, dtype, a.n_tokens, a.C, a.sy)) {
+        e = launch_clusters(gated_scan_backward_kernel<T, true>, a, smem, stream, a, pairs ? 1 : 0, 0, mx, mga, mgx, mdy);
+    } else {
+        const bool words = gated_words(a.x, dtype, a.C, a.sx) && gated_words(a.gate_a, dtype, a.C, a.sga) &&
+                           gated_words(a.gate_x, dtype, a.C, a.sgx) && gated_words(a.grad_y, dtype, a.C, a.sy);
+        e = launch_clusters(gated_scan_backward_kernel<T, false>, a, smem, stream, a, pairs ? 1 : 0, words ? 1 : 0, mx,
+                            mga, mgx, mdy);
+    }
+    return e != cudaSuccess ? e
+                            : launch_pdl(gated_lam_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, void *workspace, cudaStream_t stream)
+cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, cudaStream_t stream)
 {
-    const bool pairs = gated_pairs(a, dtype, true);
-    a.max_units = (int)gated_max_units(a.n_seqs, a.n_tokens);
-    a.cblocks = (a.C + (pairs ? 63 : 31)) / (pairs ? 64 : 32);
-    gated_carve(a, workspace);
-    a.lam_part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                           gated_workspace_bytes(a.n_seqs, a.n_tokens, a.C));
+    a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
+    a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C);
+    a.fail_waits = debug_fail_waits() ? 1 : 0;
+    const bool pairs = ((a.C | a.gsx | a.gsga | a.gsgx) & 1) == 0 &&
+                       ((reinterpret_cast<uintptr_t>(a.grad_x) | reinterpret_cast<uintptr_t>(a.grad_ga) |
+                         reinterpret_cast<uintptr_t>(a.grad_gx)) % (2 * dtype_size(dtype))) == 0;
     switch (dtype) {
-    case kF32: return pairs ? launch_backward<float, 2>(a, stream) : launch_backward<float, 1>(a, stream);
-    case kBF16: return pairs ? launch_backward<__nv_bfloat16, 2>(a, stream) : launch_backward<__nv_bfloat16, 1>(a, stream);
-    case kF16: return pairs ? launch_backward<__half, 2>(a, stream) : launch_backward<__half, 1>(a, stream);
+    case kF32: return launch_backward<float>(a, pairs, dtype, stream);
+    case kBF16: return launch_backward<__nv_bfloat16>(a, pairs, dtype, stream);
+    case kF16: return launch_backward<__half>(a, pairs, dtype, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -3,16 +3,23 @@
 The gated linear recurrence, the RMS norm with the residual's addition, the row
 quantiser and the 8-bit integer matrix product of ``libssmscan.so`` on torch
 tensors.  Every function runs on the current CUDA stream of its tensors' device,
-or on ``stream``; what it allocates (outputs not given, workspaces) belongs to
+or on its keyword argument ``stream``; what it allocates (outputs not given, workspaces) belongs to
 that stream.  Tensors are [rows, width] with contiguous rows; rows may be further
 apart than their width (slices of a wider tensor).  Formulas and rules are those
 of ``include/ssmscan.h``.
 """
 from __future__ import annotations
 
+import contextlib
+import functools
+
 import torch
 
 from .binding import SSM_OK, SsmScanError, load
+
+# torch's own short ways to the current device and stream (a stream object takes 2 us to make)
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: -2)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -32,20 +39,21 @@ def _bad(t, name, dtype, dev, shape):
 
 def _rows(t, name, dtype, dev, shape):
     """(pointer, row stride) of a checked [rows, width] tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.shape != shape:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or t.shape != shape:
         raise _bad(t, name, dtype, dev, shape)
-    rows, width = shape
     s0, s1 = t.stride()
-    if rows <= 1:
-        s0 = max(s0, width)                       # a single row's stride says nothing
-    if (s1 != 1 and width > 1) or s0 < width:
-        raise _bad(t, name, dtype, dev, shape)
+    if s1 != 1 or s0 < shape[1]:
+        rows, width = shape
+        if rows <= 1:
+            s0 = max(s0, width)                   # a single row's stride says nothing
+        if (s1 != 1 and width > 1) or s0 < width:
+            raise _bad(t, name, dtype, dev, shape)
     return t.data_ptr(), s0
 
 
 def _flat(t, name, dtype, dev, shape):
     """Pointer of a checked contiguous tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
         raise _bad(t, name, dtype, dev, shape)
     return t.data_ptr()
 
@@ -53,7 +61,7 @@ def _flat(t, name, dtype, dev, shape):
 def _dtype(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("the operators run on CUDA tensors only")
     if t.dim() != 2:
         raise ValueError(f"{name} must be [rows, width], got {t.dim()} dimensions")
@@ -63,30 +71,47 @@ def _dtype(t, name):
     return code
 
 
-class _On:
-    """The launching device and stream: ``with _On(dev, stream) as handle``.  Allocations inside
-    belong to the stream."""
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The tensors' device and the launching stream made current: what is allocated inside belongs
+    to that stream."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(stream):
+            yield
 
-    def __init__(self, dev, stream):
-        self.dev, self.stream, self.stack = dev, stream, []
 
-    def __enter__(self):
-        if self.dev.index != torch.cuda.current_device():
-            self.stack.append(torch.cuda.device(self.dev))
-            self.stack[-1].__enter__()
-        s = self.stream
-        if s is None:
-            return torch.cuda.current_stream(self.dev).cuda_stream
-        if not hasattr(s, "cuda_stream"):
-            s = torch.cuda.ExternalStream(int(s), device=self.dev)
-        self.stack.append(torch.cuda.stream(s))
-        self.stack[-1].__enter__()
-        return s.cuda_stream
+def _placed(fn):
+    """Adds ``stream=None`` to an operator whose first argument says the device: the call itself runs
+    with that device and stream current."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if (not isinstance(first, torch.Tensor) or not first.is_cuda or
+                (stream is None and first.get_device() == _current_device())):
+            return fn(first, *args, **kw)         # (what is no CUDA tensor is refused there)
+        with _on(first.device, stream):
+            return fn(first, *args, **kw)
+    return call
 
-    def __exit__(self, *exc):
-        while self.stack:
-            self.stack.pop().__exit__(*exc)
-        return False
+
+def _rows_out(t, name, dtype, dev, shape):
+    """(tensor, pointer, row stride): `t` checked, or a new tensor."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr(), shape[1]
+    return (t, *_rows(t, name, dtype, dev, shape))
+
+
+def _flat_out(t, name, dtype, dev, shape):
+    """(tensor, pointer): `t` checked, or a new tensor."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _flat(t, name, dtype, dev, shape)
 
 
 def _workspace(given, need, dev):
@@ -104,9 +129,9 @@ def _workspace(given, need, dev):
 # ---- gated linear recurrence ----
 
 
-def gated_scan_workspace_bytes(n_seqs, n_tokens, channels, training=False) -> int:
-    """Bytes of workspace of ``ssm_gated_scan`` (training: with chunk_states, and of the backward pass)."""
-    return int(load().ssm_gated_scan_workspace_bytes(int(n_seqs), int(n_tokens), int(channels), int(bool(training))))
+def gated_scan_backward_workspace_bytes(n_seqs, n_tokens, channels) -> int:
+    """Bytes of workspace of ``ssm_gated_scan_backward``."""
+    return int(load().ssm_gated_scan_backward_workspace_bytes(int(n_seqs), int(n_tokens), int(channels)))
 
 
 def gated_scan_chunk_states(n_seqs, n_tokens, channels, device="cuda"):
@@ -115,8 +140,9 @@ def gated_scan_chunk_states(n_seqs, n_tokens, channels, device="cuda"):
     return torch.empty((chunks, int(channels)), dtype=torch.float32, device=device)
 
 
+@_placed
 def ssm_gated_scan(state_slots, x, gate_a, gate_x, lam, seq_starts, seq_lens, resume_flags, y=None, *,
-                   decay_scale=8.0, chunk_states=None, workspace=None, stream=None):
+                   decay_scale=8.0, chunk_states=None):
     """Gated linear recurrence (``ssm_gated_scan``): with r = sigmoid(gate_a), i = sigmoid(gate_x),
     a = exp(-decay_scale softplus(lam) r),
 
@@ -142,24 +168,19 @@ def ssm_gated_scan(state_slots, x, gate_a, gate_x, lam, seq_starts, seq_lens, re
     pc = None
     if chunk_states is not None:
         pc = _flat(chunk_states, "chunk_states", f32, dev, (lib.ssm_gated_scan_chunks(n, T, C), C))
-    with _On(dev, stream) as handle:
-        if y is None:
-            y = torch.empty(shape, dtype=dt, device=dev)
-        py, sy = _rows(y, "y", dt, dev, shape)
-        ws, nb = None, 0
-        if n != T or pc is not None or workspace is not None:
-            need = lib.ssm_gated_scan_workspace_bytes(n, T, C, 0 if pc is None else 1)
-            ws, nb, workspace = _workspace(workspace, need, dev)
-        rc = lib.ssm_gated_scan(slots, px, pa, pg, plam, decay_scale, py, ps, pl, pr, n, T, C, code, sx, sa, sg, sy,
-                                pc, ws, nb, handle)
+    handle = _raw_stream(dev.index)
+    y, py, sy = _rows_out(y, "y", dt, dev, shape)
+    rc = lib.ssm_gated_scan(slots, px, pa, pg, plam, decay_scale, py, ps, pl, pr, n, T, C, code, sx, sa, sg, sy,
+                            pc, handle)
     if rc != SSM_OK:
         raise SsmScanError(rc, "ssm_gated_scan")
     return y
 
 
+@_placed
 def ssm_gated_scan_backward(grad_y, x, gate_a, gate_x, lam, chunk_states, seq_starts, seq_lens, resume_flags, *,
                             decay_scale=8.0, grad_state=None, grad_x=None, grad_gate_a=None, grad_gate_x=None,
-                            grad_lam=None, grad_initial_state=None, workspace=None, stream=None):
+                            grad_lam=None, grad_initial_state=None, workspace=None):
     """Gradients of ``ssm_gated_scan`` (``ssm_gated_scan_backward``) from the gradient of y and
     optionally of the slots after the call (grad_state [n, C] fp32); chunk_states as filled by the
     forward call.  Outputs are allocated if not given.  Returns
@@ -179,26 +200,15 @@ def ssm_gated_scan_backward(grad_y, x, gate_a, gate_x, lam, chunk_states, seq_st
     ps, pl, pr = (_flat(seq_starts, "seq_starts", i32, dev, one), _flat(seq_lens, "seq_lens", i32, dev, one),
                   _flat(resume_flags, "resume_flags", i32, dev, one))
     pgs = None if grad_state is None else _flat(grad_state, "grad_state", f32, dev, (n, C))
-    with _On(dev, stream) as handle:
-        if grad_x is None:
-            grad_x = torch.empty(shape, dtype=dt, device=dev)
-        if grad_gate_a is None:
-            grad_gate_a = torch.empty(shape, dtype=dt, device=dev)
-        if grad_gate_x is None:
-            grad_gate_x = torch.empty(shape, dtype=dt, device=dev)
-        if grad_lam is None:
-            grad_lam = torch.empty((C,), dtype=f32, device=dev)
-        if grad_initial_state is None:
-            grad_initial_state = torch.empty((n, C), dtype=f32, device=dev)
-        qx, tx = _rows(grad_x, "grad_x", dt, dev, shape)
-        qa, ta = _rows(grad_gate_a, "grad_gate_a", dt, dev, shape)
-        qg, tg = _rows(grad_gate_x, "grad_gate_x", dt, dev, shape)
-        ql = _flat(grad_lam, "grad_lam", f32, dev, (C,))
-        q0 = _flat(grad_initial_state, "grad_initial_state", f32, dev, (n, C))
-        need = max(256, lib.ssm_gated_scan_workspace_bytes(n, T, C, 1))
-        ws, nb, workspace = _workspace(workspace, need, dev)
-        rc = lib.ssm_gated_scan_backward(py, pgs, px, pa, pg, plam, decay_scale, pc, ps, pl, pr, n, T, C, code,
-                                         sx, sa, sg, sy, qx, qa, qg, tx, ta, tg, ql, q0, ws, nb, handle)
+    handle = _raw_stream(dev.index)
+    grad_x, qx, tx = _rows_out(grad_x, "grad_x", dt, dev, shape)
+    grad_gate_a, qa, ta = _rows_out(grad_gate_a, "grad_gate_a", dt, dev, shape)
+    grad_gate_x, qg, tg = _rows_out(grad_gate_x, "grad_gate_x", dt, dev, shape)
+    grad_lam, ql = _flat_out(grad_lam, "grad_lam", f32, dev, (C,))
+    grad_initial_state, q0 = _flat_out(grad_initial_state, "grad_initial_state", f32, dev, (n, C))
+    ws, nb, workspace = _workspace(workspace, lib.ssm_gated_scan_backward_workspace_bytes(n, T, C), dev)
+    rc = lib.ssm_gated_scan_backward(py, pgs, px, pa, pg, plam, decay_scale, pc, ps, pl, pr, n, T, C, code,
+                                     sx, sa, sg, sy, qx, qa, qg, tx, ta, tg, ql, q0, ws, nb, handle)
     if rc != SSM_OK:
         raise SsmScanError(rc, "ssm_gated_scan_backward")
     return grad_x, grad_gate_a, grad_gate_x, grad_lam, grad_initial_state
@@ -207,8 +217,8 @@ def ssm_gated_scan_backward(grad_y, x, gate_a, gate_x, lam, chunk_states, seq_st
 # ---- RMS norm with the residual's addition; row quantiser ----
 
 
-def ssm_add_norm(x, weight, residual=None, *, eps=1e-6, quant=None, residual_out=None, out=None, scales=None,
-                 stream=None):
+@_placed
+def ssm_add_norm(x, weight, residual=None, *, eps=1e-6, quant=None, residual_out=None, out=None, scales=None):
     """RMS norm with the residual's addition (``ssm_add_norm``): h = x + residual in the residual's
     type, y = h / sqrt(mean(h^2) + eps) * weight per row.
 
@@ -229,31 +239,24 @@ def ssm_add_norm(x, weight, residual=None, *, eps=1e-6, quant=None, residual_out
         pr, sr = _rows(residual, "residual", rdt, dev, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    with _On(dev, stream) as handle:
-        ph, sh, h = None, 0, x
-        if residual is not None:
-            h = torch.empty(shape, dtype=rdt, device=dev) if residual_out is None else residual_out
-            ph, sh = _rows(h, "residual_out", rdt, dev, shape)
-        py, pc, ps = None, None, None
-        if quant is None:
-            if out is None:
-                out = torch.empty(shape, dtype=dt, device=dev)
-            py, so = _rows(out, "out", dt, dev, shape)
-        else:
-            if out is None:
-                out = torch.empty(shape, dtype=torch.int8, device=dev)
-            if scales is None:
-                scales = torch.empty((T,), dtype=torch.float32, device=dev)
-            pc, so = _rows(out, "out", torch.int8, dev, shape)
-            ps = _flat(scales, "scales", torch.float32, dev, (T,))
-        rc = load().ssm_add_norm(px, pr, pw, eps, ph, py, pc, ps, T, D, code, rcode, sx, sr, sh, so, handle)
+    handle = _raw_stream(dev.index)
+    ph, sh, h = None, 0, x
+    if residual is not None:
+        h, ph, sh = _rows_out(residual_out, "residual_out", rdt, dev, shape)
+    py, pc, ps = None, None, None
+    if quant is None:
+        out, py, so = _rows_out(out, "out", dt, dev, shape)
+    else:
+        out, pc, so = _rows_out(out, "out", torch.int8, dev, shape)
+        scales, ps = _flat_out(scales, "scales", torch.float32, dev, (T,))
+    rc = load().ssm_add_norm(px, pr, pw, eps, ph, py, pc, ps, T, D, code, rcode, sx, sr, sh, so, handle)
     if rc != SSM_OK:
         raise SsmScanError(rc, "ssm_add_norm")
     return (out, h) if quant is None else (out, scales, h)
 
 
-def ssm_add_norm_backward(grad_y, h, weight, *, grad_h=None, eps=1e-6, grad_in=None, grad_weight=None, workspace=None,
-                          stream=None):
+@_placed
+def ssm_add_norm_backward(grad_y, h, weight, *, grad_h=None, eps=1e-6, grad_in=None, grad_weight=None, workspace=None):
     """Gradient of ``ssm_add_norm`` (``ssm_add_norm_backward``): grad_y [T, D] in y's type, h as the
     forward call returned it, grad_h (h's type) the gradient that reaches h from elsewhere.
     Returns (grad_in [T, D] in h's type: the gradient of x and of residual alike, grad_weight [D] fp32)."""
@@ -265,35 +268,28 @@ def ssm_add_norm_backward(grad_y, h, weight, *, grad_h=None, eps=1e-6, grad_in=N
     pw = _flat(weight, "weight", torch.float32, dev, (D,))
     pr, sr = (None, 0) if grad_h is None else _rows(grad_h, "grad_h", hdt, dev, shape)
     lib = load()
-    with _On(dev, stream) as handle:
-        if grad_in is None:
-            grad_in = torch.empty(shape, dtype=hdt, device=dev)
-        if grad_weight is None:
-            grad_weight = torch.empty((D,), dtype=torch.float32, device=dev)
-        pi, si = _rows(grad_in, "grad_in", hdt, dev, shape)
-        pq = _flat(grad_weight, "grad_weight", torch.float32, dev, (D,))
-        ws, nb, workspace = _workspace(workspace, lib.ssm_add_norm_backward_workspace_bytes(T, D), dev)
-        rc = lib.ssm_add_norm_backward(pg, ph, pw, eps, pr, pi, pq, T, D, code, hcode, sg, sh, sr, si, ws, nb, handle)
+    handle = _raw_stream(dev.index)
+    grad_in, pi, si = _rows_out(grad_in, "grad_in", hdt, dev, shape)
+    grad_weight, pq = _flat_out(grad_weight, "grad_weight", torch.float32, dev, (D,))
+    ws, nb, workspace = _workspace(workspace, lib.ssm_add_norm_backward_workspace_bytes(T, D), dev)
+    rc = lib.ssm_add_norm_backward(pg, ph, pw, eps, pr, pi, pq, T, D, code, hcode, sg, sh, sr, si, ws, nb, handle)
     if rc != SSM_OK:
         raise SsmScanError(rc, "ssm_add_norm_backward")
     return grad_in, grad_weight
 
 
-def ssm_quantize_rows(x, codes=None, scales=None, *, stream=None):
+@_placed
+def ssm_quantize_rows(x, codes=None, scales=None):
     """Rows in 8 bits with a scale each (``ssm_quantize_rows``): x [T, D] fp32, bf16 or fp16.
     Returns (codes [T, D] int8, scales [T] fp32), codes * scales being x to half a step."""
     code = _dtype(x, "x")
     dev, shape = x.device, x.shape
     T, D = shape
     px, sx = _rows(x, "x", x.dtype, dev, shape)
-    with _On(dev, stream) as handle:
-        if codes is None:
-            codes = torch.empty(shape, dtype=torch.int8, device=dev)
-        if scales is None:
-            scales = torch.empty((T,), dtype=torch.float32, device=dev)
-        pc, sc = _rows(codes, "codes", torch.int8, dev, shape)
-        rc = load().ssm_quantize_rows(px, pc, _flat(scales, "scales", torch.float32, dev, (T,)), T, D, code, sx, sc,
-                                      handle)
+    handle = _raw_stream(dev.index)
+    codes, pc, sc = _rows_out(codes, "codes", torch.int8, dev, shape)
+    scales, ps = _flat_out(scales, "scales", torch.float32, dev, (T,))
+    rc = load().ssm_quantize_rows(px, pc, ps, T, D, code, sx, sc, handle)
     if rc != SSM_OK:
         raise SsmScanError(rc, "ssm_quantize_rows")
     return codes, scales
@@ -302,8 +298,8 @@ def ssm_quantize_rows(x, codes=None, scales=None, *, stream=None):
 # ---- 8-bit integer matrix product ----
 
 
-def ssm_int8_matmul(x, x_scales, w, w_scales, *, bias=None, out=None, out_dtype=torch.bfloat16, workspace=None,
-                    stream=None):
+@_placed
+def ssm_int8_matmul(x, x_scales, w, w_scales, *, bias=None, out=None, out_dtype=torch.bfloat16, workspace=None):
     """8-bit integer matrix product (``ssm_int8_matmul``):
     out[t, n] = (sum_k x[t, k] w[n, k]) x_scales[t] w_scales[n] + bias[n].
 
@@ -326,12 +322,10 @@ def ssm_int8_matmul(x, x_scales, w, w_scales, *, bias=None, out=None, out_dtype=
     pxs, pws = _flat(x_scales, "x_scales", f32, dev, (T,)), _flat(w_scales, "w_scales", f32, dev, (N,))
     pb = None if bias is None else _flat(bias, "bias", f32, dev, (N,))
     lib = load()
-    with _On(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((T, N), dtype=out_dtype, device=dev)
-        po, so = _rows(out, "out", out_dtype, dev, (T, N))
-        ws, nb, workspace = _workspace(workspace, lib.ssm_int8_matmul_workspace_bytes(px, pw, T, N, K, sx, sw), dev)
-        rc = lib.ssm_int8_matmul(px, pxs, pw, pws, pb, po, T, N, K, code, sx, sw, so, ws, nb, handle)
+    handle = _raw_stream(dev.index)
+    out, po, so = _rows_out(out, "out", out_dtype, dev, (T, N))
+    ws, nb, workspace = _workspace(workspace, lib.ssm_int8_matmul_workspace_bytes(px, pw, T, N, K, sx, sw), dev)
+    rc = lib.ssm_int8_matmul(px, pxs, pw, pws, pb, po, T, N, K, code, sx, sw, so, ws, nb, handle)
     if rc != SSM_OK:
         raise SsmScanError(rc, "ssm_int8_matmul")
     return out

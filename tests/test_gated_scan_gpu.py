@@ -252,9 +252,21 @@ def test_other_stream_and_graph():
 
 def test_refuses_small_workspace():
     c = _case(64, [100], seed=17)
-    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    _, _, ch = _forward(c, train=True)
+    ws = torch.empty(128, dtype=torch.uint8, device="cuda")
     with pytest.raises(pkg.SsmScanError) as e:
-        _forward(c, workspace=ws)
+        _backward(c, ch, workspace=ws)
     assert e.value.status == -1
-    need = layers.gated_scan_workspace_bytes(1, 100, 64)
-    _check_forward(c, *_forward(c, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))[:2])
+    need = layers.gated_scan_backward_workspace_bytes(1, 100, 64)
+    _check_backward(c, _backward(c, ch, workspace=torch.empty(need, dtype=torch.uint8, device="cuda")))
+
+
+@pytest.mark.parametrize("C", [30, 64, 129])
+@pytest.mark.parametrize("lens", [[1024], [2100], [600, 1, 0, 1500], [64 * 8] * 3])
+def test_time_shared_by_a_cluster(lens, C):
+    """Few channels and long sequences: clusters of 2 to 8 blocks, lengths that leave some of them
+    without a chunk, forward and backward."""
+    c = _case(C, lens, resume=[1] * len(lens), seed=C + len(lens))
+    y, slots, ch = _forward(c, train=True)
+    _check_forward(c, y, slots)
+    _check_backward(c, _backward(c, ch))

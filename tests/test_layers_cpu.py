@@ -26,7 +26,7 @@ def _call(fn, defaults, **over):
 
 
 SCAN = dict(p_state=P, p_x=P, p_ga=P, p_gx=P, p_lam=P, scale=8.0, p_y=P, p_starts=P, p_lens=P, p_resume=P, n=2, T=8,
-            C=16, dtype=1, sx=16, sga=16, sgx=16, sy=16, p_chunks=0, p_ws=P, ws=1 << 20, p_stream=0)
+            C=16, dtype=1, sx=16, sga=16, sgx=16, sy=16, p_chunks=0, p_stream=0)
 
 
 @pytest.mark.parametrize("over,expect", [
@@ -36,20 +36,18 @@ SCAN = dict(p_state=P, p_x=P, p_ga=P, p_gx=P, p_lam=P, scale=8.0, p_y=P, p_start
     (dict(p_state=0), INV), (dict(p_x=0), INV), (dict(p_ga=0), INV), (dict(p_gx=0), INV), (dict(p_lam=0), INV),
     (dict(p_y=0), INV), (dict(p_starts=0), INV), (dict(p_lens=0), INV), (dict(p_resume=0), INV),
     (dict(p_state=P + 2), INV), (dict(p_x=P + 1), INV), (dict(p_y=P + 1), INV), (dict(dtype=0, p_ga=P + 2), INV),
-    (dict(p_chunks=P + 1), INV), (dict(p_ws=0), INV), (dict(p_ws=P + 16), INV), (dict(ws=100), INV),
-    (dict(n=1, T=2**31 - 1, C=4096, sx=4096, sga=4096, sgx=4096, sy=4096), UNS),
+    (dict(p_chunks=P + 1), INV), (dict(n=2**31 - 1, C=64, sx=64, sga=64, sgx=64, sy=64), UNS),
 ])
 def test_gated_scan_refuses(lib, over, expect):
     assert _call(lib.ssm_gated_scan, SCAN, **over) == expect
 
 
 def test_gated_scan_nothing_to_do(lib):
-    assert _call(lib.ssm_gated_scan, SCAN, n=0, p_state=0, p_x=0, p_ws=0) == 0
+    assert _call(lib.ssm_gated_scan, SCAN, n=0, p_state=0, p_x=0) == 0
     assert lib.ssm_gated_scan_chunks(2, 100, 8) >= 2 + 100 // 4096
     assert lib.ssm_gated_scan_chunks(-1, 100, 8) == 0 and lib.ssm_gated_scan_chunks(1, 1, 0) == 0
-    assert lib.ssm_gated_scan_workspace_bytes(16, 16, 64, 0) == 0
-    assert lib.ssm_gated_scan_workspace_bytes(16, 16, 64, 1) > 0
-    assert lib.ssm_gated_scan_workspace_bytes(16, 17, 64, 0) > 0
+    assert lib.ssm_gated_scan_backward_workspace_bytes(16, 16, 64) > 0
+    assert lib.ssm_gated_scan_backward_workspace_bytes(0, 16, 64) == 0
 
 
 BACK = dict(p_gy=P, p_gs=P, p_x=P, p_ga=P, p_gx=P, p_lam=P, scale=8.0, p_chunks=P, p_starts=P, p_lens=P, p_resume=P,
@@ -61,7 +59,7 @@ BACK = dict(p_gy=P, p_gs=P, p_x=P, p_ga=P, p_gx=P, p_lam=P, scale=8.0, p_chunks=
     (dict(n=-1), INV), (dict(C=-4), INV), (dict(dtype=7), INV), (dict(scale=-1.0), INV), (dict(sgy=3), INV),
     (dict(tx=3), INV), (dict(ta=3), INV), (dict(tg=3), INV), (dict(p_gy=0), INV), (dict(p_x=0), INV),
     (dict(p_chunks=0), INV), (dict(p_dx=0), INV), (dict(p_da=0), INV), (dict(p_dg=0), INV), (dict(p_dlam=0), INV),
-    (dict(p_lam=0), INV), (dict(p_ws=0), INV), (dict(ws=256), INV), (dict(p_ws=P + 4), INV), (dict(p_dx=P + 1), INV),
+    (dict(p_lam=0), INV), (dict(p_ws=0), INV), (dict(ws=100), INV), (dict(p_ws=P + 4), INV), (dict(p_dx=P + 1), INV),
     (dict(p_d0=P + 2), INV), (dict(p_gs=P + 1), INV), (dict(p_resume=0), INV),
 ])
 def test_gated_scan_backward_refuses(lib, over, expect):
