@@ -67,6 +67,32 @@ __host__ __device__ __forceinline__ long long gated_chunk_row(int n_seqs, int se
     return j == 0 ? seq : n_seqs + t0 / kGatedChunk + j;
 }
 
+// Which sequence the n-th job takes: with up to 32 sequences the longest first, so that
+// the longest walk does not begin when the others end (each lane holds one length;
+// the n-th has n lengths before it).
+__device__ __forceinline__ int gated_job_seq(const GatedArgs &a, int n, int lane)
+{
+    if (a.n_seqs > 32 || a.n_seqs == 1)
+        return n;
+    const int mine = lane < a.n_seqs ? a.seq_lens[lane] : 0;
+    int before = 0;
+    for (int k = 0; k < a.n_seqs; ++k) {
+        const int other = __shfl_sync(kFullMask, mine, k);
+        before += other > mine || (other == mine && k < lane) ? 1 : 0;
+    }
+    return __ffs(__ballot_sync(kFullMask, lane < a.n_seqs && before == n)) - 1;
+}
+
+// Blocks of the cluster that a sequence of this length has work for; the others leave at once.
+__device__ __forceinline__ int gated_ranks(int len, int cluster)
+{
+    const int chunks = (len + kGatedChunk - 1) / kGatedChunk;
+    int r = 1;
+    while (r < cluster && r < chunks)
+        r *= 2;
+    return r;
+}
+
 // A sequence's token range; one that is not inside the packed rows counts as empty.
 __device__ __forceinline__ int gated_seq_len(const GatedArgs &a, int seq, long long &t0)
 {
@@ -100,6 +126,13 @@ __device__ __forceinline__ float rcp(float v)
     return r;
 }
 
+__device__ __forceinline__ float rsq(float v)
+{
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 1 / (1 + e^-v) from the hardware exponential and reciprocal (a few 1e-7
@@ -110,6 +143,33 @@ __device__ __forceinline__ float2 sigmoid2(float2 v)
     const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
     return make_float2(rcp(d.x), rcp(d.y));
 }
+
+// Both gates of a token's two channels, r = sigmoid(ga) and i = sigmoid(gx), with one
+// reciprocal for the four: the special-function unit (16 results a cycle and SM)
+// bounds these kernels, and four denominators below 2^31 have a product below
+// 2^124.  So only for gates above kGateLow; `low` ones take a reciprocal each.
+constexpr float kGateLow = -21.f;         // e^21 < 2^31
+
+template <bool LOW>
+__device__ __forceinline__ void gates2(float2 ga, float2 gx, float2 &r, float2 &i)
+{
+    if (LOW) {
+        r = sigmoid2(ga);
+        i = sigmoid2(gx);
+        return;
+    }
+    const float2 ta = mul2(ga, both(-kLog2e)), tx = mul2(gx, both(-kLog2e));
+    const float2 da = add2(make_float2(ex2(ta.x), ex2(ta.y)), both(1.f));
+    const float2 dx = add2(make_float2(ex2(tx.x), ex2(tx.y)), both(1.f));
+    const float2 q = mul2(da, dx);
+    const float inv = rcp(q.x * q.y);
+    const float2 iq = mul2(make_float2(q.y, q.x), both(inv));       // 1 / q
+    r = mul2(iq, dx);
+    i = mul2(iq, da);
+}
+
+// The smaller of m and the pair's values (a NaN is passed over: it comes through any path).
+__device__ __forceinline__ float min_pair(float m, float2 v) { return fminf(m, fminf(v.x, v.y)); }
 
 __device__ __forceinline__ float sigmoid_f(float v) { return rcp(1.f + ex2(v * -kLog2e)); }
 
@@ -138,9 +198,9 @@ __device__ __forceinline__ Decay decay_of(float2 v)
     Decay r;
     r.a = make_float2(nx ? 1.f - s.x : e.x, ny ? 1.f - s.y : e.y);
     const float2 m2 = fma2(d, r.a, d);
-    // m2 = 0 (a closed gate) gives m ~ 1e-19, whose products with the gate's
+    // m2 = 0 (a closed gate) gives 1/m ~ 1e19, whose products with the gate's
     // vanishing derivative are zero, and not 0 / 0
-    r.im = make_float2(rsqrtf(fmaxf(m2.x, 1e-38f)), rsqrtf(fmaxf(m2.y, 1e-38f)));
+    r.im = make_float2(rsq(fmaxf(m2.x, 2e-38f)), rsq(fmaxf(m2.y, 2e-38f)));
     r.m = mul2(m2, r.im);
     return r;
 }

@@ -79,11 +79,13 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
     __shared__ GatedExchange ex;
     __shared__ uint64_t full[S];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int R = a.cluster, rank = blockIdx.x % R, job = blockIdx.x / R;
-    const int seq = job / a.cblocks, cb = job - seq * a.cblocks;
+    const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
+    const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
     const int cap = a.fail_waits ? 0 : (int)tc::kSpinLimit;
     long long t0;
-    const int len = gated_seq_len(a, seq, t0);
+    const int len = gated_seq_len(a, seq, t0), R = gated_ranks(len, a.cluster);
+    if (rank >= R)
+        return;
     if (tid == 0) {
         exchange_init(ex);
         for (int i = 0; i < S; ++i)
@@ -142,23 +144,31 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
         }
         // the run from zero: h[i] and the product of decays p[i] up to token i
         float2 h[L], p[L], hh = both(0.f), pp = both(1.f);
-        auto run = [&](auto whole) {
+        auto run = [&](auto whole, auto low) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 if (whole.value || i < cnt) {
                     const int at = (warp * L + i) * kGatedCh + 2 * lane;
-                    const Decay d = decay_of(mul2(rate, sigmoid2(load_pair(bga + at))));
-                    hh = fma2(d.a, hh, mul2(mul2(d.m, sigmoid2(load_pair(bgx + at))), load_pair(bx + at)));
+                    float2 r, g;
+                    gates2<low.value>(load_pair(bga + at), load_pair(bgx + at), r, g);
+                    const Decay d = decay_of(mul2(rate, r));
+                    hh = fma2(d.a, hh, mul2(mul2(d.m, g), load_pair(bx + at)));
                     pp = mul2(pp, d.a);
                 }
                 h[i] = hh;
                 p[i] = pp;
             }
         };
-        if (cnt >= L)
-            run(Flag<true>());
+        float least = 0.f;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int at = (warp * L + i) * kGatedCh + 2 * lane;
+            least = min_pair(min_pair(least, load_pair(bga + at)), load_pair(bgx + at));
+        }
+        if (cnt >= L && __all_sync(kFullMask, least > kGateLow))
+            run(Flag<true>(), Flag<false>());
         else
-            run(Flag<false>());
+            run(Flag<false>(), Flag<true>());
         float2 (*tp)[32] = tot_p[k & 1], (*th)[32] = tot_h[k & 1];
         tp[warp][lane] = pp;
         th[warp][lane] = hh;

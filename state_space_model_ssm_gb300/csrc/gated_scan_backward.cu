@@ -45,11 +45,17 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
     __shared__ GatedExchange ex;
     __shared__ uint64_t full[S];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int R = a.cluster, rank = blockIdx.x % R, job = blockIdx.x / R;
-    const int seq = job / a.cblocks, cb = job - seq * a.cblocks;
+    const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
+    const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
     const int cap = a.fail_waits ? 0 : (int)tc::kSpinLimit;
     long long t0;
-    const int len = gated_seq_len(a, seq, t0);
+    const int len = gated_seq_len(a, seq, t0), R = gated_ranks(len, a.cluster);
+    if (rank >= R) {                                        // this rank's share of dlam
+        if (warp == 0)
+            for (int c = cb * kGatedCh + lane; c < min(a.C, (cb + 1) * kGatedCh); c += 32)
+                a.lam_part[((long long)seq * a.cluster + rank) * a.C + c] = 0.f;
+        return;
+    }
     if (tid == 0) {
         exchange_init(ex);
         for (int i = 0; i < S; ++i)
@@ -119,15 +125,17 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
         }
         // decays dec[i] and inputs hb[i] of the run; its maps of h and of E
         float2 dec[L], hb[L], hh = both(0.f), pp = both(1.f), ee = both(0.f);
-        auto run = [&](auto whole) {
+        auto run = [&](auto whole, auto low) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 dec[i] = both(1.f);
                 hb[i] = both(0.f);
                 if (whole.value || i < cnt) {
                     const int at = (warp * L + i) * kGatedCh + 2 * lane;
-                    const Decay d = decay_of(mul2(rate, sigmoid2(load_pair(bga + at))));
-                    hb[i] = mul2(mul2(d.m, sigmoid2(load_pair(bgx + at))), load_pair(bx + at));
+                    float2 r, g;
+                    gates2<low.value>(load_pair(bga + at), load_pair(bgx + at), r, g);
+                    const Decay d = decay_of(mul2(rate, r));
+                    hb[i] = mul2(mul2(d.m, g), load_pair(bx + at));
                     dec[i] = d.a;
                     hh = fma2(d.a, hh, hb[i]);
                     pp = mul2(pp, d.a);
@@ -135,10 +143,17 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
                 }
             }
         };
-        if (cnt >= L)
-            run(Flag<true>());
+        float least = 0.f;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int at = (warp * L + i) * kGatedCh + 2 * lane;
+            least = min_pair(min_pair(least, load_pair(bga + at)), load_pair(bgx + at));
+        }
+        const bool fast = cnt >= L && __all_sync(kFullMask, least > kGateLow);
+        if (fast)
+            run(Flag<true>(), Flag<false>());
         else
-            run(Flag<false>());
+            run(Flag<false>(), Flag<true>());
         float2 (*tp)[32] = tot_p[half], (*th)[32] = tot_h[half], (*te)[32] = tot_e[half];
         tp[warp][lane] = pp;
         th[warp][lane] = hh;
@@ -190,23 +205,32 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
         T *ox = static_cast<T *>(a.grad_x) + t * a.gsx + c0;
         T *oa = static_cast<T *>(a.grad_ga) + t * a.gsga + c0;
         T *og = static_cast<T *>(a.grad_gx) + t * a.gsgx + c0;
+        auto gradients = [&](auto whole, auto low) {
 #pragma unroll
-        for (int i = L - 1; i >= 0; --i)
-            if (inside && i < cnt) {
-                const int at = (warp * L + i) * kGatedCh + 2 * lane;
-                const float2 g = add2(load_pair(bdy + at), E);
-                E = mul2(dec[i], g);
-                const float2 r = sigmoid2(load_pair(bga + at)), gi = sigmoid2(load_pair(bgx + at));
-                const float2 v = mul2(rate, r);
-                const Decay d = decay_of(v);
-                const float2 ix = mul2(gi, load_pair(bx + at)), gm = mul2(g, d.m);
-                // d log a = g (a h - a^2 ix / m)
-                const float2 dla = mul2(mul2(g, d.a), fma2(mul2(d.a, d.im), make_float2(-ix.x, -ix.y), hb[i]));
-                part = fma2(dla, r, part);
-                store_pair(ox + i * a.gsx, mul2(gm, gi), pairs, two);
-                store_pair(og + i * a.gsgx, mul2(mul2(gm, ix), make_float2(1.f - gi.x, 1.f - gi.y)), pairs, two);
-                store_pair(oa + i * a.gsga, mul2(mul2(dla, v), make_float2(r.x - 1.f, r.y - 1.f)), pairs, two);
-            }
+            for (int i = L - 1; i >= 0; --i)
+                if (whole.value || i < cnt) {
+                    const int at = (warp * L + i) * kGatedCh + 2 * lane;
+                    const float2 g = add2(load_pair(bdy + at), E);
+                    E = mul2(dec[i], g);
+                    float2 r, gi;
+                    gates2<low.value>(load_pair(bga + at), load_pair(bgx + at), r, gi);
+                    const float2 v = mul2(rate, r);
+                    const Decay d = decay_of(v);
+                    const float2 ix = mul2(gi, load_pair(bx + at)), gm = mul2(g, d.m);
+                    // d log a = g (a h - a^2 ix / m)
+                    const float2 dla = mul2(mul2(g, d.a), fma2(mul2(d.a, d.im), make_float2(-ix.x, -ix.y), hb[i]));
+                    part = fma2(dla, r, part);
+                    if (inside) {
+                        store_pair(ox + i * a.gsx, mul2(gm, gi), pairs, two);
+                        store_pair(og + i * a.gsgx, mul2(gm, fma2(make_float2(-ix.x, -ix.y), gi, ix)), pairs, two);
+                        store_pair(oa + i * a.gsga, mul2(dla, fma2(v, r, make_float2(-v.x, -v.y))), pairs, two);
+                    }
+                }
+        };
+        if (fast)
+            gradients(Flag<true>(), Flag<false>());
+        else
+            gradients(Flag<false>(), Flag<true>());
         if (S == 1 && k + 1 < rounds) {
             __syncthreads();                                // the stage is read
             fetch(k + 1);
@@ -227,7 +251,7 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
 #pragma unroll
         for (int w = 0; w < W; ++w)
             sum = add2(sum, tot_p[0][w][lane]);
-        float *to = a.lam_part + ((long long)seq * R + rank) * a.C + c0;
+        float *to = a.lam_part + ((long long)seq * a.cluster + rank) * a.C + c0;
         to[0] = sum.x;
         if (two)
             to[1] = sum.y;

@@ -1,7 +1,7 @@
 """Error bounds of the layer operators on the GPU, from the count of fp32 roundings (u = 2^-24 each).
 
 Per gate: __expf carries 2 ulp (4u) and its argument's rounding, 1.5 |v| u, and the
-division 2 ulp, so a sigmoid is within (1.5 |v| + 10) u; log a adds softplus and two
+shared reciprocal of four denominators 7 u, so a sigmoid is within (1.5 |v| + 12) u; log a adds softplus and two
 products (8 u); a = exp(log a) has |log a| times that plus 6 u; m = sqrt(1 - a^2) has
 half the relative error of 1 - a^2: that of 2 log a (series, 2 log a < 1/4) or of a^2
 times a^2 / (1 - a^2) <= 3.6 (above), plus 8 u.  The state's error follows the
@@ -33,8 +33,8 @@ def np64(t):
 def gate_errors(gate_a, gate_x, la, a):
     """Relative errors (in units of 1) of r, i, log a, a and m."""
     with np.errstate(invalid="ignore"):
-        er = np.where(np.isfinite(gate_a), (1.5 * np.abs(gate_a) + 10) * U, 10 * U)
-        ei = np.where(np.isfinite(gate_x), (1.5 * np.abs(gate_x) + 10) * U, 10 * U)
+        er = np.where(np.isfinite(gate_a), (1.5 * np.abs(gate_a) + 12) * U, 12 * U)
+        ei = np.where(np.isfinite(gate_x), (1.5 * np.abs(gate_x) + 12) * U, 12 * U)
     el = er + 8 * U
     ea = np.abs(la) * (el + 2 * U) + 6 * U
     em = 0.5 * np.maximum(el, np.minimum(3.6, a * a / np.maximum(1 - a * a, 1e-30)) * 2 * ea) + 8 * U
