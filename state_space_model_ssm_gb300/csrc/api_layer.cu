@@ -57,7 +57,7 @@ size_t ssm_gated_scan_backward_workspace_bytes(int n_seqs, int n_tokens, int cha
 {
     if (n_seqs <= 0 || gated_sizes(n_seqs, n_tokens, channels) != SSM_OK)
         return 0;
-    return (size_t)n_seqs * ssm::gated_cluster(n_seqs, n_tokens, channels) * channels * sizeof(float);
+    return (size_t)n_seqs * ssm::gated_cluster(n_seqs, n_tokens, channels, false) * channels * sizeof(float);
 }
 
 int ssm_gated_scan(float *state_slots, const void *x, const void *gate_a, const void *gate_x, const float *lam,

@@ -11,7 +11,7 @@
 // its a_t and H the state it leaves from zero, and two such maps compose: (P2, H2)
 // after (P1, H1) is (P1 P2, P2 H1 + H2).  A block owns 64 channels of one sequence and
 // walks its time chunks of 64 tokens with the state carried in registers; inside a
-// chunk its 8 warps take 8 tokens each from zero and put their maps together
+// chunk its warps take a run of tokens each from zero and put their maps together
 // through shared memory.  Where that leaves too few blocks, a cluster of R blocks
 // shares the sequence: in a round its blocks take R consecutive chunks, send each
 // other their chunk's map (16 bytes a channel pair, by asynchronous stores into the
@@ -29,9 +29,12 @@
 
 namespace ssm {
 
-constexpr int kGatedLen = 8;                               // tokens a thread holds in registers
-constexpr int kGatedWarps = 8;                             // runs of kGatedLen tokens per block
-constexpr int kGatedChunk = kGatedLen * kGatedWarps;       // tokens of a time chunk
+constexpr int kGatedChunk = 64;                            // tokens of a time chunk
+// A block's warps and the tokens of a warp's run, in registers: the forward kernel 8 x 8
+// (its barriers cost more than the longer runs), the backward kernel 16 x 4 (it needs
+// twice the registers a token).
+constexpr int kForwardWarps = 8, kForwardRun = kGatedChunk / kForwardWarps;
+constexpr int kBackwardWarps = 16, kBackwardRun = kGatedChunk / kBackwardWarps;
 constexpr int kGatedCh = 64;                               // channels of a block: two a lane
 constexpr int kGatedTile = kGatedChunk * kGatedCh;
 constexpr int kGatedMaxCluster = 8;
@@ -168,9 +171,6 @@ __device__ __forceinline__ void gates2(float2 ga, float2 gx, float2 &r, float2 &
     i = mul2(iq, da);
 }
 
-// The smaller of m and the pair's values (a NaN is passed over: it comes through any path).
-__device__ __forceinline__ float min_pair(float m, float2 v) { return fminf(m, fminf(v.x, v.y)); }
-
 __device__ __forceinline__ float sigmoid_f(float v) { return rcp(1.f + ex2(v * -kLog2e)); }
 
 // One token's decay of two channels.  d = 1 - a with v = -log a >= 0: for v < 1/4
@@ -214,6 +214,73 @@ __device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpre
 __device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) { return pair(*reinterpret_cast<const __nv_bfloat162 *>(p)); }
 __device__ __forceinline__ float2 load_pair(const __half *p) { return pair(*reinterpret_cast<const __half2 *>(p)); }
 
+// Whether a warp's run of gates stays above kGateLow (a NaN is passed over: it comes
+// through any path).  Minima on the stored type: one instruction for two values.
+__device__ __forceinline__ float2 min_pairs(float2 a, float2 b) { return make_float2(fminf(a.x, b.x), fminf(a.y, b.y)); }
+__device__ __forceinline__ __nv_bfloat162 min_pairs(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmin2(a, b); }
+__device__ __forceinline__ __half2 min_pairs(__half2 a, __half2 b) { return __hmin2(a, b); }
+template <class T>
+struct PairOf;
+template <>
+struct PairOf<float> { using type = float2; };
+template <>
+struct PairOf<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <>
+struct PairOf<__half> { using type = __half2; };
+
+template <class T, int L>
+__device__ __forceinline__ bool gates_above(const T *ga, const T *gx)
+{
+    using P = typename PairOf<T>::type;
+    P least = *reinterpret_cast<const P *>(ga);
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        least = min_pairs(least, *reinterpret_cast<const P *>(ga + i * kGatedCh));
+        least = min_pairs(least, *reinterpret_cast<const P *>(gx + i * kGatedCh));
+    }
+    const float2 v = pair(least);
+    return __all_sync(kFullMask, fminf(v.x, v.y) > kGateLow);
+}
+
+// The gates of a run of L tokens (rows kGatedCh apart in shared memory).
+template <bool LOW, int L, class T>
+__device__ __forceinline__ void gates_run(const T *ga, const T *gx, float2 (&r)[L], float2 (&g)[L])
+{
+    if (LOW) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            gates2<true>(load_pair(ga + i * kGatedCh), load_pair(gx + i * kGatedCh), r[i], g[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const float2 ta = mul2(load_pair(ga + i * kGatedCh), both(-kLog2e));
+        const float2 tx = mul2(load_pair(gx + i * kGatedCh), both(-kLog2e));
+        r[i] = make_float2(ex2(ta.x), ex2(ta.y));
+        g[i] = make_float2(ex2(tx.x), ex2(tx.y));
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const float2 da = add2(r[i], both(1.f)), dx = add2(g[i], both(1.f)), q = mul2(da, dx);
+        const float inv = rcp(q.x * q.y);
+        const float2 iq = mul2(make_float2(q.y, q.x), both(inv));
+        r[i] = mul2(iq, dx);
+        g[i] = mul2(iq, da);
+    }
+}
+
+// Decays and their roots of a run of L tokens.
+template <int L>
+__device__ __forceinline__ void decay_run(float2 rate, const float2 (&r)[L], float2 (&a)[L], float2 (&m)[L])
+{
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const Decay d = decay_of(mul2(rate, r[i]));
+        a[i] = d.a;
+        m[i] = d.m;
+    }
+}
+
 // v to p and p + 1: one store where the rows allow it (`pairs`: every row starts
 // on a pair), the second element only inside the row (`two`).
 template <class T>
@@ -247,7 +314,7 @@ __device__ __forceinline__ void gated_copy(T *dst, const void *src, long long st
     const T *p = static_cast<const T *>(src) + t * stride + c;
     constexpr int E = 4 / sizeof(T);
     if (words) {
-        for (int i = threadIdx.x; i < kGatedTile / E; i += 32 * kGatedWarps) {
+        for (int i = threadIdx.x; i < kGatedTile / E; i += blockDim.x) {
             const int row = i / (kGatedCh / E), col = i % (kGatedCh / E) * E;
             if (row < n && c + col < C)                     // (pairs: C is even)
                 cp_async4(dst + i * E, p + row * stride + col);
@@ -256,7 +323,7 @@ __device__ __forceinline__ void gated_copy(T *dst, const void *src, long long st
         }
         return;
     }
-    for (int i = threadIdx.x; i < kGatedTile; i += 32 * kGatedWarps) {
+    for (int i = threadIdx.x; i < kGatedTile; i += blockDim.x) {
         const int row = i / kGatedCh, col = i % kGatedCh;
         dst[i] = row < n && c + col < C ? p[row * stride + col] : from_float<T>(0.f);
     }
@@ -277,17 +344,41 @@ __device__ __forceinline__ void send_map(uint32_t dst, uint32_t bar, uint32_t ra
                  ::"r"(dst), "r"(bar), "r"(rank), "f"(m.p.x), "f"(m.p.y), "f"(m.h.x), "f"(m.h.y) : "memory");
 }
 
-// Shared memory of the exchange: maps by round parity and sender.
+// Shared memory of the exchange: maps by round and sender.  A block sends round k + 1's
+// map before it reads round k's, so a peer can be three rounds ahead of one
+// that has not read round k yet: four buffers.
+constexpr int kGatedBufs = 4;
 struct GatedExchange {
-    GatedMsg msg[2][kGatedMaxCluster][32];
-    uint64_t bar[2];
+    GatedMsg *msg;                      // [kGatedBufs][cluster][32], in dynamic shared memory
+    uint64_t *bar;                      // [kGatedBufs]
+    int cluster;
+    __device__ __forceinline__ GatedMsg &at(int k, int rank, int lane) const
+    {
+        return msg[(k % kGatedBufs * cluster + rank) * 32 + lane];
+    }
 };
+constexpr size_t gated_exchange_bytes(int cluster) { return cluster > 1 ? kGatedBufs * cluster * 32 * sizeof(GatedMsg) : 0; }
+
+// Poll an mbarrier phase; false after `cap` polls.
+__device__ __forceinline__ bool gated_wait(uint64_t *bar, uint32_t parity, int cap)
+{
+    const uint32_t addr = tc::smem_u32(bar);
+    for (int it = 0; it < cap; ++it) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}\n"
+                     : "=r"(done) : "r"(addr), "r"(parity) : "memory");
+        if (done)
+            return true;
+    }
+    return false;
+}
 
 // Once at the kernel's start (thread 0), before gated_cluster_start.
-__device__ __forceinline__ void exchange_init(GatedExchange &x)
+__device__ __forceinline__ void exchange_init(const GatedExchange &x)
 {
-    tc::mbar_init(&x.bar[0], 1);
-    tc::mbar_init(&x.bar[1], 1);
+    for (int i = 0; i < kGatedBufs; ++i)
+        tc::mbar_init(&x.bar[i], 1);
 }
 
 // Every block of the cluster runs and has its barriers (all threads).
@@ -312,17 +403,18 @@ __device__ __forceinline__ void gated_cluster_end(int cluster)
 }
 
 // Round k's map of this block (rank) to the others (one whole warp).
-__device__ __forceinline__ void exchange_send(GatedExchange &x, int k, int rank, int cluster, int lane, const GatedMsg &m)
+__device__ __forceinline__ void exchange_send(const GatedExchange &x, int k, int rank, int cluster, int lane,
+                                              const GatedMsg &m)
 {
-    const int b = k & 1;
-    x.msg[b][rank][lane] = m;
+    const int b = k % kGatedBufs;
+    x.at(k, rank, lane) = m;
     __syncwarp();                                           // before the arrival that publishes it
     if (lane == 0)
         tc::mbar_expect_tx(&x.bar[b], (cluster - 1) * 32 * sizeof(GatedMsg));
     __syncwarp();
     for (int r = 0; r < cluster; ++r)
         if (r != rank)
-            send_map(tc::smem_u32(&x.msg[b][rank][lane]), tc::smem_u32(&x.bar[b]), r, m);
+            send_map(tc::smem_u32(&x.at(k, rank, lane)), tc::smem_u32(&x.bar[b]), r, m);
 }
 
 // A tensor map of [T][C] rows in boxes of kGatedChunk x kGatedCh.
@@ -342,10 +434,16 @@ __device__ __forceinline__ void tma_rows(void *dst, const GatedMap *map, int c, 
                  : "memory");
 }
 
+// Round k's maps of the other blocks are here.
+__device__ __forceinline__ bool exchange_wait(const GatedExchange &x, int k, int cap)
+{
+    return gated_wait(&x.bar[k % kGatedBufs], (k / kGatedBufs) & 1, cap);
+}
+
 // Host side.
 long long gated_chunk_rows(long long n_seqs, long long n_tokens);
-// Blocks of a cluster for these sizes (gated_scan.cu).
-int gated_cluster(int n_seqs, int n_tokens, int C);
+// Blocks of a cluster for these sizes (gated_scan.cu); wide: the forward kernel on fp32.
+int gated_cluster(int n_seqs, int n_tokens, int C, bool wide);
 // False where TMA cannot describe the rows (address or stride no multiple of 16 bytes).
 bool gated_map(GatedMap *map, const void *p, int dtype, int n_tokens, int C, long long stride);
 // Whether 4-byte copies of a tensor's rows are aligned (its pairs, for 16-bit types).
@@ -355,14 +453,15 @@ cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, cudaStream_t stre
 
 // `kernel` over n_seqs x cblocks clusters.
 template <class... KArgs, class... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), const GatedArgs &a, size_t smem, cudaStream_t stream, Args &&...args)
+cudaError_t launch_clusters(void (*kernel)(KArgs...), const GatedArgs &a, int warps, size_t smem, cudaStream_t stream,
+                            Args &&...args)
 {
     cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.n_seqs * a.cblocks * a.cluster));
-    cfg.blockDim = dim3(32 * kGatedWarps);
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -55,29 +55,31 @@ gated_step_kernel(const GatedArgs a, int pairs)
 
 // ---- walk over time ----
 // Block: 64 channels of one sequence (of one rank of the cluster), 8 warps; a lane
-// owns two channels, a warp 8 tokens of the chunk.  Per chunk: decays and inputs from
-// shared memory, the warp's run from zero in registers, the runs' maps through
-// shared memory (one barrier), then every warp composes the maps before its own
-// onto the carried state and stores y.  TMA fills the rows of later chunks into
-// the stages meanwhile.
+// owns two channels, a warp 8 tokens of the chunk.  Per round: decays and inputs of
+// the next chunk from shared memory, the warp's run from zero in registers, the
+// runs' maps to the other warps and the chunk's map to the other blocks; then the
+// round before: every warp composes the maps before its own onto the carried state
+// and stores y.  So the maps travel while the next chunk is worked on (waiting
+// for them at once took 2000 of 5400 cycles a round), and TMA fills the stages of
+// later chunks.  Two runs in registers: two blocks an SM.
 template <class T, bool TMA>
 struct GatedForward {
-    static constexpr int kStages = TMA && sizeof(T) == 2 ? 3 : 2;      // 24 KB a stage (48 KB fp32)
+    static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;  // 24 KB a stage (48 KB for fp32)
     static constexpr size_t kSmem = 128 + kStages * 3 * kGatedTile * sizeof(T);
 };
 
 template <class T, bool TMA>
-__global__ void __launch_bounds__(32 * kGatedWarps, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(32 * kForwardWarps, 2)
 gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
                   const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx)
 {
     griddep_entry();
-    constexpr int L = kGatedLen, W = kGatedWarps, S = GatedForward<T, TMA>::kStages;
+    constexpr int L = kForwardRun, W = kForwardWarps, S = GatedForward<T, TMA>::kStages;
     extern __shared__ __align__(128) unsigned char raw[];
     T *buf = reinterpret_cast<T *>(align128(raw));
-    __shared__ float2 tot_p[2][W][32], tot_h[2][W][32];
-    __shared__ GatedExchange ex;
-    __shared__ uint64_t full[S];
+    __shared__ float2 tot_p[3][W][32], tot_h[3][W][32];
+    __shared__ uint64_t full[S], exbar[kGatedBufs];
+    const GatedExchange ex{reinterpret_cast<GatedMsg *>(buf + S * 3 * kGatedTile), exbar, a.cluster};
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
     const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
@@ -128,13 +130,14 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
         }
     }
     bool ok = true;
-    for (int k = 0; k < rounds; ++k) {
+    // round k's run from zero: h[i] and the product of decays p[i] up to token i; its maps sent
+    auto begin = [&](int k, float2 (&h)[L], float2 (&p)[L]) {
         const int j = k * R + rank;                         // this block's chunk
         const int cnt = min(L, len - j * kGatedChunk - warp * L);
         const T *bx = buf + k % S * 3 * kGatedTile, *bga = bx + kGatedTile, *bgx = bga + kGatedTile;
         if (TMA) {
             if (len > j * kGatedChunk)
-                ok = ok && tc::mbar_wait(&full[k % S], (k / S) & 1, cap);
+                ok = ok && gated_wait(&full[k % S], (k / S) & 1, cap);
         } else {
             if (k + S - 1 < rounds)
                 cp_async_wait<S - 1>();
@@ -142,63 +145,60 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
                 cp_async_wait<0>();
             __syncthreads();
         }
-        // the run from zero: h[i] and the product of decays p[i] up to token i
-        float2 h[L], p[L], hh = both(0.f), pp = both(1.f);
+        const int at = warp * L * kGatedCh + 2 * lane;
+        float2 hh = both(0.f), pp = both(1.f);
         auto run = [&](auto whole, auto low) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 if (whole.value || i < cnt) {
-                    const int at = (warp * L + i) * kGatedCh + 2 * lane;
                     float2 r, g;
-                    gates2<low.value>(load_pair(bga + at), load_pair(bgx + at), r, g);
+                    gates2<low.value>(load_pair(bga + at + i * kGatedCh), load_pair(bgx + at + i * kGatedCh), r, g);
                     const Decay d = decay_of(mul2(rate, r));
-                    hh = fma2(d.a, hh, mul2(mul2(d.m, g), load_pair(bx + at)));
+                    hh = fma2(d.a, hh, mul2(mul2(d.m, g), load_pair(bx + at + i * kGatedCh)));
                     pp = mul2(pp, d.a);
                 }
                 h[i] = hh;
                 p[i] = pp;
             }
         };
-        float least = 0.f;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int at = (warp * L + i) * kGatedCh + 2 * lane;
-            least = min_pair(min_pair(least, load_pair(bga + at)), load_pair(bgx + at));
-        }
-        if (cnt >= L && __all_sync(kFullMask, least > kGateLow))
+        if (cnt >= L && gates_above<T, L>(bga + at, bgx + at))
             run(Flag<true>(), Flag<false>());
         else
             run(Flag<false>(), Flag<true>());
-        float2 (*tp)[32] = tot_p[k & 1], (*th)[32] = tot_h[k & 1];
-        tp[warp][lane] = pp;
-        th[warp][lane] = hh;
+        tot_p[k % 3][warp][lane] = pp;
+        tot_h[k % 3][warp][lane] = hh;
         __syncthreads();                                    // the runs' maps are there, the stage is read
         if (k + S < rounds)
             fetch(k + S);
-        if (R > 1) {
-            if (warp == 0) {
-                GatedMsg m{both(1.f), both(0.f)};
+        if (R > 1 && warp == 0) {
+            GatedMsg m{both(1.f), both(0.f)};
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    m.h = fma2(tp[w][lane], m.h, th[w][lane]);
-                    m.p = mul2(m.p, tp[w][lane]);
-                }
-                exchange_send(ex, k, rank, R, lane, m);
+            for (int w = 0; w < W; ++w) {
+                m.h = fma2(tot_p[k % 3][w][lane], m.h, tot_h[k % 3][w][lane]);
+                m.p = mul2(m.p, tot_p[k % 3][w][lane]);
             }
-            ok = ok && tc::mbar_wait(&ex.bar[k & 1], (k >> 1) & 1, cap);
+            exchange_send(ex, k, rank, R, lane, m);
+        }
+    };
+    // round k's states and its y
+    auto finish = [&](int k, const float2 (&h)[L], const float2 (&p)[L]) {
+        const int j = k * R + rank;
+        const int cnt = min(L, len - j * kGatedChunk - warp * L);
+        float2 mine = s, next = s;                          // the states entering this block's chunk and the next round
+        if (R > 1) {
+            ok = ok && exchange_wait(ex, k, cap);
             __syncwarp();
+#pragma unroll
+            for (int r = 0; r < kGatedMaxCluster; ++r)
+                if (r < R) {
+                    if (r == rank)
+                        mine = next;
+                    const GatedMsg &m = ex.at(k, r, lane);
+                    next = fma2(m.p, next, m.h);
+                }
         }
         if (!ok)
-            s = both(__int_as_float(0x7fc00000));           // a wait gave up: seen in y and in the slot
-        // the states entering this block's chunk, this warp's run, and the next round
-        float2 mine = s, next = s;
-        if (R > 1) {
-            for (int r = 0; r < R; ++r) {
-                if (r == rank)
-                    mine = next;
-                next = fma2(ex.msg[k & 1][r][lane].p, next, ex.msg[k & 1][r][lane].h);
-            }
-        }
+            mine = next = both(__int_as_float(0x7fc00000)); // a wait gave up: seen in y and in the slot
         if (a.chunk_states && warp == 0 && inside && len > j * kGatedChunk) {
             float *cs = a.chunk_states + gated_chunk_row(a.n_seqs, seq, t0, j) * a.C + c0;
             cs[0] = mine.x;
@@ -210,15 +210,34 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
         for (int w = 0; w < W; ++w) {
             if (w == warp)
                 run_s = mine;
-            mine = fma2(tp[w][lane], mine, th[w][lane]);
+            mine = fma2(tot_p[k % 3][w][lane], mine, tot_h[k % 3][w][lane]);
         }
         s = R > 1 ? next : mine;
         if (inside) {
             T *y = static_cast<T *>(a.y) + (t0 + j * (long long)kGatedChunk + warp * L) * a.sy + c0;
+            if (cnt >= L && pairs) {
 #pragma unroll
-            for (int i = 0; i < L; ++i)
-                if (i < cnt)
-                    store_pair(y + i * a.sy, fma2(p[i], run_s, h[i]), pairs, two);
+                for (int i = 0; i < L; ++i)
+                    store_pair(y + i * a.sy, fma2(p[i], run_s, h[i]), true, true);
+            } else {
+#pragma unroll
+                for (int i = 0; i < L; ++i)
+                    if (i < cnt)
+                        store_pair(y + i * a.sy, fma2(p[i], run_s, h[i]), pairs, two);
+            }
+        }
+    };
+    float2 h0[L], p0[L], h1[L], p1[L];
+    if (rounds > 0)
+        begin(0, h0, p0);
+    for (int k = 0; k < rounds; k += 2) {
+        if (k + 1 < rounds)
+            begin(k + 1, h1, p1);
+        finish(k, h0, p0);
+        if (k + 1 < rounds) {
+            if (k + 2 < rounds)
+                begin(k + 2, h0, p0);
+            finish(k + 1, h1, p1);
         }
     }
     if (rank == 0 && warp == 0 && inside) {                 // (an empty sequence: what it began with)
@@ -240,11 +259,11 @@ cudaError_t launch_forward(GatedArgs a, bool pairs, int dtype, cudaStream_t stre
     GatedMap mx, mga, mgx;
     if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
         gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx))
-        return launch_clusters(gated_scan_kernel<T, true>, a, GatedForward<T, true>::kSmem, stream, a, pairs ? 1 : 0, 0,
+        return launch_clusters(gated_scan_kernel<T, true>, a, kForwardWarps, GatedForward<T, true>::kSmem + gated_exchange_bytes(a.cluster), stream, a, pairs ? 1 : 0, 0,
                                mx, mga, mgx);
     const bool words = gated_words(a.x, dtype, a.C, a.sx) && gated_words(a.gate_a, dtype, a.C, a.sga) &&
                        gated_words(a.gate_x, dtype, a.C, a.sgx);
-    return launch_clusters(gated_scan_kernel<T, false>, a, GatedForward<T, false>::kSmem, stream, a, pairs ? 1 : 0,
+    return launch_clusters(gated_scan_kernel<T, false>, a, kForwardWarps, GatedForward<T, false>::kSmem + gated_exchange_bytes(a.cluster), stream, a, pairs ? 1 : 0,
                            words ? 1 : 0, mx, mga, mgx);
 }
 
@@ -265,13 +284,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 
 long long gated_chunk_rows(long long n_seqs, long long n_tokens) { return n_seqs + n_tokens / kGatedChunk + 1; }
 
-// Enough blocks that one sequence alone fills the device (two blocks an SM), but no
-// more blocks a sequence than it has chunks on average.
-int gated_cluster(int n_seqs, int n_tokens, int C)
+// As many blocks a sequence as fit the device at once (two an SM; one where fp32
+// stages and the exchange of four or more blocks fill shared memory), and at
+// most one for every two chunks it has on average.  The lengths are not known here: of
+// more than four sequences a sixth are taken to be long.  Forward / backward in us
+// with 1, 2, 4, 8 blocks (64 channel blocks unless stated):
+//   1 x 4096 bf16                88 55 44 51     225 129 104 109
+//   12 uneven, 7889 tokens bf16  131 81 93 120   255 184 192 236
+//   4 x 16384 fp32, 32 blocks    346 312 407 499 1186 795 801 817
+//   32 x 512 bf16, 32 blocks     69 89 113 180   158 185 217 292
+//   1 x 16384 bf16, 1 block      338 203 104 56  876 490 255 138
+int gated_cluster(int n_seqs, int n_tokens, int C, bool wide)
 {
     const long long cb = (C + kGatedCh - 1) / kGatedCh, chunks = (long long)n_tokens / n_seqs / kGatedChunk;
+    const long long uneven = n_seqs <= 4 ? n_seqs : n_seqs / 6 > 2 ? n_seqs / 6 : 2;
     int r = 1;
-    while (r < kGatedMaxCluster && cb * r < 300 && 2 * r <= chunks)
+    while (r < kGatedMaxCluster && 4 * r <= chunks && uneven * cb * 2 * r <= (wide && r >= 2 ? 152 : 304))
         r *= 2;
     return r;
 }
@@ -301,7 +329,7 @@ bool gated_words(const void *p, int dtype, int C, long long stride)
 cudaError_t launch_gated_scan(GatedArgs a, int dtype, cudaStream_t stream)
 {
     a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
-    a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C);
+    a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C, dtype == kF32);
     a.fail_waits = debug_fail_waits() ? 1 : 0;
     bool pairs = ((a.C | a.sy) & 1) == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * dtype_size(dtype)) == 0;
     if (a.n_tokens == a.n_seqs && !a.chunk_states)          // the step kernel loads pairs too

@@ -32,18 +32,18 @@ struct GatedBackward {
 };
 
 template <class T, bool TMA>
-__global__ void __launch_bounds__(32 * kGatedWarps, 3)
+__global__ void __launch_bounds__(32 * kBackwardWarps, 2)
 gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
                            const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx,
                            const __grid_constant__ GatedMap mdy)
 {
     griddep_entry();
-    constexpr int L = kGatedLen, W = kGatedWarps, S = GatedBackward<T>::kStages;
+    constexpr int L = kBackwardRun, W = kBackwardWarps, S = GatedBackward<T>::kStages;
     extern __shared__ __align__(128) unsigned char raw[];
     T *buf = reinterpret_cast<T *>(align128(raw));
-    __shared__ float2 tot_p[2][W][32], tot_h[2][W][32], tot_e[2][W][32];
-    __shared__ GatedExchange ex;
-    __shared__ uint64_t full[S];
+    __shared__ float2 tot_p[W][32], tot_h[W][32], tot_e[W][32], enter[W][32], arrive[W][32];
+    __shared__ uint64_t full[S], exbar[kGatedBufs];
+    const GatedExchange ex{reinterpret_cast<GatedMsg *>(buf + S * 4 * kGatedTile), exbar, a.cluster};
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
     const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
@@ -104,19 +104,14 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
     }
     bool ok = true;
     for (int k = 0; k < rounds; ++k) {
-        const int j = chunk_of(k), half = k & 1;
+        const int j = chunk_of(k);
         const bool some = len > j * kGatedChunk;            // this block's chunk has tokens
         const int cnt = min(L, len - j * kGatedChunk - warp * L);
         const T *bx = buf + k % S * 4 * kGatedTile, *bga = bx + kGatedTile, *bgx = bga + kGatedTile,
                 *bdy = bgx + kGatedTile;
-        float2 h = both(0.f);                               // the state entering the chunk
-        if (inside && some) {
-            const float *cs = a.chunk_states + gated_chunk_row(a.n_seqs, seq, t0, j) * a.C + c0;
-            h = make_float2(__ldg(cs), two ? __ldg(cs + 1) : 0.f);
-        }
         if (TMA) {
             if (some) {
-                ok = ok && tc::mbar_wait(&full[k % S], (phases >> (k % S)) & 1, cap);
+                ok = ok && gated_wait(&full[k % S], (phases >> (k % S)) & 1, cap);
                 phases ^= 1u << (k % S);
             }
         } else {
@@ -143,58 +138,58 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
                 }
             }
         };
-        float least = 0.f;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int at = (warp * L + i) * kGatedCh + 2 * lane;
-            least = min_pair(min_pair(least, load_pair(bga + at)), load_pair(bgx + at));
-        }
-        const bool fast = cnt >= L && __all_sync(kFullMask, least > kGateLow);
+        const bool fast = cnt >= L && gates_above<T, L>(bga + warp * L * kGatedCh + 2 * lane, bgx + warp * L * kGatedCh + 2 * lane);
         if (fast)
             run(Flag<true>(), Flag<false>());
         else
             run(Flag<false>(), Flag<true>());
-        float2 (*tp)[32] = tot_p[half], (*th)[32] = tot_h[half], (*te)[32] = tot_e[half];
-        tp[warp][lane] = pp;
-        th[warp][lane] = hh;
-        te[warp][lane] = ee;
+        tot_p[warp][lane] = pp;
+        tot_h[warp][lane] = hh;
+        tot_e[warp][lane] = ee;
         __syncthreads();                                    // the runs' maps are there, the round before is done
         if (S == 2 && k + 1 < rounds)
             fetch(k + 1);
-        if (R > 1) {
-            if (warp == 0) {
+        if (warp == 1) {                                    // the states entering the runs
+            float2 h = both(0.f);
+            if (inside && some) {
+                const float *cs = a.chunk_states + gated_chunk_row(a.n_seqs, seq, t0, j) * a.C + c0;
+                h = make_float2(__ldg(cs), two ? __ldg(cs + 1) : 0.f);
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                enter[w][lane] = h;
+                h = fma2(tot_p[w][lane], h, tot_h[w][lane]);
+            }
+        }
+        if (warp == 0) {
+            float2 mine = s, next = s;                      // the E arriving at this block's chunk and at the next round
+            if (R > 1) {
                 GatedMsg m{both(1.f), both(0.f)};
 #pragma unroll
                 for (int w = W - 1; w >= 0; --w) {
-                    m.h = fma2(tp[w][lane], m.h, te[w][lane]);
-                    m.p = mul2(m.p, tp[w][lane]);
+                    m.h = fma2(tot_p[w][lane], m.h, tot_e[w][lane]);
+                    m.p = mul2(m.p, tot_p[w][lane]);
                 }
                 exchange_send(ex, k, rank, R, lane, m);
+                ok = ok && exchange_wait(ex, k, cap);
+                __syncwarp();
+                for (int r = R - 1; r >= 0; --r) {
+                    if (r == rank)
+                        mine = next;
+                    next = fma2(ex.at(k, r, lane).p, next, ex.at(k, r, lane).h);
+                }
             }
-            ok = ok && tc::mbar_wait(&ex.bar[half], (k >> 1) & 1, cap);
-            __syncwarp();
-        }
-        if (!ok)
-            s = both(__int_as_float(0x7fc00000));
-        // the E arriving at this block's chunk, at this warp's run, and at the next round
-        float2 mine = s, next = s;
-        if (R > 1) {
-            for (int r = R - 1; r >= 0; --r) {
-                if (r == rank)
-                    mine = next;
-                next = fma2(ex.msg[half][r][lane].p, next, ex.msg[half][r][lane].h);
-            }
-        }
-        float2 E = mine;
+            if (!ok)
+                mine = next = both(__int_as_float(0x7fc00000));
 #pragma unroll
-        for (int w = W - 1; w >= 0; --w) {
-            if (w == warp)
-                E = mine;
-            mine = fma2(tp[w][lane], mine, te[w][lane]);
+            for (int w = W - 1; w >= 0; --w) {              // the E arriving at the runs
+                arrive[w][lane] = mine;
+                mine = fma2(tot_p[w][lane], mine, tot_e[w][lane]);
+            }
+            s = R > 1 ? next : mine;
         }
-        s = R > 1 ? next : mine;
-        for (int w = 0; w < warp; ++w)
-            h = fma2(tp[w][lane], h, th[w][lane]);
+        __syncthreads();
+        float2 h = enter[warp][lane], E = arrive[warp][lane];
 #pragma unroll
         for (int i = 0; i < L; ++i) {                       // hb[i]: b_i -> h_{i-1}
             const float2 before = h;
@@ -244,13 +239,13 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
             g[1] = resume ? s.y : 0.f;
     }
     __syncthreads();
-    tot_p[0][warp][lane] = part;
+    tot_p[warp][lane] = part;
     __syncthreads();
     if (warp == 0 && inside) {
         float2 sum = both(0.f);
 #pragma unroll
         for (int w = 0; w < W; ++w)
-            sum = add2(sum, tot_p[0][w][lane]);
+            sum = add2(sum, tot_p[w][lane]);
         float *to = a.lam_part + ((long long)seq * a.cluster + rank) * a.C + c0;
         to[0] = sum.x;
         if (two)
@@ -289,15 +284,15 @@ cudaError_t launch_backward(const GatedArgs &a, bool pairs, int dtype, cudaStrea
 {
     GatedMap mx, mga, mgx, mdy;
     cudaError_t e;
-    constexpr size_t smem = GatedBackward<T>::kSmem;
+    const size_t smem = GatedBackward<T>::kSmem + gated_exchange_bytes(a.cluster);
     if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
         gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx) &&
         gated_map(&mdy, a.grad_y, dtype, a.n_tokens, a.C, a.sy)) {
-        e = launch_clusters(gated_scan_backward_kernel<T, true>, a, smem, stream, a, pairs ? 1 : 0, 0, mx, mga, mgx, mdy);
+        e = launch_clusters(gated_scan_backward_kernel<T, true>, a, kBackwardWarps, smem, stream, a, pairs ? 1 : 0, 0, mx, mga, mgx, mdy);
     } else {
         const bool words = gated_words(a.x, dtype, a.C, a.sx) && gated_words(a.gate_a, dtype, a.C, a.sga) &&
                            gated_words(a.gate_x, dtype, a.C, a.sgx) && gated_words(a.grad_y, dtype, a.C, a.sy);
-        e = launch_clusters(gated_scan_backward_kernel<T, false>, a, smem, stream, a, pairs ? 1 : 0, words ? 1 : 0, mx,
+        e = launch_clusters(gated_scan_backward_kernel<T, false>, a, kBackwardWarps, smem, stream, a, pairs ? 1 : 0, words ? 1 : 0, mx,
                             mga, mgx, mdy);
     }
     return e != cudaSuccess ? e
@@ -309,7 +304,7 @@ cudaError_t launch_backward(const GatedArgs &a, bool pairs, int dtype, cudaStrea
 cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, cudaStream_t stream)
 {
     a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
-    a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C);
+    a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C, false);
     a.fail_waits = debug_fail_waits() ? 1 : 0;
     const bool pairs = ((a.C | a.gsx | a.gsga | a.gsgx) & 1) == 0 &&
                        ((reinterpret_cast<uintptr_t>(a.grad_x) | reinterpret_cast<uintptr_t>(a.grad_ga) |
