@@ -198,7 +198,7 @@ size_t ssm_add_norm_backward_workspace_bytes(int rows, int width)
 {
     if (rows < 0 || width <= 0 || width > kMaxRowWidth)
         return 0;
-    return (size_t)ssm::add_norm_parts(rows) * width * sizeof(float);
+    return (size_t)ssm::add_norm_parts(rows, width) * width * sizeof(float);
 }
 
 int ssm_add_norm_backward(const void *grad_y, const void *h, const float *weight, float eps, const void *grad_h,

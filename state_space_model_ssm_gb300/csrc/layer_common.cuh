@@ -36,28 +36,32 @@ struct alignas(sizeof(T) * V) Vec {
     T v[V];
 };
 
+// They move as integer words: an access chosen at run time between a vector and its
+// elements then has two different types and cannot be merged into one with the
+// vector's alignment.
+template <int BYTES>
+struct WordsOf;
+template <>
+struct WordsOf<16> { using type = uint4; };
+template <>
+struct WordsOf<8> { using type = uint2; };
+template <>
+struct WordsOf<4> { using type = uint32_t; };
+
 template <class T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec(const T *p)
 {
-    return *reinterpret_cast<const Vec<T, V> *>(p);
+    using W = typename WordsOf<sizeof(T) * V>::type;
+    Vec<T, V> v;
+    *reinterpret_cast<W *>(&v) = *reinterpret_cast<const W *>(p);
+    return v;
 }
 
 template <class T, int V>
 __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &v)
 {
-    *reinterpret_cast<Vec<T, V> *>(p) = v;
-}
-
-__device__ __forceinline__ int ld_acquire(const int *p)
-{
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void st_release(int *p, int v)
-{
-    asm volatile("st.release.gpu.global.s32 [%0], %1;\n" ::"l"(p), "r"(v) : "memory");
+    using W = typename WordsOf<sizeof(T) * V>::type;
+    *reinterpret_cast<W *>(p) = *reinterpret_cast<const W *>(&v);
 }
 
 // Debug mode (SSM_SCAN_CHECK=1; api.cu): whether it is on, the sequence table
@@ -73,7 +77,7 @@ int debug_read_status(const int *status, cudaStream_t stream);
 cudaError_t launch_add_norm(const void *x, const void *residual, const float *w, float eps, void *h, void *y,
                             int8_t *codes, float *scales, int rows, int D, int dx, int dr, long long sx,
                             long long sr, long long sh, long long sy, cudaStream_t st);
-int add_norm_parts(int rows);             // rows of the gradient's workspace ([parts][D] fp32)
+int add_norm_parts(int rows, int D);      // rows of the gradient's workspace ([parts][D] fp32)
 cudaError_t launch_add_norm_backward(const void *gy, const void *h, const void *gh, const float *w, float eps,
                                      void *gin, float *gw, float *part, int rows, int D, int dy, int dr,
                                      long long sgy, long long sh, long long sgh, long long sgi, cudaStream_t st);
