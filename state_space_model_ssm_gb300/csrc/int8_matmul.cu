@@ -25,7 +25,7 @@
 //
 // Roles: one warp loads weights (and 8-bit tokens) by TMA, one fp16 tokens, one
 // issues the MMAs, 8 convert and afterwards write the result (thread: one output
-// channel, NT / 2 tokens).  They hand stages of 64 terms to each other through
+// channel, NT / 2 tokens).  They hand stages of 128 terms to each other through
 // mbarriers.  With few tiles the terms are split over the blocks of a cluster, whose
 // integer sums meet in the first block's shared memory: no workspace, and the
 // same bits as without a split.
@@ -45,11 +45,8 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;                    // output channels of a block
-constexpr int kTerms = 64;                    // terms of a stage
-constexpr int kFold = 16;                     // stages whose sum is exact in fp32: 16 x 64 x 2^14 = 2^24
-constexpr int kWStages = 6;                   // weight stages (8 KB each)
-constexpr int kABufs = 4;                     // converted weight stages in tensor memory (32 columns each)
-constexpr int kXRing = 5;                     // fp16 token stages
+constexpr int kTerms = 128;                   // terms of a stage (with 64, issuing a stage took longer than its products)
+constexpr int kFold = 8;                      // stages whose sum is exact in fp32: 8 x 128 x 2^14 = 2^24
 constexpr int kConvWarps = 8;                 // two groups of four: a group converts every other stage
 constexpr int kGroupWarps = 4;
 constexpr int kWarpW = 8, kWarpMma = 9, kWarpX = 10;
@@ -64,20 +61,24 @@ struct I8Args {
     int fail_waits;
 };
 
-// Shared memory (bytes; tiles 1024-aligned).
+// Shared memory (bytes; tiles 1024-aligned) and tensor memory of a block.  Few
+// tokens: two blocks an SM; many: one, with all of shared memory in stages.
 template <int NT, bool XCONV>
 struct I8Layout {
-    static constexpr int kXStages = XCONV ? kABufs : kXRing;
-    static constexpr int kXTile = NT * 128;                 // 64 fp16 terms of NT tokens
+    static constexpr int kWStages = NT == 256 ? 2 : 3;      // weight stages, 16 KB each
+    static constexpr int kABufs = NT <= 64 ? 2 : 4;         // converted weight stages in tensor memory
+    static constexpr int kACols = kTerms / 2;               // columns of one
+    static constexpr int kXStages = XCONV ? kABufs : NT == 128 ? 4 : 3;
+    static constexpr int kXTile = NT * 128;                 // 64 fp16 terms of NT tokens; two to a stage
     static constexpr int kW = 0;
     static constexpr int kX = kW + kWStages * kRows * kTerms;
-    static constexpr int kXi = kX + kXStages * kXTile;      // 8-bit tokens of a weight stage
+    static constexpr int kXi = kX + kXStages * 2 * kXTile;  // 8-bit tokens of a weight stage
     static constexpr int kRed = kXi + (XCONV ? kWStages * NT * kTerms : 0);
-    static int red_bytes(int split) { return (split - 1) * NT * kRows * 4; }
-    // mbarriers (after the split's sums, whose size the launch knows)
-    static constexpr int kBars = 2 * kWStages + 2 * kXRing + 2 * kABufs + 4;
-    static int total(int split) { return kRed + red_bytes(split) + kBars * 8 + 16 + NT * 4; }
-    static constexpr int kTmem = NT + 32 * kABufs <= 256 ? 256 : 512;
+    static constexpr int red_bytes(int split) { return (split - 1) * NT * kRows * 4; }
+    // mbarriers (after the split's sums, whose size the launch knows), then the tokens' scales
+    static constexpr int kBars = 2 * kWStages + 2 * kXStages + 2 * kABufs + 4;
+    static constexpr int total(int split) { return kRed + red_bytes(split) + kBars * 8 + 16 + NT * 4; }
+    static constexpr int kTmem = NT + kACols * kABufs <= 256 ? 256 : 512;
 };
 
 // Shared-memory descriptor of a K-major tile of 128-byte rows with the 128-byte
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 64 ? 2 : 1)
 int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
     using L = I8Layout<NT, XCONV>;
+    constexpr int kWStages = L::kWStages, kABufs = L::kABufs, kXRing = L::kXStages;
     griddep_entry();
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
@@ -301,8 +303,9 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
                     break;
                 }
                 if (elect_one()) {
-                    mbar_expect_tx(xfull + x.s, L::kXTile);
-                    tma_2d(base + L::kX + x.s * L::kXTile, &xmap, (k0 + i) * kTerms, m0, xfull + x.s);
+                    mbar_expect_tx(xfull + x.s, 2 * L::kXTile);
+                    for (int b = 0; b < 2; ++b)
+                        tma_2d(base + L::kX + (2 * x.s + b) * L::kXTile, &xmap, (k0 + i) * kTerms + 64 * b, m0, xfull + x.s);
                 }
                 x.next();
             }
@@ -328,11 +331,12 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
             }
             fence_after();
             if (elect_one()) {
-                const uint64_t bd = bd0 + x.s * (L::kXTile >> 4);
-                const uint32_t at = tmem_a + 32 * ab.s;
+                const uint64_t bd = bd0 + x.s * (2 * L::kXTile >> 4);
+                const uint32_t at = tmem_a + L::kACols * ab.s;
 #pragma unroll
                 for (int kk = 0; kk < kTerms / 16; ++kk)
-                    mma_f16_ts(tmem, at + 8 * kk, bd + 2 * kk, id, left != kFold || kk > 0);
+                    mma_f16_ts(tmem, at + 8 * kk, bd + (kk / 4) * (L::kXTile >> 4) + 2 * (kk % 4), id,
+                               left != kFold || kk > 0);
                 commit_bar(b_aempty + 8 * ab.s);
                 if (!XCONV)
                     commit_bar(b_xempty + 8 * x.s);
@@ -404,14 +408,13 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
                 ok = false;
                 break;
             }
-            // this thread's weight row, 16-byte chunks of the 64-byte swizzle
+            // this thread's weight row, 16-byte chunks of the 128-byte swizzle
             const unsigned char *wr = sm + L::kW + s * kRows * kTerms + row * kTerms;
-            const int sw = (row >> 1) & 3;
-            uint4 c[4];
+            uint4 c[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                c[j] = *reinterpret_cast<const uint4 *>(wr + ((j ^ sw) << 4));
-            constexpr int XW = XCONV ? NT / 8 : 1;
+            for (int j = 0; j < 8; ++j)
+                c[j] = *reinterpret_cast<const uint4 *>(wr + ((j ^ (row & 7)) << 4));
+            constexpr int XW = XCONV ? NT / 4 : 1;
             uint32_t xw[XW];
             if (XCONV)
 #pragma unroll
@@ -420,31 +423,33 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
             __syncwarp();
             if (lane == 0)
                 arrive_bar(b_wempty + 8 * s);
-            uint32_t h[2][16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t *o = h[j >> 1] + 8 * (j & 1);
-                bytes_to_half(c[j].x, o[0], o[1]);
-                bytes_to_half(c[j].y, o[2], o[3]);
-                bytes_to_half(c[j].z, o[4], o[5]);
-                bytes_to_half(c[j].w, o[6], o[7]);
-            }
             ok = wait_bar(b_aempty + 8 * b, ab.phase ^ 1, cap);
             if (!__all_sync(kFullMask, ok)) {
                 ok = false;
                 break;
             }
             fence_after();
-            tmem_st16u(tmem_a + lanes + 32 * b, h[0]);
-            tmem_st16u(tmem_a + lanes + 32 * b + 16, h[1]);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                uint32_t h[16];
+                bytes_to_half(c[j].x, h[0], h[1]);
+                bytes_to_half(c[j].y, h[2], h[3]);
+                bytes_to_half(c[j].z, h[4], h[5]);
+                bytes_to_half(c[j].w, h[6], h[7]);
+                bytes_to_half(c[j + 1].x, h[8], h[9]);
+                bytes_to_half(c[j + 1].y, h[10], h[11]);
+                bytes_to_half(c[j + 1].z, h[12], h[13]);
+                bytes_to_half(c[j + 1].w, h[14], h[15]);
+                tmem_st16u(tmem_a + lanes + L::kACols * b + 8 * j, h);
+            }
             if (XCONV) {
 #pragma unroll
                 for (int j = 0; j < XW; ++j) {
-                    const int e = row + 128 * j, t = e >> 4, w = e & 15;
+                    const int e = row + 128 * j, t = e >> 5, w = e & 31;    // word w (4 terms) of token t
                     uint2 v;
                     bytes_to_half(xw[j], v.x, v.y);
-                    *reinterpret_cast<uint2 *>(sm + L::kX + b * L::kXTile + t * 128 + (((w >> 1) ^ (t & 7)) << 4) +
-                                               (w & 1) * 8) = v;
+                    *reinterpret_cast<uint2 *>(sm + L::kX + (2 * b + (w >> 4)) * L::kXTile + t * 128 +
+                                               ((((w & 15) >> 1) ^ (t & 7)) << 4) + (w & 1) * 8) = v;
                 }
                 fence_async_smem();
             }
@@ -594,8 +599,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// [rows][width] of bytes or fp16 in boxes of kTerms x box_rows; zeros outside.
-bool encode_rows(CUtensorMap *map, const void *p, bool half, int width, int rows, long long stride_bytes, int box_rows,
+// [rows][width] of bytes or fp16 in boxes of `terms` x box_rows; zeros outside.
+bool encode_rows(CUtensorMap *map, const void *p, bool half, int terms, int width, int rows, long long stride_bytes, int box_rows,
                  CUtensorMapSwizzle swizzle)
 {
     const auto fn = encode_fn();
@@ -603,7 +608,7 @@ bool encode_rows(CUtensorMap *map, const void *p, bool half, int width, int rows
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)stride_bytes};
-    const cuuint32_t box[2] = {kTerms, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)terms, (cuuint32_t)box_rows}, step[2] = {1, 1};
     return fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p),
               dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -629,9 +634,9 @@ Shape pick_shape(int M, int N, int K, bool x_tma)
     while (s.nt > 64 && tn * ((M + s.nt - 1) / s.nt) < 152)
         s.nt /= 2;
     if (s.nt <= 64) {
-        const int stages = (K + kTerms - 1) / kTerms, most = s.nt == 16 ? 6 : s.nt == 32 ? 4 : 2;
+        const int stages = (K + kTerms - 1) / kTerms, most = s.nt == 16 ? 6 : s.nt == 32 ? 3 : 2;
         const long long tiles = tn * ((M + s.nt - 1) / s.nt);
-        while (s.split < most && tiles * (s.split + 1) <= 304 && stages / (s.split + 1) >= 4)
+        while (s.split < most && tiles * (s.split + 1) <= (s.nt == 64 ? 152 : 304) && stages / (s.split + 1) >= 2)
             ++s.split;
     }
     s.xconv = s.nt <= 64 && x_tma;
@@ -701,9 +706,9 @@ cudaError_t launch_int8_matmul(const int8_t *x, const float *xs, const int8_t *w
     const long long wb = pack_w ? ((long long)N * (kp / 16) + 255) / 256 : 0;
     p.xblocks = (unsigned)xb;
     CUtensorMap wmap, xmap;
-    if (!encode_rows(&wmap, pack_w ? p.wp : w, false, K, N, pack_w ? kp : sw, kRows, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !(s.xconv ? encode_rows(&xmap, x, false, K, M, sx, s.nt, CU_TENSOR_MAP_SWIZZLE_NONE)
-                  : encode_rows(&xmap, p.x16, true, K, M, (long long)kp * 2, s.nt, CU_TENSOR_MAP_SWIZZLE_128B)))
+    if (!encode_rows(&wmap, pack_w ? p.wp : w, false, kTerms, K, N, pack_w ? kp : sw, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !(s.xconv ? encode_rows(&xmap, x, false, kTerms, K, M, sx, s.nt, CU_TENSOR_MAP_SWIZZLE_NONE)
+                  : encode_rows(&xmap, p.x16, true, 64, K, M, (long long)kp * 2, s.nt, CU_TENSOR_MAP_SWIZZLE_128B)))
         return cudaErrorInvalidValue;
     if (xb + wb > 0) {
         const cudaError_t e = launch_pdl(int8_pack_kernel, dim3((unsigned)(xb + wb)), dim3(256), 0, st, p);
