@@ -392,9 +392,27 @@ __device__ __forceinline__ void gated_cluster_start(int cluster)
     }
 }
 
-// No block leaves while a peer may still send to it (all threads).
-__device__ __forceinline__ void gated_cluster_end(int cluster)
+// After a wait that gave up: NaN into this block's rows of tokens from chunk j0 on (every
+// step-th chunk, down to 0 or up to the end), channels c .. c + 63.
+template <class T>
+__device__ __forceinline__ void gated_poison(T *out, long long stride, long long t0, int len, int j0, int step, int c, int C)
 {
+    const int width = min(kGatedCh, C - c);
+    for (int j = j0; j >= 0 && (step < 0 || j * kGatedChunk < len); j += step)
+        for (int i = threadIdx.x; i < kGatedChunk * width; i += blockDim.x) {
+            const int t = j * kGatedChunk + i / width;
+            if (t < len)
+                out[(t0 + t) * stride + c + i % width] = from_float<T>(__int_as_float(0x7fc00000));
+        }
+}
+
+// No block leaves while a peer may still send to it (all threads).  After a wait that gave
+// up (ok false) maps may be on their way still: they get 20 us to land.
+__device__ __forceinline__ void gated_cluster_end(int cluster, bool ok)
+{
+    if (!ok && cluster > 1)
+        for (int i = 0; i < 20; ++i)
+            __nanosleep(1000);
     __syncwarp();
     if (cluster > 1) {
         asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");

@@ -96,12 +96,15 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
     }
     gated_cluster_start(R);
     const int rounds = (len + kGatedChunk * R - 1) / (kGatedChunk * R);
+    uint32_t filled = 0, fill_parity = 0;                   // (thread 0) by stage: filled at all; an odd number of times
     auto fetch = [&](int k) {                               // round k's rows into its stage
         const int j = k * R + rank, t = (int)t0 + j * kGatedChunk, n = min(kGatedChunk, len - j * kGatedChunk);
         T *to = buf + k % S * 3 * kGatedTile;
         if (TMA) {
             if (tid == 0 && n > 0) {
                 uint64_t *bar = &full[k % S];
+                filled |= 1u << (k % S);
+                fill_parity ^= 1u << (k % S);
                 tc::mbar_expect_tx(bar, 3 * kGatedTile * sizeof(T));
                 tma_rows(to, &mx, cb * kGatedCh, t, bar);
                 tma_rows(to + kGatedTile, &mga, cb * kGatedCh, t, bar);
@@ -167,10 +170,10 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
             run(Flag<false>(), Flag<true>());
         tot_p[k % 3][warp][lane] = pp;
         tot_h[k % 3][warp][lane] = hh;
-        __syncthreads();                                    // the runs' maps are there, the stage is read
-        if (k + S < rounds)
+        ok = __syncthreads_and(ok);                         // the runs' maps are there, the stage is read
+        if (ok && k + S < rounds)
             fetch(k + S);
-        if (R > 1 && warp == 0) {
+        if (ok && R > 1 && warp == 0) {
             GatedMsg m{both(1.f), both(0.f)};
 #pragma unroll
             for (int w = 0; w < W; ++w) {
@@ -228,17 +231,34 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
         }
     };
     float2 h0[L], p0[L], h1[L], p1[L];
+    int done = 0;
     if (rounds > 0)
         begin(0, h0, p0);
-    for (int k = 0; k < rounds; k += 2) {
-        if (k + 1 < rounds)
-            begin(k + 1, h1, p1);
-        finish(k, h0, p0);
-        if (k + 1 < rounds) {
-            if (k + 2 < rounds)
-                begin(k + 2, h0, p0);
-            finish(k + 1, h1, p1);
+    for (; done < rounds && ok; done += 2) {
+        if (done + 1 < rounds)
+            begin(done + 1, h1, p1);
+        if (!ok)
+            break;
+        finish(done, h0, p0);
+        if (done + 1 < rounds) {
+            if (done + 2 < rounds)
+                begin(done + 2, h0, p0);
+            if (!ok)
+                break;
+            finish(done + 1, h1, p1);
         }
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) {                                              // a wait gave up: NaN, once the copies in flight have landed
+        s = both(__int_as_float(0x7fc00000));
+        gated_poison(static_cast<T *>(a.y), a.sy, t0, len, (done > 2 ? done - 2 : 0) * R + rank, R, cb * kGatedCh, a.C);
+        if (TMA && tid == 0)
+            for (int i = 0; i < S; ++i)
+                if (filled >> i & 1)
+                    gated_wait(&full[i], (fill_parity >> i & 1) ^ 1, (int)tc::kSpinLimit);
+        if (!TMA)
+            cp_async_wait<0>();
+        __syncthreads();
     }
     if (rank == 0 && warp == 0 && inside) {                 // (an empty sequence: what it began with)
         float *slot = a.state + (long long)seq * a.C + c0;
@@ -246,7 +266,7 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
         if (two)
             slot[1] = s.y;
     }
-    gated_cluster_end(R);
+    gated_cluster_end(R, ok);
 }
 
 template <class T>

@@ -67,12 +67,15 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
     // the chunk of this block's n-th round, the last tokens first (it may lie past the end: no tokens)
     auto chunk_of = [&](int n) { return (rounds - 1 - n) * R + rank; };
     uint32_t phases = 0;                                    // parity of each stage's next fill
+    uint32_t filled = 0, fill_parity = 0;                   // (thread 0) by stage: filled at all; an odd number of times
     auto fetch = [&](int k) {
         const int j = chunk_of(k), t = (int)t0 + j * kGatedChunk, n = min(kGatedChunk, len - j * kGatedChunk);
         T *to = buf + k % S * 4 * kGatedTile;
         if (TMA) {
             if (tid == 0 && n > 0) {
                 uint64_t *bar = &full[k % S];
+                filled |= 1u << (k % S);
+                fill_parity ^= 1u << (k % S);
                 tc::mbar_expect_tx(bar, 4 * kGatedTile * sizeof(T));
                 tma_rows(to, &mx, cb * kGatedCh, t, bar);
                 tma_rows(to + kGatedTile, &mga, cb * kGatedCh, t, bar);
@@ -103,7 +106,8 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
         }
     }
     bool ok = true;
-    for (int k = 0; k < rounds; ++k) {
+    int k = 0;
+    for (; k < rounds; ++k) {
         const int j = chunk_of(k);
         const bool some = len > j * kGatedChunk;            // this block's chunk has tokens
         const int cnt = min(L, len - j * kGatedChunk - warp * L);
@@ -146,7 +150,9 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
         tot_p[warp][lane] = pp;
         tot_h[warp][lane] = hh;
         tot_e[warp][lane] = ee;
-        __syncthreads();                                    // the runs' maps are there, the round before is done
+        ok = __syncthreads_and(ok);                         // the runs' maps are there, the round before is done
+        if (!ok)
+            break;
         if (S == 2 && k + 1 < rounds)
             fetch(k + 1);
         if (warp == 1) {                                    // the states entering the runs
@@ -231,6 +237,21 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
             fetch(k + 1);
         }
     }
+    ok = __syncthreads_and(ok);
+    if (!ok) {                                              // a wait gave up: NaN, once the copies in flight have landed
+        s = part = both(__int_as_float(0x7fc00000));
+        const int from = chunk_of(k > 0 ? k - 1 : 0);
+        gated_poison(static_cast<T *>(a.grad_x), a.gsx, t0, len, from, -R, cb * kGatedCh, a.C);
+        gated_poison(static_cast<T *>(a.grad_ga), a.gsga, t0, len, from, -R, cb * kGatedCh, a.C);
+        gated_poison(static_cast<T *>(a.grad_gx), a.gsgx, t0, len, from, -R, cb * kGatedCh, a.C);
+        if (TMA && tid == 0)
+            for (int i = 0; i < S; ++i)
+                if (filled >> i & 1)
+                    gated_wait(&full[i], (fill_parity >> i & 1) ^ 1, (int)tc::kSpinLimit);
+        if (!TMA)
+            cp_async_wait<0>();
+        __syncthreads();
+    }
     if (rank == 0 && warp == 0 && inside && a.grad_state0) {
         const bool resume = a.resume[seq] != 0;
         float *g = a.grad_state0 + (long long)seq * a.C + c0;
@@ -251,7 +272,7 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
         if (two)
             to[1] = sum.y;
     }
-    gated_cluster_end(R);
+    gated_cluster_end(R, ok);
 }
 
 // dlam from the blocks' sums, in a fixed order: a block of 8 warps owns 32
