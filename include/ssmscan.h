@@ -452,10 +452,10 @@ typedef enum {
  *   chunk_states NULL, or (training) fp32 [ssm_gated_scan_chunks(...)][channels],
  *                out: the state entering each time chunk, which the backward
  *                pass reads
- * Where n_tokens == n_seqs and chunk_states is NULL (one token a sequence) the
- * call steps every sequence token by token; otherwise blocks walk the sequences'
- * time chunks, with the time of a sequence shared by a cluster of blocks where
- * there are few sequences and channels.  One launch, no workspace, the same bits
+ * With 16 tokens a sequence or fewer on average (decode: one each) the call steps
+ * every sequence token by token; otherwise blocks walk the sequences' time
+ * chunks, with the time of a sequence shared by a cluster of blocks where there
+ * are few sequences and channels.  One launch, no workspace, the same bits
  * every time.  The cluster's waits are bounded: on giving up y and the slots
  * behind it become NaN.  y must not overlap an input.
  * Errors: SSM_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, strides

@@ -9,27 +9,20 @@ namespace ssm {
 
 namespace {
 
-// ---- one token a sequence (decode), or any lengths token by token ----
-// A thread owns two channels of one sequence and steps through its tokens: one
-// token is a handful of loads in flight at once and one launch.
+// ---- short sequences (decode: one token each; any lengths are right) ----
+// A thread owns two channels of one sequence and steps through its tokens, four
+// tokens' loads at a time: one launch, a handful of loads in flight at once.
 template <class T>
 __global__ void __launch_bounds__(128)
 gated_step_kernel(const GatedArgs a, int pairs)
 {
     griddep_entry();
+    constexpr int B = 4;
     const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * 2;
     if (c0 >= a.C)
         return;
     const bool two = c0 + 1 < a.C;
     const float2 lam = make_float2(__ldg(a.lam + c0), two ? __ldg(a.lam + c0 + 1) : 0.f);
-    auto load = [&](const void *base, long long at) {
-        const T *p = static_cast<const T *>(base) + at + c0;
-        if (pairs) {
-            const Vec<T, 2> v = load_vec<T, 2>(p);
-            return make_float2(to_float(v.v[0]), to_float(v.v[1]));
-        }
-        return make_float2(to_float(p[0]), two ? to_float(p[1]) : 0.f);
-    };
     for (int seq = blockIdx.y; seq < a.n_seqs; seq += gridDim.y) {
         long long t0;
         const int len = gated_seq_len(a, seq, t0);
@@ -38,14 +31,30 @@ gated_step_kernel(const GatedArgs a, int pairs)
         if (a.resume[seq] != 0)
             h = make_float2(slot[0], two ? slot[1] : 0.f);
         float2 rate;
-        for (int t = 0; t < len; ++t) {
-            const float2 x = load(a.x, (t0 + t) * a.sx), ga = load(a.gate_a, (t0 + t) * a.sga);
-            const float2 gx = load(a.gate_x, (t0 + t) * a.sgx);
+        for (int t = 0; t < len; t += B) {
+            float2 x[B], ga[B], gx[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k)
+                if (t + k < len) {
+                    x[k] = global_pair<T>(a.x, (t0 + t + k) * a.sx + c0, pairs, two);
+                    ga[k] = global_pair<T>(a.gate_a, (t0 + t + k) * a.sga + c0, pairs, two);
+                    gx[k] = global_pair<T>(a.gate_x, (t0 + t + k) * a.sgx + c0, pairs, two);
+                }
             if (t == 0)
                 rate = make_float2(a.decay_scale * softplus_f(lam.x), a.decay_scale * softplus_f(lam.y));
-            const Decay d = decay_of(mul2(rate, sigmoid2(ga)));
-            h = fma2(d.a, h, mul2(mul2(d.m, sigmoid2(gx)), x));
-            store_pair(static_cast<T *>(a.y) + (t0 + t) * a.sy + c0, h, pairs, two);
+            if (a.chunk_states && t % kGatedChunk == 0) {
+                float *cs = a.chunk_states + gated_chunk_row(a.n_seqs, seq, t0, t / kGatedChunk) * a.C + c0;
+                cs[0] = h.x;
+                if (two)
+                    cs[1] = h.y;
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k)
+                if (t + k < len) {
+                    const Decay d = decay_of(mul2(rate, sigmoid2(ga[k])));
+                    h = fma2(d.a, h, mul2(mul2(d.m, sigmoid2(gx[k])), x[k]));
+                    store_pair(static_cast<T *>(a.y) + (t0 + t + k) * a.sy + c0, h, pairs, two);
+                }
         }
         slot[0] = h.x;
         if (two)
@@ -272,7 +281,7 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
 template <class T>
 cudaError_t launch_forward(GatedArgs a, bool pairs, int dtype, cudaStream_t stream)
 {
-    if (a.n_tokens == a.n_seqs && !a.chunk_states) {
+    if (gated_short(a)) {
         const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)(a.n_seqs < 65535 ? a.n_seqs : 65535));
         return launch_pdl(gated_step_kernel<T>, grid, dim3(128), 0, stream, a, pairs ? 1 : 0);
     }
@@ -352,7 +361,7 @@ cudaError_t launch_gated_scan(GatedArgs a, int dtype, cudaStream_t stream)
     a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C, dtype == kF32);
     a.fail_waits = debug_fail_waits() ? 1 : 0;
     bool pairs = ((a.C | a.sy) & 1) == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * dtype_size(dtype)) == 0;
-    if (a.n_tokens == a.n_seqs && !a.chunk_states)          // the step kernel loads pairs too
+    if (gated_short(a))                                     // the step kernel loads pairs too
         pairs = pairs && ((a.sx | a.sga | a.sgx) & 1) == 0 &&
                 ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate_a) |
                   reinterpret_cast<uintptr_t>(a.gate_x)) % (2 * dtype_size(dtype))) == 0;

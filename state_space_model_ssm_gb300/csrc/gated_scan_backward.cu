@@ -275,6 +275,110 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
     gated_cluster_end(R, ok);
 }
 
+// ---- short sequences ----
+// A thread owns two channels of one sequence.  From the last chunk to the first it
+// steps h through the chunk, keeping the state before every fourth token, and then
+// takes the fours from the last to the first: their decays and inputs again, and
+// the gradients.
+template <class T>
+__global__ void __launch_bounds__(128)
+gated_step_backward_kernel(const GatedArgs a, int pairs)
+{
+    griddep_entry();
+    constexpr int B = 4, RUNS = kGatedChunk / B;
+    const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * 2;
+    if (c0 >= a.C)
+        return;
+    const bool two = c0 + 1 < a.C;
+    const float2 rate = make_float2(a.decay_scale * softplus_f(__ldg(a.lam + c0)),
+                                    two ? a.decay_scale * softplus_f(__ldg(a.lam + c0 + 1)) : 0.f);
+    for (int seq = blockIdx.y; seq < a.n_seqs; seq += gridDim.y) {
+        long long t0;
+        const int len = gated_seq_len(a, seq, t0);
+        float2 E = both(0.f), part = both(0.f);
+        if (a.grad_state) {
+            const float *g = a.grad_state + (long long)seq * a.C + c0;
+            E = make_float2(g[0], two ? g[1] : 0.f);
+        }
+        for (int j = (len + kGatedChunk - 1) / kGatedChunk - 1; j >= 0; --j) {
+            const long long tc = t0 + (long long)j * kGatedChunk;
+            const int n = min(kGatedChunk, len - j * kGatedChunk), runs = (n + B - 1) / B;
+            const float *cs = a.chunk_states + gated_chunk_row(a.n_seqs, seq, t0, j) * a.C + c0;
+            float2 h = make_float2(__ldg(cs), two ? __ldg(cs + 1) : 0.f), entry[RUNS];
+#pragma unroll 1
+            for (int r = 0; r < runs; ++r) {
+                entry[r] = h;
+                if (r + 1 == runs)
+                    break;
+                float2 x[B], ga[B], gx[B];
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                    const long long t = tc + r * B + k;
+                    x[k] = global_pair<T>(a.x, t * a.sx + c0, pairs, two);
+                    ga[k] = global_pair<T>(a.gate_a, t * a.sga + c0, pairs, two);
+                    gx[k] = global_pair<T>(a.gate_x, t * a.sgx + c0, pairs, two);
+                }
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                    const Decay d = decay_of(mul2(rate, sigmoid2(ga[k])));
+                    h = fma2(d.a, h, mul2(mul2(d.m, sigmoid2(gx[k])), x[k]));
+                }
+            }
+#pragma unroll 1
+            for (int r = runs - 1; r >= 0; --r) {
+                const int cnt = min(B, n - r * B);
+                float2 x[B], ga[B], gx[B], dy[B], before[B];
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                    if (k < cnt) {
+                        const long long t = tc + r * B + k;
+                        x[k] = global_pair<T>(a.x, t * a.sx + c0, pairs, two);
+                        ga[k] = global_pair<T>(a.gate_a, t * a.sga + c0, pairs, two);
+                        gx[k] = global_pair<T>(a.gate_x, t * a.sgx + c0, pairs, two);
+                        dy[k] = global_pair<T>(a.grad_y, t * a.sy + c0, pairs, two);
+                    }
+                h = entry[r];
+                Decay d[B];
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                    if (k < cnt) {
+                        before[k] = h;
+                        ga[k] = sigmoid2(ga[k]);
+                        gx[k] = sigmoid2(gx[k]);
+                        d[k] = decay_of(mul2(rate, ga[k]));
+                        h = fma2(d[k].a, h, mul2(mul2(d[k].m, gx[k]), x[k]));
+                    }
+#pragma unroll
+                for (int k = B - 1; k >= 0; --k)
+                    if (k < cnt) {
+                        const long long t = tc + r * B + k;
+                        const float2 g = add2(dy[k], E), v = mul2(rate, ga[k]);
+                        E = mul2(d[k].a, g);
+                        const float2 ix = mul2(gx[k], x[k]), gm = mul2(g, d[k].m);
+                        const float2 dla = mul2(E, fma2(mul2(d[k].a, d[k].im), make_float2(-ix.x, -ix.y), before[k]));
+                        part = fma2(dla, ga[k], part);
+                        store_pair(static_cast<T *>(a.grad_x) + t * a.gsx + c0, mul2(gm, gx[k]), pairs, two);
+                        store_pair(static_cast<T *>(a.grad_gx) + t * a.gsgx + c0,
+                                   mul2(gm, fma2(make_float2(-ix.x, -ix.y), gx[k], ix)), pairs, two);
+                        store_pair(static_cast<T *>(a.grad_ga) + t * a.gsga + c0,
+                                   mul2(dla, fma2(v, ga[k], make_float2(-v.x, -v.y))), pairs, two);
+                    }
+            }
+        }
+        if (a.grad_state0) {
+            const bool resume = a.resume[seq] != 0;
+            float *g = a.grad_state0 + (long long)seq * a.C + c0;
+            g[0] = resume ? E.x : 0.f;
+            if (two)
+                g[1] = resume ? E.y : 0.f;
+        }
+        float *to = a.lam_part + (long long)seq * a.cluster * a.C + c0;    // (short sequences: one block each)
+        to[0] = part.x;
+        if (two)
+            to[1] = part.y;
+    }
+}
+
 // dlam from the blocks' sums, in a fixed order: a block of 8 warps owns 32
 // channels, warp w adds rows w, w + 8, ...
 __global__ void __launch_bounds__(256)
@@ -305,6 +409,16 @@ cudaError_t launch_backward(const GatedArgs &a, bool pairs, int dtype, cudaStrea
 {
     GatedMap mx, mga, mgx, mdy;
     cudaError_t e;
+    if (gated_short(a)) {
+        const bool in = ((a.sx | a.sga | a.sgx | a.sy) & 1) == 0 &&
+                        ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate_a) |
+                          reinterpret_cast<uintptr_t>(a.gate_x) | reinterpret_cast<uintptr_t>(a.grad_y)) %
+                         (2 * sizeof(T))) == 0;
+        const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)(a.n_seqs < 65535 ? a.n_seqs : 65535));
+        e = launch_pdl(gated_step_backward_kernel<T>, grid, dim3(128), 0, stream, a, pairs && in ? 1 : 0);
+        return e != cudaSuccess ? e
+                                : launch_pdl(gated_lam_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, stream, a);
+    }
     const size_t smem = GatedBackward<T>::kSmem + gated_exchange_bytes(a.cluster);
     if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
         gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx) &&

@@ -270,3 +270,16 @@ def test_time_shared_by_a_cluster(lens, C):
     y, slots, ch = _forward(c, train=True)
     _check_forward(c, y, slots)
     _check_backward(c, _backward(c, ch))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("C", [1, 33, 64])
+def test_many_short_sequences_and_a_long_one(C, dtype):
+    """The stepping kernels (16 tokens a sequence or fewer on average): single tokens, fours, odd
+    lengths, empty sequences, and one that spans several chunks; forward and backward."""
+    lens = [1, 4, 0, 7, 8, 16, 3, 0, 200, 64, 65] + [2] * 25
+    c = _case(C, lens, dtype=DTYPES[dtype], seed=C + 40, fused=C == 64)
+    assert sum(lens) <= 16 * len(lens)
+    y, slots, ch = _forward(c, train=True)
+    _check_forward(c, y, slots)
+    _check_backward(c, _backward(c, ch))
