@@ -557,10 +557,11 @@ int ssm_quantize_rows(const void *x, int8_t *codes, float *scales, int rows, int
  * SSM_ERR_UNSUPPORTED above); the scales and the bias are applied in fp32.
  * workspace: 256-byte aligned, at least ssm_int8_matmul_workspace_bytes(...)
  * of the same operands, sizes and strides (0: none is needed); scratch, not
- * shared by calls that overlap on the GPU.  It holds the tokens as fp16 when
- * there are more than 64 or their rows are not 16-byte aligned, and the weights
- * when theirs are not: keep weights in rows that are a multiple of 16 bytes apart.
- * The kernel's waits are bounded; a block that gives up writes NaN.
+ * shared by calls that overlap on the GPU.  With more than 64 tokens it holds
+ * them as fp16, and the weights if their rows are not 16-byte aligned; with up
+ * to 64, either operand whose rows are not, both if inner is no multiple of 16.
+ * So keep weights in whole, aligned multiples of 16 bytes.
+ * The waits of the many-token kernel are bounded; a block that gives up writes NaN.
  */
 int ssm_int8_matmul(const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales, const float *bias,
                     void *out, int rows, int out_features, int inner, int out_dtype, long long x_stride,

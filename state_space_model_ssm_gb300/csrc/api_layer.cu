@@ -34,7 +34,7 @@ int int8_sizes(int rows, int out_features, int inner)
     if (rows < 0 || out_features <= 0 || inner <= 0)
         return SSM_ERR_INVALID_ARG;
     // blocks of the smallest tiles, and of the repacking kernel
-    const long long tiles = (rows / 16 + 1LL) * (out_features / 128 + 1LL) * 8;
+    const long long tiles = (rows / 128 + 1LL) * (out_features / 128 + 1LL);
     const long long cells = ((long long)rows + out_features) * (inner / 16 + 1LL) / 256 + 2;
     return inner > kMaxInner || tiles > INT_MAX || cells > INT_MAX ? SSM_ERR_UNSUPPORTED : SSM_OK;
 }

@@ -10,28 +10,26 @@
 // (1024 terms) the accumulator is moved to 32-bit integers in registers and
 // starts again from zero, so the sum is the exact integer for every input.
 //
-// A block owns 128 output channels and NT tokens, M = 128 channels x N = NT tokens
-// x K: the weights are the A operand, which the tensor core reads from tensor
-// memory.  They cross HBM, L2 and shared memory as bytes and become fp16 on their
-// way from shared to tensor memory: 8 warps turn each byte b into the fp16
-// number 1024 + (b ^ 0x80) by placing it under the constant's exponent, and
-// subtract 1152 (5 instructions for 4 values).  So a weight costs one byte of
-// bandwidth in every place that is short of it.  The tokens are the B operand, K-major in
-// shared memory with the 128-byte swizzle: for few tokens (NT <= 64) they arrive
-// as bytes too and the same warps convert them; for many, a kernel in front has
-// written them as fp16 once, since every block of a column of tiles reads them.
-// Rows that TMA cannot describe (an address or a stride that is no multiple of
-// 16) are repacked by that kernel.
+// More than 64 tokens (int8_tile_kernel).  A block owns 128 output channels and NT
+// tokens, M = 128 channels x N = NT tokens x K: the weights are the A operand, which
+// the tensor core reads from tensor memory.  They cross HBM, L2 and shared memory as
+// bytes and become fp16 on their way from shared to tensor memory: 8 warps turn each
+// byte b into the fp16 number 1024 + (b ^ 0x80) by placing it under the constant's
+// exponent, and subtract 1152 (5 instructions for 4 values).  So a weight costs one
+// byte of bandwidth in every place that is short of it.  The tokens are the B operand,
+// K-major in shared memory with the 128-byte swizzle; a kernel in front has written
+// them as fp16 once, since every block of a column of tiles reads them.  Weights that
+// TMA cannot describe (an address or a stride that is no multiple of 16) are repacked
+// by that kernel.
 //
-// Roles: one warp loads weights (and 8-bit tokens) by TMA, one fp16 tokens, one
-// issues the MMAs, 8 convert and afterwards write the result (thread: one output
-// channel, NT / 2 tokens).  They hand stages of 128 terms to each other through
-// mbarriers.  With few tiles the terms are split over the blocks of a cluster, whose
-// integer sums meet in the first block's shared memory: no workspace, and the
-// same bits as without a split.
+// Roles: one warp loads weights by TMA, one fp16 tokens, one issues the MMAs, 8
+// convert and afterwards write the result (thread: one output channel, NT / 2
+// tokens).  They hand stages of 128 terms to each other through mbarriers.  Every wait
+// is bounded; a block that gave up drains its copies and products, frees its tensor
+// memory and writes NaN.
 //
-// Every wait is bounded; a block that gave up drains its copies and products,
-// frees its tensor memory and writes NaN.
+// Up to 64 tokens (int8_few_kernel) the weights are read once and their bytes are the
+// bound, so the work is spread over warps and not over tiles; see there.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -57,28 +55,24 @@ struct I8Args {
     void *out;
     int M, N, K;
     long long so;
-    int tiles_m, tiles_n, split;              // token tiles, channel tiles, blocks of a cluster
+    int tiles_m, tiles_n;                     // token tiles, channel tiles
     int fail_waits;
 };
 
-// Shared memory (bytes; tiles 1024-aligned) and tensor memory of a block.  Few
-// tokens: two blocks an SM; many: one, with all of shared memory in stages.
-template <int NT, bool XCONV>
+// Shared memory (bytes; tiles 1024-aligned) and tensor memory of a block, one an SM.
+template <int NT>
 struct I8Layout {
     static constexpr int kWStages = NT == 256 ? 2 : 3;      // weight stages, 16 KB each
-    static constexpr int kABufs = NT <= 64 ? 2 : 4;         // converted weight stages in tensor memory
+    static constexpr int kABufs = 4;                        // converted weight stages in tensor memory
     static constexpr int kACols = kTerms / 2;               // columns of one
-    static constexpr int kXStages = XCONV ? kABufs : NT == 128 ? 4 : 3;
+    static constexpr int kXStages = NT == 256 ? 3 : 4;
     static constexpr int kXTile = NT * 128;                 // 64 fp16 terms of NT tokens; two to a stage
     static constexpr int kW = 0;
     static constexpr int kX = kW + kWStages * kRows * kTerms;
-    static constexpr int kXi = kX + kXStages * 2 * kXTile;  // 8-bit tokens of a weight stage
-    static constexpr int kRed = kXi + (XCONV ? kWStages * NT * kTerms : 0);
-    static constexpr int red_bytes(int split) { return (split - 1) * NT * kRows * 4; }
-    // mbarriers (after the split's sums, whose size the launch knows), then the tokens' scales
+    static constexpr int kBar = kX + kXStages * 2 * kXTile; // mbarriers, then the tokens' scales
     static constexpr int kBars = 2 * kWStages + 2 * kXStages + 2 * kABufs + 4;
-    static constexpr int total(int split) { return kRed + red_bytes(split) + kBars * 8 + 16 + NT * 4; }
-    static constexpr int kTmem = NT + kACols * kABufs <= 256 ? 256 : 512;
+    static constexpr int kTotal = kBar + kBars * 8 + 16 + NT * 4;
+    static constexpr int kTmem = 512;                       // NT + 4 x 64 columns are in use
 };
 
 // Shared-memory descriptor of a K-major tile of 128-byte rows with the 128-byte
@@ -127,25 +121,17 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
                  : "memory");
 }
 
-// C consecutive fp32 TMEM columns of this thread's lane (C = 8 or 32).
-template <int C>
-__device__ __forceinline__ void tmem_ld(uint32_t (&r)[C], uint32_t taddr)
+// 32 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32u(uint32_t (&r)[32], uint32_t taddr)
 {
-    static_assert(C == 8 || C == 32, "columns");
-    if constexpr (C == 8) {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(taddr) : "memory");
-    } else {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                       "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                       "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                       "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                     : "r"(taddr) : "memory");
-    }
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr) : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
 
@@ -199,46 +185,27 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// A shared-memory address of this block as seen in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank)
+template <class T, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void st_cluster(uint32_t addr, int v)
-{
-    asm volatile("st.shared::cluster.s32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
-
-template <class T, int NT, bool XCONV>
-__global__ void __launch_bounds__(kThreads, NT <= 64 ? 2 : 1)
-int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
-{
-    using L = I8Layout<NT, XCONV>;
+    using L = I8Layout<NT>;
     constexpr int kWStages = L::kWStages, kABufs = L::kABufs, kXRing = L::kXStages;
     griddep_entry();
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = blockIdx.x % a.split, tile = blockIdx.x / a.split;
+    const int tile = blockIdx.x;
     // Tiles in groups of 8 token tiles: the blocks that run together share weights and tokens in L2.
     const int group = tile / (8 * a.tiles_n), in_group = tile - group * 8 * a.tiles_n;
     const int gm = min(8, a.tiles_m - 8 * group);
     const int m0 = (8 * group + in_group % gm) * NT, n0 = in_group / gm * kRows;
-    const int nk = (a.K + kTerms - 1) / kTerms;
-    const int k0 = (int)((long long)nk * rank / a.split), n = (int)((long long)nk * (rank + 1) / a.split) - k0;
-    const int red = L::kRed + (a.split - 1) * NT * kRows * 4;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + red);
+    const int n = (a.K + kTerms - 1) / kTerms;              // stages
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kBar);
     uint64_t *wfull = bars, *wempty = wfull + kWStages, *xfull = wempty + kWStages, *xempty = xfull + kXRing;
     uint64_t *afull = xempty + kXRing, *aempty = afull + kABufs, *accfull = aempty + kABufs, *accempty = accfull + 1;
     uint64_t *drain = accempty + 1;
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
-    volatile int *fail = reinterpret_cast<volatile int *>(slot + 1);
     float *xsc = reinterpret_cast<float *>(slot + 4);       // the tokens' scales
     const int cap = a.fail_waits ? 0 : (int)kSpinLimit;
     const uint32_t b_wfull = smem_u32(wfull), b_wempty = smem_u32(wempty), b_xfull = smem_u32(xfull);
@@ -264,14 +231,11 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
         mbar_init(accempty, kConvWarps);
         mbar_init(drain, 1);
         mbar_init_fence();
-        *fail = 0;
     }
     for (int i = tid; i < NT; i += kThreads)
         xsc[i] = m0 + i < a.M ? __ldg(a.xs + m0 + i) : 0.f;
     fence_before();
     __syncthreads();
-    if (a.split > 1)
-        cluster_arrive();                                   // every block of the cluster runs
     fence_after();
     const uint32_t tmem = *slot, tmem_a = tmem + NT;
 
@@ -280,53 +244,44 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
         int i = 0;
         for (; i < n; ++i) {
             if (!__all_sync(kFullMask, wait_bar(b_wempty + 8 * w.s, w.phase ^ 1, cap))) {
-                *fail = 1;
                 break;
             }
             if (elect_one()) {
-                mbar_expect_tx(wfull + w.s, kRows * kTerms + (XCONV ? NT * kTerms : 0));
-                tma_2d(base + L::kW + w.s * kRows * kTerms, &wmap, (k0 + i) * kTerms, n0, wfull + w.s);
-                if (XCONV)
-                    tma_2d(base + L::kXi + w.s * NT * kTerms, &xmap, (k0 + i) * kTerms, m0, wfull + w.s);
+                mbar_expect_tx(wfull + w.s, kRows * kTerms);
+                tma_2d(base + L::kW + w.s * kRows * kTerms, &wmap, i * kTerms, n0, wfull + w.s);
             }
             w.next();
         }
         for (int j = max(0, i - kWStages); j < i; ++j)      // no copy lands after the block has gone
             wait_bar(b_wfull + 8 * (j % kWStages), (j / kWStages) & 1, (int)kSpinLimit);
     } else if (warp == kWarpX) {
-        if (!XCONV) {
-            Ring<L::kXStages> x;
-            int i = 0;
-            for (; i < n; ++i) {
-                if (!__all_sync(kFullMask, wait_bar(b_xempty + 8 * x.s, x.phase ^ 1, cap))) {
-                    *fail = 1;
-                    break;
-                }
-                if (elect_one()) {
-                    mbar_expect_tx(xfull + x.s, 2 * L::kXTile);
-                    for (int b = 0; b < 2; ++b)
-                        tma_2d(base + L::kX + (2 * x.s + b) * L::kXTile, &xmap, (k0 + i) * kTerms + 64 * b, m0, xfull + x.s);
-                }
-                x.next();
+        Ring<L::kXStages> x;
+        int i = 0;
+        for (; i < n; ++i) {
+            if (!__all_sync(kFullMask, wait_bar(b_xempty + 8 * x.s, x.phase ^ 1, cap)))
+                break;
+            if (elect_one()) {
+                mbar_expect_tx(xfull + x.s, 2 * L::kXTile);
+                for (int b = 0; b < 2; ++b)
+                    tma_2d(base + L::kX + (2 * x.s + b) * L::kXTile, &xmap, i * kTerms + 64 * b, m0, xfull + x.s);
             }
-            for (int j = max(0, i - L::kXStages); j < i; ++j)
-                wait_bar(b_xfull + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
+            x.next();
         }
+        for (int j = max(0, i - L::kXStages); j < i; ++j)
+            wait_bar(b_xfull + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
     } else if (warp == kWarpMma) {
         constexpr uint32_t id = idesc_f16(kRows, NT);
         Ring<kABufs> ab;
-        Ring<L::kXStages> x;                                // XCONV: as many token tiles as weight buffers
+        Ring<L::kXStages> x;                
         const uint64_t bd0 = desc_sw128(base + L::kX);
         uint32_t chunk = 0;
         int left = kFold;                                   // stages until the accumulator is moved
+        int issued = 0;
         for (int i = 0; i < n; ++i) {
-            bool ok = wait_bar(b_afull + 8 * ab.s, ab.phase, cap);
-            if (!XCONV)
-                ok = ok && wait_bar(b_xfull + 8 * x.s, x.phase, cap);
+            bool ok = wait_bar(b_afull + 8 * ab.s, ab.phase, cap) && wait_bar(b_xfull + 8 * x.s, x.phase, cap);
             if (left == kFold)
                 ok = ok && wait_bar(b_accempty, (chunk & 1) ^ 1, cap);
             if (!__all_sync(kFullMask, ok)) {
-                *fail = 1;
                 break;
             }
             fence_after();
@@ -338,12 +293,12 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
                     mma_f16_ts(tmem, at + 8 * kk, bd + (kk / 4) * (L::kXTile >> 4) + 2 * (kk % 4), id,
                                left != kFold || kk > 0);
                 commit_bar(b_aempty + 8 * ab.s);
-                if (!XCONV)
-                    commit_bar(b_xempty + 8 * x.s);
+                commit_bar(b_xempty + 8 * x.s);
                 if (left == 1 || i == n - 1)
                     commit_bar(b_accfull);
             }
             __syncwarp();
+            ++issued;
             if (--left == 0) {
                 left = kFold;
                 ++chunk;
@@ -355,6 +310,11 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
             commit_bar(smem_u32(drain));                    // every product issued is done before TMEM is freed
         __syncwarp();
         wait_bar(smem_u32(drain), 0, (int)kSpinLimit);
+        // ... and every arrival a commit makes has come before the block goes
+        for (int j = max(0, issued - kABufs); j < issued; ++j)
+            wait_bar(b_aempty + 8 * (j % kABufs), (j / kABufs) & 1, (int)kSpinLimit);
+        for (int j = max(0, issued - L::kXStages); j < issued; ++j)
+            wait_bar(b_xempty + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
     } else {
         const int q = warp & 3, half = warp >> 2;           // TMEM lanes 32 q ..; group, and half of the tokens
         const int row = 32 * q + lane;
@@ -362,7 +322,7 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
         constexpr int HT = NT / 2;                          // tokens of this thread
         int acc[HT];
         const int chunks = (n + kFold - 1) / kFold;
-        const bool ints = chunks > 1 || a.split > 1;
+        const bool ints = chunks > 1;
         if (ints)
 #pragma unroll
             for (int j = 0; j < HT; ++j)
@@ -370,7 +330,7 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
         int folded = 0;
         bool ok = true;
         // the accumulator into the integers
-        constexpr int LC = HT < 32 ? 8 : 32;                // columns of a TMEM load
+        constexpr int LC = 32;                              // columns of a TMEM load
         auto fold = [&]() {
             ok = ok && wait_bar(b_accfull, folded & 1, cap);
             if (__all_sync(kFullMask, ok)) {
@@ -378,7 +338,7 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
 #pragma unroll
                 for (int j = 0; j < HT; j += LC) {
                     uint32_t v[LC];
-                    tmem_ld<LC>(v, tmem + lanes + half * HT + j);
+                    tmem_ld32u(v, tmem + lanes + half * HT + j);
 #pragma unroll
                     for (int e = 0; e < LC; ++e)
                         acc[j + e] += __float2int_rn(__uint_as_float(v[e]));
@@ -414,12 +374,6 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 c[j] = *reinterpret_cast<const uint4 *>(wr + ((j ^ (row & 7)) << 4));
-            constexpr int XW = XCONV ? NT / 4 : 1;
-            uint32_t xw[XW];
-            if (XCONV)
-#pragma unroll
-                for (int j = 0; j < XW; ++j)
-                    xw[j] = *reinterpret_cast<const uint32_t *>(sm + L::kXi + s * NT * kTerms + (row + 128 * j) * 4);
             __syncwarp();
             if (lane == 0)
                 arrive_bar(b_wempty + 8 * s);
@@ -442,17 +396,6 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
                 bytes_to_half(c[j + 1].w, h[14], h[15]);
                 tmem_st16u(tmem_a + lanes + L::kACols * b + 8 * j, h);
             }
-            if (XCONV) {
-#pragma unroll
-                for (int j = 0; j < XW; ++j) {
-                    const int e = row + 128 * j, t = e >> 5, w = e & 31;    // word w (4 terms) of token t
-                    uint2 v;
-                    bytes_to_half(xw[j], v.x, v.y);
-                    *reinterpret_cast<uint2 *>(sm + L::kX + (2 * b + (w >> 4)) * L::kXTile + t * 128 +
-                                               ((((w & 15) >> 1) ^ (t & 7)) << 4) + (w & 1) * 8) = v;
-                }
-                fence_async_smem();
-            }
             tmem_wait_st();
             fence_before();
             __syncwarp();
@@ -469,82 +412,179 @@ int8_matmul_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, con
         ok = ok && wait_bar(b_accfull, (chunks - 1) & 1, cap);
         ok = __all_sync(kFullMask, ok);
         fence_after();
-        if (!ok && lane == 0)
-            *fail = 1;
-        if (rank > 0) {
-            // this block's sums to the first block: [rank - 1][token][channel]
-            cluster_wait();
-            const uint32_t to = in_block(base + L::kRed + (rank - 1) * NT * kRows * 4, 0);
+        const int c = n0 + row;
+        const bool in = c < a.N;
+        const float ws = in ? __ldg(a.ws + c) : 0.f, bias = in && a.bias ? __ldg(a.bias + c) : 0.f;
+        T *out = static_cast<T *>(a.out) + (long long)(m0 + half * HT) * a.so + c;
+        const int left = in ? a.M - m0 - half * HT : 0;     // tokens of this thread that exist
 #pragma unroll
-            for (int j = 0; j < HT; j += LC) {
-                uint32_t v[LC];
-                tmem_ld<LC>(v, tmem + lanes + half * HT + j);
+        for (int j = 0; j < HT; j += LC) {
+            uint32_t v[LC];
+            tmem_ld32u(v, tmem + lanes + half * HT + j);
 #pragma unroll
-                for (int e = 0; e < LC; ++e)
-                    st_cluster(to + ((half * HT + j + e) * kRows + row) * 4,
-                               acc[j + e] + __float2int_rn(__uint_as_float(v[e])));
-            }
-            if (!ok && lane == 0)
-                st_cluster(in_block(smem_u32(const_cast<int *>(fail)), 0), 1);
-            cluster_arrive();
-        } else {
-            if (a.split > 1) {
-                cluster_wait();
-                cluster_arrive();
-                cluster_wait();                             // the other blocks' sums are here
-            }
-            const int c = n0 + row;
-            const bool in = c < a.N;
-            const float ws = in ? __ldg(a.ws + c) : 0.f, bias = in && a.bias ? __ldg(a.bias + c) : 0.f;
-            const bool bad = a.split > 1 ? (!ok || *fail != 0) : !ok;
-            T *out = static_cast<T *>(a.out) + (long long)(m0 + half * HT) * a.so + c;
-            const int left = in ? a.M - m0 - half * HT : 0; // tokens of this thread that exist
-#pragma unroll
-            for (int j = 0; j < HT; j += LC) {
-                uint32_t v[LC];
-                tmem_ld<LC>(v, tmem + lanes + half * HT + j);
-#pragma unroll
-                for (int e = 0; e < LC; ++e) {
-                    const int col = half * HT + j + e;
-                    float sum = __uint_as_float(v[e]);
-                    if (ints) {
-                        int tot = acc[j + e] + __float2int_rn(sum);
-                        for (int r = 1; r < a.split; ++r)
-                            tot += *reinterpret_cast<const int *>(sm + L::kRed + (((r - 1) * NT + col) * kRows + row) * 4);
-                        sum = __int2float_rn(tot);
-                    }
-                    const float o = bad ? __int_as_float(0x7fc00000) : fmaf(sum * xsc[col], ws, bias);
-                    if (j + e < left)
-                        *out = from_float<T>(o);
-                    out += a.so;
-                }
+            for (int e = 0; e < LC; ++e) {
+                float sum = __uint_as_float(v[e]);
+                if (ints)
+                    sum = __int2float_rn(acc[j + e] + __float2int_rn(sum));
+                const float o = ok ? fmaf(sum * xsc[half * HT + j + e], ws, bias) : __int_as_float(0x7fc00000);
+                if (j + e < left)
+                    *out = from_float<T>(o);
+                out += a.so;
             }
         }
         fence_before();
     }
-    __syncwarp();
-    // the other warps' share of the cluster's barriers
-    if (a.split > 1 && warp >= kConvWarps) {
-        cluster_wait();
-        cluster_arrive();
-        if (rank == 0)
-            cluster_wait();
-    }
     __syncthreads();
-    if (a.split > 1 && rank > 0)
-        cluster_wait();
+    __syncwarp();
     if (warp == kWarpMma) {
         fence_after();
         tmem_dealloc(tmem, L::kTmem);
     }
 }
 
-// Tokens as fp16 rows of `kp` elements (blocks below `xblocks`), weights as rows
-// of `kp` bytes (the others); 16 values a thread.
+// Up to 64 tokens.  Each weight byte is read once, from HBM into the registers of the
+// lane that multiplies it, with no shared memory, barrier or tensor memory between
+// (so nothing waits): a warp owns 16 MT channels and every `warps`-th chunk of 64
+// terms, and each lane loads 16 consecutive bytes of two of its rows (MT: twice), kAhead
+// chunks ahead.  In a 16 x 8 x 16 product the lanes of a quarter hold terms 2 t, 2 t + 1, 2 t + 8,
+// 2 t + 9; which terms those are is free as long as both operands agree, so lane t
+// takes the 16 bytes at 16 t of the chunk, four a product, and no lane ever needs
+// another's bytes.  The tokens are loaded alike; their few rows stay in L1.  Sums leave
+// fp32 every 1024 terms and are added as integers (in any order: exact) in shared
+// memory, where the warps of a block meet.
+constexpr int kFewTokens = 64, kChunk = 64, kFewWarps = 16;
+constexpr int kFewFold = 1024 / kChunk;
+constexpr int kFewFill = 152 * 16;             // warps below which a block's share of the terms is split further
+
+struct FewArgs {
+    const int8_t *x, *w;                      // rows 16-byte aligned, K a multiple of 16
+    const float *xs, *ws, *bias;
+    void *out;
+    int M, N, K;
+    long long sx, sw, so;
+};
+
+// 16 weights, each read once: past L1.
+__device__ __forceinline__ uint4 load_once(const int8_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <class T, int MT, int NG>                          // 16 MT channels, 8 NG tokens
+__global__ void __launch_bounds__(32 * kFewWarps / MT)
+int8_few_kernel(const FewArgs a)
+{
+    griddep_entry();
+    constexpr int kAhead = 4 / MT;
+    constexpr int C = 16 * MT, CS = C + 4;                  // CS: the sums of a quarter's tokens fall in different banks
+    __shared__ int sums[8 * NG * CS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int g = lane >> 2, t = lane & 3, n0 = blockIdx.x * C;
+    for (int i = tid; i < 8 * NG * CS; i += blockDim.x)
+        sums[i] = 0;
+    __syncthreads();
+
+    const int chunks = (a.K + kChunk - 1) / kChunk;
+    const int8_t *wp[2 * MT], *xp[NG];
+    bool wok[2 * MT], xok[NG];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+        wok[i] = n0 + 8 * i + g < a.N;
+        wp[i] = a.w + (wok[i] ? n0 + 8 * i + g : 0) * a.sw + 16 * t;
+    }
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+        xok[j] = 8 * j + g < a.M;
+        xp[j] = a.x + (xok[j] ? 8 * j + g : 0) * a.sx + 16 * t;
+    }
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 wv[kAhead][2 * MT];
+    auto fetch = [&](uint4 (&v)[2 * MT], int c) {
+        const bool in = c * kChunk + 16 * t < a.K;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+            v[i] = in && wok[i] ? load_once(wp[i] + c * kChunk) : zero;
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        fetch(wv[u], warp + u * warps);
+
+    float acc[MT][NG][4] = {};
+    auto fold = [&]() {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    atomicAdd(sums + (8 * j + 2 * t + (e & 1)) * CS + 16 * i + g + 8 * (e >> 1), __float2int_rn(acc[i][j][e]));
+                    acc[i][j][e] = 0.f;
+                }
+    };
+    int left = kFewFold;
+    for (int c0 = warp; c0 < chunks; c0 += kAhead * warps) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = c0 + u * warps;                   // past the end: zeros
+            const bool in = c * kChunk + 16 * t < a.K;
+            uint32_t h[2 * MT][8];                          // this lane's weights as fp16
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                bytes_to_half(wv[u][i].x, h[i][0], h[i][1]);
+                bytes_to_half(wv[u][i].y, h[i][2], h[i][3]);
+                bytes_to_half(wv[u][i].z, h[i][4], h[i][5]);
+                bytes_to_half(wv[u][i].w, h[i][6], h[i][7]);
+            }
+            fetch(wv[u], c + kAhead * warps);
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const uint4 xv = in && xok[j] ? __ldg(reinterpret_cast<const uint4 *>(xp[j] + c * kChunk)) : zero;
+                uint32_t b[8];
+                bytes_to_half(xv.x, b[0], b[1]);
+                bytes_to_half(xv.y, b[2], b[3]);
+                bytes_to_half(xv.z, b[4], b[5]);
+                bytes_to_half(xv.w, b[6], b[7]);
+#pragma unroll
+                for (int s = 0; s < 8; s += 2)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        mma_16816(acc[i][j], h[2 * i][s], h[2 * i + 1][s], h[2 * i][s + 1], h[2 * i + 1][s + 1], b[s], b[s + 1]);
+            }
+        }
+        left -= kAhead;
+        if (left == 0) {
+            fold();
+            left = kFewFold;
+        }
+    }
+    if (left != kFewFold)
+        fold();
+    __syncthreads();
+    T *out = static_cast<T *>(a.out);
+    for (int i = tid; i < 8 * NG * C; i += blockDim.x) {
+        const int m = i / C, c = n0 + i % C;
+        if (m < a.M && c < a.N)
+            out[m * a.so + c] = from_float<T>(fmaf(__int2float_rn(sums[m * CS + i % C]) * __ldg(a.xs + m), __ldg(a.ws + c),
+                                                   a.bias ? __ldg(a.bias + c) : 0.f));
+    }
+}
+
+// Tokens as rows of `kp` fp16 values, or bytes where `x16` is NULL (blocks below
+// `xblocks`), weights as rows of `kp` bytes (the others); 16 values a thread.
 struct PackArgs {
     const int8_t *x, *w;
     __half *x16;
-    int8_t *wp;
+    int8_t *xp, *wp;
     int M, N, K, kp;
     long long sx, sw;
     unsigned xblocks;
@@ -572,7 +612,7 @@ int8_pack_kernel(const PackArgs a)
             if (k + e < a.K)
                 v[e >> 2] |= (uint32_t)(uint8_t)src[e] << (8 * (e & 3));
     }
-    if (tokens) {
+    if (tokens && a.x16) {
         uint4 o[2];
         bytes_to_half(v[0], o[0].x, o[0].y);
         bytes_to_half(v[1], o[0].z, o[0].w);
@@ -582,7 +622,7 @@ int8_pack_kernel(const PackArgs a)
         dst[0] = o[0];
         dst[1] = o[1];
     } else {
-        *reinterpret_cast<uint4 *>(a.wp + r * a.kp + k) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4 *>((tokens ? a.xp : a.wp) + r * a.kp + k) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
 
@@ -600,8 +640,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 }
 
 // [rows][width] of bytes or fp16 in boxes of `terms` x box_rows; zeros outside.
-bool encode_rows(CUtensorMap *map, const void *p, bool half, int terms, int width, int rows, long long stride_bytes, int box_rows,
-                 CUtensorMapSwizzle swizzle)
+bool encode_rows(CUtensorMap *map, const void *p, bool half, int terms, int width, int rows, long long stride_bytes,
+                 int box_rows)
 {
     const auto fn = encode_fn();
     if (!fn)
@@ -610,116 +650,113 @@ bool encode_rows(CUtensorMap *map, const void *p, bool half, int terms, int widt
     const cuuint64_t strides[1] = {(cuuint64_t)stride_bytes};
     const cuuint32_t box[2] = {(cuuint32_t)terms, (cuuint32_t)box_rows}, step[2] = {1, 1};
     return fn(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p),
-              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool tma_rows(const void *p, long long stride) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride) & 15) == 0; }
 
-// Tokens of a tile, blocks of a cluster, and whether tokens stay bytes.
-struct Shape {
-    int nt, split;
-    bool xconv;
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Which kernel runs, and what has to be packed for it.
+struct Plan {
+    bool few, pack_x, pack_w;
+    size_t x_bytes, w_bytes;                  // workspace of either
 };
 
-Shape pick_shape(int M, int N, int K, bool x_tma)
+Plan plan(const void *x, const void *w, int M, int N, int K, long long sx, long long sw)
 {
-    const long long tn = (N + kRows - 1) / kRows;
-    Shape s{256, 1, false};
-    for (int nt : {16, 32, 64, 128, 256})
-        if (M <= nt || nt == 256) {
-            s.nt = nt;
-            break;
-        }
-    while (s.nt > 64 && tn * ((M + s.nt - 1) / s.nt) < 152)
-        s.nt /= 2;
-    if (s.nt <= 64) {
-        const int stages = (K + kTerms - 1) / kTerms, most = s.nt == 16 ? 6 : s.nt == 32 ? 3 : 2;
-        const long long tiles = tn * ((M + s.nt - 1) / s.nt);
-        while (s.split < most && tiles * (s.split + 1) <= (s.nt == 64 ? 152 : 304) && stages / (s.split + 1) >= 2)
-            ++s.split;
-    }
-    s.xconv = s.nt <= 64 && x_tma;
-    return s;
+    Plan p;
+    p.few = M <= kFewTokens;
+    // int8_few_kernel loads whole 16-byte words; TMA fills what is past a row's end
+    const bool whole = !p.few || K % 16 == 0;
+    const size_t kp = ((size_t)K + 15) / 16 * 16;
+    p.pack_x = !p.few || !whole || !tma_rows(x, sx);
+    p.pack_w = !whole || !tma_rows(w, sw);
+    p.x_bytes = p.pack_x ? up256((size_t)M * kp * (p.few ? 1 : 2)) : 0;
+    p.w_bytes = p.pack_w ? up256((size_t)N * kp) : 0;
+    return p;
 }
 
-template <class T, int NT, bool XCONV>
+template <class T, int NT>
 cudaError_t launch_tile(const I8Args &a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t st)
 {
-    const int smem = I8Layout<NT, XCONV>::total(a.split);
-    const auto kernel = int8_matmul_kernel<T, NT, XCONV>;
-    cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+    const auto kernel = int8_tile_kernel<T, NT>;
+    const cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), I8Layout<NT>::kTotal);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.tiles_m * a.tiles_n * a.split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.split > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, a, wmap, xmap);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_pdl(kernel, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(kThreads), I8Layout<NT>::kTotal, st, a, wmap, xmap);
+}
+
+template <class T, int MT, int NG>
+cudaError_t launch_few_shape(const FewArgs &a, cudaStream_t st)
+{
+    const int blocks = (a.N + 16 * MT - 1) / (16 * MT), chunks = (a.K + kChunk - 1) / kChunk;
+    int warps = 4;
+    while (warps < kFewWarps / MT && blocks * warps < kFewFill && chunks >= 4 * warps)
+        warps *= 2;
+    return launch_pdl(int8_few_kernel<T, MT, NG>, dim3((unsigned)blocks), dim3(32 * warps), 0, st, a);
 }
 
 template <class T>
-cudaError_t launch_type(const I8Args &a, const Shape &s, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t st)
+cudaError_t launch_few(const FewArgs &a, cudaStream_t st)
 {
-    switch (s.nt) {
-    case 16: return s.xconv ? launch_tile<T, 16, true>(a, wmap, xmap, st) : launch_tile<T, 16, false>(a, wmap, xmap, st);
-    case 32: return s.xconv ? launch_tile<T, 32, true>(a, wmap, xmap, st) : launch_tile<T, 32, false>(a, wmap, xmap, st);
-    case 64: return s.xconv ? launch_tile<T, 64, true>(a, wmap, xmap, st) : launch_tile<T, 64, false>(a, wmap, xmap, st);
-    case 128: return launch_tile<T, 128, false>(a, wmap, xmap, st);
-    default: return launch_tile<T, 256, false>(a, wmap, xmap, st);
-    }
+    if (a.M <= 8)
+        return launch_few_shape<T, 1, 1>(a, st);
+    if (a.M <= 16)
+        return launch_few_shape<T, 1, 2>(a, st);
+    if (a.M <= 32)
+        return launch_few_shape<T, 1, 4>(a, st);
+    return launch_few_shape<T, 2, 8>(a, st);
 }
-
-size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
 
 size_t int8_matmul_workspace_bytes(const void *x, const void *w, int M, int N, int K, long long sx, long long sw)
 {
-    const Shape s = pick_shape(M, N, K, tma_rows(x, sx));
-    const size_t kp = ((size_t)K + 15) / 16 * 16;
-    return (s.xconv ? 0 : up256((size_t)M * kp * 2)) + (tma_rows(w, sw) ? 0 : up256((size_t)N * kp));
+    const Plan p = plan(x, w, M, N, K, sx, sw);
+    return p.x_bytes + p.w_bytes;
 }
 
 cudaError_t launch_int8_matmul(const int8_t *x, const float *xs, const int8_t *w, const float *ws, const float *bias,
                                void *out, int M, int N, int K, int dtype, long long sx, long long sw, long long so,
                                void *workspace, cudaStream_t st)
 {
-    const Shape s = pick_shape(M, N, K, tma_rows(x, sx));
-    const bool pack_w = !tma_rows(w, sw);
+    const Plan pl = plan(x, w, M, N, K, sx, sw);
     const int kp = (K + 15) / 16 * 16;
-    PackArgs p{};
-    p.x = x; p.w = w; p.M = M; p.N = N; p.K = K; p.kp = kp; p.sx = sx; p.sw = sw;
-    p.x16 = static_cast<__half *>(workspace);
-    p.wp = static_cast<int8_t *>(workspace) + (s.xconv ? 0 : up256((size_t)M * kp * 2));
-    const long long xb = s.xconv ? 0 : ((long long)M * (kp / 16) + 255) / 256;
-    const long long wb = pack_w ? ((long long)N * (kp / 16) + 255) / 256 : 0;
-    p.xblocks = (unsigned)xb;
-    CUtensorMap wmap, xmap;
-    if (!encode_rows(&wmap, pack_w ? p.wp : w, false, kTerms, K, N, pack_w ? kp : sw, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !(s.xconv ? encode_rows(&xmap, x, false, kTerms, K, M, sx, s.nt, CU_TENSOR_MAP_SWIZZLE_NONE)
-                  : encode_rows(&xmap, p.x16, true, 64, K, M, (long long)kp * 2, s.nt, CU_TENSOR_MAP_SWIZZLE_128B)))
-        return cudaErrorInvalidValue;
-    if (xb + wb > 0) {
+    int8_t *xp = static_cast<int8_t *>(workspace), *wp = xp + pl.x_bytes;
+    if (pl.pack_x || pl.pack_w) {
+        const long long xb = pl.pack_x ? ((long long)M * (kp / 16) + 255) / 256 : 0;
+        const long long wb = pl.pack_w ? ((long long)N * (kp / 16) + 255) / 256 : 0;
+        const PackArgs p{x, w, pl.few ? nullptr : reinterpret_cast<__half *>(xp), xp, wp, M, N, K, kp, sx, sw, (unsigned)xb};
         const cudaError_t e = launch_pdl(int8_pack_kernel, dim3((unsigned)(xb + wb)), dim3(256), 0, st, p);
         if (e != cudaSuccess)
             return e;
     }
-    I8Args a{xs, ws, bias, out, M, N, K, so, (M + s.nt - 1) / s.nt, (N + kRows - 1) / kRows, s.split, debug_fail_waits() ? 1 : 0};
+    if (pl.few) {
+        const FewArgs a{pl.pack_x ? xp : x, pl.pack_w ? wp : w, xs, ws, bias, out, M, N, kp,
+                        pl.pack_x ? kp : sx, pl.pack_w ? kp : sw, so};
+        switch (dtype) {
+        case kF32: return launch_few<float>(a, st);
+        case kBF16: return launch_few<__nv_bfloat16>(a, st);
+        case kF16: return launch_few<__half>(a, st);
+        default: return cudaErrorInvalidValue;
+        }
+    }
+    // 256 tokens a block, or 128 where that leaves SMs without a block
+    const int tiles_n = (N + kRows - 1) / kRows;
+    const int nt = (long long)tiles_n * ((M + 255) / 256) < 152 ? 128 : 256;
+    CUtensorMap wmap, xmap;
+    if (!encode_rows(&wmap, pl.pack_w ? wp : w, false, kTerms, K, N, pl.pack_w ? kp : sw, kRows) ||
+        !encode_rows(&xmap, xp, true, 64, K, M, (long long)kp * 2, nt))
+        return cudaErrorInvalidValue;
+    const I8Args a{xs, ws, bias, out, M, N, K, so, (M + nt - 1) / nt, tiles_n, debug_fail_waits() ? 1 : 0};
     switch (dtype) {
-    case kF32: return launch_type<float>(a, s, wmap, xmap, st);
-    case kBF16: return launch_type<__nv_bfloat16>(a, s, wmap, xmap, st);
-    case kF16: return launch_type<__half>(a, s, wmap, xmap, st);
+    case kF32: return nt == 128 ? launch_tile<float, 128>(a, wmap, xmap, st) : launch_tile<float, 256>(a, wmap, xmap, st);
+    case kBF16:
+        return nt == 128 ? launch_tile<__nv_bfloat16, 128>(a, wmap, xmap, st)
+                         : launch_tile<__nv_bfloat16, 256>(a, wmap, xmap, st);
+    case kF16: return nt == 128 ? launch_tile<__half, 128>(a, wmap, xmap, st) : launch_tile<__half, 256>(a, wmap, xmap, st);
     default: return cudaErrorInvalidValue;
     }
 }
