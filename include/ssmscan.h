@@ -557,9 +557,10 @@ int ssm_quantize_rows(const void *x, int8_t *codes, float *scales, int rows, int
  * SSM_ERR_UNSUPPORTED above); the scales and the bias are applied in fp32.
  * workspace: 256-byte aligned, at least ssm_int8_matmul_workspace_bytes(...)
  * of the same operands, sizes and strides (0: none is needed); scratch, not
- * shared by calls that overlap on the GPU.  With more than 64 tokens it holds
- * them as fp16, and the weights if their rows are not 16-byte aligned; with up
- * to 64, either operand whose rows are not, both if inner is no multiple of 16.
+ * shared by calls that overlap on the GPU.  It holds the weights if their
+ * rows are not 16-byte aligned, and with many tokens (more than 64, or 32 and 8192
+ * channels) the tokens as fp16; with few, either operand whose rows are not 16-byte
+ * aligned, and both if inner is no multiple of 16.
  * So keep weights in whole, aligned multiples of 16 bytes.
  * The waits of the many-token kernel are bounded; a block that gives up writes NaN.
  */

@@ -10,7 +10,7 @@
 // (1024 terms) the accumulator is moved to 32-bit integers in registers and
 // starts again from zero, so the sum is the exact integer for every input.
 //
-// More than 64 tokens (int8_tile_kernel).  A block owns 128 output channels and NT
+// Many tokens (int8_tile_kernel).  A block owns 128 output channels and NT
 // tokens, M = 128 channels x N = NT tokens x K: the weights are the A operand, which
 // the tensor core reads from tensor memory.  They cross HBM, L2 and shared memory as
 // bytes and become fp16 on their way from shared to tensor memory: 8 warps turn each
@@ -28,7 +28,7 @@
 // is bounded; a block that gave up drains its copies and products, frees its tensor
 // memory and writes NaN.
 //
-// Up to 64 tokens (int8_few_kernel) the weights are read once and their bytes are the
+// With few tokens (int8_few_kernel) the weights are read once and their bytes are the
 // bound, so the work is spread over warps and not over tiles; see there.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -103,11 +103,12 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const void *map, int c0, in
                  ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)) : "memory");
 }
 
-// Four signed bytes as fp16: lo = bytes 0, 1 and hi = bytes 2, 3.
+// Four signed bytes as fp16: lo = bytes 0, 2 and hi = bytes 1, 3 (the terms' order
+// within a product is free as long as weights and tokens agree, and a mask is cheaper
+// than putting neighbours side by side).
 __device__ __forceinline__ void bytes_to_half(uint32_t b, uint32_t &lo, uint32_t &hi)
 {
-    const uint32_t u = b ^ 0x80808080u;
-    const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), h = __byte_perm(u, 0x64646464u, 0x4342);
+    const uint32_t l = (b & 0x00FF00FFu) ^ 0x64806480u, h = (b >> 8 & 0x00FF00FFu) ^ 0x64806480u;
     const uint32_t off = 0xE480E480u;                       // -1152 twice
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(l), "r"(off));
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(h), "r"(off));
@@ -442,18 +443,29 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
     }
 }
 
-// Up to 64 tokens.  Each weight byte is read once, from HBM into the registers of the
-// lane that multiplies it, with no shared memory, barrier or tensor memory between
-// (so nothing waits): a warp owns 16 MT channels and every `warps`-th chunk of 64
-// terms, and each lane loads 16 consecutive bytes of two of its rows (MT: twice), kAhead
-// chunks ahead.  In a 16 x 8 x 16 product the lanes of a quarter hold terms 2 t, 2 t + 1, 2 t + 8,
-// 2 t + 9; which terms those are is free as long as both operands agree, so lane t
-// takes the 16 bytes at 16 t of the chunk, four a product, and no lane ever needs
-// another's bytes.  The tokens are loaded alike; their few rows stay in L1.  Sums leave
-// fp32 every 1024 terms and are added as integers (in any order: exact) in shared
-// memory, where the warps of a block meet.
+// Few tokens.  Each weight byte is read once, from HBM into the registers of the lane
+// that multiplies it, with no shared memory, barrier or tensor memory between (so
+// nothing waits): a warp owns 16 MT channels and every `warps`-th run of kAhead chunks
+// of 64 terms, and each lane loads 16 consecutive bytes of 2 MT of its rows, kAhead
+// chunks ahead.  In a 16 x 8 x 16 product a lane holds four terms of its rows; which terms
+// those are is free as long as both operands agree, so lane t of a quarter takes the
+// 16 bytes at 16 t of the chunk, four to a product, and no lane ever needs another's
+// bytes.  The tokens are loaded alike; their few rows stay in L1.  Sums leave fp32
+// every 1024 terms and are added as integers (in any order: exact) in shared memory,
+// where the warps of a block meet.
+//
+// Measured with weights of 12288 x 4096 from HBM (7.6 us at the copy rate): 13.2 us for
+// 1 and 8 tokens, 15.7 for 16, 22.5 for 32.  From 16 tokens on the conversion of the tokens,
+// which every warp repeats, is what it waits for (without the products: 15.8 of
+// 18.2 us at the time); below, one wave of blocks that starts, streams and ends as one.
+// Runs of four chunks instead of single ones: 16.4 -> 15.7 at 16 tokens; two chunks
+// ahead 16.3, eight 16.8; fewer registers (80 a thread) for more warps 18.0.
 constexpr int kFewTokens = 64, kChunk = 64, kFewWarps = 16;
 constexpr int kFewFold = 1024 / kChunk;
+// 33 to 64 tokens: a block of the tile kernel takes 24 us for 4096 terms however few
+// channels there are, this kernel 13.5 us for 4096 channels and 37.7 for 12288.  Up to
+// 32 tokens it is the faster one at 12288 channels too (23 us against 24).
+constexpr int kFewWide = 8192;
 constexpr int kFewFill = 152 * 16;             // warps below which a block's share of the terms is split further
 
 struct FewArgs {
@@ -468,7 +480,7 @@ struct FewArgs {
 __device__ __forceinline__ uint4 load_once(const int8_t *p)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
@@ -476,12 +488,12 @@ __device__ __forceinline__ uint4 load_once(const int8_t *p)
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 template <class T, int MT, int NG>                          // 16 MT channels, 8 NG tokens
-__global__ void __launch_bounds__(32 * kFewWarps / MT)
+__global__ void __launch_bounds__(32 * kFewWarps / MT, 1)
 int8_few_kernel(const FewArgs a)
 {
     griddep_entry();
@@ -495,29 +507,31 @@ int8_few_kernel(const FewArgs a)
     __syncthreads();
 
     const int chunks = (a.K + kChunk - 1) / kChunk;
+    // A row that is not there stands for row 0 (its sums are not written), and so do
+    // tokens past the last term (their weights are zeros).
     const int8_t *wp[2 * MT], *xp[NG];
-    bool wok[2 * MT], xok[NG];
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-        wok[i] = n0 + 8 * i + g < a.N;
-        wp[i] = a.w + (wok[i] ? n0 + 8 * i + g : 0) * a.sw + 16 * t;
-    }
+    for (int i = 0; i < 2 * MT; ++i)
+        wp[i] = a.w + (n0 + 8 * i + g < a.N ? n0 + 8 * i + g : 0) * a.sw;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-        xok[j] = 8 * j + g < a.M;
-        xp[j] = a.x + (xok[j] ? 8 * j + g : 0) * a.sx + 16 * t;
-    }
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 wv[kAhead][2 * MT];
+    for (int j = 0; j < NG; ++j)
+        xp[j] = a.x + (8 * j + g < a.M ? 8 * j + g : 0) * a.sx;
+    uint4 wv[kAhead][2 * MT], xv[NG];
     auto fetch = [&](uint4 (&v)[2 * MT], int c) {
-        const bool in = c * kChunk + 16 * t < a.K;
+        const int k = c * kChunk + 16 * t;
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i)
-            v[i] = in && wok[i] ? load_once(wp[i] + c * kChunk) : zero;
+            v[i] = k < a.K ? load_once(wp[i] + k) : make_uint4(0, 0, 0, 0);
+    };
+    auto token = [&](int j, int c) {
+        return __ldg(reinterpret_cast<const uint4 *>(xp[j] + min(c * kChunk + 16 * t, a.K - 16)));
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-        fetch(wv[u], warp + u * warps);
+        fetch(wv[u], warp * kAhead + u);
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+        xv[j] = token(j, warp * kAhead);
 
     float acc[MT][NG][4] = {};
     auto fold = [&]() {
@@ -532,11 +546,10 @@ int8_few_kernel(const FewArgs a)
                 }
     };
     int left = kFewFold;
-    for (int c0 = warp; c0 < chunks; c0 += kAhead * warps) {
+    for (int c0 = warp * kAhead; c0 < chunks; c0 += kAhead * warps) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int c = c0 + u * warps;                   // past the end: zeros
-            const bool in = c * kChunk + 16 * t < a.K;
+            const int c = c0 + u;                           // past the end: zeros
             uint32_t h[2 * MT][8];                          // this lane's weights as fp16
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
@@ -548,12 +561,12 @@ int8_few_kernel(const FewArgs a)
             fetch(wv[u], c + kAhead * warps);
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                const uint4 xv = in && xok[j] ? __ldg(reinterpret_cast<const uint4 *>(xp[j] + c * kChunk)) : zero;
                 uint32_t b[8];
-                bytes_to_half(xv.x, b[0], b[1]);
-                bytes_to_half(xv.y, b[2], b[3]);
-                bytes_to_half(xv.z, b[4], b[5]);
-                bytes_to_half(xv.w, b[6], b[7]);
+                bytes_to_half(xv[j].x, b[0], b[1]);
+                bytes_to_half(xv[j].y, b[2], b[3]);
+                bytes_to_half(xv[j].z, b[4], b[5]);
+                bytes_to_half(xv[j].w, b[6], b[7]);
+                xv[j] = token(j, u + 1 < kAhead ? c + 1 : c0 + kAhead * warps);
 #pragma unroll
                 for (int s = 0; s < 8; s += 2)
 #pragma unroll
@@ -667,7 +680,7 @@ struct Plan {
 Plan plan(const void *x, const void *w, int M, int N, int K, long long sx, long long sw)
 {
     Plan p;
-    p.few = M <= kFewTokens;
+    p.few = M <= kFewTokens && (M <= 32 || N < kFewWide);
     // int8_few_kernel loads whole 16-byte words; TMA fills what is past a row's end
     const bool whole = !p.few || K % 16 == 0;
     const size_t kp = ((size_t)K + 15) / 16 * 16;

@@ -38,7 +38,7 @@ def _check(x, xs, w, ws, bias, out):
 
 SIZES = [(1, 1, 1), (1, 8, 16), (3, 5, 7), (1, 300, 64), (2, 257, 1000), (16, 128, 128), (17, 130, 129), (33, 64, 4096),
          (64, 192, 513), (65, 127, 2048), (128, 128, 64), (129, 300, 96), (200, 1000, 1003), (256, 256, 256),
-         (300, 520, 1536), (777, 401, 80)]
+         (300, 520, 1536), (777, 401, 80), (40, 8200, 160), (64, 8191, 1040)]
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
