@@ -811,8 +811,6 @@ int debug_check_sequences(const int32_t *seq_starts, const int32_t *seq_lens, in
     return check_metadata(m, stream);
 }
 
-int debug_read_status(const int *status, cudaStream_t stream) { return read_status(status, stream); }
-
 }  // namespace ssm
 
 extern "C" {

@@ -71,7 +71,6 @@ bool debug_checks();
 bool debug_fail_waits();                  // SSM_SCAN_TEST_FAIL_WAITS=1: bounded waits give up at once
 int debug_check_sequences(const int32_t *seq_starts, const int32_t *seq_lens, int n_seqs, int n_tokens,
                           cudaStream_t stream);
-int debug_read_status(const int *status, cudaStream_t stream);
 
 // add_norm.cu.  w null: the row quantiser.  dx, dr: types of x / y and of the residual.
 cudaError_t launch_add_norm(const void *x, const void *residual, const float *w, float eps, void *h, void *y,
