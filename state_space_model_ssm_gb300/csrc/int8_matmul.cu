@@ -457,7 +457,7 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
 // Measured with weights of 12288 x 4096 from HBM (7.6 us at the copy rate): 13.2 us for
 // 1 and 8 tokens, 15.7 for 16, 22.5 for 32.  From 16 tokens on the conversion of the tokens,
 // which every warp repeats, is what it waits for (without the products: 15.8 of
-// 18.2 us at the time); below, one wave of blocks that starts, streams and ends as one.
+// 18.2 us at the time), with 16 warps an SM.
 // Runs of four chunks instead of single ones: 16.4 -> 15.7 at 16 tokens; two chunks
 // ahead 16.3, eight 16.8; fewer registers (80 a thread) for more warps 18.0.
 constexpr int kFewTokens = 64, kChunk = 64, kFewWarps = 16;
