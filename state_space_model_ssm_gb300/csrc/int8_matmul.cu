@@ -62,7 +62,10 @@ struct I8Args {
 // Shared memory (bytes; tiles 1024-aligned) and tensor memory of a block, one an SM.
 template <int NT>
 struct I8Layout {
-    static constexpr int kWStages = NT == 256 ? 2 : 3;      // weight stages, 16 KB each
+    // Weight stages, 16 KB each.  An even number, so that a group meets every use of its
+    // stages: with three it met every other one, and its parity wait could pass on the use before.
+    static constexpr int kWStages = NT == 256 ? 2 : 4;
+    static_assert(kWStages % 2 == 0, "two converting groups");
     static constexpr int kABufs = 4;                        // converted weight stages in tensor memory
     static constexpr int kACols = kTerms / 2;               // columns of one
     static constexpr int kXStages = NT == 256 ? 3 : 4;
@@ -126,14 +129,14 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
 __device__ __forceinline__ void tmem_ld32u(uint32_t (&r)[32], uint32_t taddr)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
                    "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
                    "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
                    "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(taddr) : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
 
 // Place in a ring of N stages and the parity of its current round: a full
@@ -375,9 +378,6 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 c[j] = *reinterpret_cast<const uint4 *>(wr + ((j ^ (row & 7)) << 4));
-            __syncwarp();
-            if (lane == 0)
-                arrive_bar(b_wempty + 8 * s);
             ok = wait_bar(b_aempty + 8 * b, ab.phase ^ 1, cap);
             if (!__all_sync(kFullMask, ok)) {
                 ok = false;
@@ -400,8 +400,12 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
             tmem_wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
+                // the bytes are in tensor memory now: only here is their stage given back (given
+                // back before the wait above, single rows came out as the next stage's)
+                arrive_bar(b_wempty + 8 * s);
                 arrive_bar(b_afull + 8 * b);
+            }
             w.next();
             w.next();
             ab.next();

@@ -90,3 +90,14 @@ def test_chain_norm_projection():
     out = pkg.ssm_int8_matmul(q, s, wq, ws, out_dtype=torch.float32)
     ref = (q.double() * s.double()[:, None]) @ (wq.double() * ws.double()[:, None]).t()
     close(out, ref.cpu().numpy(), 4 * U * np.abs(ref.cpu().numpy()))
+
+
+@pytest.mark.parametrize("M,N,K", [(8192, 2048, 1024), (1024, 16384, 1024), (2500, 8192, 2048)])
+def test_many_tiles_are_exact_every_time(M, N, K):
+    """Many waves of tiles of either width, repeated: every sum is the integer (small enough for an exact fp32 product)."""
+    g = torch.Generator().manual_seed(3)
+    x, w = (torch.randint(-60, 61, (r, K), generator=g).to(torch.int8).cuda() for r in (M, N))
+    ref = x.float() @ w.float().t()                        # below 2^24: exact in any order
+    xs, ws = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    for _ in range(30):
+        assert torch.equal(pkg.ssm_int8_matmul(x, xs, w, ws, out_dtype=torch.float32), ref)
