@@ -763,9 +763,12 @@ cudaError_t launch_int8_matmul(const int8_t *x, const float *xs, const int8_t *w
     // 256 tokens a block, or 128 where that leaves SMs without a block
     const int tiles_n = (N + kRows - 1) / kRows;
     const int nt = (long long)tiles_n * ((M + 255) / 256) < 152 ? 128 : 256;
+    // The packed tokens are kp values wide, zeros past the last term: bytes_to_half puts a word's
+    // terms in the order 0, 2, 1, 3, so term K - 1 may stand at place K (K = 4 m + 2).  The weights'
+    // bytes lie in natural order until the kernel converts them.
     CUtensorMap wmap, xmap;
     if (!encode_rows(&wmap, pl.pack_w ? wp : w, false, kTerms, K, N, pl.pack_w ? kp : sw, kRows) ||
-        !encode_rows(&xmap, xp, true, 64, K, M, (long long)kp * 2, nt))
+        !encode_rows(&xmap, xp, true, 64, kp, M, (long long)kp * 2, nt))
         return cudaErrorInvalidValue;
     const I8Args a{xs, ws, bias, out, M, N, K, so, (M + nt - 1) / nt, tiles_n, debug_fail_waits() ? 1 : 0};
     switch (dtype) {
