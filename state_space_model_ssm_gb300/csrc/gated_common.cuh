@@ -150,7 +150,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 v)
 // Both gates of a token's two channels, r = sigmoid(ga) and i = sigmoid(gx), with one
 // reciprocal for the four: the special-function unit (16 results a cycle and SM)
 // bounds these kernels, and four denominators below 2^31 have a product below
-// 2^124.  So only for gates above kGateLow; `low` ones take a reciprocal each.
+// 2^124.  So only for gates above kGateLow; `low` ones take a reciprocal each.  So do
+// runs with a NaN: through the shared reciprocal it would reach the other channel.
 constexpr float kGateLow = -21.f;         // e^21 < 2^31
 
 template <bool LOW>
@@ -214,11 +215,17 @@ __device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpre
 __device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) { return pair(*reinterpret_cast<const __nv_bfloat162 *>(p)); }
 __device__ __forceinline__ float2 load_pair(const __half *p) { return pair(*reinterpret_cast<const __half2 *>(p)); }
 
-// Whether a warp's run of gates stays above kGateLow (a NaN is passed over: it comes
-// through any path).  Minima on the stored type: one instruction for two values.
-__device__ __forceinline__ float2 min_pairs(float2 a, float2 b) { return make_float2(fminf(a.x, b.x), fminf(a.y, b.y)); }
-__device__ __forceinline__ __nv_bfloat162 min_pairs(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmin2(a, b); }
-__device__ __forceinline__ __half2 min_pairs(__half2 a, __half2 b) { return __hmin2(a, b); }
+// Whether all of a warp's run of gates are above kGateLow; a NaN is not.  Minima that
+// keep a NaN, on the stored type: one instruction for two 16-bit values.
+__device__ __forceinline__ float min_or_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 min_pairs(float2 a, float2 b) { return make_float2(min_or_nan(a.x, b.x), min_or_nan(a.y, b.y)); }
+__device__ __forceinline__ __nv_bfloat162 min_pairs(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmin2_nan(a, b); }
+__device__ __forceinline__ __half2 min_pairs(__half2 a, __half2 b) { return __hmin2_nan(a, b); }
 template <class T>
 struct PairOf;
 template <>
@@ -239,7 +246,7 @@ __device__ __forceinline__ bool gates_above(const T *ga, const T *gx)
         least = min_pairs(least, *reinterpret_cast<const P *>(gx + i * kGatedCh));
     }
     const float2 v = pair(least);
-    return __all_sync(kFullMask, fminf(v.x, v.y) > kGateLow);
+    return __all_sync(kFullMask, v.x > kGateLow && v.y > kGateLow);
 }
 
 // The gates of a run of L tokens (rows kGatedCh apart in shared memory).
