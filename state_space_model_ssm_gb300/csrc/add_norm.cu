@@ -11,8 +11,9 @@
 // one reduction and the row is read once; the codes depend on no order of
 // summation (a product, a maximum, a quotient and a rounding, each exact or
 // rounded once).  A row of zeros has f = FLT_MAX and codes 0; a row with a NaN or
-// an infinity has scale NaN, so its values are NaN.  The quantiser is the same
-// with v = x and inv = 1.
+// an infinity in h or v has codes 0 and scale NaN, so its values are NaN (an infinite
+// or NaN h makes v infinite or NaN whatever the weight, so only v is looked at: a NaN
+// counts as an infinite maximum).  The quantiser is the same with v = x and inv = 1.
 //
 // Gradient, with n = h inv and s = mean(n w gy):
 //   grad_in = grad_h + inv (w gy - n s),  grad_w = sum over rows of gy n
@@ -107,6 +108,14 @@ struct NormArgs {
     long long sx, sr, sh, sy;       // row strides (elements) of x, residual, h and y / codes
 };
 
+// The larger one; a NaN if either is one.
+__device__ __forceinline__ float max_or_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Sums of a and maxima of b over the row's threads (blockDim.x of them), the
 // same in every thread.  red: 2 x 32 floats a row of the block.
 __device__ __forceinline__ void row_reduce(float &a, float &b, float *red)
@@ -184,12 +193,14 @@ __global__ void __launch_bounds__(norm_threads(V, NV)) add_norm_kernel(const Nor
                 ss = fmaf(h, h, ss);
                 v[j][q] = MODE == kNormCodes ? __fmul_rn(h, w.v[q]) : h;
                 if (MODE != kNormOut)
-                    top = fmaxf(top, fabsf(v[j][q]));
+                    top = max_or_nan(top, fabsf(v[j][q]));
             }
             if (hrow)
                 store_slot<TR, V, LAY>(hrow, c * V - m, D, rv[j]);
         }
     }
+    if (MODE != kNormOut && top != top)
+        top = __int_as_float(0x7f800000);                  // (the row's maximum passes over NaN)
     row_reduce(ss, top, red);
     const float inv = 1.f / sqrtf(ss / (float)D + a.eps);
     if (MODE == kNormOut) {
@@ -254,11 +265,8 @@ __global__ void __launch_bounds__(norm_threads(V, NV)) add_norm_kernel(const Nor
                 store_slot<int8_t, V, LAY>(codes, e0, D, o);
         }
     }
-    if (threadIdx.x == 0) {
-        // a NaN among the values does not reach the maximum, but it does reach the sum
-        const float one = MODE == kCodesOnly ? (ss == ss ? 1.f : ss) : inv;
-        a.scales[row] = top <= FLT_MAX ? one / f : __int_as_float(0x7fc00000);
-    }
+    if (threadIdx.x == 0)
+        a.scales[row] = top <= FLT_MAX ? (MODE == kCodesOnly ? 1.f : inv) / f : __int_as_float(0x7fc00000);
 }
 
 // ---- gradient ----
