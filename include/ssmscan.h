@@ -457,7 +457,8 @@ typedef enum {
  * chunks, with the time of a sequence shared by a cluster of blocks where there
  * are few sequences and channels.  One launch, no workspace, the same bits
  * every time.  The cluster's waits are bounded: on giving up y and the slots
- * behind it become NaN.  y must not overlap an input.
+ * behind it become NaN (and a block's y up to two rounds of chunks before it).
+ * y must not overlap an input.
  * Errors: SSM_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, strides
  * below channels), SSM_ERR_UNSUPPORTED (more than 2^28 (sequence, 64 channels)
  * pairs), SSM_ERR_CUDA.

@@ -118,15 +118,19 @@ bool check_env()
 // kernels' bounded waits give up at once, so a test sees the timeout path
 // (status word, SSM_ERR_TIMEOUT under SSM_SCAN_CHECK) without a stalled GPU.
 // Their drain of the copies and products in flight keeps its full bound.
-bool fail_waits_env()
+// At 2 the gated scan's clusters lose one warp's wait only (debug_fail_waits);
+// to every other kernel it is the same as 1.
+int fail_waits_mode()
 {
     static int v = -1;
     if (v < 0) {
         const char *e = std::getenv("SSM_SCAN_TEST_FAIL_WAITS");
-        v = (e && e[0] && std::strcmp(e, "0") != 0) ? 1 : 0;
+        v = (e && e[0] && std::strcmp(e, "0") != 0) ? (std::strcmp(e, "2") == 0 ? 2 : 1) : 0;
     }
-    return v == 1;
+    return v;
 }
+
+bool fail_waits_env() { return fail_waits_mode() != 0; }
 
 // Debug mode: SSM_ERR_TIMEOUT when a kernel's bounded wait gave up (the
 // device status word is nonzero); synchronises the stream.
@@ -801,7 +805,7 @@ namespace ssm {
 
 bool debug_checks() { return check_env(); }
 
-bool debug_fail_waits() { return fail_waits_env(); }
+int debug_fail_waits() { return fail_waits_mode(); }
 
 int debug_check_sequences(const int32_t *seq_starts, const int32_t *seq_lens, int n_seqs, int n_tokens,
                           cudaStream_t stream)

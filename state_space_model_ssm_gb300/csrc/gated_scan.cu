@@ -92,7 +92,9 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
     const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
-    const int cap = a.fail_waits ? 0 : (int)tc::kSpinLimit;
+    const int cap = a.fail_waits == 1 ? 0 : (int)tc::kSpinLimit;
+    // the exchange's limit after the first round: with the hook at 2 one warp gives up, and the peers soon after
+    const int late_cap = a.fail_waits != 2 ? cap : rank == 1 && warp == 3 ? 0 : 1 << 12;
     long long t0;
     const int len = gated_seq_len(a, seq, t0), R = gated_ranks(len, a.cluster);
     if (rank >= R)
@@ -141,7 +143,9 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
             s = make_float2(slot[0], two ? slot[1] : 0.f);
         }
     }
-    bool ok = true;
+    // ok: no wait of this thread gave up; live: none of the block's had at the last barrier, so
+    // the whole block goes on or stops by it (one warp may give up in a round that others finish)
+    bool ok = true, live = true;
     // round k's run from zero: h[i] and the product of decays p[i] up to token i; its maps sent
     auto begin = [&](int k, float2 (&h)[L], float2 (&p)[L]) {
         const int j = k * R + rank;                         // this block's chunk
@@ -179,10 +183,10 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
             run(Flag<false>(), Flag<true>());
         tot_p[k % 3][warp][lane] = pp;
         tot_h[k % 3][warp][lane] = hh;
-        ok = __syncthreads_and(ok);                         // the runs' maps are there, the stage is read
-        if (ok && k + S < rounds)
+        ok = live = __syncthreads_and(ok);                  // the runs' maps are there, the stage is read
+        if (live && k + S < rounds)
             fetch(k + S);
-        if (ok && R > 1 && warp == 0) {
+        if (live && R > 1 && warp == 0) {
             GatedMsg m{both(1.f), both(0.f)};
 #pragma unroll
             for (int w = 0; w < W; ++w) {
@@ -198,7 +202,7 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
         const int cnt = min(L, len - j * kGatedChunk - warp * L);
         float2 mine = s, next = s;                          // the states entering this block's chunk and the next round
         if (R > 1) {
-            ok = ok && exchange_wait(ex, k, cap);
+            ok = ok && exchange_wait(ex, k, k > 0 ? late_cap : cap);
             __syncwarp();
 #pragma unroll
             for (int r = 0; r < kGatedMaxCluster; ++r)
@@ -243,16 +247,16 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
     int done = 0;
     if (rounds > 0)
         begin(0, h0, p0);
-    for (; done < rounds && ok; done += 2) {
+    for (; done < rounds && live; done += 2) {
         if (done + 1 < rounds)
             begin(done + 1, h1, p1);
-        if (!ok)
+        if (!live)
             break;
         finish(done, h0, p0);
         if (done + 1 < rounds) {
             if (done + 2 < rounds)
                 begin(done + 2, h0, p0);
-            if (!ok)
+            if (!live)
                 break;
             finish(done + 1, h1, p1);
         }
@@ -359,7 +363,7 @@ cudaError_t launch_gated_scan(GatedArgs a, int dtype, cudaStream_t stream)
 {
     a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
     a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C, dtype == kF32);
-    a.fail_waits = debug_fail_waits() ? 1 : 0;
+    a.fail_waits = debug_fail_waits();
     bool pairs = ((a.C | a.sy) & 1) == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * dtype_size(dtype)) == 0;
     if (gated_short(a))                                     // the step kernel loads pairs too
         pairs = pairs && ((a.sx | a.sga | a.sgx) & 1) == 0 &&

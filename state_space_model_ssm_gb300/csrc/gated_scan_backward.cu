@@ -47,7 +47,9 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
     const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
-    const int cap = a.fail_waits ? 0 : (int)tc::kSpinLimit;
+    const int cap = a.fail_waits == 1 ? 0 : (int)tc::kSpinLimit;
+    // as in the forward kernel (one warp waits for the block here)
+    const int late_cap = a.fail_waits != 2 ? cap : rank == 1 ? 0 : 1 << 12;
     long long t0;
     const int len = gated_seq_len(a, seq, t0), R = gated_ranks(len, a.cluster);
     if (rank >= R) {                                        // this rank's share of dlam
@@ -177,7 +179,7 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
                     m.p = mul2(m.p, tot_p[w][lane]);
                 }
                 exchange_send(ex, k, rank, R, lane, m);
-                ok = ok && exchange_wait(ex, k, cap);
+                ok = ok && exchange_wait(ex, k, k > 0 ? late_cap : cap);
                 __syncwarp();
                 for (int r = R - 1; r >= 0; --r) {
                     if (r == rank)
@@ -440,7 +442,7 @@ cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, cudaStream_t stre
 {
     a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
     a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C, false);
-    a.fail_waits = debug_fail_waits() ? 1 : 0;
+    a.fail_waits = debug_fail_waits();
     const bool pairs = ((a.C | a.gsx | a.gsga | a.gsgx) & 1) == 0 &&
                        ((reinterpret_cast<uintptr_t>(a.grad_x) | reinterpret_cast<uintptr_t>(a.grad_ga) |
                          reinterpret_cast<uintptr_t>(a.grad_gx)) % (2 * dtype_size(dtype))) == 0;

@@ -68,7 +68,9 @@ __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &v)
 // checked on the host, and a kernel's status word read back.  The last two
 // synchronise and return an ssm_status.
 bool debug_checks();
-bool debug_fail_waits();                  // SSM_SCAN_TEST_FAIL_WAITS=1: bounded waits give up at once
+// SSM_SCAN_TEST_FAIL_WAITS: 0, 1 (bounded waits give up at once) or 2 (in the gated scan's
+// clusters one warp's wait does, from the second round on; else as 1)
+int debug_fail_waits();
 int debug_check_sequences(const int32_t *seq_starts, const int32_t *seq_lens, int n_seqs, int n_tokens,
                           cudaStream_t stream);
 
