@@ -413,17 +413,18 @@ __device__ __forceinline__ void gated_poison(T *out, long long stride, long long
         }
 }
 
-// No block leaves while a peer may still send to it (all threads).  After a wait that gave
-// up (ok false) maps may be on their way still: they get 20 us to land.
+// No block leaves while a peer may still send to it (all threads).  A block whose waits all
+// came through has met every map sent to it.  After a wait that gave up (ok false) maps may be
+// on their way still: past the barrier no more are sent, and these get 20 us to land.
 __device__ __forceinline__ void gated_cluster_end(int cluster, bool ok)
 {
-    if (!ok && cluster > 1)
-        for (int i = 0; i < 20; ++i)
-            __nanosleep(1000);
     __syncwarp();
     if (cluster > 1) {
         asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
+        if (!ok)
+            for (int i = 0; i < 20; ++i)
+                __nanosleep(1000);
     }
 }
 
