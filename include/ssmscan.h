@@ -453,10 +453,12 @@ typedef enum {
  *                out: the state entering each time chunk, which the backward
  *                pass reads
  * With 16 tokens a sequence or fewer on average (decode: one each) the call steps
- * every sequence token by token; otherwise blocks walk the sequences' time
- * chunks, with the time of a sequence shared by a cluster of blocks where there
- * are few sequences and channels.  One launch, no workspace, the same bits
- * every time.  The cluster's waits are bounded: on giving up y and the slots
+ * the sequences token by token, but for those of more than 32 tokens in a call of
+ * more than 128 tokens whose number is not that of the sequences; otherwise, and
+ * for those, blocks walk a sequence's time chunks, with the time of a sequence
+ * shared by a cluster of blocks where there are few sequences and channels.  One
+ * launch (two for a call that may have both), no workspace, the same bits every
+ * time.  The cluster's waits are bounded: on giving up y and the slots
  * behind it become NaN (and a block's y up to two rounds of chunks before it).
  * y must not overlap an input.
  * Errors: SSM_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, strides

@@ -16,7 +16,7 @@
 // shares the sequence: in a round its blocks take R consecutive chunks, send each
 // other their chunk's map (16 bytes a channel pair, by asynchronous stores into the
 // peers' shared memory), and each composes the maps before its own.  Every input
-// is read once, there is one launch, no workspace and no word in global memory
+// is read once, there is no workspace and no word in global memory
 // that anybody waits for; the order of every operation is fixed, so the bits are too.
 //
 // A first version cut time into chunks for independent blocks that passed their
@@ -60,6 +60,7 @@ struct GatedArgs {
     int cblocks;                        // blocks of kGatedCh channels
     int cluster;                        // blocks that share a sequence's time
     int fail_waits;                     // test hook: bounded waits give up at once
+    int step_most;                      // stepping kernels: longest sequence they take
 };
 
 // Row of chunk_states for chunk j of a sequence that starts at token t0: the first
@@ -86,16 +87,6 @@ __device__ __forceinline__ int gated_job_seq(const GatedArgs &a, int n, int lane
     return __ffs(__ballot_sync(kFullMask, lane < a.n_seqs && before == n)) - 1;
 }
 
-// Blocks of the cluster that a sequence of this length has work for; the others leave at once.
-__device__ __forceinline__ int gated_ranks(int len, int cluster)
-{
-    const int chunks = (len + kGatedChunk - 1) / kGatedChunk;
-    int r = 1;
-    while (r < cluster && r < chunks)
-        r *= 2;
-    return r;
-}
-
 // A sequence's token range; one that is not inside the packed rows counts as empty.
 __device__ __forceinline__ int gated_seq_len(const GatedArgs &a, int seq, long long &t0)
 {
@@ -105,6 +96,54 @@ __device__ __forceinline__ int gated_seq_len(const GatedArgs &a, int seq, long l
         return (int)len;
     t0 = 0;
     return 0;
+}
+
+// Sequences that a call of short ones leaves to the walk: those of more than step_most
+// tokens, in order.  A block asks for the n-th of them with n growing (all threads; the
+// same answer in each), so it reads the table once; -1 past the last one.
+template <int WARPS>
+struct GatedLongs {
+    static constexpr int kEach = 4;                         // lengths a thread reads at a time
+    uint32_t (*masks)[WARPS];                               // [kEach][WARPS], in shared memory
+    int base = 0, before = 0;                               // lengths passed, long ones among them
+    __device__ __forceinline__ int find(const GatedArgs &a, long long n)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        for (; base < a.n_seqs; base += kEach * 32 * WARPS) {
+            __syncthreads();                                // the masks have been read
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int s = base + (e * WARPS + warp) * 32 + lane;
+                long long t0;
+                const unsigned m = __ballot_sync(kFullMask, s < a.n_seqs && gated_seq_len(a, s, t0) > a.step_most);
+                if (lane == 0)
+                    masks[e][warp] = m;
+            }
+            __syncthreads();
+            int seen = before;
+            for (int e = 0; e < kEach * WARPS; ++e) {
+                unsigned m = masks[e / WARPS][e % WARPS];
+                if (n < seen + __popc(m)) {
+                    for (; seen < n; ++seen)
+                        m &= m - 1;
+                    return base + e * 32 + __ffs(m) - 1;
+                }
+                seen += __popc(m);
+            }
+            before = seen;
+        }
+        return -1;
+    }
+};
+
+// Blocks of the cluster that a sequence of this length has work for; the others leave at once.
+__device__ __forceinline__ int gated_ranks(int len, int cluster)
+{
+    const int chunks = (len + kGatedChunk - 1) / kGatedChunk;
+    int r = 1;
+    while (r < cluster && r < chunks)
+        r *= 2;
+    return r;
 }
 
 __device__ __forceinline__ float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
@@ -413,6 +452,12 @@ __device__ __forceinline__ void gated_poison(T *out, long long stride, long long
         }
 }
 
+// An mbarrier's place given back before it is initialised again (one thread; nobody waits for it).
+__device__ __forceinline__ void mbar_inval(uint64_t *mbar)
+{
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(tc::smem_u32(mbar)) : "memory");
+}
+
 // No block leaves while a peer may still send to it (all threads).  A block whose waits all
 // came through has met every map sent to it.  After a wait that gave up (ok false) maps may be
 // on their way still: past the barrier no more are sent, and these get 20 us to land.
@@ -472,6 +517,30 @@ __device__ __forceinline__ bool exchange_wait(const GatedExchange &x, int k, int
 // forward 73 with the walk, 11 stepping; backward 132, 39.
 inline bool gated_short(const GatedArgs &a) { return (long long)a.n_tokens <= 16LL * a.n_seqs; }
 
+// Among many short sequences a long one would be stepped by one thread a channel pair, so a
+// call of short ones steps those of up to kGatedStep tokens and walks the others, one block
+// each for 64 channels, in a launch of its own before it, whose blocks leave if there are
+// none.  us with 4096 channels, bf16, forward / backward, everything stepped against this:
+//   255 x 1 and 3800 tokens       2640 / 5390     96 / 300
+//   100 x 1 and 64                  26 / 65       10 / 20
+//   250 x 1 and 50 x 64             64 / 263      62 / 136
+//   250 x 1 and 50 x 40             35 / 166      55 / 125   (512 channels: 16 / 36, 13 / 24)
+//   256 x 8                         20.5 / 116    22.4 / 128
+// (limits of 64 and 16 tokens instead of 32: 26 / 75 for the second line, 52 / 109 against
+// 20.5 / 87 for 250 x 1 and 50 x 20.)  Not with 128 tokens or fewer, the longest of which
+// costs 48 us stepped, where the launch would cost every call 2 to 4 us (10 x 10: 5.4 / 11.5
+// against 7.5 / 16.3); nor with as many tokens as sequences, a decode step as in ssm_scan
+// (other lengths are right there too, stepped).
+constexpr int kGatedStep = 32;
+inline bool gated_mixed(const GatedArgs &a) { return a.n_tokens > 4 * kGatedStep && a.n_tokens != a.n_seqs; }
+// Blocks of that launch: two an SM where there can be work for four, else one (256 x 8 tokens
+// of 512 channels, no long one: 7.3 us against 10.5; 600 x 1 and 100 x 100 of 4096: 316 against 171).
+inline unsigned gated_mixed_blocks(const GatedArgs &a)
+{
+    const long long most = (long long)(a.n_tokens / (kGatedStep + 1)) * a.cblocks;
+    return (unsigned)(most < 152 ? most : most < 608 ? 152 : 304);
+}
+
 // Two neighbouring elements of a row in global memory (`pairs`: one access).
 template <class T>
 __device__ __forceinline__ float2 global_pair(const void *base, long long at, bool pairs, bool two)
@@ -495,16 +564,19 @@ bool gated_words(const void *p, int dtype, int C, long long stride);
 cudaError_t launch_gated_scan(GatedArgs a, int dtype, cudaStream_t stream);
 cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, cudaStream_t stream);
 
-// `kernel` over n_seqs x cblocks clusters.
+// Blocks of a walk over every sequence.
+inline unsigned gated_walk_blocks(const GatedArgs &a) { return (unsigned)((long long)a.n_seqs * a.cblocks * a.cluster); }
+
+// `kernel` over `blocks` blocks in clusters of a.cluster.
 template <class... KArgs, class... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), const GatedArgs &a, int warps, size_t smem, cudaStream_t stream,
-                            Args &&...args)
+cudaError_t launch_clusters(void (*kernel)(KArgs...), const GatedArgs &a, unsigned blocks, int warps, size_t smem,
+                            cudaStream_t stream, Args &&...args)
 {
     cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.n_seqs * a.cblocks * a.cluster));
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

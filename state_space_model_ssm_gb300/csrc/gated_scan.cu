@@ -1,5 +1,7 @@
 // Forward kernels of the gated linear recurrence (sm_103a); the mathematics and
 // the walk over time are in gated_common.cuh.
+#include <climits>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -9,7 +11,7 @@ namespace ssm {
 
 namespace {
 
-// ---- short sequences (decode: one token each; any lengths are right) ----
+// ---- short sequences (decode: one token each; any lengths up to step_most are right) ----
 // A thread owns two channels of one sequence and steps through its tokens, four
 // tokens' loads at a time: one launch, a handful of loads in flight at once.
 template <class T>
@@ -30,6 +32,8 @@ gated_step_kernel(const GatedArgs a, int pairs)
         float2 h = both(0.f);
         if (a.resume[seq] != 0)
             h = make_float2(slot[0], two ? slot[1] : 0.f);
+        if (len > a.step_most)                              // the walk has done it
+            continue;
         float2 rate;
         for (int t = 0; t < len; t += B) {
             float2 x[B], ga[B], gx[B];
@@ -71,18 +75,18 @@ gated_step_kernel(const GatedArgs a, int pairs)
 // and stores y.  So the maps travel while the next chunk is worked on (waiting
 // for them at once took 2000 of 5400 cycles a round), and TMA fills the stages of
 // later chunks.  Two runs in registers: two blocks an SM.
+// LONGS: the long sequences of a call of short ones, a block taking one after another.
 template <class T, bool TMA>
 struct GatedForward {
     static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;  // 24 KB a stage (48 KB for fp32)
     static constexpr size_t kSmem = 128 + kStages * 3 * kGatedTile * sizeof(T);
 };
 
-template <class T, bool TMA>
-__global__ void __launch_bounds__(32 * kForwardWarps, 2)
-gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
-                  const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx)
+template <class T, bool TMA, bool LONGS>
+__device__ __forceinline__ void
+gated_walk(const GatedArgs &a, const int seq, const int cb, const int rank, const int pairs, const int words,
+           const GatedMap &mx, const GatedMap &mga, const GatedMap &mgx)
 {
-    griddep_entry();
     constexpr int L = kForwardRun, W = kForwardWarps, S = GatedForward<T, TMA>::kStages;
     extern __shared__ __align__(128) unsigned char raw[];
     T *buf = reinterpret_cast<T *>(align128(raw));
@@ -90,8 +94,6 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
     __shared__ uint64_t full[S], exbar[kGatedBufs];
     const GatedExchange ex{reinterpret_cast<GatedMsg *>(buf + S * 3 * kGatedTile), exbar, a.cluster};
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
-    const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
     const int cap = a.fail_waits == 1 ? 0 : (int)tc::kSpinLimit;
     // the exchange's limit after the first round: with the hook at 2 one warp gives up, and the peers soon after
     const int late_cap = a.fail_waits != 2 ? cap : rank == 1 && warp == 3 ? 0 : 1 << 12;
@@ -280,24 +282,71 @@ gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant
             slot[1] = s.y;
     }
     gated_cluster_end(R, ok);
+    if (LONGS) {                                            // the barriers' places for the next sequence
+        __syncthreads();
+        if (tid == 0) {
+            for (int i = 0; i < S; ++i)
+                mbar_inval(&full[i]);
+            for (int i = 0; i < kGatedBufs; ++i)
+                mbar_inval(&exbar[i]);
+        }
+    }
 }
 
-template <class T>
-cudaError_t launch_forward(GatedArgs a, bool pairs, int dtype, cudaStream_t stream)
+template <class T, bool TMA, bool LONGS>
+__global__ void __launch_bounds__(32 * kForwardWarps, 2)
+gated_scan_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
+                  const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx)
 {
-    if (gated_short(a)) {
-        const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)(a.n_seqs < 65535 ? a.n_seqs : 65535));
-        return launch_pdl(gated_step_kernel<T>, grid, dim3(128), 0, stream, a, pairs ? 1 : 0);
+    griddep_entry();
+    if constexpr (LONGS) {
+        __shared__ uint32_t masks[GatedLongs<kForwardWarps>::kEach][kForwardWarps];
+        GatedLongs<kForwardWarps> longs{masks};
+        for (long long u = blockIdx.x;; u += gridDim.x) {
+            const int seq = longs.find(a, u / a.cblocks);
+            if (seq < 0)
+                return;
+            gated_walk<T, TMA, true>(a, seq, (int)(u % a.cblocks), 0, pairs, words, mx, mga, mgx);
+        }
+    } else {
+        const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
+        gated_walk<T, TMA, false>(a, gated_job_seq(a, job / a.cblocks, threadIdx.x & 31), job % a.cblocks, rank, pairs, words,
+                                  mx, mga, mgx);
     }
+}
+
+// The walk over every sequence, or over the long ones of a call of short ones.
+template <class T, bool LONGS>
+cudaError_t launch_walk(const GatedArgs &a, bool pairs, int dtype, cudaStream_t stream)
+{
+    const unsigned blocks = LONGS ? gated_mixed_blocks(a) : gated_walk_blocks(a);
     GatedMap mx, mga, mgx;
     if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
         gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx))
-        return launch_clusters(gated_scan_kernel<T, true>, a, kForwardWarps, GatedForward<T, true>::kSmem + gated_exchange_bytes(a.cluster), stream, a, pairs ? 1 : 0, 0,
+        return launch_clusters(gated_scan_kernel<T, true, LONGS>, a, blocks, kForwardWarps,
+                               GatedForward<T, true>::kSmem + gated_exchange_bytes(a.cluster), stream, a, pairs ? 1 : 0, 0,
                                mx, mga, mgx);
     const bool words = gated_words(a.x, dtype, a.C, a.sx) && gated_words(a.gate_a, dtype, a.C, a.sga) &&
                        gated_words(a.gate_x, dtype, a.C, a.sgx);
-    return launch_clusters(gated_scan_kernel<T, false>, a, kForwardWarps, GatedForward<T, false>::kSmem + gated_exchange_bytes(a.cluster), stream, a, pairs ? 1 : 0,
+    return launch_clusters(gated_scan_kernel<T, false, LONGS>, a, blocks, kForwardWarps,
+                           GatedForward<T, false>::kSmem + gated_exchange_bytes(a.cluster), stream, a, pairs ? 1 : 0,
                            words ? 1 : 0, mx, mga, mgx);
+}
+
+// pairs: y's rows take pairs; all: those of every tensor (the stepping kernel loads them too).
+template <class T>
+cudaError_t launch_forward(GatedArgs a, bool pairs, bool all, int dtype, cudaStream_t stream)
+{
+    if (!gated_short(a))
+        return launch_walk<T, false>(a, pairs, dtype, stream);
+    if (gated_mixed(a)) {
+        a.step_most = kGatedStep;
+        const cudaError_t e = launch_walk<T, true>(a, pairs, dtype, stream);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)(a.n_seqs < 65535 ? a.n_seqs : 65535));
+    return launch_pdl(gated_step_kernel<T>, grid, dim3(128), 0, stream, a, all ? 1 : 0);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
@@ -364,15 +413,15 @@ cudaError_t launch_gated_scan(GatedArgs a, int dtype, cudaStream_t stream)
     a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
     a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C, dtype == kF32);
     a.fail_waits = debug_fail_waits();
-    bool pairs = ((a.C | a.sy) & 1) == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * dtype_size(dtype)) == 0;
-    if (gated_short(a))                                     // the step kernel loads pairs too
-        pairs = pairs && ((a.sx | a.sga | a.sgx) & 1) == 0 &&
-                ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate_a) |
-                  reinterpret_cast<uintptr_t>(a.gate_x)) % (2 * dtype_size(dtype))) == 0;
+    a.step_most = INT_MAX;
+    const bool pairs = ((a.C | a.sy) & 1) == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * dtype_size(dtype)) == 0;
+    const bool all = pairs && ((a.sx | a.sga | a.sgx) & 1) == 0 &&
+                     ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate_a) |
+                       reinterpret_cast<uintptr_t>(a.gate_x)) % (2 * dtype_size(dtype))) == 0;
     switch (dtype) {
-    case kF32: return launch_forward<float>(a, pairs, dtype, stream);
-    case kBF16: return launch_forward<__nv_bfloat16>(a, pairs, dtype, stream);
-    case kF16: return launch_forward<__half>(a, pairs, dtype, stream);
+    case kF32: return launch_forward<float>(a, pairs, all, dtype, stream);
+    case kBF16: return launch_forward<__nv_bfloat16>(a, pairs, all, dtype, stream);
+    case kF16: return launch_forward<__half>(a, pairs, all, dtype, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -15,6 +15,8 @@
 // thread's tokens gives P, H and E.  The state entering a chunk was saved by the
 // forward pass (fp32: h is recomputed in registers instead of read back rounded);
 // E is carried from the last chunk to the first as the forward kernel carries h.
+#include <climits>
+
 #include "gated_common.cuh"
 
 namespace ssm {
@@ -31,13 +33,12 @@ struct GatedBackward {
     static constexpr size_t kSmem = 128 + kStages * 4 * kGatedTile * sizeof(T);
 };
 
-template <class T, bool TMA>
-__global__ void __launch_bounds__(32 * kBackwardWarps, 2)
-gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
-                           const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx,
-                           const __grid_constant__ GatedMap mdy)
+// LONGS: the long sequences of a call of short ones, a block taking one after another.
+template <class T, bool TMA, bool LONGS>
+__device__ __forceinline__ void
+gated_walk_back(const GatedArgs &a, const int seq, const int cb, const int rank, const int pairs, const int words,
+                const GatedMap &mx, const GatedMap &mga, const GatedMap &mgx, const GatedMap &mdy)
 {
-    griddep_entry();
     constexpr int L = kBackwardRun, W = kBackwardWarps, S = GatedBackward<T>::kStages;
     extern __shared__ __align__(128) unsigned char raw[];
     T *buf = reinterpret_cast<T *>(align128(raw));
@@ -45,8 +46,6 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
     __shared__ uint64_t full[S], exbar[kGatedBufs];
     const GatedExchange ex{reinterpret_cast<GatedMsg *>(buf + S * 4 * kGatedTile), exbar, a.cluster};
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
-    const int seq = gated_job_seq(a, job / a.cblocks, lane), cb = job % a.cblocks;
     const int cap = a.fail_waits == 1 ? 0 : (int)tc::kSpinLimit;
     // as in the forward kernel (one warp waits for the block here)
     const int late_cap = a.fail_waits != 2 ? cap : rank == 1 ? 0 : 1 << 12;
@@ -275,6 +274,38 @@ gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid
             to[1] = sum.y;
     }
     gated_cluster_end(R, ok);
+    if (LONGS) {                                            // the barriers' places for the next sequence
+        __syncthreads();
+        if (tid == 0) {
+            for (int i = 0; i < S; ++i)
+                mbar_inval(&full[i]);
+            for (int i = 0; i < kGatedBufs; ++i)
+                mbar_inval(&exbar[i]);
+        }
+    }
+}
+
+template <class T, bool TMA, bool LONGS>
+__global__ void __launch_bounds__(32 * kBackwardWarps, 2)
+gated_scan_backward_kernel(const GatedArgs a, int pairs, int words, const __grid_constant__ GatedMap mx,
+                           const __grid_constant__ GatedMap mga, const __grid_constant__ GatedMap mgx,
+                           const __grid_constant__ GatedMap mdy)
+{
+    griddep_entry();
+    if constexpr (LONGS) {
+        __shared__ uint32_t masks[GatedLongs<kBackwardWarps>::kEach][kBackwardWarps];
+        GatedLongs<kBackwardWarps> longs{masks};
+        for (long long u = blockIdx.x;; u += gridDim.x) {
+            const int seq = longs.find(a, u / a.cblocks);
+            if (seq < 0)
+                return;
+            gated_walk_back<T, TMA, true>(a, seq, (int)(u % a.cblocks), 0, pairs, words, mx, mga, mgx, mdy);
+        }
+    } else {
+        const int rank = blockIdx.x % a.cluster, job = blockIdx.x / a.cluster;
+        gated_walk_back<T, TMA, false>(a, gated_job_seq(a, job / a.cblocks, threadIdx.x & 31), job % a.cblocks, rank, pairs,
+                                       words, mx, mga, mgx, mdy);
+    }
 }
 
 // ---- short sequences ----
@@ -302,6 +333,8 @@ gated_step_backward_kernel(const GatedArgs a, int pairs)
             const float *g = a.grad_state + (long long)seq * a.C + c0;
             E = make_float2(g[0], two ? g[1] : 0.f);
         }
+        if (len > a.step_most)                              // the walk has done it
+            continue;
         for (int j = (len + kGatedChunk - 1) / kGatedChunk - 1; j >= 0; --j) {
             const long long tc = t0 + (long long)j * kGatedChunk;
             const int n = min(kGatedChunk, len - j * kGatedChunk), runs = (n + B - 1) / B;
@@ -406,31 +439,43 @@ gated_lam_kernel(const GatedArgs a)
     }
 }
 
-template <class T>
-cudaError_t launch_backward(const GatedArgs &a, bool pairs, int dtype, cudaStream_t stream)
+// The walk over every sequence, or over the long ones of a call of short ones.
+template <class T, bool LONGS>
+cudaError_t launch_walk_back(const GatedArgs &a, bool pairs, int dtype, cudaStream_t stream)
 {
+    const unsigned blocks = LONGS ? gated_mixed_blocks(a) : gated_walk_blocks(a);
+    const size_t smem = GatedBackward<T>::kSmem + gated_exchange_bytes(a.cluster);
     GatedMap mx, mga, mgx, mdy;
-    cudaError_t e;
-    if (gated_short(a)) {
+    if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
+        gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx) &&
+        gated_map(&mdy, a.grad_y, dtype, a.n_tokens, a.C, a.sy))
+        return launch_clusters(gated_scan_backward_kernel<T, true, LONGS>, a, blocks, kBackwardWarps, smem, stream, a,
+                               pairs ? 1 : 0, 0, mx, mga, mgx, mdy);
+    const bool words = gated_words(a.x, dtype, a.C, a.sx) && gated_words(a.gate_a, dtype, a.C, a.sga) &&
+                       gated_words(a.gate_x, dtype, a.C, a.sgx) && gated_words(a.grad_y, dtype, a.C, a.sy);
+    return launch_clusters(gated_scan_backward_kernel<T, false, LONGS>, a, blocks, kBackwardWarps, smem, stream, a,
+                           pairs ? 1 : 0, words ? 1 : 0, mx, mga, mgx, mdy);
+}
+
+template <class T>
+cudaError_t launch_backward(GatedArgs a, bool pairs, int dtype, cudaStream_t stream)
+{
+    cudaError_t e = cudaSuccess;
+    if (!gated_short(a)) {
+        e = launch_walk_back<T, false>(a, pairs, dtype, stream);
+    } else {
+        if (gated_mixed(a)) {
+            a.step_most = kGatedStep;
+            e = launch_walk_back<T, true>(a, pairs, dtype, stream);
+            if (e != cudaSuccess)
+                return e;
+        }
         const bool in = ((a.sx | a.sga | a.sgx | a.sy) & 1) == 0 &&
                         ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.gate_a) |
                           reinterpret_cast<uintptr_t>(a.gate_x) | reinterpret_cast<uintptr_t>(a.grad_y)) %
                          (2 * sizeof(T))) == 0;
         const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)(a.n_seqs < 65535 ? a.n_seqs : 65535));
         e = launch_pdl(gated_step_backward_kernel<T>, grid, dim3(128), 0, stream, a, pairs && in ? 1 : 0);
-        return e != cudaSuccess ? e
-                                : launch_pdl(gated_lam_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, stream, a);
-    }
-    const size_t smem = GatedBackward<T>::kSmem + gated_exchange_bytes(a.cluster);
-    if (gated_map(&mx, a.x, dtype, a.n_tokens, a.C, a.sx) && gated_map(&mga, a.gate_a, dtype, a.n_tokens, a.C, a.sga) &&
-        gated_map(&mgx, a.gate_x, dtype, a.n_tokens, a.C, a.sgx) &&
-        gated_map(&mdy, a.grad_y, dtype, a.n_tokens, a.C, a.sy)) {
-        e = launch_clusters(gated_scan_backward_kernel<T, true>, a, kBackwardWarps, smem, stream, a, pairs ? 1 : 0, 0, mx, mga, mgx, mdy);
-    } else {
-        const bool words = gated_words(a.x, dtype, a.C, a.sx) && gated_words(a.gate_a, dtype, a.C, a.sga) &&
-                           gated_words(a.gate_x, dtype, a.C, a.sgx) && gated_words(a.grad_y, dtype, a.C, a.sy);
-        e = launch_clusters(gated_scan_backward_kernel<T, false>, a, kBackwardWarps, smem, stream, a, pairs ? 1 : 0, words ? 1 : 0, mx,
-                            mga, mgx, mdy);
     }
     return e != cudaSuccess ? e
                             : launch_pdl(gated_lam_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, stream, a);
@@ -443,6 +488,7 @@ cudaError_t launch_gated_scan_backward(GatedArgs a, int dtype, cudaStream_t stre
     a.cblocks = (a.C + kGatedCh - 1) / kGatedCh;
     a.cluster = gated_cluster(a.n_seqs, a.n_tokens, a.C, false);
     a.fail_waits = debug_fail_waits();
+    a.step_most = INT_MAX;
     const bool pairs = ((a.C | a.gsx | a.gsga | a.gsgx) & 1) == 0 &&
                        ((reinterpret_cast<uintptr_t>(a.grad_x) | reinterpret_cast<uintptr_t>(a.grad_ga) |
                          reinterpret_cast<uintptr_t>(a.grad_gx)) % (2 * dtype_size(dtype))) == 0;
