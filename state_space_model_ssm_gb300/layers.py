@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import functools
+import inspect
 
 import torch
 
@@ -88,13 +89,16 @@ def _on(dev, stream):
 def _placed(fn):
     """Adds ``stream=None`` to an operator whose first argument says the device: the call itself runs
     with that device and stream current."""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if (not isinstance(first, torch.Tensor) or not first.is_cuda or
                 (stream is None and first.get_device() == _current_device())):
-            return fn(first, *args, **kw)         # (what is no CUDA tensor is refused there)
+            return fn(*args, **kw)                # (what is no CUDA tensor is refused there)
         with _on(first.device, stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 
