@@ -7,6 +7,11 @@ or on its keyword argument ``stream``; what it allocates (outputs not given, wor
 that stream.  Tensors are [rows, width] with contiguous rows; rows may be further
 apart than their width (slices of a wider tensor).  Formulas and rules are those
 of ``include/ssmscan.h``.
+
+No function here is recorded by torch's autograd: outputs never require a gradient, also where an
+input does, so a training step calls the backward functions itself (as ``examples/gated_layer.py``
+does).  A ``workspace=`` that is given has to hold at least what the operator's
+``..._workspace_bytes`` says; calls that overlap on the GPU need one each.
 """
 from __future__ import annotations
 
@@ -259,6 +264,11 @@ def ssm_add_norm(x, weight, residual=None, *, eps=1e-6, quant=None, residual_out
     return (out, h) if quant is None else (out, scales, h)
 
 
+def add_norm_backward_workspace_bytes(rows, width) -> int:
+    """Bytes of workspace of ``ssm_add_norm_backward``."""
+    return int(load().ssm_add_norm_backward_workspace_bytes(int(rows), int(width)))
+
+
 @_placed
 def ssm_add_norm_backward(grad_y, h, weight, *, grad_h=None, eps=1e-6, grad_in=None, grad_weight=None, workspace=None):
     """Gradient of ``ssm_add_norm`` (``ssm_add_norm_backward``): grad_y [T, D] in y's type, h as the
@@ -300,6 +310,16 @@ def ssm_quantize_rows(x, codes=None, scales=None):
 
 
 # ---- 8-bit integer matrix product ----
+
+
+def int8_matmul_workspace_bytes(x, w) -> int:
+    """Bytes of workspace of ``ssm_int8_matmul`` for these operands (their addresses and strides count; 0: none)."""
+    for t, name in ((x, "x"), (w, "w")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise TypeError(f"{name} must be a 2-dimensional torch.Tensor")
+    px, sx = _rows(x, "x", torch.int8, x.device, x.shape)
+    pw, sw = _rows(w, "w", torch.int8, x.device, (w.shape[0], x.shape[1]))
+    return int(load().ssm_int8_matmul_workspace_bytes(px, pw, x.shape[0], w.shape[0], x.shape[1], sx, sw))
 
 
 @_placed
