@@ -453,6 +453,8 @@ cudaError_t launch_norm_t(const NormArgs &a, cudaStream_t st)
                          reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
     if (aligned)
         return launch_norm_v<TX, TR, V, MODE, kAligned>(a, st);
+    if constexpr (MODE == kCodesOnly)                      // x's are the only rows that count
+        return launch_norm_v<TX, TR, V, MODE, kAlike>(a, st);
     // rows of x, residual, h and y at the same offset from a boundary, row after row
     const long long mx = reinterpret_cast<uintptr_t>(a.x) / sizeof(TX) % V;
     auto alike = [&](const void *t, size_t size, long long stride) {
@@ -463,15 +465,21 @@ cudaError_t launch_norm_t(const NormArgs &a, cudaStream_t st)
     return same ? launch_norm_v<TX, TR, V, MODE, kAlike>(a, st) : launch_norm_v<TX, TR, V, MODE, kElements>(a, st);
 }
 
+template <class TX, int MODE>
+cudaError_t launch_norm_r(const NormArgs &a, int dr, cudaStream_t st)
+{
+    if constexpr (MODE != kCodesOnly && sizeof(TX) == 2)   // the quantiser has no residual
+        if (dr == kF32)
+            return launch_norm_t<TX, float, MODE>(a, st);
+    return launch_norm_t<TX, TX, MODE>(a, st);
+}
+
 template <int MODE>
 cudaError_t launch_norm(const NormArgs &a, int dx, int dr, cudaStream_t st)
 {
     if (dx == kF32)
-        return launch_norm_t<float, float, MODE>(a, st);
-    if (dx == kBF16)
-        return dr == kF32 ? launch_norm_t<__nv_bfloat16, float, MODE>(a, st)
-                          : launch_norm_t<__nv_bfloat16, __nv_bfloat16, MODE>(a, st);
-    return dr == kF32 ? launch_norm_t<__half, float, MODE>(a, st) : launch_norm_t<__half, __half, MODE>(a, st);
+        return launch_norm_r<float, MODE>(a, dr, st);
+    return dx == kBF16 ? launch_norm_r<__nv_bfloat16, MODE>(a, dr, st) : launch_norm_r<__half, MODE>(a, dr, st);
 }
 
 template <class TY, class TR, int V, int LAY>

@@ -288,45 +288,6 @@ __device__ __forceinline__ bool gates_above(const T *ga, const T *gx)
     return __all_sync(kFullMask, v.x > kGateLow && v.y > kGateLow);
 }
 
-// The gates of a run of L tokens (rows kGatedCh apart in shared memory).
-template <bool LOW, int L, class T>
-__device__ __forceinline__ void gates_run(const T *ga, const T *gx, float2 (&r)[L], float2 (&g)[L])
-{
-    if (LOW) {
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-            gates2<true>(load_pair(ga + i * kGatedCh), load_pair(gx + i * kGatedCh), r[i], g[i]);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-        const float2 ta = mul2(load_pair(ga + i * kGatedCh), both(-kLog2e));
-        const float2 tx = mul2(load_pair(gx + i * kGatedCh), both(-kLog2e));
-        r[i] = make_float2(ex2(ta.x), ex2(ta.y));
-        g[i] = make_float2(ex2(tx.x), ex2(tx.y));
-    }
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-        const float2 da = add2(r[i], both(1.f)), dx = add2(g[i], both(1.f)), q = mul2(da, dx);
-        const float inv = rcp(q.x * q.y);
-        const float2 iq = mul2(make_float2(q.y, q.x), both(inv));
-        r[i] = mul2(iq, dx);
-        g[i] = mul2(iq, da);
-    }
-}
-
-// Decays and their roots of a run of L tokens.
-template <int L>
-__device__ __forceinline__ void decay_run(float2 rate, const float2 (&r)[L], float2 (&a)[L], float2 (&m)[L])
-{
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-        const Decay d = decay_of(mul2(rate, r[i]));
-        a[i] = d.a;
-        m[i] = d.m;
-    }
-}
-
 // v to p and p + 1: one store where the rows allow it (`pairs`: every row starts
 // on a pair), the second element only inside the row (`two`).
 template <class T>
