@@ -480,11 +480,12 @@ struct FewArgs {
     long long sx, sw, so;
 };
 
-// 16 weights, each read once: past L1.
+// 16 weights, each read once: past L1.  Volatile, or the compiler could take it for a function of
+// the address alone and move it above the wait for the kernel that packs the weights.
 __device__ __forceinline__ uint4 load_once(const int8_t *p)
 {
     uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }

@@ -42,6 +42,22 @@ def test_product(M, N, K):
         assert torch.equal(call(workspace=shared).double(), x.double() @ w.double().t())
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 400, 1003), (16, 2000, 500), (64, 130, 999), (200, 400, 1003)])
+def test_product_packs_before_it_reads(M, N, K):
+    """Calls without a pause, each with operands of its own through one workspace."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    ops = [[torch.randint(-128, 128, (r, K), generator=g, device="cuda").to(torch.int8) for r in (M, N)] for _ in range(12)]
+    one = [torch.ones(r, device="cuda") for r in (M, N)]
+    ws = torch.empty(pkg.int8_matmul_workspace_bytes(*ops[0]), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty(M, N, device="cuda") for _ in ops]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (x, w), out in zip(ops, outs):
+            pkg.ssm_int8_matmul(x, one[0], w, one[1], out=out, workspace=ws)
+    for (x, w), out in zip(ops, outs):
+        assert torch.equal(out.double(), x.double() @ w.double().t())
+
+
 def test_norm_gradient():
     T, D = 40, 100
     g, h, w = torch.randn(T, D, device="cuda"), torch.randn(T, D, device="cuda"), torch.ones(D, device="cuda")
