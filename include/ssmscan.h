@@ -463,7 +463,7 @@ typedef enum {
  * y must not overlap an input.
  * Errors: SSM_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, strides
  * below channels), SSM_ERR_UNSUPPORTED (more than 2^28 (sequence, 64 channels)
- * pairs), SSM_ERR_CUDA.
+ * pairs or 2^31 - 513 tokens), SSM_ERR_CUDA.
  */
 int ssm_gated_scan(float *state_slots, const void *x, const void *gate_a, const void *gate_x, const float *lam,
                    float decay_scale, void *y, const int32_t *seq_starts, const int32_t *seq_lens,
@@ -557,7 +557,8 @@ int ssm_quantize_rows(const void *x, int8_t *codes, float *scales, int rows, int
  *   x_scales [rows], w_scales [out_features], bias [out_features] or NULL: fp32
  *   out [rows][out_features] of out_dtype
  * The sum is the exact integer, rounded once to fp32 (inner at most 131071;
- * SSM_ERR_UNSUPPORTED above); the scales and the bias are applied in fp32.
+ * SSM_ERR_UNSUPPORTED above, as for more than 2^31 - 257 rows or channels); the
+ * scales and the bias are applied in fp32.
  * workspace: 256-byte aligned, at least ssm_int8_matmul_workspace_bytes(...)
  * of the same operands, sizes and strides (0: none is needed); scratch, not
  * shared by calls that overlap on the GPU.  It holds the weights if their

@@ -430,8 +430,8 @@ template <class TX, class TR, int V, int MODE, int LAY>
 cudaError_t launch_norm_v(const NormArgs &a, cudaStream_t st)
 {
     const RowShape s = row_shape(a.D, V, LAY, 256);
-    const int rows = s.threads == 32 ? 4 : 1;
-    const dim3 grid((unsigned)((a.rows + rows - 1) / rows)), block(s.threads, rows);
+    const unsigned rows = s.threads == 32 ? 4 : 1;
+    const dim3 grid(((unsigned)a.rows + rows - 1) / rows), block(s.threads, rows);
     if (s.threads > norm_threads(V, s.nv))
         return cudaErrorInvalidValue;
     switch (s.nv) {

@@ -13,6 +13,9 @@ namespace {
 
 constexpr int kMaxRowWidth = 16384;       // one row lives in a block's registers
 constexpr int kMaxInner = 131071;         // 131071 * 128 * 128 < 2^31
+// The kernels count tokens (rows, channels) in 32 bits, up to one round of a cluster (one tile) past the last.
+constexpr int kMaxTokens = INT_MAX - ssm::kGatedChunk * ssm::kGatedMaxCluster;
+constexpr int kMaxTiled = INT_MAX - 256;
 
 bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -26,7 +29,7 @@ int gated_sizes(int n_seqs, int n_tokens, int channels)
     if (n_seqs < 0 || n_tokens < 0 || channels <= 0)
         return SSM_ERR_INVALID_ARG;
     const long long blocks = (long long)n_seqs * ((channels + ssm::kGatedCh - 1LL) / ssm::kGatedCh) * ssm::kGatedMaxCluster;
-    return blocks > INT_MAX ? SSM_ERR_UNSUPPORTED : SSM_OK;
+    return blocks > INT_MAX || n_tokens > kMaxTokens ? SSM_ERR_UNSUPPORTED : SSM_OK;
 }
 
 int int8_sizes(int rows, int out_features, int inner)
@@ -36,7 +39,7 @@ int int8_sizes(int rows, int out_features, int inner)
     // blocks of the smallest tiles, and of the repacking kernel
     const long long tiles = (rows / 128 + 1LL) * (out_features / 128 + 1LL);
     const long long cells = ((long long)rows + out_features) * (inner / 16 + 1LL) / 256 + 2;
-    return inner > kMaxInner || tiles > INT_MAX || cells > INT_MAX ? SSM_ERR_UNSUPPORTED : SSM_OK;
+    return inner > kMaxInner || rows > kMaxTiled || out_features > kMaxTiled || tiles > INT_MAX || cells > INT_MAX ? SSM_ERR_UNSUPPORTED : SSM_OK;
 }
 
 int gated_debug_check(const int32_t *starts, const int32_t *lens, int n_seqs, int n_tokens, cudaStream_t stream)
