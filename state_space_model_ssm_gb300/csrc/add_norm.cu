@@ -527,7 +527,7 @@ cudaError_t launch_add_norm(const void *x, const void *residual, const float *w,
 // 40 / 46, 16384 x 512 71 / 31).
 int add_norm_parts(int rows, int D)
 {
-    const int most = D >= 2048 ? 304 : 912;
+    const int most = (D >= 2048 ? 2 : 6) * kSms;
     return rows < most ? (rows < 1 ? 1 : rows) : most;
 }
 

@@ -366,19 +366,10 @@ struct GatedExchange {
 };
 constexpr size_t gated_exchange_bytes(int cluster) { return cluster > 1 ? kGatedBufs * cluster * 32 * sizeof(GatedMsg) : 0; }
 
-// Poll an mbarrier phase; false after `cap` polls.
+// Wait for an mbarrier phase; false after `cap` polls.
 __device__ __forceinline__ bool gated_wait(uint64_t *bar, uint32_t parity, int cap)
 {
-    const uint32_t addr = tc::smem_u32(bar);
-    for (int it = 0; it < cap; ++it) {
-        uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}\n"
-                     : "=r"(done) : "r"(addr), "r"(parity) : "memory");
-        if (done)
-            return true;
-    }
-    return false;
+    return tc::mbar_poll(tc::smem_u32(bar), parity, cap);
 }
 
 // Once at the kernel's start (thread 0), before gated_cluster_start.
@@ -499,7 +490,7 @@ inline bool gated_mixed(const GatedArgs &a) { return a.n_tokens > 4 * kGatedStep
 inline unsigned gated_mixed_blocks(const GatedArgs &a)
 {
     const long long most = (long long)(a.n_tokens / (kGatedStep + 1)) * a.cblocks;
-    return (unsigned)(most < 152 ? most : most < 608 ? 152 : 304);
+    return (unsigned)(most < kSms ? most : most < 4 * kSms ? kSms : 2 * kSms);
 }
 
 // Two neighbouring elements of a row in global memory (`pairs`: one access).

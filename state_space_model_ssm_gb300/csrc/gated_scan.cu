@@ -2,9 +2,6 @@
 // the walk over time are in gated_common.cuh.
 #include <climits>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "gated_common.cuh"
 
 namespace ssm {
@@ -349,7 +346,9 @@ cudaError_t launch_forward(GatedArgs a, bool pairs, bool all, int dtype, cudaStr
     return launch_pdl(gated_step_kernel<T>, grid, dim3(128), 0, stream, a, all ? 1 : 0);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *p = nullptr;
@@ -361,8 +360,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     }();
     return fn;
 }
-
-}  // namespace
 
 long long gated_chunk_rows(long long n_seqs, long long n_tokens) { return n_seqs + n_tokens / kGatedChunk + 1; }
 
@@ -381,14 +378,14 @@ int gated_cluster(int n_seqs, int n_tokens, int C, bool wide)
     const long long cb = (C + kGatedCh - 1) / kGatedCh, chunks = (long long)n_tokens / n_seqs / kGatedChunk;
     const long long uneven = n_seqs <= 4 ? n_seqs : n_seqs / 6 > 2 ? n_seqs / 6 : 2;
     int r = 1;
-    while (r < kGatedMaxCluster && 4 * r <= chunks && uneven * cb * 2 * r <= (wide && r >= 2 ? 152 : 304))
+    while (r < kGatedMaxCluster && 4 * r <= chunks && uneven * cb * 2 * r <= (wide && r >= 2 ? kSms : 2 * kSms))
         r *= 2;
     return r;
 }
 
 bool gated_map(GatedMap *map, const void *p, int dtype, int n_tokens, int C, long long stride)
 {
-    const auto fn = encode_fn();
+    const auto fn = tensor_map_encoder();
     const long long bytes = stride * dtype_size(dtype);
     static_assert(sizeof(CUtensorMap) == sizeof(map->image), "tensor map size");
     if (!fn || n_tokens <= 0 || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) & 15) != 0 || bytes >= 1LL << 40)

@@ -25,8 +25,8 @@ namespace {
 
 // The chunk's rows stay in shared memory for both passes over them (the gates are
 // computed twice: their registers would cost half the resident blocks).  Two stages
-// of 32 KB for 16-bit types; fp32 rows take 64 KB, there one stage at three
-// blocks per SM, whose other blocks cover the wait.
+// of 32 KB for 16-bit types; fp32 rows take 64 KB, there one stage.  Two blocks an SM
+// in either case (512 threads of 64 registers), the other of which covers the wait.
 template <class T>
 struct GatedBackward {
     static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;

@@ -30,9 +30,6 @@
 //
 // With few tokens (int8_few_kernel) the weights are read once and their bytes are the
 // bound, so the work is spread over warps and not over tiles; see there.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "layer_common.cuh"
 #include "tc_common.cuh"
 
@@ -154,20 +151,6 @@ struct Ring {
     }
 };
 
-// Poll an mbarrier phase (shared-memory address); false after `cap` polls.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int cap)
-{
-    for (int it = 0; it < cap; ++it) {
-        uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}\n"
-                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (done)
-            return true;
-    }
-    return false;
-}
-
 __device__ __forceinline__ void arrive_bar(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
@@ -247,7 +230,7 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
         Ring<kWStages> w;
         int i = 0;
         for (; i < n; ++i) {
-            if (!__all_sync(kFullMask, wait_bar(b_wempty + 8 * w.s, w.phase ^ 1, cap))) {
+            if (!__all_sync(kFullMask, mbar_poll(b_wempty + 8 * w.s, w.phase ^ 1, cap))) {
                 break;
             }
             if (elect_one()) {
@@ -257,12 +240,12 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
             w.next();
         }
         for (int j = max(0, i - kWStages); j < i; ++j)      // no copy lands after the block has gone
-            wait_bar(b_wfull + 8 * (j % kWStages), (j / kWStages) & 1, (int)kSpinLimit);
+            mbar_poll(b_wfull + 8 * (j % kWStages), (j / kWStages) & 1, (int)kSpinLimit);
     } else if (warp == kWarpX) {
         Ring<L::kXStages> x;
         int i = 0;
         for (; i < n; ++i) {
-            if (!__all_sync(kFullMask, wait_bar(b_xempty + 8 * x.s, x.phase ^ 1, cap)))
+            if (!__all_sync(kFullMask, mbar_poll(b_xempty + 8 * x.s, x.phase ^ 1, cap)))
                 break;
             if (elect_one()) {
                 mbar_expect_tx(xfull + x.s, 2 * L::kXTile);
@@ -272,7 +255,7 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
             x.next();
         }
         for (int j = max(0, i - L::kXStages); j < i; ++j)
-            wait_bar(b_xfull + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
+            mbar_poll(b_xfull + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
     } else if (warp == kWarpMma) {
         constexpr uint32_t id = idesc_f16(kRows, NT);
         Ring<kABufs> ab;
@@ -282,9 +265,9 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
         int left = kFold;                                   // stages until the accumulator is moved
         int issued = 0;
         for (int i = 0; i < n; ++i) {
-            bool ok = wait_bar(b_afull + 8 * ab.s, ab.phase, cap) && wait_bar(b_xfull + 8 * x.s, x.phase, cap);
+            bool ok = mbar_poll(b_afull + 8 * ab.s, ab.phase, cap) && mbar_poll(b_xfull + 8 * x.s, x.phase, cap);
             if (left == kFold)
-                ok = ok && wait_bar(b_accempty, (chunk & 1) ^ 1, cap);
+                ok = ok && mbar_poll(b_accempty, (chunk & 1) ^ 1, cap);
             if (!__all_sync(kFullMask, ok)) {
                 break;
             }
@@ -313,12 +296,12 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
         if (elect_one())
             commit_bar(smem_u32(drain));                    // every product issued is done before TMEM is freed
         __syncwarp();
-        wait_bar(smem_u32(drain), 0, (int)kSpinLimit);
+        mbar_poll(smem_u32(drain), 0, (int)kSpinLimit);
         // ... and every arrival a commit makes has come before the block goes
         for (int j = max(0, issued - kABufs); j < issued; ++j)
-            wait_bar(b_aempty + 8 * (j % kABufs), (j / kABufs) & 1, (int)kSpinLimit);
+            mbar_poll(b_aempty + 8 * (j % kABufs), (j / kABufs) & 1, (int)kSpinLimit);
         for (int j = max(0, issued - L::kXStages); j < issued; ++j)
-            wait_bar(b_xempty + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
+            mbar_poll(b_xempty + 8 * (j % L::kXStages), (j / L::kXStages) & 1, (int)kSpinLimit);
     } else {
         const int q = warp & 3, half = warp >> 2;           // TMEM lanes 32 q ..; group, and half of the tokens
         const int row = 32 * q + lane;
@@ -336,7 +319,7 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
         // the accumulator into the integers
         constexpr int LC = 32;                              // columns of a TMEM load
         auto fold = [&]() {
-            ok = ok && wait_bar(b_accfull, folded & 1, cap);
+            ok = ok && mbar_poll(b_accfull, folded & 1, cap);
             if (__all_sync(kFullMask, ok)) {
                 fence_after();
 #pragma unroll
@@ -367,7 +350,7 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
                 fold_at += kFold;
             }
             const uint32_t s = w.s, b = ab.s;
-            ok = ok && wait_bar(b_wfull + 8 * s, w.phase, cap);
+            ok = ok && mbar_poll(b_wfull + 8 * s, w.phase, cap);
             if (!__all_sync(kFullMask, ok)) {
                 ok = false;
                 break;
@@ -378,7 +361,7 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 c[j] = *reinterpret_cast<const uint4 *>(wr + ((j ^ (row & 7)) << 4));
-            ok = wait_bar(b_aempty + 8 * b, ab.phase ^ 1, cap);
+            ok = mbar_poll(b_aempty + 8 * b, ab.phase ^ 1, cap);
             if (!__all_sync(kFullMask, ok)) {
                 ok = false;
                 break;
@@ -414,7 +397,7 @@ int8_tile_kernel(const I8Args a, const __grid_constant__ CUtensorMap wmap, const
         if (ok)
             while (folded < chunks - 1)
                 fold();
-        ok = ok && wait_bar(b_accfull, (chunks - 1) & 1, cap);
+        ok = ok && mbar_poll(b_accfull, (chunks - 1) & 1, cap);
         ok = __all_sync(kFullMask, ok);
         fence_after();
         const int c = n0 + row;
@@ -470,7 +453,7 @@ constexpr int kFewFold = 1024 / kChunk;
 // channels there are, this kernel 13.5 us for 4096 channels and 37.7 for 12288.  Up to
 // 32 tokens it is the faster one at 12288 channels too (23 us against 24).
 constexpr int kFewWide = 8192;
-constexpr int kFewFill = 152 * 16;             // warps below which a block's share of the terms is split further
+constexpr int kFewFill = kSms * 16;             // warps below which a block's share of the terms is split further
 
 struct FewArgs {
     const int8_t *x, *w;                      // rows 16-byte aligned, K a multiple of 16
@@ -644,24 +627,11 @@ int8_pack_kernel(const PackArgs a)
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess || q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 // [rows][width] of bytes or fp16 in boxes of `terms` x box_rows; zeros outside.
 bool encode_rows(CUtensorMap *map, const void *p, bool half, int terms, int width, int rows, long long stride_bytes,
                  int box_rows)
 {
-    const auto fn = encode_fn();
+    const auto fn = tensor_map_encoder();
     if (!fn)
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
@@ -763,7 +733,7 @@ cudaError_t launch_int8_matmul(const int8_t *x, const float *xs, const int8_t *w
     }
     // 256 tokens a block, or 128 where that leaves SMs without a block
     const int tiles_n = (N + kRows - 1) / kRows;
-    const int nt = (long long)tiles_n * ((M + 255) / 256) < 152 ? 128 : 256;
+    const int nt = (long long)tiles_n * ((M + 255) / 256) < kSms ? 128 : 256;
     // The packed tokens are kp values wide, zeros past the last term: bytes_to_half puts a word's
     // terms in the order 0, 2, 1, 3, so term K - 1 may stand at place K (K = 4 m + 2).  The weights'
     // bytes lie in natural order until the kernel converts them.

@@ -4,12 +4,17 @@
 // statistic is held in fp32 (or in exact integers).
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "scan_common.cuh"
 
 namespace ssm {
+
+// SMs of a GB300, the one device this is built for.  Launch shapes count on it; results do not.
+constexpr int kSms = 152;
 
 // Element types of the ABI (ssm_dtype).
 enum { kF32 = 0, kBF16 = 1, kF16 = 2 };
@@ -63,6 +68,9 @@ __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &v)
     using W = typename WordsOf<sizeof(T) * V>::type;
     *reinterpret_cast<W *>(p) = *reinterpret_cast<const W *>(&v);
 }
+
+// cuTensorMapEncodeTiled, or null without a driver that has it (gated_scan.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Debug mode (SSM_SCAN_CHECK=1; api.cu): whether it is on, the sequence table
 // checked on the host, and a kernel's status word read back.  The last two

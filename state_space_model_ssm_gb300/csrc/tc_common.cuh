@@ -14,7 +14,7 @@
 namespace ssm {
 namespace tc {
 
-constexpr long kSpinLimit = 1L << 24;       // mbarrier polls before a wait gives up (~seconds)
+constexpr long kSpinLimit = 1L << 24;       // mbarrier polls before a wait gives up (tens of seconds)
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {
@@ -151,6 +151,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *mbar, uint32_t parity, long 
             return true;
         if (it > 16)
             __nanosleep(64);
+    }
+    return false;
+}
+
+// The same without a pause between polls (1.3 us each while nothing comes), for waits of less
+// than that; `mbar` as a shared-memory address.
+__device__ __forceinline__ bool mbar_poll(uint32_t mbar, uint32_t parity, int limit)
+{
+    for (int it = 0; it < limit; ++it) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}\n"
+                     : "=r"(done) : "r"(mbar), "r"(parity) : "memory");
+        if (done)
+            return true;
     }
     return false;
 }
