@@ -58,3 +58,40 @@ def test_one_warp_gives_up_late():
     build.build()
     r = subprocess.run([sys.executable, "-c", CHILD], cwd=ROOT, env=env, capture_output=True, text=True, timeout=240)
     assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
+
+
+CHILD_MIXED = textwrap.dedent("""
+    import torch
+    import state_space_model_ssm_gb300 as pkg
+    from oracle import layers as ol
+    from tests.layer_helpers import close, gated_bounds, np64
+    from tests.test_gated_scan_gpu import _backward, _case, _forward, _ref_args
+
+    # long sequences among short ones: 40 of them on 20 blocks of channels, so that blocks take several
+    lens = ([1] * 9 + [70]) * 40 + [1] * 200
+    long = torch.tensor([n > 32 for n in lens])
+    rows = torch.cat([torch.full((n,), n > 32) for n in lens])
+    for C in (1280, 96):
+        c = _case(C, lens, resume=[1] * len(lens), seed=C)
+        y, slots, ch = _forward(c, train=True)
+        ch.nan_to_num_(0.0)
+        grads = _backward(c, ch)
+        torch.cuda.synchronize()
+        args = _ref_args(c)
+        y_ref, s_ref = ol.gated_scan(*args)
+        b = gated_bounds(*args)
+        assert torch.isnan(y[rows]).all() and torch.isnan(slots[long]).all()
+        close(y[~rows], y_ref[~rows.numpy()], b["y"][~rows.numpy()])
+        close(slots[~long], s_ref[~long.numpy()], b["slots"][~long.numpy()])
+        assert all(torch.isnan(g[rows]).all() and not torch.isnan(g[~rows]).any() for g in grads[:3])
+        assert torch.isnan(grads[3]).all() and torch.isnan(grads[4][long]).all() and not torch.isnan(grads[4][~long]).any()
+    print("ok")
+""")
+
+
+def test_long_sequences_among_short_ones_give_up():
+    """With SSM_SCAN_TEST_FAIL_WAITS=1 every wait of the walk gives up at once: NaN in the long sequences, one
+    after another on the same block, and the stepped ones as they should be."""
+    env = dict(os.environ, SSM_SCAN_TEST_FAIL_WAITS="1", PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", CHILD_MIXED], cwd=ROOT, env=env, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
