@@ -441,9 +441,11 @@ typedef enum {
  *     r = sigmoid(gate_a[t,c]),  i = sigmoid(gate_x[t,c])
  *     log a = -decay_scale * softplus(lam[c]) * r,  a = exp(log a)
  *     h_t = a h_{t-1} + sqrt(1 - a^2) i x[t,c],  y[t,c] = h_t
- * h is the fp32 state of the sequence's slot; packed tokens, seq_starts,
- * seq_lens and resume_flags as for ssm_scan (a fresh sequence never reads its
- * slot; a zero-length one leaves zeros if fresh and its slot if resuming).  A
+ * at every token.  (Some models take i x[t,c] without the root at the first token of
+ * a fresh sequence; there is no flag for that.)  h is the fp32 state of the
+ * sequence's slot; packed tokens, seq_starts, seq_lens and resume_flags as for
+ * ssm_scan (a fresh sequence never reads its slot; a zero-length one leaves zeros
+ * if fresh and its slot if resuming).  A
  * sequence whose range is not inside [0, n_tokens) counts as empty; ranges that
  * overlap are not supported (SSM_SCAN_CHECK=1 reports both).
  *   state_slots  [n_seqs][channels] fp32, in/out

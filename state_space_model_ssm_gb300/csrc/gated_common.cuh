@@ -187,9 +187,10 @@ __device__ __forceinline__ float2 sigmoid2(float2 v)
 }
 
 // Both gates of a token's two channels, r = sigmoid(ga) and i = sigmoid(gx), with one
-// reciprocal for the four: the special-function unit (16 results a cycle and SM)
-// bounds these kernels, and four denominators below 2^31 have a product below
-// 2^124.  So only for gates above kGateLow; `low` ones take a reciprocal each.  So do
+// reciprocal for the four: a special-function result costs eight times an fma's issue
+// (16 a cycle and SM; with this the unit is 19 % busy in the forward walk, whose
+// bound is the latency of its own arithmetic), and four denominators below 2^31
+// have a product below 2^124.  So only for gates above kGateLow; `low` ones take a reciprocal each.  So do
 // runs with a NaN: through the shared reciprocal it would reach the other channel.
 constexpr float kGateLow = -21.f;         // e^21 < 2^31
 

@@ -157,6 +157,7 @@ def ssm_gated_scan(state_slots, x, gate_a, gate_x, lam, seq_starts, seq_lens, re
 
         h_t = a h_{t-1} + sqrt(1 - a^2) i x_t,   y_t = h_t
 
+    at every token, a fresh sequence's first one too.
     state_slots [n, C] fp32 (updated in place); x, gate_a, gate_x [T, C] fp32, bf16 or fp16 (slices
     of one projection are fine); lam [C] fp32; seq_starts, seq_lens, resume_flags [n] int32.
     chunk_states: a tensor of ``gated_scan_chunk_states`` to fill for the backward pass.
