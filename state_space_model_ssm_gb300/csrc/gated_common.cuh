@@ -111,6 +111,7 @@ struct GatedLongs {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         for (; base < a.n_seqs; base += kEach * 32 * WARPS) {
             __syncthreads();                                // the masks have been read
+            unsigned any = 0;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
                 const int s = base + (e * WARPS + warp) * 32 + lane;
@@ -118,8 +119,10 @@ struct GatedLongs {
                 const unsigned m = __ballot_sync(kFullMask, s < a.n_seqs && gated_seq_len(a, s, t0) > a.step_most);
                 if (lane == 0)
                     masks[e][warp] = m;
+                any |= m;
             }
-            __syncthreads();
+            if (!__syncthreads_or(any != 0))                // the usual case: no long one here
+                continue;
             int seen = before;
             for (int e = 0; e < kEach * WARPS; ++e) {
                 unsigned m = masks[e / WARPS][e % WARPS];
@@ -474,20 +477,21 @@ inline bool gated_short(const GatedArgs &a) { return (long long)a.n_tokens <= 16
 // call of short ones steps those of up to kGatedStep tokens and walks the others, one block
 // each for 64 channels, in a launch of its own before it, whose blocks leave if there are
 // none.  us with 4096 channels, bf16, forward / backward, everything stepped against this:
-//   255 x 1 and 3800 tokens       2640 / 5390     96 / 300
-//   100 x 1 and 64                  26 / 65       10 / 20
-//   250 x 1 and 50 x 64             64 / 263      62 / 136
-//   250 x 1 and 50 x 40             35 / 166      55 / 125   (512 channels: 16 / 36, 13 / 24)
-//   256 x 8                         20.5 / 116    22.4 / 128
-// (limits of 64 and 16 tokens instead of 32: 26 / 75 for the second line, 52 / 109 against
-// 20.5 / 87 for 250 x 1 and 50 x 20.)  Not with 128 tokens or fewer, the longest of which
-// costs 48 us stepped, where the launch would cost every call 2 to 4 us (10 x 10: 5.4 / 11.5
-// against 7.5 / 16.3); nor with as many tokens as sequences, a decode step as in ssm_scan
-// (other lengths are right there too, stepped).
+//   255 x 1 and 3800 tokens       2640 / 5390     96 / 296
+//   100 x 1 and 64                  26 / 65        9.4 / 20
+//   250 x 1 and 50 x 64             64 / 263      61 / 136
+//   250 x 1 and 50 x 40             35 / 166      55 / 124   (512 channels: 16 / 36, 16 / 32)
+//   256 x 8                         20.5 / 116    21.5 / 126
+//   64 x 4                           5.2 / 13.5    6.4 / 14.7
+// (limits of 64 and 16 tokens instead of 32: 26 / 60 for the second line, 52 / 108 against
+// 19 / 84 for 250 x 1 and 50 x 20.)  Not with 128 tokens or fewer, the longest of which
+// costs 48 / 115 us stepped, where the launch would cost every call its share (10 x 10:
+// 5.4 / 10.8 against 6.7 / 12.9); nor with as many tokens as sequences, a decode step as in
+// ssm_scan (other lengths are right there too, stepped).
 constexpr int kGatedStep = 32;
 inline bool gated_mixed(const GatedArgs &a) { return a.n_tokens > 4 * kGatedStep && a.n_tokens != a.n_seqs; }
 // Blocks of that launch: two an SM where there can be work for four, else one (256 x 8 tokens
-// of 512 channels, no long one: 7.3 us against 10.5; 600 x 1 and 100 x 100 of 4096: 316 against 171).
+// of 512 channels, no long one: 6.4 us against 9.5; 600 x 1 and 100 x 100 of 4096: 310 against 169).
 inline unsigned gated_mixed_blocks(const GatedArgs &a)
 {
     const long long most = (long long)(a.n_tokens / (kGatedStep + 1)) * a.cblocks;
