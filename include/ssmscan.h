@@ -577,6 +577,163 @@ int ssm_int8_matmul(const int8_t *x, const float *x_scales, const int8_t *w, con
 size_t ssm_int8_matmul_workspace_bytes(const int8_t *x, const int8_t *w, int rows, int out_features, int inner,
                                        long long x_stride, long long w_stride);
 
+/*
+ * Operators that a selective-scan model is trained and served with: the
+ * selective scan with a decay for each channel and state, the short causal
+ * convolution in front of it, and the cross entropy of a projection onto a large
+ * vocabulary.  Rules as for the layer operators above.
+ */
+
+/*
+ * Selective scan with a decay for each channel and state (ssm_scan has one for
+ * each head).  For token t of a sequence, channel c of group g = c / (channels /
+ * n_groups) and state n:
+ *     v = dt[t,c] + dt_bias[c];  step = v, or with dt_softplus v > 20 ? v : log1p(exp(v))
+ *     h[c,n] = exp(step A[c,n]) h[c,n] + step x[t,c] B[t,g,n]
+ *     p = sum_n h[c,n] C[t,g,n] + D[c] x[t,c];  y[t,c] = p z[t,c] sigmoid(z[t,c])
+ * Packed tokens, seq_starts, seq_lens, resume_flags and slots as for ssm_scan (a
+ * fresh sequence never reads its slot; a zero-length one leaves zeros if fresh and
+ * its slot if resuming).  A sequence whose range is not inside [0, n_tokens)
+ * counts as empty; ranges that overlap are not supported (SSM_SCAN_CHECK=1
+ * reports both).
+ *   state_slots  [n_seqs][channels][d_state] fp32, in/out
+ *   x, dt, y     [n_tokens][channels] of dtype;  z the same, or NULL: y = p
+ *   B, C         [n_tokens][n_groups][d_state] of dtype (contiguous within a token)
+ *   A            [channels][d_state] fp32, finite;  D, dt_bias [channels] fp32 or NULL (zeros)
+ *   chunk_states NULL, or (training) fp32 [ssm_selective_scan_chunks(...)][channels][d_state],
+ *                out: the state entering every 16 tokens, which the backward pass reads
+ * d_state 1 .. 128 (SSM_ERR_UNSUPPORTED above).  Where sequences and channels alone
+ * do not fill the device, long sequences run as parallel segments, whose states pass
+ * through the workspace; the sums depend on the sizes only (the same bits every time).
+ * y must not overlap an input.
+ * workspace: 256-byte aligned, ssm_selective_scan_workspace_bytes(...) (0: none is
+ * needed); scratch, not shared by calls that overlap on the GPU.
+ */
+int ssm_selective_scan(float *state_slots, const void *x, const void *dt, const float *A, const void *B, const void *C,
+                       const float *D, const void *z, const float *dt_bias, int dt_softplus, void *y,
+                       const int32_t *seq_starts, const int32_t *seq_lens, const int32_t *resume_flags, int n_seqs,
+                       int n_tokens, int channels, int d_state, int n_groups, int dtype, long long x_stride,
+                       long long dt_stride, long long B_stride, long long C_stride, long long z_stride,
+                       long long y_stride, float *chunk_states, void *workspace, size_t workspace_bytes, void *stream);
+
+size_t ssm_selective_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, int d_state, int n_groups);
+
+/* Rows of chunk_states for these sizes; 0 for invalid ones. */
+long long ssm_selective_scan_chunks(int n_seqs, int n_tokens);
+
+/*
+ * Gradients of ssm_selective_scan.  Takes the forward call's inputs, metadata and
+ * chunk_states, the gradient of y (grad_y) and optionally of the slots after the
+ * call (grad_state, or NULL), and writes
+ *   grad_x, grad_dt, grad_z   [n_tokens][channels] of dtype, grad_B, grad_C
+ *                [n_tokens][n_groups][d_state] of dtype (tokens owned by no
+ *                sequence are not written; grad_z with z, else NULL)
+ *   grad_A       [channels][d_state], grad_D, grad_dt_bias [channels] fp32 (the last two with
+ *                their inputs, else NULL), zeros when n_seqs is 0
+ *   grad_initial_state  [n_seqs][channels][d_state] fp32 or NULL: gradient of the slots
+ *                before the call (zeros for fresh sequences)
+ * Sums over tokens and channels are fp32 in a fixed order.  The states are
+ * recomputed from chunk_states.  workspace: as above,
+ * ssm_selective_scan_backward_workspace_bytes(...).  Outputs must not overlap inputs.
+ */
+int ssm_selective_scan_backward(const void *grad_y, const float *grad_state, const void *x, const void *dt,
+                                const float *A, const void *B, const void *C, const float *D, const void *z,
+                                const float *dt_bias, int dt_softplus, const float *chunk_states,
+                                const int32_t *seq_starts, const int32_t *seq_lens, const int32_t *resume_flags,
+                                int n_seqs, int n_tokens, int channels, int d_state, int n_groups, int dtype,
+                                long long grad_y_stride, long long x_stride, long long dt_stride, long long B_stride,
+                                long long C_stride, long long z_stride, void *grad_x, void *grad_dt, float *grad_A,
+                                void *grad_B, void *grad_C, float *grad_D, void *grad_z, float *grad_dt_bias,
+                                float *grad_initial_state, long long grad_x_stride, long long grad_dt_stride,
+                                long long grad_B_stride, long long grad_C_stride, long long grad_z_stride,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+size_t ssm_selective_scan_backward_workspace_bytes(int n_seqs, int n_tokens, int channels, int d_state, int n_groups);
+
+/*
+ * Short causal convolution: ssm_conv1d's operation on rows of any of the three
+ * types with strides (slices of a projection), with or without SiLU:
+ *     v[t,c] = bias[c] + sum_u weight[c,u] stream[t+u,c];  out = silu ? v sigmoid(v) : v
+ * where a sequence's stream is its slot's kernel_size - 1 inputs (zeros when fresh)
+ * followed by its tokens, and the slot afterwards holds the stream's last
+ * kernel_size - 1 entries.
+ *   x, out      [n_tokens][channels] of dtype;  weight [channels][kernel_size] fp32
+ *   bias        [channels] fp32 or NULL
+ *   conv_state  [n_seqs][channels][kernel_size-1] fp32, in/out (NULL allowed for kernel_size 1)
+ *   kernel_size 1 .. 8 (SSM_ERR_UNSUPPORTED above)
+ * out must not overlap an input.  Fastest with rows and slots of whole 8-byte (16-bit types) or
+ * 16-byte words and channels a multiple of 4.
+ */
+int ssm_causal_conv(const void *x, const float *weight, const float *bias, float *conv_state, void *out,
+                    const int32_t *seq_starts, const int32_t *seq_lens, const int32_t *resume_flags, int n_seqs,
+                    int n_tokens, int channels, int kernel_size, int silu, int dtype, long long x_stride,
+                    long long out_stride, void *stream);
+
+/*
+ * Gradients of ssm_causal_conv.  initial_state: what the slots held before the
+ * forward call, with resume_flags; both NULL where every sequence was fresh (one
+ * without the other is SSM_ERR_INVALID_ARG, but for kernel_size 1, which has no slots).
+ * grad_state: the gradient of the slots after the call, or NULL.
+ *   grad_x       [n_tokens][channels] of dtype (tokens owned by no sequence are not written)
+ *   grad_weight  [channels][kernel_size], grad_bias [channels] fp32 (with bias, else NULL), summed in a
+ *                fixed order; zeros when n_seqs is 0
+ *   grad_initial_state  as the slots, or NULL (zeros for fresh sequences)
+ * workspace: 256-byte aligned, ssm_causal_conv_backward_workspace_bytes(...).
+ */
+int ssm_causal_conv_backward(const void *grad_out, const float *grad_state, const void *x, const float *weight,
+                             const float *bias, const float *initial_state, const int32_t *seq_starts,
+                             const int32_t *seq_lens, const int32_t *resume_flags, int n_seqs, int n_tokens,
+                             int channels, int kernel_size, int silu, int dtype, long long grad_out_stride,
+                             long long x_stride, void *grad_x, float *grad_weight, float *grad_bias,
+                             float *grad_initial_state, long long grad_x_stride, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+size_t ssm_causal_conv_backward_workspace_bytes(int n_seqs, int n_tokens, int channels, int kernel_size);
+
+/*
+ * Softmax cross entropy of a projection onto a large vocabulary, without the
+ * logits in memory:
+ *     l[t,v] = sum_d hidden[t,d] weight[v,d];  lse[t] = log sum_v exp(l[t,v])
+ *     loss[t] = lse[t] - l[t,targets[t]]
+ * A row whose target is ignore_index has loss and lse 0, takes no work, and nothing that
+ * stands in it reaches a result.  A target outside [0, vocab) otherwise makes its row's loss
+ * NaN (and in the backward pass grad_hidden of the row and grad_weight).
+ *   hidden [rows][width], weight [vocab][width] of dtype: SSM_BF16 or SSM_F16
+ *          (SSM_ERR_UNSUPPORTED for SSM_F32, and for width above 65536)
+ *   targets [rows] int32, or int64 with targets_64;  loss, lse [rows] fp32
+ * Sums are fp32.  workspace: 256-byte aligned,
+ * ssm_linear_cross_entropy_workspace_bytes(weight, ..., 0): the rows that count, back to
+ * back, the parts of the sums, and the weights if their rows are not 16-byte
+ * aligned; scratch, not shared by calls that overlap on the GPU.
+ * The waits are bounded; where one gives up, results are NaN.
+ */
+int ssm_linear_cross_entropy(const void *hidden, const void *weight, const void *targets, int targets_64,
+                             long long ignore_index, float *loss, float *lse, int rows, int vocab, int width, int dtype,
+                             long long hidden_stride, long long weight_stride, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * Gradients of ssm_linear_cross_entropy's loss: with G[t,v] = (exp(l[t,v] - lse[t]) -
+ * [v = targets[t]]) grad_loss[t],
+ *     grad_hidden = G weight (zeros for ignored rows),   grad_weight = G^T hidden
+ * both in dtype.  lse as the forward call wrote it; its own gradient is not
+ * taken.  The logits are recomputed in pieces of the vocabulary; G of a piece is held
+ * in dtype relative to the largest |grad_loss| (fp16: times 2^15), so each of its terms is rounded
+ * to half a step before the products; the sums are fp32 and rounded once.
+ * grad_weight may be NULL (a frozen projection): it is not computed.
+ * workspace: as above with backward = 1: also one piece of G (256 MB, or for large calls 16 bytes an
+ * element of hidden) and, where there are several, grad_hidden in fp32.
+ */
+int ssm_linear_cross_entropy_backward(const float *grad_loss, const void *hidden, const void *weight,
+                                      const void *targets, int targets_64, long long ignore_index, const float *lse,
+                                      void *grad_hidden, void *grad_weight, int rows, int vocab, int width, int dtype,
+                                      long long hidden_stride, long long weight_stride, long long grad_hidden_stride,
+                                      long long grad_weight_stride, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+size_t ssm_linear_cross_entropy_workspace_bytes(const void *weight, int rows, int vocab, int width,
+                                                long long weight_stride, int backward);
+
 /* Text for a status code (static storage; never NULL). */
 const char *ssm_status_string(int status);
 

@@ -100,7 +100,20 @@ def load():
                     ("ssm_add_norm_backward_workspace_bytes", S, [_I] * 2),
                     ("ssm_quantize_rows", _I, [_P] * 3 + [_I] * 3 + [L] * 2 + [_P]),
                     ("ssm_int8_matmul", _I, [_P] * 6 + [_I] * 4 + [L] * 3 + [_P, S, _P]),
-                    ("ssm_int8_matmul_workspace_bytes", S, [_P] * 2 + [_I] * 3 + [L] * 2)):
+                    ("ssm_int8_matmul_workspace_bytes", S, [_P] * 2 + [_I] * 3 + [L] * 2),
+                    ("ssm_selective_scan", _I, [_P] * 9 + [_I] + [_P] * 4 + [_I] * 6 + [L] * 6 + [_P, _P, S, _P]),
+                    ("ssm_selective_scan_workspace_bytes", S, [_I] * 5),
+                    ("ssm_selective_scan_chunks", L, [_I] * 2),
+                    ("ssm_selective_scan_backward", _I, [_P] * 10 + [_I] + [_P] * 4 + [_I] * 6 + [L] * 6 + [_P] * 9 +
+                     [L] * 5 + [_P, S, _P]),
+                    ("ssm_selective_scan_backward_workspace_bytes", S, [_I] * 5),
+                    ("ssm_causal_conv", _I, [_P] * 8 + [_I] * 6 + [L] * 2 + [_P]),
+                    ("ssm_causal_conv_backward", _I, [_P] * 9 + [_I] * 6 + [L] * 2 + [_P] * 4 + [L, _P, S, _P]),
+                    ("ssm_causal_conv_backward_workspace_bytes", S, [_I] * 4),
+                    ("ssm_linear_cross_entropy", _I, [_P] * 3 + [_I, L] + [_P] * 2 + [_I] * 4 + [L] * 2 + [_P, S, _P]),
+                    ("ssm_linear_cross_entropy_backward", _I, [_P] * 4 + [_I, L] + [_P] * 3 + [_I] * 4 + [L] * 4 +
+                     [_P, S, _P]),
+                    ("ssm_linear_cross_entropy_workspace_bytes", S, [_P] + [_I] * 3 + [L, _I])):
                 getattr(lib, name).restype = res
                 getattr(lib, name).argtypes = args
             lib.ssm_status_string.restype = ctypes.c_char_p

@@ -1,0 +1,639 @@
+// Softmax cross entropy of a projection onto a large vocabulary, and its gradients,
+// without the logits in memory (sm_103a):
+//
+//   l[t,v] = sum_d h[t,d] w[v,d],  lse[t] = log sum_v exp l[t,v],  loss[t] = lse[t] - l[t,target[t]]
+//   G[t,v] = (exp(l[t,v] - lse[t]) - [v = target[t]]) grad_loss[t],  grad h = G w,  grad w = G^T h
+//
+// Tokens whose target is ignored are left out before anything is multiplied: a first pass counts
+// them, a second one writes the hidden rows of the others back to back (zeros up to a whole
+// tile), so ignored tokens cost nothing and whatever stands in their rows reaches no sum.  How
+// many remain is known on the device only; the products take it from there.
+//
+// Forward: a product (pair_gemm.cuh) whose epilogue keeps, for each row and 128 columns, the
+// largest logit and the sum of the exponentials above it, and the target's logit; a small kernel
+// joins them.  Backward, in pieces of the vocabulary: the product again, with G of the piece as
+// its output in the inputs' 16-bit type; then grad h += G w and grad w = G^T h of the
+// piece, whose operands the tensor cores read in either orientation.  Operations bound it: 2 T V D
+// forward, 2 T V D again and 4 T V D backward.
+//
+// Roundings: G is rounded to 16 bits for its products (half a step of each term; the sums
+// are fp32, and what is written is rounded once).  It is held relative to the largest |grad_loss|,
+// so that a mean's 1 / T is no rounding, and for fp16 2^15 times that, so that probabilities down to
+// 2^-29 keep all their bits; the sums get the factors back in fp32.
+#include <atomic>
+
+#include "pair_gemm.cuh"
+
+namespace ssm {
+
+namespace {
+
+constexpr int kCountRows = 1024;              // rows of a block of the counting kernel
+constexpr int kPackRows = 16;                 // rows of a block of the packing kernel
+constexpr int kGroupM = 16;                   // row tiles that share the vocabulary's rows in L2
+
+struct LossArgs {
+    const void *h, *w, *target, *grad_loss_lse;
+    const float *grad_loss, *lse_in;
+    float *loss, *lse;
+    void *grad_h, *grad_w;
+    int T, V, D, wide;                        // wide: 64-bit targets
+    long long sh, sw, sgh, sgw, ignore;
+    int dp;                                   // packed row length
+    // workspace
+    int *counts;                              // [blocks + 1] kept rows of each kCountRows
+    float *tops;                              // [blocks] largest |grad_loss| of them
+    int *index;                               // [T] row of each kept one
+    int *label;                               // [T rounded up to a tile] its target, -1 past the end
+    float *scale;                             // its grad_loss relative to the largest, times the type's factor
+    float *row_lse;
+    float *label_logit;                       // [T]
+    float2 *part;                             // [2 vocabulary tiles][T rounded up]
+    void *hp, *wp, *G;
+    float *acc;                               // [T rounded up][D] fp32: grad h of the pieces so far
+    int t_pad, blocks;                        // T rounded up to a tile
+    float factor;                             // 2^15 for fp16, else 1
+    int v0, vp, first_piece, last_piece;      // a piece of the vocabulary
+    int fail_waits;
+};
+
+__device__ __forceinline__ long long target_of(const LossArgs &a, int t)
+{
+    return a.wide ? static_cast<const long long *>(a.target)[t] : (long long)static_cast<const int32_t *>(a.target)[t];
+}
+
+// Kept rows, and the largest |grad_loss| of them (a NaN counts as none: its row is NaN by itself).
+__global__ void __launch_bounds__(256)
+loss_count_kernel(const LossArgs a)
+{
+    griddep_entry();
+    __shared__ int ns[8];
+    __shared__ float ms[8];
+    const int tid = threadIdx.x, t0 = blockIdx.x * kCountRows;
+    int n = 0;
+    float m = 0.f;
+    for (int t = t0 + tid; t < min(a.T, t0 + kCountRows); t += 256)
+        if (target_of(a, t) != a.ignore) {
+            ++n;
+            if (a.grad_loss)
+                m = fmaxf(m, fabsf(a.grad_loss[t]));
+        }
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2) {
+        n += __shfl_xor_sync(kFullMask, n, off);
+        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, off));
+    }
+    if ((tid & 31) == 0) {
+        ns[tid >> 5] = n;
+        ms[tid >> 5] = m;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 1; i < 8; ++i) {
+            n += ns[i];
+            m = fmaxf(m, ms[i]);
+        }
+        a.counts[blockIdx.x] = n;
+        a.tops[blockIdx.x] = m;
+    }
+}
+
+// Sum of the counts of the blocks before `block` (all threads of a warp), and the largest top of all.
+__device__ __forceinline__ int counted(const LossArgs &a, int block)
+{
+    int n = 0;
+    for (int i = threadIdx.x & 31; i < block; i += 32)
+        n += a.counts[i];
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2)
+        n += __shfl_xor_sync(kFullMask, n, off);
+    return n;
+}
+
+__device__ __forceinline__ float largest(const LossArgs &a)
+{
+    float m = 0.f;
+    for (int i = threadIdx.x & 31; i < a.blocks; i += 32)
+        m = fmaxf(m, a.tops[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2)
+        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, off));
+    return m;
+}
+
+// Kept rows back to back, zeros after them up to a whole tile; outputs of ignored rows.
+template <class T>
+__global__ void __launch_bounds__(256)
+loss_pack_kernel(const LossArgs a)
+{
+    griddep_entry();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = blockIdx.x * kPackRows;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.h) | (uintptr_t)(a.sh * 2)) & 15) == 0;
+    T *hp = static_cast<T *>(a.hp);
+    const float top = a.grad_loss ? largest(a) : 0.f;
+    int before = 0, at_block = -1;
+    for (int r = r0 + warp; r < r0 + kPackRows; r += 8) {
+        const bool real = r < a.T;
+        const long long label = real ? target_of(a, r) : 0;
+        if (real && label == a.ignore) {
+            if (lane == 0 && a.loss)
+                a.loss[r] = a.lse[r] = 0.f;
+            if (a.grad_h)
+                for (int d = lane; d < a.D; d += 32)
+                    static_cast<T *>(a.grad_h)[r * a.sgh + d] = from_float<T>(0.f);
+            continue;
+        }
+        // kept rows before this one; past the last row: rows of zeros behind all kept ones
+        const int block = real ? r / kCountRows : a.blocks;
+        if (block != at_block) {
+            before = counted(a, block);
+            at_block = block;
+        }
+        int at = before;
+        if (real) {
+            int n = 0;
+            for (int t = block * kCountRows + lane; t < r; t += 32)
+                n += target_of(a, t) != a.ignore ? 1 : 0;
+#pragma unroll
+            for (int off = 16; off >= 1; off /= 2)
+                n += __shfl_xor_sync(kFullMask, n, off);
+            at += n;
+        } else {
+            at += r - a.T;
+            if (at >= (before + pair::kTileM - 1) / pair::kTileM * pair::kTileM)
+                continue;
+        }
+        const T *src = static_cast<const T *>(a.h) + (real ? r * a.sh : 0);
+        T *dst = hp + (long long)at * a.dp;
+        for (int d = lane * 8; d < a.dp; d += 256) {
+            Vec<T, 8> v;
+            if (real && vec && d + 8 <= a.D) {
+                v = load_vec<T, 8>(src + d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v.v[i] = real && d + i < a.D ? src[d + i] : from_float<T>(0.f);
+            }
+            store_vec<T, 8>(dst + d, v);
+        }
+        if (lane == 0) {
+            const bool in = label >= 0 && label < a.V;
+            a.label[at] = real && in ? (int)label : -1;
+            if (real)
+                a.index[at] = r;
+            if (a.grad_loss) {
+                // a target outside the vocabulary has no loss: NaN
+                const float g = real ? a.grad_loss[r] : 0.f;
+                a.scale[at] = real && !in ? __int_as_float(0x7fc00000) : g == 0.f ? 0.f : g / top * a.factor;
+                a.row_lse[at] = real ? a.lse_in[r] : 0.f;
+            }
+        }
+    }
+}
+
+// Weight rows that TMA cannot describe, as rows of dp values.
+template <class T>
+__global__ void __launch_bounds__(256)
+loss_pack_weight_kernel(const LossArgs a)
+{
+    griddep_entry();
+    const int per = a.dp / 8;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, r = i / per;
+    const int d = (int)(i - r * per) * 8;
+    if (r >= a.V)
+        return;
+    const T *src = static_cast<const T *>(a.w) + r * a.sw + d;
+    Vec<T, 8> v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v.v[e] = d + e < a.D ? src[e] : from_float<T>(0.f);
+    store_vec<T, 8>(static_cast<T *>(a.wp) + r * a.dp + d, v);
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Largest logit (times log2 e) and the sum of the exponentials above it, of 128 columns of a row.
+struct StatsEpilogue {
+    const LossArgs &a;
+    int rows;
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    {
+        const int label = row < rows ? a.label[row] : -1;
+        float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < pair::kHalf; j += 32) {
+            float v[32];
+            pair::columns(v, at, j, ok, any);
+            const int c = col + j;
+            if (label >= c && label < c + 32) {
+                float own = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    own = label == c + i ? v[i] : own;
+                a.label_logit[row] = own;
+            }
+            if (c + 32 > a.V) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = c + i < a.V ? v[i] : -INFINITY;
+            }
+            float top = v[0];                               // (a maximum drops a NaN; its exponential keeps it)
+#pragma unroll
+            for (int i = 1; i < 32; ++i)
+                top = fmaxf(top, v[i]);
+            top = fmaxf(m, top * kLog2e);
+            if (top == -INFINITY) {                         // columns past the last, logits of -inf, or NaN alone
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    s = v[i] != v[i] ? v[i] : s;
+                continue;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                sum += ex2(fmaf(v[i], kLog2e, -top));
+            s = fmaf(s, ex2(m - top), sum);
+            m = top;
+        }
+        if (row < rows)
+            a.part[(long long)(col / pair::kHalf) * a.t_pad + row] = make_float2(ok ? m : __int_as_float(0x7fc00000), s);
+    }
+};
+
+template <bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+loss_stats_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, const __grid_constant__ CUtensorMap wmap)
+{
+    griddep_entry();
+    const int rows = counted(a, a.blocks);
+    pair::run<BF16, false, false>(pair::Shape{rows, a.V, a.D}, kGroupM, hmap, wmap, a.fail_waits, StatsEpilogue{a, rows});
+}
+
+// G of a piece: rows up to a whole tile, zeros past the rows and past the vocabulary.
+template <class T>
+struct GradEpilogue {
+    const LossArgs &a;
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    {
+        const int label = a.label[row] - a.v0;
+        const float scale = a.scale[row], lse = a.row_lse[row] * kLog2e;
+        T *out = static_cast<T *>(a.G) + (long long)row * a.vp + col;
+        const int left = a.V - a.v0;                        // of the piece's columns that exist
+#pragma unroll 1
+        for (int j = 0; j < pair::kHalf; j += 32) {
+            float v[32];
+            pair::columns(v, at, j, ok, any);
+            const int c = col + j;
+            Vec<T, 8> o[4];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float p = ex2(fmaf(v[i], kLog2e, -lse)) - (label == c + i ? 1.f : 0.f);
+                o[i / 8].v[i % 8] = from_float<T>(c + i < left ? p * scale : 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                store_vec<T, 8>(out + j + 8 * i, o[i]);
+        }
+    }
+};
+
+template <class T, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+loss_grad_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, const __grid_constant__ CUtensorMap wmap)
+{
+    griddep_entry();
+    const int rows = counted(a, a.blocks);
+    pair::run<BF16, false, false>(pair::Shape{rows, a.vp, a.D}, kGroupM, hmap, wmap, a.fail_waits, GradEpilogue<T>{a});
+}
+
+// grad h: added up over the pieces in fp32, the last one writes the rows where they belong.
+template <class T>
+struct HiddenEpilogue {
+    const LossArgs &a;
+    int rows;
+    float back;
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    {
+        const bool in = row < rows;
+        float *acc = a.acc + (long long)row * a.dp + col;
+        T *out = in && a.last_piece ? static_cast<T *>(a.grad_h) + a.index[row] * a.sgh + col : nullptr;
+#pragma unroll 1
+        for (int j = 0; j < pair::kHalf; j += 32) {
+            float v[32];
+            pair::columns(v, at, j, ok, any);
+            if (!in || col + j >= a.D)
+                continue;
+            // rows of acc are dp long: whole groups of 8
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                if (col + j + i >= a.dp)
+                    break;
+                float4 *p = reinterpret_cast<float4 *>(acc + j + i);
+                if (!a.first_piece) {
+                    const float4 q = *p;
+                    v[i] += q.x; v[i + 1] += q.y; v[i + 2] += q.z; v[i + 3] += q.w;
+                }
+                if (!a.last_piece)
+                    *p = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+            if (a.last_piece)
+                write_row<T>(out + j, v, a.D - col - j, back);
+        }
+    }
+    template <class U>
+    static __device__ __forceinline__ void write_row(U *out, const float (&v)[32], int left, float back)
+    {
+        if (left >= 32 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                Vec<U, 8> o;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    o.v[k] = from_float<U>(v[i + k] * back);
+                store_vec<U, 8>(out + i, o);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < left)
+                    out[i] = from_float<U>(v[i] * back);
+        }
+    }
+};
+
+template <class T, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+loss_hidden_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap wmap)
+{
+    griddep_entry();
+    const int rows = counted(a, a.blocks);
+    const HiddenEpilogue<T> epi{a, rows, largest(a) / a.factor};
+    pair::run<BF16, false, true>(pair::Shape{rows, a.D, min(a.vp, a.V - a.v0)}, kGroupM, gmap, wmap, a.fail_waits, epi);
+}
+
+template <class T>
+struct WeightEpilogue {
+    const LossArgs &a;
+    float back;
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    {
+        const int v = a.v0 + row;
+        const bool in = v < a.V && row < a.vp;
+        T *out = static_cast<T *>(a.grad_w) + (in ? v * a.sgw : 0) + col;
+#pragma unroll 1
+        for (int j = 0; j < pair::kHalf; j += 32) {
+            float x[32];
+            pair::columns(x, at, j, ok, any);
+            if (in && col + j < a.D)
+                HiddenEpilogue<T>::write_row(out + j, x, a.D - col - j, back);
+        }
+    }
+};
+
+template <class T, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+loss_weight_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap hmap)
+{
+    griddep_entry();
+    const int rows = counted(a, a.blocks);
+    const WeightEpilogue<T> epi{a, largest(a) / a.factor};
+    pair::run<BF16, true, true>(pair::Shape{min(a.vp, a.V - a.v0), a.D, rows}, kGroupM, gmap, hmap, a.fail_waits, epi);
+}
+
+// lse and loss of every kept row from its parts: 32 rows a block, the parts over 8 lanes of threads.
+__global__ void __launch_bounds__(256)
+loss_join_kernel(const LossArgs a, int parts)
+{
+    griddep_entry();
+    __shared__ float2 sh[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
+    const int rows = counted(a, a.blocks);
+    if (blockIdx.x * 32 >= rows)
+        return;
+    float m = -INFINITY, s = 0.f;
+    bool bad = false;
+    if (row < rows)
+        for (int p = warp; p < parts; p += 8) {
+            const float2 q = a.part[(long long)p * a.t_pad + row];
+            bad = bad || q.x != q.x || q.y != q.y;
+            const float top = fmaxf(m, q.x);
+            if (top == -INFINITY)
+                continue;
+            s = s * ex2(m - top) + q.y * ex2(q.x - top);
+            m = top;
+        }
+    sh[warp][lane] = make_float2(bad ? __int_as_float(0x7fc00000) : m, s);
+    __syncthreads();
+    if (warp != 0 || row >= rows)
+        return;
+    for (int w = 1; w < 8; ++w) {
+        const float2 q = sh[w][lane];
+        bad = bad || q.x != q.x;
+        const float top = fmaxf(m, q.x);
+        if (top == -INFINITY)
+            continue;
+        s = s * ex2(m - top) + q.y * ex2(q.x - top);
+        m = top;
+    }
+    // log s: s is at least 1 but for the approximate exponentials
+    const float lse = bad ? __int_as_float(0x7fc00000) : fmaf(m, kLn2, logf(s));
+    const int t = a.index[row], label = a.label[row];
+    a.lse[t] = lse;
+    a.loss[t] = label < 0 ? __int_as_float(0x7fc00000) : lse - a.label_logit[row];
+}
+
+// ---- host ----
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+bool encode(CUtensorMap *map, const void *p, bool bf16, long long width, long long rows, long long stride, int box_rows)
+{
+    const auto fn = tensor_map_encoder();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(p), dims,
+              strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What lies where in the workspace.
+struct Plan {
+    int t_pad, blocks, dp, pieces, vp;
+    bool pack_w;
+    size_t counts, tops, index, label, scale, row_lse, logit, part, hp, wp, G, acc, total;
+};
+
+Plan plan(const void *w, int T, int V, int D, long long sw, bool backward)
+{
+    Plan p;
+    p.t_pad = (T + pair::kTileM - 1) / pair::kTileM * pair::kTileM;
+    p.blocks = (T + kCountRows - 1) / kCountRows;
+    p.dp = (D + 7) / 8 * 8;
+    p.pack_w = ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)(sw * 2)) & 15) != 0;
+    // G of a piece: up to 256 MB, or four times the hidden rows' fp32 sums (which every piece reads and writes)
+    const size_t room = (size_t)16 * p.t_pad * p.dp > ((size_t)256 << 20) ? (size_t)16 * p.t_pad * p.dp : (size_t)256 << 20;
+    const long long fits = (long long)(room / ((size_t)p.t_pad * 2) / pair::kTileN * pair::kTileN);
+    const long long all = ((long long)V + pair::kTileN - 1) / pair::kTileN * pair::kTileN;
+    const long long most = fits < pair::kTileN ? pair::kTileN : fits;
+    p.pieces = (int)((all + most - 1) / most);
+    p.vp = (int)((all / pair::kTileN + p.pieces - 1) / p.pieces * pair::kTileN);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t v = at;
+        at += up256(bytes);
+        return v;
+    };
+    p.counts = take((size_t)p.blocks * 4);
+    p.tops = take((size_t)p.blocks * 4);
+    p.index = take((size_t)T * 4);
+    p.label = take((size_t)p.t_pad * 4);
+    p.hp = take((size_t)p.t_pad * p.dp * 2);
+    p.wp = p.pack_w ? take((size_t)V * p.dp * 2) : at;
+    if (backward) {
+        p.scale = take((size_t)p.t_pad * 4);
+        p.row_lse = take((size_t)p.t_pad * 4);
+        p.G = take((size_t)p.t_pad * p.vp * 2);
+        p.acc = p.pieces > 1 ? take((size_t)p.t_pad * p.dp * 4) : at;
+        p.logit = p.part = 0;
+    } else {
+        p.logit = take((size_t)T * 4);
+        p.part = take((size_t)(all / pair::kHalf) * p.t_pad * sizeof(float2));
+        p.scale = p.row_lse = p.G = p.acc = 0;
+    }
+    p.total = at;
+    return p;
+}
+
+// Pairs of SMs that run at once (the pairs' tiles are dealt out among them).
+template <class K>
+int resident_pairs(K kernel)
+{
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return kSms / 2;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kSms);
+        cfg.blockDim = dim3(pair::kThreads);
+        cfg.dynamicSmemBytes = pair::Smem::kTotal;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
+            n = kSms / 2;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <class K>
+cudaError_t launch_pairs(K kernel, long long tiles, cudaStream_t st, const LossArgs &a, const CUtensorMap &x, const CUtensorMap &y)
+{
+    const cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), pair::Smem::kTotal);
+    if (e != cudaSuccess)
+        return e;
+    const long long pairs = resident_pairs(kernel);
+    return launch_pdl(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(pair::kThreads),
+                      pair::Smem::kTotal, st, a, x, y);
+}
+
+long long tiles_of(long long m, long long n)
+{
+    return ((m + pair::kTileM - 1) / pair::kTileM) * ((n + pair::kTileN - 1) / pair::kTileN);
+}
+
+template <class T, bool BF16>
+cudaError_t launch_loss(LossArgs a, const Plan &p, bool backward, cudaStream_t st)
+{
+    cudaError_t e = launch_pdl(loss_count_kernel, dim3(p.blocks), dim3(256), 0, st, a);
+    if (e == cudaSuccess)
+        e = launch_pdl(loss_pack_kernel<T>, dim3((a.T + pair::kTileM + kPackRows - 1) / kPackRows), dim3(256), 0, st, a);
+    if (e == cudaSuccess && p.pack_w)
+        e = launch_pdl(loss_pack_weight_kernel<T>, dim3((unsigned)(((long long)a.V * (a.dp / 8) + 255) / 256)), dim3(256), 0, st, a);
+    if (e != cudaSuccess)
+        return e;
+    const void *w = p.pack_w ? a.wp : a.w;
+    const long long sw = p.pack_w ? a.dp : a.sw;
+    CUtensorMap hmap, wmap;
+    if (!encode(&hmap, a.hp, BF16, a.dp, p.t_pad, a.dp, 128) || !encode(&wmap, w, BF16, a.D, a.V, sw, 128))
+        return cudaErrorInvalidValue;
+    if (!backward) {
+        e = launch_pairs(loss_stats_kernel<BF16>, tiles_of(a.T, a.V), st, a, hmap, wmap);
+        if (e != cudaSuccess)
+            return e;
+        const int parts = (a.V + pair::kHalf - 1) / pair::kHalf;
+        return launch_pdl(loss_join_kernel, dim3((a.T + 31) / 32), dim3(256), 0, st, a, parts);
+    }
+    CUtensorMap hmap_n, gmap, gmap_m;
+    if (!encode(&hmap_n, a.hp, BF16, a.dp, p.t_pad, a.dp, 64) || !encode(&gmap, a.G, BF16, p.vp, p.t_pad, p.vp, 128) ||
+        !encode(&gmap_m, a.G, BF16, p.vp, p.t_pad, p.vp, 64))
+        return cudaErrorInvalidValue;
+    for (int i = 0; i < p.pieces; ++i) {
+        a.v0 = i * p.vp;
+        a.vp = p.vp;
+        a.first_piece = i == 0;
+        a.last_piece = i == p.pieces - 1;
+        const long long rows = (long long)a.V - a.v0 < a.vp ? a.V - a.v0 : a.vp;       // of the piece
+        const unsigned char *wv = static_cast<const unsigned char *>(w) + (size_t)a.v0 * sw * 2;
+        CUtensorMap wpiece, wpiece_n;
+        if (!encode(&wpiece, wv, BF16, a.D, rows, sw, 128) || !encode(&wpiece_n, wv, BF16, a.D, rows, sw, 64))
+            return cudaErrorInvalidValue;
+        e = launch_pairs(loss_grad_kernel<T, BF16>, tiles_of(a.T, a.vp), st, a, hmap, wpiece);
+        if (e == cudaSuccess)
+            e = launch_pairs(loss_hidden_kernel<T, BF16>, tiles_of(a.T, a.D), st, a, gmap, wpiece_n);
+        if (e == cudaSuccess && a.grad_w)
+            e = launch_pairs(loss_weight_kernel<T, BF16>, tiles_of(rows, a.D), st, a, gmap_m, hmap_n);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t cross_entropy_workspace_bytes(const void *w, int T, int V, int D, long long sw, bool backward)
+{
+    return plan(w, T, V, D, sw, backward).total;
+}
+
+cudaError_t launch_cross_entropy(const CrossEntropy &c, void *workspace, bool backward, cudaStream_t st)
+{
+    const Plan p = plan(c.w, c.T, c.V, c.D, c.sw, backward);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    LossArgs a{};
+    a.h = c.h; a.w = c.w; a.target = c.target; a.grad_loss = c.grad_loss; a.lse_in = c.lse_in;
+    a.loss = c.loss; a.lse = c.lse; a.grad_h = c.grad_h; a.grad_w = c.grad_w;
+    a.T = c.T; a.V = c.V; a.D = c.D; a.wide = c.wide; a.ignore = c.ignore;
+    a.sh = c.sh; a.sw = c.sw; a.sgh = c.sgh; a.sgw = c.sgw;
+    a.dp = p.dp; a.t_pad = p.t_pad; a.blocks = p.blocks;
+    a.counts = reinterpret_cast<int *>(ws + p.counts);
+    a.tops = reinterpret_cast<float *>(ws + p.tops);
+    a.index = reinterpret_cast<int *>(ws + p.index);
+    a.label = reinterpret_cast<int *>(ws + p.label);
+    a.scale = reinterpret_cast<float *>(ws + p.scale);
+    a.row_lse = reinterpret_cast<float *>(ws + p.row_lse);
+    a.label_logit = reinterpret_cast<float *>(ws + p.logit);
+    a.part = reinterpret_cast<float2 *>(ws + p.part);
+    a.hp = ws + p.hp; a.wp = ws + p.wp; a.G = ws + p.G;
+    a.acc = reinterpret_cast<float *>(ws + p.acc);
+    a.factor = c.dtype == kF16 ? 32768.f : 1.f;
+    a.fail_waits = debug_fail_waits() ? 1 : 0;
+    return c.dtype == kBF16 ? launch_loss<__nv_bfloat16, true>(a, p, backward, st) : launch_loss<__half, false>(a, p, backward, st);
+}
+
+}  // namespace ssm

@@ -52,6 +52,8 @@ template <>
 struct WordsOf<8> { using type = uint2; };
 template <>
 struct WordsOf<4> { using type = uint32_t; };
+template <>
+struct WordsOf<2> { using type = uint16_t; };
 
 template <class T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec(const T *p)
@@ -90,6 +92,37 @@ int add_norm_parts(int rows, int D);      // rows of the gradient's workspace ([
 cudaError_t launch_add_norm_backward(const void *gy, const void *h, const void *gh, const float *w, float eps,
                                      void *gin, float *gw, float *part, int rows, int D, int dy, int dr,
                                      long long sgy, long long sh, long long sgh, long long sgi, cudaStream_t st);
+
+// causal_conv.cu
+struct CausalConv {
+    const void *x;
+    const float *w, *bias;
+    float *state;
+    void *out;
+    const int32_t *starts, *lens, *resume;
+    int n_seqs, n_tokens, channels, K, silu, dtype;
+    long long sx, so;
+    const void *grad_out;
+    const float *state0, *grad_state;
+    void *grad_x;
+    float *grad_w, *grad_bias, *grad_state0, *part;
+    long long sgo, sgx;
+};
+size_t causal_conv_backward_workspace_bytes(int n_seqs, int n_tokens, int channels, int K);
+long long causal_conv_blocks(int n_seqs, int n_tokens, int channels);
+cudaError_t launch_causal_conv(const CausalConv &c, bool backward, cudaStream_t st);
+
+// cross_entropy.cu
+struct CrossEntropy {
+    const void *h, *w, *target;
+    const float *grad_loss, *lse_in;
+    float *loss, *lse;
+    void *grad_h, *grad_w;
+    int T, V, D, wide, dtype;
+    long long sh, sw, sgh, sgw, ignore;
+};
+size_t cross_entropy_workspace_bytes(const void *w, int T, int V, int D, long long sw, bool backward);
+cudaError_t launch_cross_entropy(const CrossEntropy &c, void *workspace, bool backward, cudaStream_t st);
 
 // int8_matmul.cu
 size_t int8_matmul_workspace_bytes(const void *x, const void *w, int M, int N, int K, long long sx, long long sw);

@@ -1,0 +1,328 @@
+// Shared parts of the selective scan with a decay for each channel and state
+// (selective_scan.cu, selective_scan_backward.cu).
+//
+//   v = dt + dt_bias, step = v, or softplus(v) = v > 20 ? v : log1p(exp(v))
+//   h[c,n] <- exp(step[c] A[c,n]) h[c,n] + step[c] x[c] B[g,n]
+//   p[c] = sum_n h[c,n] C[g,n] + D[c] x[c],   y[c] = p[c] z[c] sigmoid(z[c])
+//
+// Every state has its own decay, so there is no matrix form: the work is one
+// exponential and about five multiplications an element (token, channel, state).
+// A warp owns a tile of channels with all their states: LN lanes share CH channels
+// and each holds NP of their states, so a lane has CH x NP independent recurrences
+// in registers.  What a lane reads from shared memory for a token (CH steps and inputs,
+// NP values of B and of C) serves all of them: with single channels a lane
+// the reads of B and C cost more than the arithmetic.  Two states go into one packed fp32
+// instruction; the exponential is the hardware's 2^x of the rounded product
+// step * (A log2(e)), within 2 ulp and 2^-24 of its argument.
+//
+// Time: a unit is a sequence, or one of its segments of `seg` tokens where sequences
+// and channels alone do not fill the device.  Then a pass before composes each
+// segment's state from zero, and a small one walks the segments.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace ssm {
+
+constexpr int kSelChunk = 16;             // tokens a warp stages at a time; a saved state each in training
+constexpr int kSelWarps = 4;              // warps of a block: neighbouring channel tiles of one unit
+constexpr int kSelMaxState = 128;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct SelArgs {
+    float *state;
+    const void *x, *dt, *z, *B, *C;
+    const float *A, *D, *bias;
+    void *y;
+    const int32_t *starts, *lens, *resume;
+    int n_seqs, n_tokens, channels, N, groups, softplus;
+    long long sx, sdt, sz, sB, sC, sy;
+    float *chunk_states;
+    int seg;                              // tokens of a segment, 0: units are whole sequences
+    const int2 *units;                    // (sequence, segment)
+    const int *first;                     // [n_seqs + 1]: a sequence's first unit; the last entry: how many there are
+    float *unit_state, *unit_step;        // [units][channels][N], [units][channels]
+    // backward
+    const void *grad_y;
+    const float *grad_state;
+    long long sgy, sgx, sgdt, sgz, sgB, sgC;
+    void *grad_x, *grad_dt, *grad_z, *grad_B, *grad_C;
+    float *grad_A, *grad_D, *grad_bias, *grad_state0;
+    float *part_A, *part_D, *part_bias;   // [units][channels][N], [units][channels] twice
+    float *part_B, *part_C;               // [channel blocks][n_tokens][groups N]
+    int max_units, cblocks;
+};
+
+// Row of chunk_states for chunk j of a sequence that starts at token t0: the first chunk's by
+// the sequence, the others' by their position.  n_seqs + n_tokens / 16 + 1 rows.
+__host__ __device__ __forceinline__ long long sel_chunk_row(int n_seqs, int seq, long long t0, int j)
+{
+    return j == 0 ? seq : n_seqs + t0 / kSelChunk + j;
+}
+
+// A sequence's token range; one that is not inside the packed rows counts as empty.
+__device__ __forceinline__ int sel_seq_len(const SelArgs &a, int seq, long long &t0)
+{
+    t0 = a.starts[seq];
+    const long long len = a.lens[seq];
+    if (t0 >= 0 && len > 0 && t0 + len <= a.n_tokens)
+        return (int)len;
+    t0 = 0;
+    return 0;
+}
+
+// A unit: tokens [begin, end) of sequence seq, whose first token is t0.
+struct SelUnit {
+    int seq, k, begin, end, len;
+    long long t0;
+    bool last;                            // of its sequence
+};
+
+__device__ __forceinline__ bool sel_unit(const SelArgs &a, int u, SelUnit &s)
+{
+    s.seq = u;
+    s.k = 0;
+    if (a.seg) {
+        if (u >= a.first[a.n_seqs])
+            return false;
+        const int2 v = a.units[u];
+        s.seq = v.x;
+        s.k = v.y;
+    }
+    s.len = sel_seq_len(a, s.seq, s.t0);
+    s.begin = a.seg * s.k;
+    s.end = a.seg ? min(s.len, s.begin + a.seg) : s.len;
+    s.last = s.end == s.len;
+    return true;
+}
+
+// Channel tiles: WC channels of one group; a block has kSelWarps neighbours of one group.
+struct SelTile {
+    int c0, c1, g;                        // channels [c0, c1), at most WC of them
+};
+
+__host__ __device__ __forceinline__ int sel_group_blocks(int channels, int groups, int wc)
+{
+    return (channels / groups + wc * kSelWarps - 1) / (wc * kSelWarps);
+}
+
+template <int WC>
+__device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int cblock, int warp)
+{
+    const int per = sel_group_blocks(a.channels, a.groups, WC), cg = a.channels / a.groups;
+    SelTile t;
+    t.g = cblock / per;
+    const int in_group = ((cblock - t.g * per) * kSelWarps + warp) * WC;
+    t.c0 = t.g * cg + min(in_group, cg);
+    t.c1 = t.g * cg + min(in_group + WC, cg);
+    return t;
+}
+
+// ---- arithmetic ----
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return d;
+}
+
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float ex2(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+
+__device__ __forceinline__ float rcp(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// softplus with its derivative's e = exp(-|v|).  log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3:
+// the series 2 s (1 + s^2/3 + s^4/5 + ...) to s^14 leaves (1/9)^8 / 17 < 2^-29 of it, and keeps the
+// relative accuracy of small e, which a logarithm of 1 + e would lose.
+__device__ __forceinline__ float softplus_of(float v, float &e)
+{
+    e = ex2(-fabsf(v) * kLog2e);
+    const float s = e * rcp(2.f + e), q = s * s;
+    float r = fmaf(q, 1.f / 15, 1.f / 13);
+    r = fmaf(q, r, 1.f / 11);
+    r = fmaf(q, r, 1.f / 9);
+    r = fmaf(q, r, 1.f / 7);
+    r = fmaf(q, r, 1.f / 5);
+    r = fmaf(q, r, 1.f / 3);
+    r = 2.f * fmaf(s * q, r, s);
+    return v > 20.f ? v : fmaxf(v, 0.f) + r;
+}
+
+// The discretised step and its derivative by dt.
+__device__ __forceinline__ float sel_step(float v, bool softplus, float &slope)
+{
+    slope = 1.f;
+    if (!softplus)
+        return v;
+    float e;
+    const float s = softplus_of(v, e);
+    slope = v > 20.f ? 1.f : (v >= 0.f ? 1.f : e) * rcp(1.f + e);
+    return s;
+}
+
+// sigmoid(v); v times it is 0 times v where exp(-v) overflows (v below -88).
+__device__ __forceinline__ float sigmoid_of(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
+
+// CNT sums over LANES lanes STRIDE apart, each of the lanes ending with max(1, CNT / LANES) of
+// them in v[0..]: as long as there are two values to a lane, a lane keeps half and sends
+// the other.  `at`: which value v[0] is; `mine`: whether this lane is the first of
+// those that hold the same.
+template <int CNT, int LANES, int STRIDE>
+__device__ __forceinline__ void lanes_sum(float (&v)[CNT], int lane, int &at, bool &mine)
+{
+    const int l = lane / STRIDE;
+    at = 0;
+    mine = true;
+    int width = CNT;
+#pragma unroll
+    for (int off = LANES / 2; off >= 1; off /= 2) {
+        const bool up = (l & off) != 0;
+        if (width > 1) {
+            width /= 2;
+#pragma unroll
+            for (int m = 0; m < CNT / 2; ++m)
+                if (m < width) {
+                    const float keep = up ? v[m + width] : v[m], send = up ? v[m] : v[m + width];
+                    v[m] = keep + __shfl_xor_sync(kFullMask, send, off * STRIDE);
+                }
+            at += up ? width : 0;
+        } else {
+            v[0] += __shfl_xor_sync(kFullMask, v[0], off * STRIDE);
+            mine = mine && !up;
+        }
+    }
+}
+
+// CH consecutive floats of shared memory.
+template <int CH>
+__device__ __forceinline__ void load_floats(float (&v)[CH], const float *p)
+{
+    if constexpr (CH % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < CH; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + i);
+            v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+        }
+    } else if constexpr (CH % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < CH; i += 2) {
+            const float2 q = *reinterpret_cast<const float2 *>(p + i);
+            v[i] = q.x; v[i + 1] = q.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            v[i] = p[i];
+    }
+}
+
+template <int NP>
+__device__ __forceinline__ void load_pairs(float2 (&v)[NP / 2], const float *p)
+{
+#pragma unroll
+    for (int i = 0; i < NP / 4; ++i) {
+        const float4 q = *reinterpret_cast<const float4 *>(p + 4 * i);
+        v[2 * i] = make_float2(q.x, q.y);
+        v[2 * i + 1] = make_float2(q.z, q.w);
+    }
+}
+
+// A lane's NP states of one channel out of a row of N (and back): four at a time where rows allow.
+template <int NP>
+__device__ __forceinline__ void read_states(float2 (&v)[NP / 2], const float *row, int n0, int N, bool vec, bool there)
+{
+#pragma unroll
+    for (int i = 0; i < NP; i += 4) {
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there && vec) {
+            if (n0 + i < N)
+                q = *reinterpret_cast<const float4 *>(row + n0 + i);
+        } else if (there) {
+            if (n0 + i < N) q.x = row[n0 + i];
+            if (n0 + i + 1 < N) q.y = row[n0 + i + 1];
+            if (n0 + i + 2 < N) q.z = row[n0 + i + 2];
+            if (n0 + i + 3 < N) q.w = row[n0 + i + 3];
+        }
+        v[i / 2] = make_float2(q.x, q.y);
+        v[i / 2 + 1] = make_float2(q.z, q.w);
+    }
+}
+
+template <int NP>
+__device__ __forceinline__ void write_states(float *row, const float2 (&v)[NP / 2], int n0, int N, bool vec)
+{
+#pragma unroll
+    for (int i = 0; i < NP; i += 4) {
+        const float4 q = make_float4(v[i / 2].x, v[i / 2].y, v[i / 2 + 1].x, v[i / 2 + 1].y);
+        if (vec) {
+            if (n0 + i < N)
+                *reinterpret_cast<float4 *>(row + n0 + i) = q;
+        } else {
+            if (n0 + i < N) row[n0 + i] = q.x;
+            if (n0 + i + 1 < N) row[n0 + i + 1] = q.y;
+            if (n0 + i + 2 < N) row[n0 + i + 2] = q.z;
+            if (n0 + i + 3 < N) row[n0 + i + 3] = q.w;
+        }
+    }
+}
+
+// States past the last one are kept at zero: an infinite input would make them NaN (0 times
+// infinity), and their zeros of C would not take that out of a sum.
+template <int NP>
+__device__ __forceinline__ void drop_padding(float2 (&v)[NP / 2], int n0, int N)
+{
+#pragma unroll
+    for (int j = 0; j < NP / 2; ++j)
+        v[j] = make_float2(n0 + 2 * j < N ? v[j].x : 0.f, n0 + 2 * j + 1 < N ? v[j].y : 0.f);
+}
+
+// cnt rows of N values of B or C as fp32 rows of NN, zeros past N, by the block's threads.
+template <class T, int NN>
+__device__ __forceinline__ void stage_rows(float *dst, const T *src, long long stride, int N, int cnt)
+{
+    for (int i = threadIdx.x; i < cnt * NN; i += 32 * kSelWarps) {
+        const int t = i / NN, n = i % NN;
+        dst[i] = n < N ? to_float(src[t * stride + n]) : 0.f;
+    }
+}
+
+// Launches: host side of both passes (selective_scan.cu).
+struct SelShape {
+    int wc, cblocks, tiles;               // channels of a warp; blocks of channels; warps of channels
+};
+SelShape sel_shape(int channels, int N, int groups, bool backward);
+// Tokens of a segment (0: whole sequences) and the bound on units.
+int sel_segment(int n_seqs, int n_tokens, const SelShape &s, bool backward);
+int sel_max_units(int n_seqs, int n_tokens, int seg);
+long long sel_chunk_rows(long long n_seqs, long long n_tokens);
+cudaError_t launch_sel_plan(const SelArgs &a, int2 *units, int *first, cudaStream_t st);   // a.max_units bounds it
+size_t sel_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, int N, int groups);
+cudaError_t launch_selective_scan(SelArgs a, int dtype, void *workspace, cudaStream_t st);
+size_t sel_backward_workspace_bytes(int n_seqs, int n_tokens, int channels, int N, int groups);
+cudaError_t launch_selective_scan_backward(SelArgs a, int dtype, void *workspace, cudaStream_t st);
+
+}  // namespace ssm
