@@ -77,25 +77,14 @@ __device__ __forceinline__ void commit_own(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
-// Arrive on an mbarrier of the pair's first block.
+// Arrive on an mbarrier of the pair's first block.  What it tells of has been done by then (a copy whose
+// mbarrier was waited for, loads of tensor memory that were waited for), so no wider
+// release is asked for: at the cluster's scope it and the wait became memory barriers, 1900 cycles a
+// stage where the products take 512.
 __device__ __forceinline__ void arrive_first(uint32_t bar)
 {
     asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}\n" ::"r"(bar) : "memory");
-}
-
-// mbar_poll for arrivals of the other block.
-__device__ __forceinline__ bool poll_cluster(uint32_t mbar, uint32_t parity, int limit)
-{
-    for (int it = 0; it < limit; ++it) {
-        uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}\n"
-                     : "=r"(done) : "r"(mbar), "r"(parity) : "memory");
-        if (done)
-            return true;
-    }
-    return false;
+                 "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}\n" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -217,12 +206,12 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
         Ring<2> acc;
         bool ok = true;
         for (int tile = pair_id; tile < tiles && ok && n_k > 0; tile += pairs) {
-            ok = __all_sync(kFullMask, poll_cluster(accempty + 8 * acc.s, acc.phase ^ 1, cap));
+            ok = __all_sync(kFullMask, mbar_poll(accempty + 8 * acc.s, acc.phase ^ 1, cap));
             if (!ok)
                 break;
             const uint32_t d = tmem + kTileN * acc.s;
             for (int k = 0; k < n_k; ++k) {
-                ok = mbar_poll(full + 8 * r.s, r.phase, cap) && poll_cluster(peer + 8 * r.s, r.phase, cap);
+                ok = mbar_poll(full + 8 * r.s, r.phase, cap) && mbar_poll(peer + 8 * r.s, r.phase, cap);
                 ok = __all_sync(kFullMask, ok);
                 if (!ok)
                     break;
