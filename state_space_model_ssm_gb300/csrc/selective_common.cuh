@@ -7,9 +7,9 @@
 //
 // Every state has its own decay, so there is no matrix form: the work is one
 // exponential and about five multiplications an element (token, channel, state).
-// A warp owns a tile of channels with all their states: LN lanes share CH channels
-// and each holds NP of their states, so a lane has CH x NP independent recurrences
-// in registers.  What a lane reads from shared memory for a token (CH steps and inputs,
+// A warp owns a tile of channels with all their states: LN lanes share four channels
+// and each holds NP of their states, so a lane has 4 x NP independent recurrences
+// in registers.  What a lane reads from shared memory for a token (four steps and inputs,
 // NP values of B and of C) serves all of them: with single channels a lane
 // the reads of B and C cost more than the arithmetic.  Two states go into one packed fp32
 // instruction; the exponential is the hardware's 2^x of the rounded product
@@ -24,7 +24,8 @@
 
 namespace ssm {
 
-constexpr int kSelChunk = 16;             // tokens a warp stages at a time; a saved state each in training
+constexpr int kSelChunk = 16;             // tokens for each of which training saves a state
+constexpr int kSelCh = 4;                 // channels of a lane
 constexpr int kSelWarps = 4;              // warps of a block: neighbouring channel tiles of one unit
 constexpr int kSelMaxState = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -51,6 +52,7 @@ struct SelArgs {
     float *part_A, *part_D, *part_bias;   // [units][channels][N], [units][channels] twice
     float *part_B, *part_C;               // [channel blocks][n_tokens][groups N]
     int max_units, cblocks;
+    int pairs;                            // two channels of every row are one aligned word
 };
 
 // Row of chunk_states for chunk j of a sequence that starts at token t0: the first chunk's by
@@ -155,37 +157,136 @@ __device__ __forceinline__ float rcp(float v)
     return r;
 }
 
-// softplus with its derivative's e = exp(-|v|).  log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3:
-// the series 2 s (1 + s^2/3 + s^4/5 + ...) to s^14 leaves (1/9)^8 / 17 < 2^-29 of it, and keeps the
-// relative accuracy of small e, which a logarithm of 1 + e would lose.
-__device__ __forceinline__ float softplus_of(float v, float &e)
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
-    e = ex2(-fabsf(v) * kLog2e);
-    const float s = e * rcp(2.f + e), q = s * s;
-    float r = fmaf(q, 1.f / 15, 1.f / 13);
-    r = fmaf(q, r, 1.f / 11);
-    r = fmaf(q, r, 1.f / 9);
-    r = fmaf(q, r, 1.f / 7);
-    r = fmaf(q, r, 1.f / 5);
-    r = fmaf(q, r, 1.f / 3);
-    r = 2.f * fmaf(s * q, r, s);
-    return v > 20.f ? v : fmaxf(v, 0.f) + r;
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return d;
 }
 
-// The discretised step and its derivative by dt.
-__device__ __forceinline__ float sel_step(float v, bool softplus, float &slope)
+__device__ __forceinline__ float2 rcp2(float2 v) { return make_float2(rcp(v.x), rcp(v.y)); }
+
+// The discretised step of two values.  softplus(v) = max(v, 0) + log1p(e) with e = exp(-|v|), and
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3: the series 2 s (1 + s^2/3 + s^4/5 + ...) to s^14
+// leaves (1/9)^8 / 17 < 2^-29 of it, and keeps the relative accuracy of small e, which a
+// logarithm of 1 + e would lose.
+__device__ __forceinline__ float2 sel_step2(float2 v, bool softplus)
 {
-    slope = 1.f;
     if (!softplus)
         return v;
-    float e;
-    const float s = softplus_of(v, e);
-    slope = v > 20.f ? 1.f : (v >= 0.f ? 1.f : e) * rcp(1.f + e);
-    return s;
+    const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
+    const float2 s = mul2(e, rcp2(add2(e, twice(2.f)))), q = mul2(s, s);
+    float2 r = fma2(q, twice(1.f / 15), twice(1.f / 13));
+    r = fma2(q, r, twice(1.f / 11));
+    r = fma2(q, r, twice(1.f / 9));
+    r = fma2(q, r, twice(1.f / 7));
+    r = fma2(q, r, twice(1.f / 5));
+    r = fma2(q, r, twice(1.f / 3));
+    const float2 s2 = add2(s, s);
+    r = fma2(mul2(s2, q), r, s2);
+    return make_float2(v.x > 20.f ? v.x : fmaxf(v.x, 0.f) + r.x, v.y > 20.f ? v.y : fmaxf(v.y, 0.f) + r.y);
+}
+
+// Its derivative by v: 1 above the threshold, else sigmoid(v).
+__device__ __forceinline__ float2 sel_slope2(float2 v, bool softplus)
+{
+    if (!softplus)
+        return twice(1.f);
+    const float2 s = rcp2(make_float2(1.f + ex2(-v.x * kLog2e), 1.f + ex2(-v.y * kLog2e)));
+    return make_float2(v.x > 20.f ? 1.f : s.x, v.y > 20.f ? 1.f : s.y);
 }
 
 // sigmoid(v); v times it is 0 times v where exp(-v) overflows (v below -88).
-__device__ __forceinline__ float sigmoid_of(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
+__device__ __forceinline__ float2 sigmoid2(float2 v)
+{
+    return rcp2(make_float2(1.f + ex2(-v.x * kLog2e), 1.f + ex2(-v.y * kLog2e)));
+}
+
+// Two neighbouring channels of a row as they lie in memory.
+template <class T>
+struct RawPair { uint32_t w; };
+template <>
+struct RawPair<float> { float2 w; };
+
+template <class T>
+__device__ __forceinline__ float2 pair_of(const RawPair<T> &r)
+{
+    Vec<T, 2> v;
+    *reinterpret_cast<uint32_t *>(&v) = r.w;
+    return make_float2(to_float(v.v[0]), to_float(v.v[1]));
+}
+template <>
+__device__ __forceinline__ float2 pair_of<float>(const RawPair<float> &r) { return r.w; }
+
+// How a warp stages pairs of channels of up to L tokens: place m of a lane is token tok(m), pair cp(m).
+template <int WC, int L>
+struct SelStage {
+    static constexpr int P = WC / 2, KC = P >= 32 ? P / 32 : 1, TI = P >= 32 ? 1 : 32 / P, M = L * P / 32;
+    static_assert(M >= 1 && L % TI == 0, "whole places");
+    static __device__ __forceinline__ int tok(int m, int lane) { return P >= 32 ? m / KC : m * TI + lane / P; }
+    static __device__ __forceinline__ int cp(int m, int lane) { return P >= 32 ? lane + 32 * (m % KC) : lane % P; }
+};
+
+// Places [m0, m0 + CNT) of cnt tokens' rows at `p` (the tile's first channel), all loads together: places past
+// the last token or channel read the last one's (their values are not used).  `pairs`: two
+// channels of a row are one aligned word.
+template <class T, int WC, int L, int CNT>
+__device__ __forceinline__ void load_places(RawPair<T> (&r)[CNT], int m0, const T *p, long long stride, int cnt, int wc, int lane,
+                                            bool pairs)
+{
+    using S = SelStage<WC, L>;
+    if (pairs) {
+#pragma unroll
+        for (int m = 0; m < CNT; ++m) {
+            const T *q = p + min(S::tok(m0 + m, lane), cnt - 1) * stride + min(2 * S::cp(m0 + m, lane), wc - 2);
+            if constexpr (sizeof(T) == 4)
+                r[m].w = *reinterpret_cast<const float2 *>(q);
+            else
+                r[m].w = *reinterpret_cast<const uint32_t *>(q);
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < CNT; ++m) {
+            const T *q = p + min(S::tok(m0 + m, lane), cnt - 1) * stride;
+            const int c = 2 * S::cp(m0 + m, lane);
+            const Vec<T, 2> v{{q[min(c, wc - 1)], q[min(c + 1, wc - 1)]}};
+            if constexpr (sizeof(T) == 4)
+                r[m].w = make_float2(v.v[0], v.v[1]);
+            else
+                r[m].w = *reinterpret_cast<const uint32_t *>(&v);
+        }
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store_pair(T *p, float2 v, bool pairs, bool second)
+{
+    if (pairs) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float2 *>(p) = v;
+        } else {
+            const Vec<T, 2> o{{from_float<T>(v.x), from_float<T>(v.y)}};
+            *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(&o);
+        }
+    } else {
+        p[0] = from_float<T>(v.x);
+        if (second)
+            p[1] = from_float<T>(v.y);
+    }
+}
+
+// Parameters of a lane's channel pairs (zeros past the tile's channels).
+template <int KC, int WC>
+__device__ __forceinline__ void read_channels(float2 (&v)[KC], const float *p, int c0, int wc, int lane)
+{
+    using S = SelStage<WC, 16>;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+        const int c = 2 * S::cp(k, lane);
+        v[k] = make_float2(p && c < wc ? __ldg(p + c0 + c) : 0.f, p && c + 1 < wc ? __ldg(p + c0 + c + 1) : 0.f);
+    }
+}
 
 // CNT sums over LANES lanes STRIDE apart, each of the lanes ending with max(1, CNT / LANES) of
 // them in v[0..]: as long as there are two values to a lane, a lane keeps half and sends
@@ -300,15 +401,30 @@ __device__ __forceinline__ void drop_padding(float2 (&v)[NP / 2], int n0, int N)
         v[j] = make_float2(n0 + 2 * j < N ? v[j].x : 0.f, n0 + 2 * j + 1 < N ? v[j].y : 0.f);
 }
 
-// cnt rows of N values of B or C as fp32 rows of NN, zeros past N, by the block's threads.
-template <class T, int NN>
-__device__ __forceinline__ void stage_rows(float *dst, const T *src, long long stride, int N, int cnt)
-{
-    for (int i = threadIdx.x; i < cnt * NN; i += 32 * kSelWarps) {
-        const int t = i / NN, n = i % NN;
-        dst[i] = n < N ? to_float(src[t * stride + n]) : 0.f;
+// L rows of N values of B or C by the block's threads: loads into registers, and later as fp32 rows of NN
+// with zeros past N.
+template <class T, int NN, int L>
+struct SelRows {
+    static constexpr int kEach = L * NN / (32 * kSelWarps) > 0 ? L * NN / (32 * kSelWarps) : 1;
+    T v[kEach];
+    __device__ __forceinline__ void load(const T *src, long long stride, int N, int cnt)
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int e = threadIdx.x + 32 * kSelWarps * i, t = e / NN, n = e % NN;
+            v[i] = src[min(t, cnt - 1) * stride + min(n, N - 1)];
+        }
     }
-}
+    __device__ __forceinline__ void store(float *dst, int N) const
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int e = threadIdx.x + 32 * kSelWarps * i, n = e % NN;
+            if (L * NN >= 32 * kSelWarps || e < L * NN)
+                dst[e] = n < N ? to_float(v[i]) : 0.f;
+        }
+    }
+};
 
 // Launches: host side of both passes (selective_scan.cu).
 struct SelShape {
@@ -316,6 +432,7 @@ struct SelShape {
 };
 SelShape sel_shape(int channels, int N, int groups, bool backward);
 // Tokens of a segment (0: whole sequences) and the bound on units.
+bool sel_pairs(const SelArgs &a, int dtype);
 int sel_segment(int n_seqs, int n_tokens, const SelShape &s, bool backward);
 int sel_max_units(int n_seqs, int n_tokens, int seg);
 long long sel_chunk_rows(long long n_seqs, long long n_tokens);

@@ -7,110 +7,20 @@
 //   grad_x    = D gp + step sum_n e B,   grad step = sum_n e (A k + x B),   grad_A = sum_t e step k
 //   grad_z    = grad_y p s (1 + z (1 - s)), s = sigmoid(z)
 //
-// Per chunk of 16 tokens, from the state the forward pass saved: the states are computed
-// again with k kept in shared memory (one exponential more an element than keeping the
-// decays too, half the memory), and with them the sums that need h; then the tokens are walked
-// backwards.  Sums over states cross the LN lanes of a channel, sums over channels the
+// Per chunk of 16 tokens, from the state the forward pass saved, eight tokens at a time: the
+// states are computed again with k kept in shared memory (one exponential more an element
+// than keeping the decays too, half the memory), and with them the sums that need h; then the
+// tokens are walked backwards.  Sums over states cross the LN lanes of a channel, sums over channels the
 // lanes, then the block's warps in shared memory, then channel blocks in a second
 // kernel: always in the same order.
 //
 // Units of time as in the forward pass: with segments, a pass before finds what each segment
 // hands to the one in front of it.
-#include "selective_common.cuh"
+#include "selective_walk.cuh"
 
 namespace ssm {
 
 namespace {
-
-constexpr int kBackCh = 2;                                  // channels of a lane
-
-// e = exp(-step A)-weighted gradient that a unit hands to the one before it, from zero.
-template <class T, int NP, int LN>
-__global__ void __launch_bounds__(32 * kSelWarps)
-sel_carry_kernel(const SelArgs a)
-{
-    griddep_entry();
-    constexpr int CH = 4, WC = 32 / LN * CH, NN = NP * LN, L = kSelChunk, KC = WC > 32 ? WC / 32 : 1;
-    __shared__ __align__(16) float s_step[kSelWarps][L * WC], s_g[kSelWarps][L * WC], s_C[2][L * NN];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane % LN, q = lane / LN, n0 = sub * NP;
-    const int cblocks = a.groups * sel_group_blocks(a.channels, a.groups, WC), u = blockIdx.x / cblocks;
-    const SelTile tile = sel_tile<WC>(a, blockIdx.x - u * cblocks, warp);
-    SelUnit s;
-    if (!sel_unit(a, u, s) || s.k == 0)                     // (the whole block)
-        return;
-    const int wc = tile.c1 - tile.c0;
-    const bool pad = a.N != NN;
-    float *step = s_step[warp], *gs = s_g[warp];
-    float2 e[CH][NP / 2], A[CH][NP / 2];
-    float total[CH], bias[KC];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        read_states<NP>(A[c], a.A + (long long)(tile.c0 + q * CH + c) * a.N, n0, a.N, false, q * CH + c < wc);
-#pragma unroll
-        for (int j = 0; j < NP / 2; ++j) {
-            A[c][j] = make_float2(A[c][j].x * kLog2e, A[c][j].y * kLog2e);
-            e[c][j] = make_float2(0.f, 0.f);
-        }
-        total[c] = 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < KC; ++k) {
-        const int c = (lane + 32 * k) % WC;
-        bias[k] = a.bias && c < wc ? __ldg(a.bias + tile.c0 + c) : 0.f;
-    }
-    const T *dt = static_cast<const T *>(a.dt) + tile.c0, *gy = static_cast<const T *>(a.grad_y) + tile.c0;
-    const T *z = a.z ? static_cast<const T *>(a.z) + tile.c0 : nullptr;
-    const T *C = static_cast<const T *>(a.C) + tile.g * a.N;
-    for (int b = s.begin + (s.end - 1 - s.begin) / L * L; b >= s.begin; b -= L) {
-        const int cnt = min(L, s.end - b);
-        const long long t0 = s.t0 + b;
-        float *Cs = s_C[b / L & 1];
-#pragma unroll 4
-        for (int m = 0; m < L * WC / 32; ++m) {
-            const int i = lane + 32 * m, t = i / WC, c = i % WC;
-            float st = 0.f, gv = 0.f, slope;
-            if (t < cnt && c < wc) {
-                st = sel_step(to_float(dt[(t0 + t) * a.sdt + c]) + bias[m % KC], a.softplus, slope);
-                gv = to_float(gy[(t0 + t) * a.sgy + c]);
-                if (z) {
-                    const float g = to_float(z[(t0 + t) * a.sz + c]);
-                    gv *= g * sigmoid_of(g);
-                }
-            }
-            step[i] = st;
-            gs[i] = gv;
-        }
-        stage_rows<T, NN>(Cs, C + t0 * a.sC, a.sC, a.N, cnt);
-        __syncthreads();
-        for (int t = cnt - 1; t >= 0; --t) {
-            float st[CH], gv[CH];
-            float2 Cv[NP / 2];
-            load_floats<CH>(st, step + t * WC + q * CH);
-            load_floats<CH>(gv, gs + t * WC + q * CH);
-            load_pairs<NP>(Cv, Cs + t * NN + n0);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                total[c] += st[c];
-#pragma unroll
-                for (int j = 0; j < NP / 2; ++j)
-                    e[c][j] = mul2(ex2_2(mul2(twice(st[c]), A[c][j])), fma2(twice(gv[c]), Cv[j], e[c][j]));
-                if (pad)
-                    drop_padding<NP>(e[c], n0, a.N);
-            }
-        }
-        __syncwarp();
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int ch = tile.c0 + q * CH + c;
-        if (q * CH + c >= wc)
-            continue;
-        write_states<NP>(a.unit_state + ((long long)u * a.channels + ch) * a.N, e[c], n0, a.N, a.N % 4 == 0);
-        if (sub == 0)
-            a.unit_step[(long long)u * a.channels + ch] = total[c];
-    }
-}
 
 // The gradient that reaches each unit from behind, in place of what the unit hands on.
 __global__ void __launch_bounds__(256)
@@ -134,23 +44,29 @@ sel_carry_combine_kernel(const SelArgs a)
     }
 }
 
-template <int NP, int LN>
+constexpr int kBackL = kSelChunk, kBackNP = 4, kKeepTokens = 8;
+
+template <int LN>
 struct BackLayout {                                         // floats of a warp, then of the block
-    static constexpr int CH = kBackCh, WC = 32 / LN * CH, NN = NP * LN, L = kSelChunk;
-    static constexpr int kRow = L * WC;
-    static constexpr int kKeep = L * 32 * CH * NP;          // k of every token: a lane's own values
-    static constexpr int kSums = L * NN;                    // grad_B, grad_C of the warp's channels
-    static constexpr int kWarp = kKeep + 5 * kRow + 2 * kSums;
+    static constexpr int WC = 32 / LN * kSelCh, NN = kBackNP * LN;
+    static constexpr int kRow = kBackL * WC;
+    static constexpr int kKeep = kKeepTokens * 32 * kSelCh * kBackNP;   // k of every token: a lane's own values
+    static constexpr int kSums = kBackL * NN;               // grad_B, grad_C of the warp's channels
+    static constexpr int kWarp = kKeep + 4 * kRow + 2 * kSums;
     static constexpr size_t kBytes = ((size_t)kWarp * kSelWarps + 2 * kSums) * sizeof(float);   // B and C last
 };
 
-template <class T, int NP, int LN>
-__global__ void __launch_bounds__(32 * kSelWarps)
+template <class T, int LN>
+__global__ void __launch_bounds__(32 * kSelWarps, 2)
 sel_backward_kernel(const SelArgs a)
 {
     griddep_entry();
-    using Y = BackLayout<NP, LN>;
-    constexpr int CH = Y::CH, WC = Y::WC, NN = Y::NN, L = kSelChunk, KC = WC > 32 ? WC / 32 : 1;
+    using Y = BackLayout<LN>;
+    constexpr int CH = kSelCh, NP = kBackNP, WC = Y::WC, NN = Y::NN, L = kBackL;
+    using S = SelStage<WC, L>;
+    constexpr int M = S::M, KC = S::KC, H = M > 8 ? 8 : M;  // places loaded together
+    constexpr int kLeft = NP * LN > 32 ? NP * LN / 32 : 1;  // sums over channels that a lane ends with
+    constexpr int kOwn = CH > LN ? CH / LN : 1;             // sums over states
     extern __shared__ __align__(16) float sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane % LN, q = lane / LN, n0 = sub * NP;
@@ -160,12 +76,13 @@ sel_backward_kernel(const SelArgs a)
     if (!sel_unit(a, u, s))                                 // (the whole block)
         return;
     const int wc = tile.c1 - tile.c0;
-    const bool pad = a.N != NN;
+    const bool pad = a.N != NN, pairs = a.pairs != 0;
     const bool vec_c = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.chunk_states) & 15) == 0;
     float *w = sm + warp * Y::kWarp;
-    float *keep = w, *step = keep + Y::kKeep, *in = step + Y::kRow, *gs = in + Y::kRow, *sa = gs + Y::kRow, *eb = sa + Y::kRow;
-    float *sB = eb + Y::kRow, *sC = sB + Y::kSums, *Bs = sm + kSelWarps * Y::kWarp, *Cs = Bs + Y::kSums;
-    float2 e[CH][NP / 2], A[CH][NP / 2], gA[CH][NP / 2];
+    // step; step x, later sum_n e B; gp; p, later sum_n e A k
+    float *keep = w, *step = keep + Y::kKeep, *in = step + Y::kRow, *gs = in + Y::kRow, *sa = gs + Y::kRow;
+    float *sB = sa + Y::kRow, *sC = sB + Y::kSums, *Bs = sm + kSelWarps * Y::kWarp, *Cs = Bs + Y::kSums;
+    float2 e[CH][NP / 2], A[CH][NP / 2], gA[CH][NP / 2], h0[CH][NP / 2];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int ch = tile.c0 + q * CH + c;
@@ -178,18 +95,16 @@ sel_backward_kernel(const SelArgs a)
                             there && a.grad_state != nullptr);
 #pragma unroll
         for (int j = 0; j < NP / 2; ++j) {
-            A[c][j] = make_float2(A[c][j].x * kLog2e, A[c][j].y * kLog2e);
+            A[c][j] = mul2(A[c][j], twice(kLog2e));
             gA[c][j] = make_float2(0.f, 0.f);
         }
     }
-    float bias[KC], D[KC], gD[KC], gbias[KC];
+    float2 bias[KC], D[KC], gD[KC], gbias[KC];
+    read_channels<KC, WC>(bias, a.bias, tile.c0, wc, lane);
+    read_channels<KC, WC>(D, a.D, tile.c0, wc, lane);
 #pragma unroll
-    for (int k = 0; k < KC; ++k) {
-        const int c = (lane + 32 * k) % WC;
-        bias[k] = a.bias && c < wc ? __ldg(a.bias + tile.c0 + c) : 0.f;
-        D[k] = a.D && c < wc ? __ldg(a.D + tile.c0 + c) : 0.f;
-        gD[k] = gbias[k] = 0.f;
-    }
+    for (int k = 0; k < KC; ++k)
+        gD[k] = gbias[k] = make_float2(0.f, 0.f);
     const T *x = static_cast<const T *>(a.x) + tile.c0, *dt = static_cast<const T *>(a.dt) + tile.c0;
     const T *z = a.z ? static_cast<const T *>(a.z) + tile.c0 : nullptr, *gy = static_cast<const T *>(a.grad_y) + tile.c0;
     const T *B = static_cast<const T *>(a.B) + tile.g * a.N, *C = static_cast<const T *>(a.C) + tile.g * a.N;
@@ -200,157 +115,200 @@ sel_backward_kernel(const SelArgs a)
     for (int b = s.end > s.begin ? s.begin + (s.end - 1 - s.begin) / L * L : -1; b >= s.begin; b -= L) {
         const int cnt = min(L, s.end - b);
         const long long t0 = s.t0 + b;
-#pragma unroll 4
-        for (int m = 0; m < L * WC / 32; ++m) {
-            const int i = lane + 32 * m, t = i / WC, c = i % WC;
-            float st = 0.f, xv = 0.f, gv = 0.f, slope;
-            if (t < cnt && c < wc) {
-                st = sel_step(to_float(dt[(t0 + t) * a.sdt + c]) + bias[m % KC], a.softplus, slope);
-                xv = to_float(x[(t0 + t) * a.sx + c]);
-                gv = to_float(gy[(t0 + t) * a.sgy + c]);
-                if (z) {
-                    const float g = to_float(z[(t0 + t) * a.sz + c]);
-                    gv *= g * sigmoid_of(g);
-                }
-            }
-            step[i] = st;
-            in[i] = st * xv;
-            gs[i] = gv;
-        }
-        stage_rows<T, NN>(Bs, B + t0 * a.sB, a.sB, a.N, cnt);
-        stage_rows<T, NN>(Cs, C + t0 * a.sC, a.sC, a.N, cnt);
-        float2 h[CH][NP / 2];
+        SelRows<T, NN, L> rB, rC;
+        rB.load(B + t0 * a.sB, a.sB, a.N, cnt);
+        rC.load(C + t0 * a.sC, a.sC, a.N, cnt);
         const float *cs = a.chunk_states + sel_chunk_row(a.n_seqs, s.seq, s.t0, b / L) * a.channels * a.N;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-            read_states<NP>(h[c], cs + (long long)(tile.c0 + q * CH + c) * a.N, n0, a.N, vec_c, q * CH + c < wc);
+            read_states<NP>(h0[c], cs + (long long)(tile.c0 + q * CH + c) * a.N, n0, a.N, vec_c, q * CH + c < wc);
+        if (wc > 0) {
+#pragma unroll
+            for (int m0 = 0; m0 < M; m0 += H) {
+                RawPair<T> rdt[H], rx[H], rg[H], rz[H];
+                load_places<T, WC, L>(rdt, m0, dt + t0 * a.sdt, a.sdt, cnt, wc, lane, pairs);
+                load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
+                load_places<T, WC, L>(rg, m0, gy + t0 * a.sgy, a.sgy, cnt, wc, lane, pairs);
+                if (z)
+                    load_places<T, WC, L>(rz, m0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    const int m = m0 + k, t = S::tok(m, lane), c = 2 * S::cp(m, lane);
+                    float2 st = sel_step2(add2(pair_of<T>(rdt[k]), bias[m % KC]), a.softplus);
+                    float2 g = pair_of<T>(rg[k]), v = mul2(st, pair_of<T>(rx[k]));
+                    if (z) {
+                        const float2 zv = pair_of<T>(rz[k]);
+                        g = mul2(g, mul2(zv, sigmoid2(zv)));
+                    }
+                    // what is not there takes no part in the sums over channels
+                    const bool one = t < cnt && c < wc, two = t < cnt && c + 1 < wc;
+                    *reinterpret_cast<float2 *>(step + t * WC + c) = make_float2(one ? st.x : 0.f, two ? st.y : 0.f);
+                    *reinterpret_cast<float2 *>(in + t * WC + c) = make_float2(one ? v.x : 0.f, two ? v.y : 0.f);
+                    *reinterpret_cast<float2 *>(gs + t * WC + c) = make_float2(one ? g.x : 0.f, two ? g.y : 0.f);
+                }
+            }
+        } else {
+            for (int i = lane; i < 3 * Y::kRow; i += 32)
+                step[i] = 0.f;
+        }
+        rB.store(Bs, a.N);
+        rC.store(Cs, a.N);
         __syncthreads();
-        for (int t = 0; t < cnt; ++t) {
-            float st[CH], uv[CH], gv[CH], p[CH], gc[NP];
-            float2 Bv[NP / 2], Cv[NP / 2], sum_c[NP / 2];
-            load_floats<CH>(st, step + t * WC + q * CH);
-            load_floats<CH>(uv, in + t * WC + q * CH);
-            load_floats<CH>(gv, gs + t * WC + q * CH);
-            load_pairs<NP>(Bv, Bs + t * NN + n0);
-            load_pairs<NP>(Cv, Cs + t * NN + n0);
+#pragma unroll 1
+        for (int first = cnt > kKeepTokens ? kKeepTokens : 0; first >= 0; first -= kKeepTokens) {
+            const int stop = min(cnt, first + kKeepTokens);
+            float2 h[CH][NP / 2];
 #pragma unroll
-            for (int j = 0; j < NP / 2; ++j)
-                sum_c[j] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                float2 sum = make_float2(0.f, 0.f), k[NP / 2];
-#pragma unroll
-                for (int j = 0; j < NP / 2; ++j) {
-                    k[j] = mul2(ex2_2(mul2(twice(st[c]), A[c][j])), h[c][j]);
-                    h[c][j] = fma2(twice(uv[c]), Bv[j], k[j]);
-                }
-                if (pad)
-                    drop_padding<NP>(h[c], n0, a.N);
-#pragma unroll
-                for (int j = 0; j < NP / 2; ++j) {
-                    sum = fma2(h[c][j], Cv[j], sum);
-                    sum_c[j] = fma2(twice(gv[c]), h[c][j], sum_c[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < NP / 2; j += 2)
-                    *reinterpret_cast<float4 *>(keep + ((t * CH + c) * (NP / 4) + j / 2) * 128 + 4 * lane) =
-                        make_float4(k[j].x, k[j].y, k[j + 1].x, k[j + 1].y);
-                p[c] = sum.x + sum.y;
-            }
-#pragma unroll
-            for (int j = 0; j < NP / 2; ++j) {
-                gc[2 * j] = sum_c[j].x;
-                gc[2 * j + 1] = sum_c[j].y;
-            }
-            int at;
-            bool mine;
-            if (z) {
-                lanes_sum<CH, LN, 1>(p, lane, at, mine);
-                if (mine)
-#pragma unroll
-                    for (int r = 0; r < (CH > LN ? CH / LN : 1); ++r)
-                        sa[t * WC + q * CH + at + r] = p[r];
-            }
-            lanes_sum<NP, 32 / LN, LN>(gc, lane, at, mine);
-            constexpr int kLeft = NP * LN > 32 ? NP * LN / 32 : 1;
-            if (mine)
-#pragma unroll
-                for (int r = 0; r < kLeft; ++r)
-                    sC[t * NN + n0 + at + r] = gc[r];
-        }
-        __syncwarp();
-        if (z) {
-#pragma unroll 4
-            for (int m = 0; m < L * WC / 32; ++m) {
-                const int i = lane + 32 * m, t = i / WC, c = i % WC;
-                if (t < cnt && c < wc) {
-                    const float g = to_float(z[(t0 + t) * a.sz + c]), sg = sigmoid_of(g);
-                    const float p = fmaf(D[m % KC], to_float(x[(t0 + t) * a.sx + c]), sa[i]);
-                    gz[(t0 + t) * a.sgz + c] = from_float<T>(to_float(gy[(t0 + t) * a.sgy + c]) * p * fmaf(g * sg, 1.f - sg, sg));
-                }
-            }
-            __syncwarp();
-        }
-        for (int t = cnt - 1; t >= 0; --t) {
-            float st[CH], uv[CH], gv[CH], s1[CH], s2[CH], gb[NP];
-            float2 Bv[NP / 2], Cv[NP / 2], sum_b[NP / 2];
-            load_floats<CH>(st, step + t * WC + q * CH);
-            load_floats<CH>(uv, in + t * WC + q * CH);
-            load_floats<CH>(gv, gs + t * WC + q * CH);
-            load_pairs<NP>(Bv, Bs + t * NN + n0);
-            load_pairs<NP>(Cv, Cs + t * NN + n0);
-#pragma unroll
-            for (int j = 0; j < NP / 2; ++j)
-                sum_b[j] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                float2 k[NP / 2], wa = make_float2(0.f, 0.f), wb = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < NP / 2; j += 2) {
-                    const float4 v = *reinterpret_cast<const float4 *>(keep + ((t * CH + c) * (NP / 4) + j / 2) * 128 + 4 * lane);
-                    k[j] = make_float2(v.x, v.y);
-                    k[j + 1] = make_float2(v.z, v.w);
-                }
+            for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int j = 0; j < NP / 2; ++j)
-                    e[c][j] = fma2(twice(gv[c]), Cv[j], e[c][j]);
-                if (pad) {
-                    drop_padding<NP>(e[c], n0, a.N);
-                    drop_padding<NP>(k, n0, a.N);
+                    h[c][j] = h0[c][j];
+#pragma unroll 1
+            for (int t = 0; t < first; ++t) {               // up to the tokens whose k is kept
+                float st[CH], uv[CH];
+                float2 Bv[NP / 2];
+                load_floats<CH>(st, step + t * WC + q * CH);
+                load_floats<CH>(uv, in + t * WC + q * CH);
+                load_pairs<NP>(Bv, Bs + t * NN + n0);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int j = 0; j < NP / 2; ++j)
+                        h[c][j] = fma2(ex2_2(mul2(twice(st[c]), A[c][j])), h[c][j], mul2(twice(uv[c]), Bv[j]));
+            }
+#pragma unroll 1
+            for (int t = first; t < stop; ++t) {
+                float st[CH], uv[CH], gv[CH], p[CH], gc[NP];
+                float2 Bv[NP / 2], Cv[NP / 2], sum_c[NP / 2];
+                load_floats<CH>(st, step + t * WC + q * CH);
+                load_floats<CH>(uv, in + t * WC + q * CH);
+                load_floats<CH>(gv, gs + t * WC + q * CH);
+                load_pairs<NP>(Bv, Bs + t * NN + n0);
+                load_pairs<NP>(Cv, Cs + t * NN + n0);
+#pragma unroll
+                for (int j = 0; j < NP / 2; ++j)
+                    sum_c[j] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    float2 sum = make_float2(0.f, 0.f), k[NP / 2];
+#pragma unroll
+                    for (int j = 0; j < NP / 2; ++j) {
+                        k[j] = mul2(ex2_2(mul2(twice(st[c]), A[c][j])), h[c][j]);
+                        h[c][j] = fma2(twice(uv[c]), Bv[j], k[j]);
+                    }
+                    if (pad) {
+                        drop_padding<NP>(h[c], n0, a.N);
+                        drop_padding<NP>(k, n0, a.N);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NP / 2; ++j) {
+                        sum = fma2(h[c][j], Cv[j], sum);
+                        sum_c[j] = fma2(twice(gv[c]), h[c][j], sum_c[j]);
+                    }
+                    *reinterpret_cast<float4 *>(keep + ((t - first) * CH + c) * 128 + 4 * lane) =
+                        make_float4(k[0].x, k[0].y, k[1].x, k[1].y);
+                    p[c] = sum.x + sum.y;
                 }
 #pragma unroll
                 for (int j = 0; j < NP / 2; ++j) {
-                    const float2 v = mul2(e[c][j], k[j]);
-                    gA[c][j] = fma2(twice(st[c]), v, gA[c][j]);
-                    wa = fma2(v, A[c][j], wa);
-                    wb = fma2(e[c][j], Bv[j], wb);
-                    sum_b[j] = fma2(twice(uv[c]), e[c][j], sum_b[j]);
-                    e[c][j] = mul2(ex2_2(mul2(twice(st[c]), A[c][j])), e[c][j]);
+                    gc[2 * j] = sum_c[j].x;
+                    gc[2 * j + 1] = sum_c[j].y;
                 }
-                s1[c] = wa.x + wa.y;
-                s2[c] = wb.x + wb.y;
-            }
+                int at;
+                bool mine;
+                if (z) {
+                    lanes_sum<CH, LN, 1>(p, lane, at, mine);
+                    if (mine)
 #pragma unroll
-            for (int j = 0; j < NP / 2; ++j) {
-                gb[2 * j] = sum_b[j].x;
-                gb[2 * j + 1] = sum_b[j].y;
-            }
-            int at;
-            bool mine;
-            lanes_sum<CH, LN, 1>(s1, lane, at, mine);
-            lanes_sum<CH, LN, 1>(s2, lane, at, mine);
-            if (mine)
-#pragma unroll
-                for (int r = 0; r < (CH > LN ? CH / LN : 1); ++r) {
-                    sa[t * WC + q * CH + at + r] = s1[r];
-                    eb[t * WC + q * CH + at + r] = s2[r];
+                        for (int r = 0; r < kOwn; ++r)
+                            sa[t * WC + q * CH + at + r] = p[r];
                 }
-            lanes_sum<NP, 32 / LN, LN>(gb, lane, at, mine);
-            constexpr int kLeft = NP * LN > 32 ? NP * LN / 32 : 1;
-            if (mine)
+                lanes_sum<NP, 32 / LN, LN>(gc, lane, at, mine);
+                if (mine)
 #pragma unroll
-                for (int r = 0; r < kLeft; ++r)
-                    sB[t * NN + n0 + at + r] = gb[r];
+                    for (int r = 0; r < kLeft; ++r)
+                        sC[t * NN + n0 + at + r] = gc[r];
+            }
+            __syncwarp();
+            if (z && wc > 0) {                              // the gate's gradient, before sa is used again
+#pragma unroll 1
+                for (int m0 = 0; m0 < M; m0 += H) {
+                    RawPair<T> rz[H], rx[H], rg[H];
+                    load_places<T, WC, L>(rz, m0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
+                    load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
+                    load_places<T, WC, L>(rg, m0, gy + t0 * a.sgy, a.sgy, cnt, wc, lane, pairs);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) {
+                        const int m = m0 + k, t = S::tok(m, lane), c = 2 * S::cp(m, lane);
+                        if (t < first || t >= stop || c >= wc)
+                            continue;
+                        const float2 zv = pair_of<T>(rz[k]), sg = sigmoid2(zv);
+                        const float2 p = fma2(D[m % KC], pair_of<T>(rx[k]), *reinterpret_cast<const float2 *>(sa + t * WC + c));
+                        const float2 rest = make_float2(1.f - sg.x, 1.f - sg.y);
+                        store_pair<T>(gz + (t0 + t) * a.sgz + c,
+                                      mul2(mul2(pair_of<T>(rg[k]), p), fma2(mul2(zv, sg), rest, sg)), pairs, c + 1 < wc);
+                    }
+                }
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int t = stop - 1; t >= first; --t) {
+                float st[CH], uv[CH], gv[CH], s1[CH], s2[CH], gb[NP];
+                float2 Bv[NP / 2], Cv[NP / 2], sum_b[NP / 2];
+                load_floats<CH>(st, step + t * WC + q * CH);
+                load_floats<CH>(uv, in + t * WC + q * CH);
+                load_floats<CH>(gv, gs + t * WC + q * CH);
+                load_pairs<NP>(Bv, Bs + t * NN + n0);
+                load_pairs<NP>(Cv, Cs + t * NN + n0);
+#pragma unroll
+                for (int j = 0; j < NP / 2; ++j)
+                    sum_b[j] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    float2 k[NP / 2], wa = make_float2(0.f, 0.f), wb = make_float2(0.f, 0.f);
+                    const float4 kv = *reinterpret_cast<const float4 *>(keep + ((t - first) * CH + c) * 128 + 4 * lane);
+                    k[0] = make_float2(kv.x, kv.y);
+                    k[1] = make_float2(kv.z, kv.w);
+#pragma unroll
+                    for (int j = 0; j < NP / 2; ++j)
+                        e[c][j] = fma2(twice(gv[c]), Cv[j], e[c][j]);
+                    if (pad)
+                        drop_padding<NP>(e[c], n0, a.N);
+#pragma unroll
+                    for (int j = 0; j < NP / 2; ++j) {
+                        const float2 v = mul2(e[c][j], k[j]);
+                        gA[c][j] = fma2(twice(st[c]), v, gA[c][j]);
+                        wa = fma2(v, A[c][j], wa);
+                        wb = fma2(e[c][j], Bv[j], wb);
+                        sum_b[j] = fma2(twice(uv[c]), e[c][j], sum_b[j]);
+                        e[c][j] = mul2(ex2_2(mul2(twice(st[c]), A[c][j])), e[c][j]);
+                    }
+                    s1[c] = wa.x + wa.y;
+                    s2[c] = wb.x + wb.y;
+                }
+#pragma unroll
+                for (int j = 0; j < NP / 2; ++j) {
+                    gb[2 * j] = sum_b[j].x;
+                    gb[2 * j + 1] = sum_b[j].y;
+                }
+                int at;
+                bool mine;
+                lanes_sum<CH, LN, 1>(s1, lane, at, mine);
+                lanes_sum<CH, LN, 1>(s2, lane, at, mine);
+                __syncwarp();                               // the inputs of this token have been read
+                if (mine)
+#pragma unroll
+                    for (int r = 0; r < kOwn; ++r) {
+                        sa[t * WC + q * CH + at + r] = s1[r];
+                        in[t * WC + q * CH + at + r] = s2[r];
+                    }
+                lanes_sum<NP, 32 / LN, LN>(gb, lane, at, mine);
+                if (mine)
+#pragma unroll
+                    for (int r = 0; r < kLeft; ++r)
+                        sB[t * NN + n0 + at + r] = gb[r];
+            }
+            __syncwarp();
         }
         __syncthreads();                                    // every warp's sums over its channels are there
         for (int i = tid; i < cnt * NN; i += 32 * kSelWarps) {
@@ -368,18 +326,26 @@ sel_backward_kernel(const SelArgs a)
                 a.part_C[at] = vc;
             }
         }
-#pragma unroll 4
-        for (int m = 0; m < L * WC / 32; ++m) {
-            const int i = lane + 32 * m, t = i / WC, c = i % WC;
-            if (t < cnt && c < wc) {
-                const float xv = to_float(x[(t0 + t) * a.sx + c]), gv = gs[i], st = step[i];
-                float slope;
-                sel_step(to_float(dt[(t0 + t) * a.sdt + c]) + bias[m % KC], a.softplus, slope);
-                const float g = fmaf(sa[i], kLn2, xv * eb[i]) * slope;
-                gx[(t0 + t) * a.sgx + c] = from_float<T>(fmaf(D[m % KC], gv, st * eb[i]));
-                gdt[(t0 + t) * a.sgdt + c] = from_float<T>(g);
-                gD[m % KC] = fmaf(gv, xv, gD[m % KC]);
-                gbias[m % KC] += g;
+        if (wc > 0) {
+#pragma unroll
+            for (int m0 = 0; m0 < M; m0 += H) {
+                RawPair<T> rdt[H], rx[H];
+                load_places<T, WC, L>(rdt, m0, dt + t0 * a.sdt, a.sdt, cnt, wc, lane, pairs);
+                load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    const int m = m0 + k, t = S::tok(m, lane), c = 2 * S::cp(m, lane), i = t * WC + c;
+                    if (t >= cnt || c >= wc)
+                        continue;
+                    const float2 xv = pair_of<T>(rx[k]), gv = *reinterpret_cast<const float2 *>(gs + i);
+                    const float2 eb = *reinterpret_cast<const float2 *>(in + i), st = *reinterpret_cast<const float2 *>(step + i);
+                    const float2 g = mul2(fma2(*reinterpret_cast<const float2 *>(sa + i), twice(kLn2), mul2(xv, eb)),
+                                          sel_slope2(add2(pair_of<T>(rdt[k]), bias[m % KC]), a.softplus));
+                    store_pair<T>(gx + (t0 + t) * a.sgx + c, fma2(D[m % KC], gv, mul2(st, eb)), pairs, c + 1 < wc);
+                    store_pair<T>(gdt + (t0 + t) * a.sgdt + c, g, pairs, c + 1 < wc);
+                    gD[m % KC] = fma2(gv, xv, gD[m % KC]);
+                    gbias[m % KC] = add2(gbias[m % KC], g);
+                }
             }
         }
         __syncthreads();                                    // ... and read
@@ -398,20 +364,25 @@ sel_backward_kernel(const SelArgs a)
             write_states<NP>(a.grad_state0 + ((long long)s.seq * a.channels + ch) * a.N, e[c], n0, a.N, false);
         }
     }
-    // lanes that hold the same channel
+    // lanes that hold the same pair of channels
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
-        if constexpr (WC < 32) {
 #pragma unroll
-            for (int off = 16; off >= WC; off /= 2) {
-                gD[k] += __shfl_xor_sync(kFullMask, gD[k], off);
-                gbias[k] += __shfl_xor_sync(kFullMask, gbias[k], off);
-            }
+        for (int off = 16; off >= S::P; off /= 2) {
+            gD[k].x += __shfl_xor_sync(kFullMask, gD[k].x, off);
+            gD[k].y += __shfl_xor_sync(kFullMask, gD[k].y, off);
+            gbias[k].x += __shfl_xor_sync(kFullMask, gbias[k].x, off);
+            gbias[k].y += __shfl_xor_sync(kFullMask, gbias[k].y, off);
         }
-        const int c = (lane + 32 * k) % WC;
-        if (c < wc && lane + 32 * k < (WC < 32 ? WC : 32 * KC)) {
-            a.part_D[(long long)u * a.channels + tile.c0 + c] = gD[k];
-            a.part_bias[(long long)u * a.channels + tile.c0 + c] = gbias[k];
+        const int c = 2 * S::cp(k, lane);
+        const long long at = (long long)u * a.channels + tile.c0 + c;
+        if (lane < S::P && c < wc) {
+            a.part_D[at] = gD[k].x;
+            a.part_bias[at] = gbias[k].x;
+        }
+        if (lane < S::P && c + 1 < wc) {
+            a.part_D[at + 1] = gD[k].y;
+            a.part_bias[at + 1] = gbias[k].y;
         }
     }
 }
@@ -468,14 +439,23 @@ sel_sum_channels_kernel(const SelArgs a, int blocks)
     }
 }
 
-template <class T, int NP, int LN>
+template <class T, int LN>
 cudaError_t launch_shape(const SelArgs &a, cudaStream_t st)
 {
-    const dim3 block(32 * kSelWarps);
-    cudaError_t e;
+    const auto kernel = sel_backward_kernel<T, LN>;
+    constexpr size_t bytes = BackLayout<LN>::kBytes;
+    const cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(kernel, dim3((unsigned)((long long)a.max_units * a.cblocks)), dim3(32 * kSelWarps), bytes, st, a);
+}
+
+template <class T>
+cudaError_t launch_type(const SelArgs &a, cudaStream_t st)
+{
+    cudaError_t e = cudaSuccess;
     if (a.seg) {
-        const int cblocks = a.groups * sel_group_blocks(a.channels, a.groups, 32 / LN * 4);
-        e = launch_pdl(sel_carry_kernel<T, NP, LN>, dim3((unsigned)((long long)a.max_units * cblocks)), block, 0, st, a);
+        e = launch_walk_states<T, kCarry>(a, a.max_units, st);
         if (e != cudaSuccess)
             return e;
         const long long n = (long long)a.n_seqs * a.channels * a.N;
@@ -483,22 +463,8 @@ cudaError_t launch_shape(const SelArgs &a, cudaStream_t st)
         if (e != cudaSuccess)
             return e;
     }
-    const auto kernel = sel_backward_kernel<T, NP, LN>;
-    constexpr size_t bytes = BackLayout<NP, LN>::kBytes;
-    e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes);
-    if (e != cudaSuccess)
-        return e;
-    return launch_pdl(kernel, dim3((unsigned)((long long)a.max_units * a.cblocks)), block, bytes, st, a);
-}
-
-template <class T>
-cudaError_t launch_type(const SelArgs &a, cudaStream_t st)
-{
-    cudaError_t e = a.N <= 8     ? launch_shape<T, 4, 2>(a, st)
-                    : a.N <= 16  ? launch_shape<T, 4, 4>(a, st)
-                    : a.N <= 32  ? launch_shape<T, 4, 8>(a, st)
-                    : a.N <= 64  ? launch_shape<T, 4, 16>(a, st)
-                                 : launch_shape<T, 4, 32>(a, st);
+    e = a.N <= 8 ? launch_shape<T, 2>(a, st) : a.N <= 16 ? launch_shape<T, 4>(a, st) : a.N <= 32 ? launch_shape<T, 8>(a, st)
+        : a.N <= 64 ? launch_shape<T, 16>(a, st) : launch_shape<T, 32>(a, st);
     if (e != cudaSuccess)
         return e;
     const long long n = (long long)a.channels * (a.N + 2);
@@ -546,6 +512,7 @@ cudaError_t launch_selective_scan_backward(SelArgs a, int dtype, void *workspace
 {
     const SelShape s = sel_shape(a.channels, a.N, a.groups, true);
     a.cblocks = s.cblocks;
+    a.pairs = sel_pairs(a, dtype);
     a.seg = sel_segment(a.n_seqs, a.n_tokens, s, true);
     a.max_units = sel_max_units(a.n_seqs, a.n_tokens, a.seg);
     unsigned char *w = static_cast<unsigned char *>(workspace);
