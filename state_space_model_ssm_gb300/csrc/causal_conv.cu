@@ -9,13 +9,15 @@
 //   grad s[j,c] = sum_u w[c,u] gv[j-u,c]  (+ the slot's gradient for the last K - 1),
 //   grad w[c,u] = sum_t gv[t,c] s[t+u,c],   grad bias = sum_t gv
 //
-// Bytes bound both: a thread owns V neighbouring channels over a span of a sequence's tokens
-// and keeps the window of inputs (and, backward, K unfinished sums of grad s) in registers, so
-// a row is read once but for K - 1 rows of halo a span.  Backward recomputes v from the
-// window.  Loads of a run of tokens are issued together.  Only the first span of a sequence
-// reads its slot, so it writes it too.  The sums over tokens of grad w and grad bias leave as
-// one row a span and are added in a second kernel in a fixed order.
-#include "layer_common.cuh"
+// Bytes bound both, if the arithmetic is packed: a thread owns two channels (neighbours where
+// rows allow 4-byte words of 16-bit types, 8-byte words of fp32; else two 128 apart, so that single
+// elements are still read side by side) over a span of a sequence's tokens, keeps the window of
+// inputs (and, backward, K unfinished sums of grad s) in registers as packed pairs, and loads
+// the next run of eight tokens while it works on one.  A row is read once but for K - 1 rows of halo a
+// span.  Backward recomputes v from the window.  Only the first span of a sequence reads its
+// slot, so it writes it too.  The sums over tokens of grad w and grad bias leave as one row a
+// span and are added in a second kernel in a fixed order.
+#include "packed.cuh"
 
 namespace ssm {
 
@@ -23,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRun = 8;                       // tokens whose loads are issued together
+constexpr int kPair = 2;                      // channels of a thread
 
 struct ConvArgs {
     const void *x;
@@ -39,8 +42,6 @@ struct ConvArgs {
     float *grad_w, *grad_bias, *grad_state0, *part;      // part [units][K + 1][C]
     long long sgo, sgx;
 };
-
-__device__ __forceinline__ float sigmoid_of(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 __device__ __forceinline__ int seq_len(const ConvArgs &a, int seq, long long &t0)
 {
@@ -84,269 +85,239 @@ __device__ __forceinline__ bool find_span(const ConvArgs &a, int u, int &seq, in
     return false;
 }
 
-// V channels' K - 1 slot entries.
-template <int V, int K>
-__device__ __forceinline__ void read_slot(float (&s)[K > 1 ? K - 1 : 1][V], const float *p)
-{
-    if constexpr (K > 1) {
-        float v[V * (K - 1)];
-        if constexpr (V == 4) {
-#pragma unroll
-            for (int i = 0; i < K - 1; ++i) {
-                const float4 q = reinterpret_cast<const float4 *>(p)[i];
-                v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
-            }
+// A thread's two channels: neighbours, or kThreads apart.
+template <bool PAIRS>
+struct Channels {
+    int c;                                                  // the first
+    bool first, second;                                     // whether they exist
+    __device__ __forceinline__ Channels(int cblock, int C)
+    {
+        c = cblock * kPair * kThreads + (PAIRS ? kPair : 1) * threadIdx.x;
+        first = c < C;
+        second = c + step() < C;
+    }
+    static __device__ __forceinline__ constexpr int step() { return PAIRS ? 1 : kThreads; }
+    __device__ __forceinline__ float2 read(const float *p, long long each) const      // p[c * each], zeros where there is none
+    {
+        return make_float2(first ? p[c * each] : 0.f, second ? p[(c + step()) * each] : 0.f);
+    }
+    __device__ __forceinline__ void write(float *p, long long each, float2 v) const
+    {
+        if (first) p[c * each] = v.x;
+        if (second) p[(c + step()) * each] = v.y;
+    }
+    // of a row of T: loads stay inside the row (a channel that is not there reads the first)
+    template <class T>
+    __device__ __forceinline__ RawPair<T> load(const T *row) const
+    {
+        if constexpr (PAIRS)
+            return load_pair(row + c);
+        else
+            return join_pair<T>(row[c], row[second ? c + kThreads : c]);
+    }
+    template <class T>
+    __device__ __forceinline__ void store(T *row, float2 v) const
+    {
+        if constexpr (PAIRS) {
+            store_word(row + c, v);
         } else {
-#pragma unroll
-            for (int i = 0; i < V * (K - 1); ++i)
-                v[i] = p[i];
+            row[c] = from_float<T>(v.x);
+            if (second)
+                row[c + kThreads] = from_float<T>(v.y);
         }
+    }
+};
+
+// The window in front of token `begin`: slot entries (zeros for a fresh sequence, whose slot is not read)
+// or, in later spans, tokens (a span is longer than the window).
+template <class T, int K, class Ch>
+__device__ __forceinline__ void first_window(float2 (&win)[K > 1 ? K - 1 : 1], const float *slots, const T *x, const ConvArgs &a,
+                                             const Ch &ch, int seq, int begin)
+{
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+    for (int u = 0; u < K - 1; ++u)
+        win[u] = make_float2(0.f, 0.f);
+    if (K == 1)
+        return;
+    if (begin > 0) {
 #pragma unroll
-            for (int u = 0; u < K - 1; ++u)
-                s[u][i] = v[i * (K - 1) + u];
+        for (int u = 0; u < K - 1; ++u)
+            win[u] = pair_of<T>(ch.load(x + (long long)(begin - (K - 1) + u) * a.sx));
+    } else if (slots && a.resume[seq] != 0) {
+#pragma unroll
+        for (int u = 0; u < K - 1; ++u)
+            win[u] = ch.read(slots + (long long)seq * a.C * (K - 1) + u, K - 1);
     }
 }
 
-template <int V, int K>
-__device__ __forceinline__ void write_slot(float *p, const float (&s)[K > 1 ? K - 1 : 1][V])
+// v of a token, and the window moved on to it.
+template <int K>
+__device__ __forceinline__ float2 taps(const float2 (&w)[K], float2 bias, float2 (&win)[K > 1 ? K - 1 : 1], float2 now)
 {
-    if constexpr (K > 1) {
-        float v[V * (K - 1)];
+    float2 v = fma2(w[K - 1], now, bias);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+    for (int u = 0; u < K - 1; ++u)
+        v = fma2(w[u], win[u], v);
 #pragma unroll
-            for (int u = 0; u < K - 1; ++u)
-                v[i * (K - 1) + u] = s[u][i];
-        if constexpr (V == 4) {
-#pragma unroll
-            for (int i = 0; i < K - 1; ++i)
-                reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V * (K - 1); ++i)
-                p[i] = v[i];
-        }
-    }
+    for (int u = 0; u + 1 < K - 1; ++u)
+        win[u] = win[u + 1];
+    if (K > 1)
+        win[K > 1 ? K - 2 : 0] = now;
+    return v;
 }
 
-// The slot's entries as inputs: zeros for a fresh sequence (whose slot is not read).
-template <int V, int K>
-__device__ __forceinline__ void first_window(float (&win)[K > 1 ? K - 1 : 1][V], const float *slots, const ConvArgs &a,
-                                             int seq, int c0)
-{
-#pragma unroll
-    for (int u = 0; u < (K > 1 ? K - 1 : 1); ++u)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            win[u][i] = 0.f;
-    if (K > 1 && slots && a.resume[seq] != 0)
-        read_slot<V, K>(win, slots + ((long long)seq * a.C + c0) * (K - 1));
-}
-
-template <class T, int V, int K>
+template <class T, bool PAIRS, int K>
 __global__ void __launch_bounds__(kThreads)
 causal_conv_kernel(const ConvArgs a)
 {
     griddep_entry();
-    const int unit = blockIdx.x / a.cblocks, c0 = ((blockIdx.x - unit * a.cblocks) * kThreads + threadIdx.x) * V;
+    const int unit = blockIdx.x / a.cblocks;
+    const Channels<PAIRS> ch(blockIdx.x - unit * a.cblocks, a.C);
     int seq, k;
-    if (!find_span(a, unit, seq, k) || c0 >= a.C)
+    if (!find_span(a, unit, seq, k) || !ch.first)
         return;
     long long t0;
     const int len = seq_len(a, seq, t0), begin = k * a.span, end = min(len, begin + a.span);
-    float w[K][V], bias[V], win[K > 1 ? K - 1 : 1][V];
+    float2 w[K], win[K > 1 ? K - 1 : 1];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int u = 0; u < K; ++u)
+        w[u] = ch.read(a.w + u, K);
+    const float2 bias = a.bias ? ch.read(a.bias, 1) : make_float2(0.f, 0.f);
+    const T *x = static_cast<const T *>(a.x) + t0 * a.sx;
+    T *out = static_cast<T *>(a.out) + t0 * a.so;
+    RawPair<T> next[kRun];
+    auto fetch = [&](int b) {
 #pragma unroll
-        for (int u = 0; u < K; ++u)
-            w[u][i] = __ldg(a.w + (long long)(c0 + i) * K + u);
-        bias[i] = a.bias ? __ldg(a.bias + c0 + i) : 0.f;
-    }
-    const T *x = static_cast<const T *>(a.x) + t0 * a.sx + c0;
-    T *out = static_cast<T *>(a.out) + t0 * a.so + c0;
-    if (k == 0) {
-        first_window<V, K>(win, a.state, a, seq, c0);
-        if constexpr (K > 1) {                              // the stream's last K - 1: of the tokens, or still of the slot
-            float last[K - 1][V];
+        for (int r = 0; r < kRun; ++r)
+            next[r] = ch.load(x + (long long)min(b + r, end - 1) * a.sx);
+    };
+    if (begin < end)
+        fetch(begin);
+    first_window<T, K>(win, a.state, x, a, ch, seq, begin);
+    if (K > 1 && k == 0) {                                  // the stream's last K - 1: of the tokens, or still of the slot
+        float *slot = a.state + (long long)seq * a.C * (K - 1);
 #pragma unroll
-            for (int u = 0; u < K - 1; ++u) {
-                const int t = len - (K - 1) + u;            // token, or slot entry t + K - 1
-                if (t >= 0) {
-                    const Vec<T, V> v = load_vec<T, V>(x + t * a.sx);
+        for (int u = 0; u < K - 1; ++u) {
+            const int t = len - (K - 1) + u;                // token, or slot entry t + K - 1
+            float2 v = make_float2(0.f, 0.f);
+            if (t >= 0)
+                v = pair_of<T>(ch.load(x + t * a.sx));
+            else
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        last[u][i] = to_float(v.v[i]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < K - 1; ++e)
-                        if (e == t + K - 1)
-#pragma unroll
-                            for (int i = 0; i < V; ++i)
-                                last[u][i] = win[e][i];
-                }
-            }
-            write_slot<V, K>(a.state + ((long long)seq * a.C + c0) * (K - 1), last);
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < K - 1; ++u) {                   // (a span is longer than the window)
-            const Vec<T, V> v = load_vec<T, V>(x + (long long)(begin - (K - 1) + u) * a.sx);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                win[u][i] = to_float(v.v[i]);
+                for (int e = 0; e < K - 1; ++e)
+                    v = e == t + K - 1 ? win[e] : v;
+            ch.write(slot + u, K - 1, v);
         }
     }
     for (int b = begin; b < end; b += kRun) {
-        Vec<T, V> in[kRun];
+        RawPair<T> in[kRun];
 #pragma unroll
         for (int r = 0; r < kRun; ++r)
-            if (b + r < end)
-                in[r] = load_vec<T, V>(x + (long long)(b + r) * a.sx);
+            in[r] = next[r];
+        if (b + kRun < end)
+            fetch(b + kRun);
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
-            if (b + r >= end)
-                break;
-            Vec<T, V> o;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float now = to_float(in[r].v[i]);
-                float v = fmaf(w[K - 1][i], now, bias[i]);
-#pragma unroll
-                for (int u = 0; u < K - 1; ++u)
-                    v = fmaf(w[u][i], win[u][i], v);
-#pragma unroll
-                for (int u = 0; u + 1 < K - 1; ++u)
-                    win[u][i] = win[u + 1][i];
-                if (K > 1)
-                    win[K > 1 ? K - 2 : 0][i] = now;
-                o.v[i] = from_float<T>(a.silu ? v * sigmoid_of(v) : v);
-            }
-            store_vec<T, V>(out + (long long)(b + r) * a.so, o);
+            const float2 v = taps<K>(w, bias, win, pair_of<T>(in[r]));
+            if (b + r < end)
+                ch.store(out + (long long)(b + r) * a.so, a.silu ? mul2(v, sigmoid2(v)) : v);
         }
     }
 }
 
-template <class T, int V, int K>
+template <class T, bool PAIRS, int K>
 __global__ void __launch_bounds__(kThreads)
 causal_conv_backward_kernel(const ConvArgs a)
 {
     griddep_entry();
-    const int unit = blockIdx.x / a.cblocks, c0 = ((blockIdx.x - unit * a.cblocks) * kThreads + threadIdx.x) * V;
+    const int unit = blockIdx.x / a.cblocks;
+    const Channels<PAIRS> ch(blockIdx.x - unit * a.cblocks, a.C);
     int seq, k;
-    if (!find_span(a, unit, seq, k) || c0 >= a.C)
+    if (!find_span(a, unit, seq, k) || !ch.first)
         return;
     long long t0;
     const int len = seq_len(a, seq, t0), begin = k * a.span, end = min(len, begin + a.span);
-    float w[K][V], bias[V], gw[K][V], gb[V], win[K > 1 ? K - 1 : 1][V];
-    float sum[K][V];                                        // unfinished gradients of stream entries t .. t + K - 1
+    const float2 zero = make_float2(0.f, 0.f);
+    float2 w[K], gw[K], gb = zero, win[K > 1 ? K - 1 : 1];
+    float2 sum[K];                                          // unfinished gradients of stream entries t .. t + K - 1
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int u = 0; u < K; ++u) {
-            w[u][i] = __ldg(a.w + (long long)(c0 + i) * K + u);
-            gw[u][i] = sum[u][i] = 0.f;
-        }
-        bias[i] = a.bias ? __ldg(a.bias + c0 + i) : 0.f;
-        gb[i] = 0.f;
+    for (int u = 0; u < K; ++u) {
+        w[u] = ch.read(a.w + u, K);
+        gw[u] = sum[u] = zero;
     }
-    const T *x = static_cast<const T *>(a.x) + t0 * a.sx + c0, *go = static_cast<const T *>(a.grad_out) + t0 * a.sgo + c0;
-    T *gx = static_cast<T *>(a.grad_x) + t0 * a.sgx + c0;
-    if (k == 0) {
-        first_window<V, K>(win, a.state0, a, seq, c0);
-    } else {
-#pragma unroll
-        for (int u = 0; u < K - 1; ++u) {
-            const Vec<T, V> v = load_vec<T, V>(x + (long long)(begin - (K - 1) + u) * a.sx);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                win[u][i] = to_float(v.v[i]);
-        }
-    }
-    const long long slot = ((long long)seq * a.C + c0) * (K - 1);
+    const float2 bias = a.bias ? ch.read(a.bias, 1) : zero;
+    const T *x = static_cast<const T *>(a.x) + t0 * a.sx, *go = static_cast<const T *>(a.grad_out) + t0 * a.sgo;
+    T *gx = static_cast<T *>(a.grad_x) + t0 * a.sgx;
+    const long long slot = (long long)seq * a.C * (K - 1);
     const bool resumed = a.grad_state0 && a.resume[seq] != 0;
     const int stop = end + K - 1;                           // the last entries need the tokens behind the span
-    for (int b = begin; b < stop; b += kRun) {
-        Vec<T, V> in[kRun], g[kRun];
+    RawPair<T> next_x[kRun], next_g[kRun];
+    auto fetch = [&](int b) {
 #pragma unroll
-        for (int r = 0; r < kRun; ++r)
-            if (b + r < stop && b + r < len) {
-                in[r] = load_vec<T, V>(x + (long long)(b + r) * a.sx);
-                g[r] = load_vec<T, V>(go + (long long)(b + r) * a.sgo);
-            }
+        for (int r = 0; r < kRun; ++r) {
+            const long long t = min(b + r, min(stop, len) - 1);
+            next_x[r] = ch.load(x + t * a.sx);
+            next_g[r] = ch.load(go + t * a.sgo);
+        }
+    };
+    if (begin < end)
+        fetch(begin);
+    first_window<T, K>(win, a.state0, x, a, ch, seq, begin);
+    for (int b = begin; b < stop; b += kRun) {
+        RawPair<T> in[kRun], g[kRun];
+#pragma unroll
+        for (int r = 0; r < kRun; ++r) {
+            in[r] = next_x[r];
+            g[r] = next_g[r];
+        }
+        if (b + kRun < stop && b + kRun < len)
+            fetch(b + kRun);
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
             const int t = b + r;
-            if (t >= stop)
-                break;
-            if (t < len) {
+            if (t < stop && t < len) {
+                const float2 now = pair_of<T>(in[r]);
+                float2 before[K > 1 ? K - 1 : 1], gv = pair_of<T>(g[r]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float now = to_float(in[r].v[i]);
-                    float v = fmaf(w[K - 1][i], now, bias[i]), gv = to_float(g[r].v[i]);
+                for (int u = 0; u < K - 1; ++u)
+                    before[u] = win[u];
+                const float2 v = taps<K>(w, bias, win, now);
+                if (a.silu) {
+                    const float2 s = sigmoid2(v);
+                    gv = mul2(gv, fma2(mul2(v, s), make_float2(1.f - s.x, 1.f - s.y), s));
+                }
+                if (t < end) {
+                    gb = add2(gb, gv);
 #pragma unroll
                     for (int u = 0; u < K - 1; ++u)
-                        v = fmaf(w[u][i], win[u][i], v);
-                    if (a.silu) {
-                        const float s = sigmoid_of(v);
-                        gv *= fmaf(v * s, 1.f - s, s);
-                    }
-                    if (t < end) {
-                        gb[i] += gv;
-#pragma unroll
-                        for (int u = 0; u < K - 1; ++u)
-                            gw[u][i] = fmaf(gv, win[u][i], gw[u][i]);
-                        gw[K - 1][i] = fmaf(gv, now, gw[K - 1][i]);
-                    }
-#pragma unroll
-                    for (int u = 0; u < K; ++u)
-                        sum[u][i] = fmaf(w[u][i], gv, sum[u][i]);
-#pragma unroll
-                    for (int u = 0; u + 1 < K - 1; ++u)
-                        win[u][i] = win[u + 1][i];
-                    if (K > 1)
-                        win[K > 1 ? K - 2 : 0][i] = now;
+                        gw[u] = fma2(gv, before[u], gw[u]);
+                    gw[K - 1] = fma2(gv, now, gw[K - 1]);
                 }
+#pragma unroll
+                for (int u = 0; u < K; ++u)
+                    sum[u] = fma2(w[u], gv, sum[u]);
             }
             // stream entry t is complete: token t - (K - 1), or entry t of the slot
-            if (t >= begin + K - 1 || k == 0) {
-                float done[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    done[i] = sum[0][i];
-                    if (K > 1 && t >= len && a.grad_state)
-                        done[i] += a.grad_state[slot + i * (K - 1) + t - len];
-                }
-                if (t >= K - 1) {
-                    Vec<T, V> o;
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        o.v[i] = from_float<T>(done[i]);
-                    store_vec<T, V>(gx + (long long)(t - (K - 1)) * a.sgx, o);
-                } else if (a.grad_state0) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        a.grad_state0[slot + i * (K - 1) + t] = resumed ? done[i] : 0.f;
-                }
+            if (t < stop && (t >= begin + K - 1 || k == 0)) {
+                float2 done = sum[0];
+                if (K > 1 && t >= len && a.grad_state)
+                    done = add2(done, ch.read(a.grad_state + slot + t - len, K - 1));
+                if (t >= K - 1)
+                    ch.store(gx + (long long)(t - (K - 1)) * a.sgx, done);
+                else if (a.grad_state0)
+                    ch.write(a.grad_state0 + slot + t, K - 1, resumed ? done : zero);
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-#pragma unroll
-                for (int u = 0; u + 1 < K; ++u)
-                    sum[u][i] = sum[u + 1][i];
-                sum[K - 1][i] = 0.f;
-            }
+            for (int u = 0; u + 1 < K; ++u)
+                sum[u] = sum[u + 1];
+            sum[K - 1] = zero;
         }
     }
-    float *part = a.part + (long long)unit * (K + 1) * a.C + c0;
+    float *part = a.part + (long long)unit * (K + 1) * a.C;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int u = 0; u < K; ++u)
-            part[(long long)u * a.C + i] = gw[u][i];
-        part[(long long)K * a.C + i] = gb[i];
-    }
+    for (int u = 0; u < K; ++u)
+        ch.write(part + (long long)u * a.C, 1, gw[u]);
+    ch.write(part + (long long)K * a.C, 1, gb);
 }
 
 // grad w and grad bias: 32 channels of one tap a block, the spans over 8 lanes of threads.
@@ -386,31 +357,31 @@ causal_conv_sum_kernel(const ConvArgs a, int K)
     }
 }
 
-template <class T, int V, int K>
+template <class T, bool PAIRS, int K>
 cudaError_t launch_kernel(ConvArgs a, bool backward, cudaStream_t st)
 {
-    a.cblocks = (a.C + kThreads * V - 1) / (kThreads * V);
+    a.cblocks = (a.C + kPair * kThreads - 1) / (kPair * kThreads);
     const dim3 grid((unsigned)((long long)a.units * a.cblocks)), block(kThreads);
     if (!backward)
-        return launch_pdl(causal_conv_kernel<T, V, K>, grid, block, 0, st, a);
-    const cudaError_t e = launch_pdl(causal_conv_backward_kernel<T, V, K>, grid, block, 0, st, a);
+        return launch_pdl(causal_conv_kernel<T, PAIRS, K>, grid, block, 0, st, a);
+    const cudaError_t e = launch_pdl(causal_conv_backward_kernel<T, PAIRS, K>, grid, block, 0, st, a);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(causal_conv_sum_kernel, dim3((a.C + 31) / 32, K + 1), dim3(256), 0, st, a, K);
 }
 
-template <class T, int V>
+template <class T, bool PAIRS>
 cudaError_t launch_taps(const ConvArgs &a, int K, bool backward, cudaStream_t st)
 {
     switch (K) {
-    case 1: return launch_kernel<T, V, 1>(a, backward, st);
-    case 2: return launch_kernel<T, V, 2>(a, backward, st);
-    case 3: return launch_kernel<T, V, 3>(a, backward, st);
-    case 4: return launch_kernel<T, V, 4>(a, backward, st);
-    case 5: return launch_kernel<T, V, 5>(a, backward, st);
-    case 6: return launch_kernel<T, V, 6>(a, backward, st);
-    case 7: return launch_kernel<T, V, 7>(a, backward, st);
-    case 8: return launch_kernel<T, V, 8>(a, backward, st);
+    case 1: return launch_kernel<T, PAIRS, 1>(a, backward, st);
+    case 2: return launch_kernel<T, PAIRS, 2>(a, backward, st);
+    case 3: return launch_kernel<T, PAIRS, 3>(a, backward, st);
+    case 4: return launch_kernel<T, PAIRS, 4>(a, backward, st);
+    case 5: return launch_kernel<T, PAIRS, 5>(a, backward, st);
+    case 6: return launch_kernel<T, PAIRS, 6>(a, backward, st);
+    case 7: return launch_kernel<T, PAIRS, 7>(a, backward, st);
+    case 8: return launch_kernel<T, PAIRS, 8>(a, backward, st);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -418,21 +389,19 @@ cudaError_t launch_taps(const ConvArgs &a, int K, bool backward, cudaStream_t st
 template <class T>
 cudaError_t launch_type(const ConvArgs &a, int K, bool backward, cudaStream_t st)
 {
-    // four channels a thread where every row and slot allows it
-    const uintptr_t rows = sizeof(T) * 4;
-    auto fits = [&](const void *p, long long stride) {
-        return (reinterpret_cast<uintptr_t>(p) % rows) == 0 && stride * (long long)sizeof(T) % (long long)rows == 0;
+    auto even = [&](const void *p, long long stride) {
+        return (reinterpret_cast<uintptr_t>(p) % (2 * sizeof(T))) == 0 && stride % 2 == 0;
     };
-    bool wide = a.C % 4 == 0 && (reinterpret_cast<uintptr_t>(backward ? a.state0 : a.state) & 15) == 0 && fits(a.x, a.sx);
-    wide = wide && (backward ? fits(a.grad_out, a.sgo) && fits(a.grad_x, a.sgx) : fits(a.out, a.so));
-    return wide ? launch_taps<T, 4>(a, K, backward, st) : launch_taps<T, 1>(a, K, backward, st);
+    bool pairs = a.C % 2 == 0 && even(a.x, a.sx);
+    pairs = pairs && (backward ? even(a.grad_out, a.sgo) && even(a.grad_x, a.sgx) : even(a.out, a.so));
+    return pairs ? launch_taps<T, true>(a, K, backward, st) : launch_taps<T, false>(a, K, backward, st);
 }
 
-// Tokens of a span: threads of about one wave, whole runs.
+// Tokens of a span: about two rounds of resident threads, whole runs.
 int span_of(int n_tokens, int channels)
 {
-    const long long each = (long long)n_tokens * ((channels + 3) / 4) / (kSms * 1024);
-    return (int)(each < 32 ? 32 : each > 256 ? 256 : (each + kRun - 1) / kRun * kRun);
+    const long long each = (long long)n_tokens * ((channels + kPair - 1) / kPair) / (kSms * 1280);
+    return (int)(each < 32 ? 32 : each > 512 ? 512 : (each + kRun - 1) / kRun * kRun);
 }
 
 int units_of(int n_seqs, int n_tokens, int span) { return n_tokens <= span ? n_seqs : n_seqs + n_tokens / span; }
@@ -446,7 +415,7 @@ size_t causal_conv_backward_workspace_bytes(int n_seqs, int n_tokens, int channe
 
 long long causal_conv_blocks(int n_seqs, int n_tokens, int channels)
 {
-    return (long long)units_of(n_seqs, n_tokens, span_of(n_tokens, channels)) * ((channels + kThreads - 1LL) / kThreads);
+    return (long long)units_of(n_seqs, n_tokens, span_of(n_tokens, channels)) * ((channels + kPair * kThreads - 1LL) / (kPair * kThreads));
 }
 
 cudaError_t launch_causal_conv(const CausalConv &c, bool backward, cudaStream_t st)

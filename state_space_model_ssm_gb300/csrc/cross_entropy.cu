@@ -22,6 +22,7 @@
 // 2^-29 keep all their bits; the sums get the factors back in fp32.
 #include <atomic>
 
+#include "packed.cuh"
 #include "pair_gemm.cuh"
 
 namespace ssm {
@@ -29,7 +30,9 @@ namespace ssm {
 namespace {
 
 constexpr int kCountRows = 1024;              // rows of a block of the counting kernel
-constexpr int kPackRows = 16;                 // rows of a block of the packing kernel
+constexpr int kPackRows = 8;                  // rows of a block of the packing kernel, a warp each
+constexpr int kCountAlone = 8192;             // rows that every packing block counts by itself, without that kernel
+constexpr int kJoinLanes = 32;                // threads that join a row's parts
 constexpr int kGroupM = 16;                   // row tiles that share the vocabulary's rows in L2
 
 struct LossArgs {
@@ -41,8 +44,10 @@ struct LossArgs {
     long long sh, sw, sgh, sgw, ignore;
     int dp;                                   // packed row length
     // workspace
-    int *counts;                              // [blocks + 1] kept rows of each kCountRows
+    int *counts;                              // [blocks] kept rows of each kCountRows
     float *tops;                              // [blocks] largest |grad_loss| of them
+    int *kept;                                // rows that are kept
+    float *top;                               // largest |grad_loss| of them
     int *index;                               // [T] row of each kept one
     int *label;                               // [T rounded up to a tile] its target, -1 past the end
     float *scale;                             // its grad_loss relative to the largest, times the type's factor
@@ -62,63 +67,62 @@ __device__ __forceinline__ long long target_of(const LossArgs &a, int t)
     return a.wide ? static_cast<const long long *>(a.target)[t] : (long long)static_cast<const int32_t *>(a.target)[t];
 }
 
-// Kept rows, and the largest |grad_loss| of them (a NaN counts as none: its row is NaN by itself).
-__global__ void __launch_bounds__(256)
-loss_count_kernel(const LossArgs a)
+// A block's sum and maximum, for all threads.
+struct Counted {
+    int n;
+    float m;
+};
+
+__device__ __forceinline__ Counted block_sum(int n, float m)
 {
-    griddep_entry();
     __shared__ int ns[8];
     __shared__ float ms[8];
-    const int tid = threadIdx.x, t0 = blockIdx.x * kCountRows;
-    int n = 0;
-    float m = 0.f;
-    for (int t = t0 + tid; t < min(a.T, t0 + kCountRows); t += 256)
-        if (target_of(a, t) != a.ignore) {
-            ++n;
-            if (a.grad_loss)
-                m = fmaxf(m, fabsf(a.grad_loss[t]));
-        }
 #pragma unroll
     for (int off = 16; off >= 1; off /= 2) {
         n += __shfl_xor_sync(kFullMask, n, off);
         m = fmaxf(m, __shfl_xor_sync(kFullMask, m, off));
     }
-    if ((tid & 31) == 0) {
-        ns[tid >> 5] = n;
-        ms[tid >> 5] = m;
+    __syncthreads();                                        // (of an earlier call)
+    if ((threadIdx.x & 31) == 0) {
+        ns[threadIdx.x >> 5] = n;
+        ms[threadIdx.x >> 5] = m;
     }
     __syncthreads();
-    if (tid == 0) {
-        for (int i = 1; i < 8; ++i) {
-            n += ns[i];
-            m = fmaxf(m, ms[i]);
-        }
-        a.counts[blockIdx.x] = n;
-        a.tops[blockIdx.x] = m;
+    Counted c{0, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        c.n += ns[i];
+        c.m = fmaxf(c.m, ms[i]);
     }
+    return c;
 }
 
-// Sum of the counts of the blocks before `block` (all threads of a warp), and the largest top of all.
-__device__ __forceinline__ int counted(const LossArgs &a, int block)
+// Kept ones of rows [t0, t1), and the largest |grad_loss| of them (a NaN counts as none: its row is NaN by
+// itself).
+__device__ __forceinline__ Counted count_rows(const LossArgs &a, int t0, int t1, bool tops)
 {
     int n = 0;
-    for (int i = threadIdx.x & 31; i < block; i += 32)
-        n += a.counts[i];
-#pragma unroll
-    for (int off = 16; off >= 1; off /= 2)
-        n += __shfl_xor_sync(kFullMask, n, off);
-    return n;
+    float m = 0.f;
+#pragma unroll 4
+    for (int t = t0 + threadIdx.x; t < t1; t += 256) {
+        const bool keep = target_of(a, t) != a.ignore;
+        n += keep ? 1 : 0;
+        if (tops)
+            m = fmaxf(m, keep ? fabsf(a.grad_loss[t]) : 0.f);
+    }
+    return block_sum(n, m);
 }
 
-__device__ __forceinline__ float largest(const LossArgs &a)
+__global__ void __launch_bounds__(256)
+loss_count_kernel(const LossArgs a)
 {
-    float m = 0.f;
-    for (int i = threadIdx.x & 31; i < a.blocks; i += 32)
-        m = fmaxf(m, a.tops[i]);
-#pragma unroll
-    for (int off = 16; off >= 1; off /= 2)
-        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, off));
-    return m;
+    griddep_entry();
+    const int t0 = blockIdx.x * kCountRows;
+    const Counted c = count_rows(a, t0, min(a.T, t0 + kCountRows), a.grad_loss != nullptr);
+    if (threadIdx.x == 0) {
+        a.counts[blockIdx.x] = c.n;
+        a.tops[blockIdx.x] = c.m;
+    }
 }
 
 // Kept rows back to back, zeros after them up to a whole tile; outputs of ignored rows.
@@ -127,66 +131,84 @@ __global__ void __launch_bounds__(256)
 loss_pack_kernel(const LossArgs a)
 {
     griddep_entry();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = blockIdx.x * kPackRows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = blockIdx.x * kPackRows, r = r0 + warp;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.h) | (uintptr_t)(a.sh * 2)) & 15) == 0;
-    T *hp = static_cast<T *>(a.hp);
-    const float top = a.grad_loss ? largest(a) : 0.f;
-    int before = 0, at_block = -1;
-    for (int r = r0 + warp; r < r0 + kPackRows; r += 8) {
-        const bool real = r < a.T;
-        const long long label = real ? target_of(a, r) : 0;
-        if (real && label == a.ignore) {
-            if (lane == 0 && a.loss)
-                a.loss[r] = a.lse[r] = 0.f;
-            if (a.grad_h)
-                for (int d = lane; d < a.D; d += 32)
-                    static_cast<T *>(a.grad_h)[r * a.sgh + d] = from_float<T>(0.f);
-            continue;
+    // kept rows before this block's, and of all of them (for the gradient's scale, and behind the last row)
+    int before;
+    Counted all;
+    if (a.T <= kCountAlone) {
+        before = count_rows(a, 0, min(r0, a.T), false).n;
+        all = count_rows(a, min(r0, a.T), a.T, false);
+        all.n += before;
+        if (a.grad_loss)
+            all.m = count_rows(a, 0, a.T, true).m;
+    } else {
+        const int whole = min(r0, a.T) / kCountRows;
+        int n = 0, every = 0;
+        float m = 0.f;
+        for (int i = threadIdx.x; i < a.blocks; i += 256) {
+            const int c = a.counts[i];
+            every += c;
+            n += i < whole ? c : 0;
+            m = fmaxf(m, a.tops[i]);
         }
-        // kept rows before this one; past the last row: rows of zeros behind all kept ones
-        const int block = real ? r / kCountRows : a.blocks;
-        if (block != at_block) {
-            before = counted(a, block);
-            at_block = block;
-        }
-        int at = before;
-        if (real) {
-            int n = 0;
-            for (int t = block * kCountRows + lane; t < r; t += 32)
-                n += target_of(a, t) != a.ignore ? 1 : 0;
+        before = block_sum(n, 0.f).n + count_rows(a, whole * kCountRows, min(r0, a.T), false).n;
+        all = block_sum(every, m);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.kept = all.n;
+        *a.top = all.m;
+    }
+    const bool real = r < a.T;
+    const long long label = real ? target_of(a, r) : 0;
+    if (real && label == a.ignore) {
+        if (lane == 0 && a.loss)
+            a.loss[r] = a.lse[r] = 0.f;
+        if (a.grad_h)
+            for (int d = lane; d < a.D; d += 32)
+                static_cast<T *>(a.grad_h)[r * a.sgh + d] = from_float<T>(0.f);
+        return;
+    }
+    int at = before;
+    if (real) {
+        const unsigned keep = __ballot_sync(kFullMask, lane < warp && target_of(a, r0 + min(lane, warp)) != a.ignore);
+        at += __popc(keep);
+    } else {
+        at = all.n + r - a.T;
+        if (at >= (all.n + pair::kTileM - 1) / pair::kTileM * pair::kTileM)
+            return;
+    }
+    const T *src = static_cast<const T *>(a.h) + (real ? r * a.sh : 0);
+    T *dst = static_cast<T *>(a.hp) + (long long)at * a.dp;
+    constexpr int kAhead = 4;
+    for (int d0 = lane * 8; d0 < a.dp; d0 += 256 * kAhead) {
+        Vec<T, 8> v[kAhead];
 #pragma unroll
-            for (int off = 16; off >= 1; off /= 2)
-                n += __shfl_xor_sync(kFullMask, n, off);
-            at += n;
-        } else {
-            at += r - a.T;
-            if (at >= (before + pair::kTileM - 1) / pair::kTileM * pair::kTileM)
-                continue;
-        }
-        const T *src = static_cast<const T *>(a.h) + (real ? r * a.sh : 0);
-        T *dst = hp + (long long)at * a.dp;
-        for (int d = lane * 8; d < a.dp; d += 256) {
-            Vec<T, 8> v;
+        for (int k = 0; k < kAhead; ++k) {
+            const int d = d0 + 256 * k;
             if (real && vec && d + 8 <= a.D) {
-                v = load_vec<T, 8>(src + d);
+                v[k] = load_vec<T, 8>(src + d);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v.v[i] = real && d + i < a.D ? src[d + i] : from_float<T>(0.f);
+                    v[k].v[i] = real && d + i < a.D ? src[d + i] : from_float<T>(0.f);
             }
-            store_vec<T, 8>(dst + d, v);
         }
-        if (lane == 0) {
-            const bool in = label >= 0 && label < a.V;
-            a.label[at] = real && in ? (int)label : -1;
-            if (real)
-                a.index[at] = r;
-            if (a.grad_loss) {
-                // a target outside the vocabulary has no loss: NaN
-                const float g = real ? a.grad_loss[r] : 0.f;
-                a.scale[at] = real && !in ? __int_as_float(0x7fc00000) : g == 0.f ? 0.f : g / top * a.factor;
-                a.row_lse[at] = real ? a.lse_in[r] : 0.f;
-            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (d0 + 256 * k < a.dp)
+                store_vec<T, 8>(dst + d0 + 256 * k, v[k]);
+    }
+    if (lane == 0) {
+        const bool in = label >= 0 && label < a.V;
+        a.label[at] = real && in ? (int)label : -1;
+        if (real)
+            a.index[at] = r;
+        if (a.grad_loss) {
+            // a target outside the vocabulary has no loss: NaN
+            const float g = real ? a.grad_loss[r] : 0.f;
+            a.scale[at] = real && !in ? __int_as_float(0x7fc00000) : g == 0.f ? 0.f : g / all.m * a.factor;
+            a.row_lse[at] = real ? a.lse_in[r] : 0.f;
         }
     }
 }
@@ -208,15 +230,6 @@ loss_pack_weight_kernel(const LossArgs a)
     for (int e = 0; e < 8; ++e)
         v.v[e] = d + e < a.D ? src[e] : from_float<T>(0.f);
     store_vec<T, 8>(static_cast<T *>(a.wp) + r * a.dp + d, v);
-}
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float v)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
 }
 
 // Largest logit (times log2 e) and the sum of the exponentials above it, of 128 columns of a row.
@@ -272,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_stats_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, const __grid_constant__ CUtensorMap wmap)
 {
     griddep_entry();
-    const int rows = counted(a, a.blocks);
+    const int rows = *a.kept;
     pair::run<BF16, false, false>(pair::Shape{rows, a.V, a.D}, kGroupM, hmap, wmap, a.fail_waits, StatsEpilogue{a, rows});
 }
 
@@ -309,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_grad_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, const __grid_constant__ CUtensorMap wmap)
 {
     griddep_entry();
-    const int rows = counted(a, a.blocks);
+    const int rows = *a.kept;
     pair::run<BF16, false, false>(pair::Shape{rows, a.vp, a.D}, kGroupM, hmap, wmap, a.fail_waits, GradEpilogue<T>{a});
 }
 
@@ -373,8 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_hidden_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap wmap)
 {
     griddep_entry();
-    const int rows = counted(a, a.blocks);
-    const HiddenEpilogue<T> epi{a, rows, largest(a) / a.factor};
+    const int rows = *a.kept;
+    const HiddenEpilogue<T> epi{a, rows, *a.top / a.factor};
     pair::run<BF16, false, true>(pair::Shape{rows, a.D, min(a.vp, a.V - a.v0)}, kGroupM, gmap, wmap, a.fail_waits, epi);
 }
 
@@ -402,51 +415,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_weight_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap hmap)
 {
     griddep_entry();
-    const int rows = counted(a, a.blocks);
-    const WeightEpilogue<T> epi{a, largest(a) / a.factor};
+    const int rows = *a.kept;
+    const WeightEpilogue<T> epi{a, *a.top / a.factor};
     pair::run<BF16, true, true>(pair::Shape{min(a.vp, a.V - a.v0), a.D, rows}, kGroupM, gmap, hmap, a.fail_waits, epi);
 }
 
-// lse and loss of every kept row from its parts: 32 rows a block, the parts over 8 lanes of threads.
-__global__ void __launch_bounds__(256)
+// (largest logit, sum) of two disjoint sets of columns.
+__device__ __forceinline__ float2 join(float2 p, float2 q)
+{
+    const float top = fmaxf(p.x, q.x);
+    if (p.x != p.x || q.x != q.x)                           // a wait gave up
+        return make_float2(__int_as_float(0x7fc00000), 0.f);
+    if (top == -INFINITY)
+        return make_float2(top, p.y + q.y);
+    return make_float2(top, p.y * ex2(p.x - top) + q.y * ex2(q.x - top));
+}
+
+// lse and loss of every kept row from its parts: 32 rows a block, the parts over 32 warps.
+__global__ void __launch_bounds__(32 * kJoinLanes)
 loss_join_kernel(const LossArgs a, int parts)
 {
     griddep_entry();
-    __shared__ float2 sh[8][32];
+    __shared__ float2 sh[kJoinLanes][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
-    const int rows = counted(a, a.blocks);
+    const int rows = *a.kept;
     if (blockIdx.x * 32 >= rows)
         return;
-    float m = -INFINITY, s = 0.f;
-    bool bad = false;
-    if (row < rows)
-        for (int p = warp; p < parts; p += 8) {
-            const float2 q = a.part[(long long)p * a.t_pad + row];
-            bad = bad || q.x != q.x || q.y != q.y;
-            const float top = fmaxf(m, q.x);
-            if (top == -INFINITY)
-                continue;
-            s = s * ex2(m - top) + q.y * ex2(q.x - top);
-            m = top;
-        }
-    sh[warp][lane] = make_float2(bad ? __int_as_float(0x7fc00000) : m, s);
-    __syncthreads();
-    if (warp != 0 || row >= rows)
-        return;
-    for (int w = 1; w < 8; ++w) {
-        const float2 q = sh[w][lane];
-        bad = bad || q.x != q.x;
-        const float top = fmaxf(m, q.x);
-        if (top == -INFINITY)
-            continue;
-        s = s * ex2(m - top) + q.y * ex2(q.x - top);
-        m = top;
+    constexpr int kRun = 8;                                 // parts whose loads are issued together
+    float2 s = make_float2(-INFINITY, 0.f);
+    for (int p0 = warp; p0 < parts; p0 += kJoinLanes * kRun) {
+        float2 q[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+            q[i] = a.part[(long long)min(p0 + i * kJoinLanes, parts - 1) * a.t_pad + min(row, rows - 1)];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+            if (p0 + i * kJoinLanes < parts)
+                s = join(s, q[i]);
     }
-    // log s: s is at least 1 but for the approximate exponentials
-    const float lse = bad ? __int_as_float(0x7fc00000) : fmaf(m, kLn2, logf(s));
-    const int t = a.index[row], label = a.label[row];
+    sh[warp][lane] = s;
+    __syncthreads();
+    // a warp's lanes join the 32 parts of one row
+    s = sh[lane][warp];
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2)
+        s = join(s, make_float2(__shfl_xor_sync(kFullMask, s.x, off), __shfl_xor_sync(kFullMask, s.y, off)));
+    const int r = blockIdx.x * 32 + warp;
+    if (lane != 0 || r >= rows)
+        return;
+    const float lse = fmaf(s.x, kLn2, logf(s.y));
+    const int t = a.index[r], label = a.label[r];
     a.lse[t] = lse;
-    a.loss[t] = label < 0 ? __int_as_float(0x7fc00000) : lse - a.label_logit[row];
+    a.loss[t] = label < 0 ? __int_as_float(0x7fc00000) : lse - a.label_logit[r];
 }
 
 // ---- host ----
@@ -470,7 +490,7 @@ bool encode(CUtensorMap *map, const void *p, bool bf16, long long width, long lo
 struct Plan {
     int t_pad, blocks, dp, pieces, vp;
     bool pack_w;
-    size_t counts, tops, index, label, scale, row_lse, logit, part, hp, wp, G, acc, total;
+    size_t counts, tops, kept, index, label, scale, row_lse, logit, part, hp, wp, G, acc, total;
 };
 
 Plan plan(const void *w, int T, int V, int D, long long sw, bool backward)
@@ -495,6 +515,7 @@ Plan plan(const void *w, int T, int V, int D, long long sw, bool backward)
     };
     p.counts = take((size_t)p.blocks * 4);
     p.tops = take((size_t)p.blocks * 4);
+    p.kept = take(8);
     p.index = take((size_t)T * 4);
     p.label = take((size_t)p.t_pad * 4);
     p.hp = take((size_t)p.t_pad * p.dp * 2);
@@ -560,7 +581,9 @@ long long tiles_of(long long m, long long n)
 template <class T, bool BF16>
 cudaError_t launch_loss(LossArgs a, const Plan &p, bool backward, cudaStream_t st)
 {
-    cudaError_t e = launch_pdl(loss_count_kernel, dim3(p.blocks), dim3(256), 0, st, a);
+    cudaError_t e = cudaSuccess;
+    if (a.T > kCountAlone)
+        e = launch_pdl(loss_count_kernel, dim3(p.blocks), dim3(256), 0, st, a);
     if (e == cudaSuccess)
         e = launch_pdl(loss_pack_kernel<T>, dim3((a.T + pair::kTileM + kPackRows - 1) / kPackRows), dim3(256), 0, st, a);
     if (e == cudaSuccess && p.pack_w)
@@ -577,7 +600,7 @@ cudaError_t launch_loss(LossArgs a, const Plan &p, bool backward, cudaStream_t s
         if (e != cudaSuccess)
             return e;
         const int parts = (a.V + pair::kHalf - 1) / pair::kHalf;
-        return launch_pdl(loss_join_kernel, dim3((a.T + 31) / 32), dim3(256), 0, st, a, parts);
+        return launch_pdl(loss_join_kernel, dim3((a.T + 31) / 32), dim3(32 * kJoinLanes), 0, st, a, parts);
     }
     CUtensorMap hmap_n, gmap, gmap_m;
     if (!encode(&hmap_n, a.hp, BF16, a.dp, p.t_pad, a.dp, 64) || !encode(&gmap, a.G, BF16, p.vp, p.t_pad, p.vp, 128) ||
@@ -623,6 +646,8 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, void *workspace, bool ba
     a.dp = p.dp; a.t_pad = p.t_pad; a.blocks = p.blocks;
     a.counts = reinterpret_cast<int *>(ws + p.counts);
     a.tops = reinterpret_cast<float *>(ws + p.tops);
+    a.kept = reinterpret_cast<int *>(ws + p.kept);
+    a.top = reinterpret_cast<float *>(ws + p.kept) + 1;
     a.index = reinterpret_cast<int *>(ws + p.index);
     a.label = reinterpret_cast<int *>(ws + p.label);
     a.scale = reinterpret_cast<float *>(ws + p.scale);

@@ -20,7 +20,7 @@
 // segment's state from zero, and a small one walks the segments.
 #pragma once
 
-#include "layer_common.cuh"
+#include "packed.cuh"
 
 namespace ssm {
 
@@ -28,8 +28,7 @@ constexpr int kSelChunk = 16;             // tokens for each of which training s
 constexpr int kSelCh = 4;                 // channels of a lane
 constexpr int kSelWarps = 4;              // warps of a block: neighbouring channel tiles of one unit
 constexpr int kSelMaxState = 128;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
+constexpr int kCombineRun = 8;            // units whose loads the combining kernels issue together
 struct SelArgs {
     float *state;
     const void *x, *dt, *z, *B, *C;
@@ -122,50 +121,7 @@ __device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int cblock, int wa
 
 // ---- arithmetic ----
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long &>(d))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
-          "l"(reinterpret_cast<unsigned long long &>(c)));
-    return d;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long &>(d))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return d;
-}
-
-__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
-
-__device__ __forceinline__ float ex2(float v)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 __device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
-
-__device__ __forceinline__ float rcp(float v)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long &>(d))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return d;
-}
-
-__device__ __forceinline__ float2 rcp2(float2 v) { return make_float2(rcp(v.x), rcp(v.y)); }
 
 // The discretised step of two values.  softplus(v) = max(v, 0) + log1p(e) with e = exp(-|v|), and
 // log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3: the series 2 s (1 + s^2/3 + s^4/5 + ...) to s^14
@@ -197,28 +153,6 @@ __device__ __forceinline__ float2 sel_slope2(float2 v, bool softplus)
     return make_float2(v.x > 20.f ? 1.f : s.x, v.y > 20.f ? 1.f : s.y);
 }
 
-// sigmoid(v); v times it is 0 times v where exp(-v) overflows (v below -88).
-__device__ __forceinline__ float2 sigmoid2(float2 v)
-{
-    return rcp2(make_float2(1.f + ex2(-v.x * kLog2e), 1.f + ex2(-v.y * kLog2e)));
-}
-
-// Two neighbouring channels of a row as they lie in memory.
-template <class T>
-struct RawPair { uint32_t w; };
-template <>
-struct RawPair<float> { float2 w; };
-
-template <class T>
-__device__ __forceinline__ float2 pair_of(const RawPair<T> &r)
-{
-    Vec<T, 2> v;
-    *reinterpret_cast<uint32_t *>(&v) = r.w;
-    return make_float2(to_float(v.v[0]), to_float(v.v[1]));
-}
-template <>
-__device__ __forceinline__ float2 pair_of<float>(const RawPair<float> &r) { return r.w; }
-
 // How a warp stages pairs of channels of up to L tokens: place m of a lane is token tok(m), pair cp(m).
 template <int WC, int L>
 struct SelStage {
@@ -238,23 +172,14 @@ __device__ __forceinline__ void load_places(RawPair<T> (&r)[CNT], int m0, const 
     using S = SelStage<WC, L>;
     if (pairs) {
 #pragma unroll
-        for (int m = 0; m < CNT; ++m) {
-            const T *q = p + min(S::tok(m0 + m, lane), cnt - 1) * stride + min(2 * S::cp(m0 + m, lane), wc - 2);
-            if constexpr (sizeof(T) == 4)
-                r[m].w = *reinterpret_cast<const float2 *>(q);
-            else
-                r[m].w = *reinterpret_cast<const uint32_t *>(q);
-        }
+        for (int m = 0; m < CNT; ++m)
+            r[m] = load_pair(p + min(S::tok(m0 + m, lane), cnt - 1) * stride + min(2 * S::cp(m0 + m, lane), wc - 2));
     } else {
 #pragma unroll
         for (int m = 0; m < CNT; ++m) {
             const T *q = p + min(S::tok(m0 + m, lane), cnt - 1) * stride;
             const int c = 2 * S::cp(m0 + m, lane);
-            const Vec<T, 2> v{{q[min(c, wc - 1)], q[min(c + 1, wc - 1)]}};
-            if constexpr (sizeof(T) == 4)
-                r[m].w = make_float2(v.v[0], v.v[1]);
-            else
-                r[m].w = *reinterpret_cast<const uint32_t *>(&v);
+            r[m] = join_pair<T>(q[min(c, wc - 1)], q[min(c + 1, wc - 1)]);
         }
     }
 }
@@ -263,12 +188,7 @@ template <class T>
 __device__ __forceinline__ void store_pair(T *p, float2 v, bool pairs, bool second)
 {
     if (pairs) {
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float2 *>(p) = v;
-        } else {
-            const Vec<T, 2> o{{from_float<T>(v.x), from_float<T>(v.y)}};
-            *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(&o);
-        }
+        store_word(p, v);
     } else {
         p[0] = from_float<T>(v.x);
         if (second)
@@ -422,6 +342,15 @@ struct SelRows {
             const int e = threadIdx.x + 32 * kSelWarps * i, n = e % NN;
             if (L * NN >= 32 * kSelWarps || e < L * NN)
                 dst[e] = n < N ? to_float(v[i]) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void store_twice(float2 *dst, int N) const
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int e = threadIdx.x + 32 * kSelWarps * i, n = e % NN;
+            if (L * NN >= 32 * kSelWarps || e < L * NN)
+                dst[e] = twice(n < N ? to_float(v[i]) : 0.f);
         }
     }
 };

@@ -60,12 +60,22 @@ sel_combine_kernel(const SelArgs a)
     const int c = (int)(e / a.N), u1 = a.first[seq + 1];
     const float A = a.A[e] * kLog2e;
     float h = a.resume[seq] != 0 ? a.state[i] : 0.f;
-    for (int u = a.first[seq]; u < u1; ++u) {
-        float *p = a.unit_state + u * width + e;
-        const float own = u + 1 < u1 ? *p : 0.f;
-        *p = h;
-        if (u + 1 < u1)
-            h = fmaf(ex2(a.unit_step[(long long)u * a.channels + c] * A), h, own);
+    // loads of a run of units together (one by one, each waited for the store before it)
+    for (int u = a.first[seq]; u < u1; u += kCombineRun) {
+        float own[kCombineRun], step[kCombineRun];
+#pragma unroll
+        for (int k = 0; k < kCombineRun; ++k) {
+            const long long v = min(u + k, u1 - 1);
+            own[k] = a.unit_state[v * width + e];
+            step[k] = a.unit_step[v * a.channels + c];
+        }
+#pragma unroll
+        for (int k = 0; k < kCombineRun; ++k) {
+            if (u + k >= u1)
+                break;
+            a.unit_state[(u + k) * width + e] = h;
+            h = fmaf(ex2(step[k] * A), h, own[k]);          // (the last unit's values are not there, and not used)
+        }
     }
 }
 

@@ -35,12 +35,21 @@ sel_carry_combine_kernel(const SelArgs a)
     const int c = (int)(e / a.N), u0 = a.first[seq];
     const float A = a.A[e] * kLog2e;
     float g = a.grad_state ? a.grad_state[i] : 0.f;
-    for (int u = a.first[seq + 1] - 1; u >= u0; --u) {
-        float *p = a.unit_state + u * width + e;
-        const float own = u > u0 ? *p : 0.f;
-        *p = g;
-        if (u > u0)
-            g = fmaf(ex2(a.unit_step[(long long)u * a.channels + c] * A), g, own);
+    for (int u = a.first[seq + 1] - 1; u >= u0; u -= kCombineRun) {
+        float own[kCombineRun], step[kCombineRun];
+#pragma unroll
+        for (int k = 0; k < kCombineRun; ++k) {
+            const long long v = max(u - k, u0);
+            own[k] = a.unit_state[v * width + e];
+            step[k] = a.unit_step[v * a.channels + c];
+        }
+#pragma unroll
+        for (int k = 0; k < kCombineRun; ++k) {
+            if (u - k < u0)
+                break;
+            a.unit_state[(u - k) * width + e] = g;
+            g = fmaf(ex2(step[k] * A), g, own[k]);          // (the first unit's values are not there, and not used)
+        }
     }
 }
 
@@ -53,7 +62,8 @@ struct BackLayout {                                         // floats of a warp,
     static constexpr int kKeep = kKeepTokens * 32 * kSelCh * kBackNP;   // k of every token: a lane's own values
     static constexpr int kSums = kBackL * NN;               // grad_B, grad_C of the warp's channels
     static constexpr int kWarp = kKeep + 4 * kRow + 2 * kSums;
-    static constexpr size_t kBytes = ((size_t)kWarp * kSelWarps + 2 * kSums) * sizeof(float);   // B and C last
+    // B and C last, each value twice: as the pair that multiplies two channels
+    static constexpr size_t kBytes = ((size_t)kWarp * kSelWarps + 4 * kSums) * sizeof(float);
 };
 
 template <class T, int LN>
@@ -81,22 +91,53 @@ sel_backward_kernel(const SelArgs a)
     float *w = sm + warp * Y::kWarp;
     // step; step x, later sum_n e B; gp; p, later sum_n e A k
     float *keep = w, *step = keep + Y::kKeep, *in = step + Y::kRow, *gs = in + Y::kRow, *sa = gs + Y::kRow;
-    float *sB = sa + Y::kRow, *sC = sB + Y::kSums, *Bs = sm + kSelWarps * Y::kWarp, *Cs = Bs + Y::kSums;
-    float2 e[CH][NP / 2], A[CH][NP / 2], gA[CH][NP / 2], h0[CH][NP / 2];
+    float *sB = sa + Y::kRow, *sC = sB + Y::kSums;
+    float2 *Bs = reinterpret_cast<float2 *>(sm + kSelWarps * Y::kWarp), *Cs = Bs + Y::kSums;
+    // Pairs of channels here (the walks pair states): the steps and inputs of two channels lie side by
+    // side in shared memory, and a sum over states needs no last addition.
+    constexpr int CP = CH / 2;
+    float2 e[CP][NP], A[CP][NP], gA[CP][NP], h0[CP][NP];
+    auto read_pair = [&](float2 (&v)[NP], const float *base, int cp, bool vec, bool given) {
+        float2 r[2][NP / 2];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int ch = tile.c0 + q * CH + c;
-        const bool there = q * CH + c < wc;
-        read_states<NP>(A[c], a.A + (long long)ch * a.N, n0, a.N, false, there);
-        if (a.seg)
-            read_states<NP>(e[c], a.unit_state + ((long long)u * a.channels + ch) * a.N, n0, a.N, a.N % 4 == 0, there);
-        else
-            read_states<NP>(e[c], a.grad_state + ((long long)s.seq * a.channels + ch) * a.N, n0, a.N, false,
-                            there && a.grad_state != nullptr);
+        for (int i = 0; i < 2; ++i) {
+            const int c = q * CH + 2 * cp + i;
+            read_states<NP>(r[i], base + (long long)(tile.c0 + c) * a.N, n0, a.N, vec, given && c < wc);
+        }
 #pragma unroll
         for (int j = 0; j < NP / 2; ++j) {
-            A[c][j] = mul2(A[c][j], twice(kLog2e));
-            gA[c][j] = make_float2(0.f, 0.f);
+            v[2 * j] = make_float2(r[0][j].x, r[1][j].x);
+            v[2 * j + 1] = make_float2(r[0][j].y, r[1][j].y);
+        }
+    };
+    auto write_pair = [&](float *base, const float2 (&v)[NP], int cp, bool vec) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = q * CH + 2 * cp + i;
+            float2 r[NP / 2];
+#pragma unroll
+            for (int j = 0; j < NP / 2; ++j)
+                r[j] = i == 0 ? make_float2(v[2 * j].x, v[2 * j + 1].x) : make_float2(v[2 * j].y, v[2 * j + 1].y);
+            if (c < wc)
+                write_states<NP>(base + (long long)(tile.c0 + c) * a.N, r, n0, a.N, vec);
+        }
+    };
+    auto drop = [&](float2 (&v)[NP]) {                      // padding states
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            v[n] = n0 + n < a.N ? v[n] : make_float2(0.f, 0.f);
+    };
+#pragma unroll
+    for (int c = 0; c < CP; ++c) {
+        read_pair(A[c], a.A, c, false, true);
+        if (a.seg)
+            read_pair(e[c], a.unit_state + (long long)u * a.channels * a.N, c, a.N % 4 == 0, true);
+        else
+            read_pair(e[c], a.grad_state + (long long)s.seq * a.channels * a.N, c, false, a.grad_state != nullptr);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            A[c][n] = mul2(A[c][n], twice(kLog2e));
+            gA[c][n] = make_float2(0.f, 0.f);
         }
     }
     float2 bias[KC], D[KC], gD[KC], gbias[KC];
@@ -111,6 +152,7 @@ sel_backward_kernel(const SelArgs a)
     T *gx = static_cast<T *>(a.grad_x) + tile.c0, *gdt = static_cast<T *>(a.grad_dt) + tile.c0;
     T *gz = z ? static_cast<T *>(a.grad_z) + tile.c0 : nullptr;
     const long long row_n = (long long)a.groups * a.N;      // a row of the partial sums of grad_B and grad_C
+    const long long part_row = (long long)(cblock % (a.cblocks / a.groups)) * a.n_tokens;
 
     for (int b = s.end > s.begin ? s.begin + (s.end - 1 - s.begin) / L * L : -1; b >= s.begin; b -= L) {
         const int cnt = min(L, s.end - b);
@@ -120,8 +162,8 @@ sel_backward_kernel(const SelArgs a)
         rC.load(C + t0 * a.sC, a.sC, a.N, cnt);
         const float *cs = a.chunk_states + sel_chunk_row(a.n_seqs, s.seq, s.t0, b / L) * a.channels * a.N;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-            read_states<NP>(h0[c], cs + (long long)(tile.c0 + q * CH + c) * a.N, n0, a.N, vec_c, q * CH + c < wc);
+        for (int c = 0; c < CP; ++c)
+            read_pair(h0[c], cs, c, vec_c, true);
         if (wc > 0) {
 #pragma unroll
             for (int m0 = 0; m0 < M; m0 += H) {
@@ -151,69 +193,66 @@ sel_backward_kernel(const SelArgs a)
             for (int i = lane; i < 3 * Y::kRow; i += 32)
                 step[i] = 0.f;
         }
-        rB.store(Bs, a.N);
-        rC.store(Cs, a.N);
+        rB.store_twice(Bs, a.N);
+        rC.store_twice(Cs, a.N);
         __syncthreads();
 #pragma unroll 1
         for (int first = cnt > kKeepTokens ? kKeepTokens : 0; first >= 0; first -= kKeepTokens) {
             const int stop = min(cnt, first + kKeepTokens);
-            float2 h[CH][NP / 2];
+            float2 h[CP][NP];
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
+            for (int c = 0; c < CP; ++c)
 #pragma unroll
-                for (int j = 0; j < NP / 2; ++j)
-                    h[c][j] = h0[c][j];
+                for (int n = 0; n < NP; ++n)
+                    h[c][n] = h0[c][n];
 #pragma unroll 1
             for (int t = 0; t < first; ++t) {               // up to the tokens whose k is kept
-                float st[CH], uv[CH];
-                float2 Bv[NP / 2];
-                load_floats<CH>(st, step + t * WC + q * CH);
-                load_floats<CH>(uv, in + t * WC + q * CH);
-                load_pairs<NP>(Bv, Bs + t * NN + n0);
+                float2 st[CP], uv[CP], Bv[NP];
+                load_pairs<CH>(st, step + t * WC + q * CH);
+                load_pairs<CH>(uv, in + t * WC + q * CH);
+                load_pairs<2 * NP>(Bv, reinterpret_cast<const float *>(Bs + t * NN + n0));
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
+                for (int c = 0; c < CP; ++c)
 #pragma unroll
-                    for (int j = 0; j < NP / 2; ++j)
-                        h[c][j] = fma2(ex2_2(mul2(twice(st[c]), A[c][j])), h[c][j], mul2(twice(uv[c]), Bv[j]));
+                    for (int n = 0; n < NP; ++n)
+                        h[c][n] = fma2(ex2_2(mul2(st[c], A[c][n])), h[c][n], mul2(uv[c], Bv[n]));
             }
 #pragma unroll 1
             for (int t = first; t < stop; ++t) {
-                float st[CH], uv[CH], gv[CH], p[CH], gc[NP];
-                float2 Bv[NP / 2], Cv[NP / 2], sum_c[NP / 2];
-                load_floats<CH>(st, step + t * WC + q * CH);
-                load_floats<CH>(uv, in + t * WC + q * CH);
-                load_floats<CH>(gv, gs + t * WC + q * CH);
-                load_pairs<NP>(Bv, Bs + t * NN + n0);
-                load_pairs<NP>(Cv, Cs + t * NN + n0);
+                float2 st[CP], uv[CP], gv[CP], Bv[NP], Cv[NP], sum_c[NP];
+                float p[CH], gc[NP];
+                load_pairs<CH>(st, step + t * WC + q * CH);
+                load_pairs<CH>(uv, in + t * WC + q * CH);
+                load_pairs<CH>(gv, gs + t * WC + q * CH);
+                load_pairs<2 * NP>(Bv, reinterpret_cast<const float *>(Bs + t * NN + n0));
+                load_pairs<2 * NP>(Cv, reinterpret_cast<const float *>(Cs + t * NN + n0));
 #pragma unroll
-                for (int j = 0; j < NP / 2; ++j)
-                    sum_c[j] = make_float2(0.f, 0.f);
+                for (int c = 0; c < CP; ++c) {
+                    float2 sum = make_float2(0.f, 0.f), k[NP];
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    float2 sum = make_float2(0.f, 0.f), k[NP / 2];
-#pragma unroll
-                    for (int j = 0; j < NP / 2; ++j) {
-                        k[j] = mul2(ex2_2(mul2(twice(st[c]), A[c][j])), h[c][j]);
-                        h[c][j] = fma2(twice(uv[c]), Bv[j], k[j]);
+                    for (int n = 0; n < NP; ++n) {
+                        k[n] = mul2(ex2_2(mul2(st[c], A[c][n])), h[c][n]);
+                        h[c][n] = fma2(uv[c], Bv[n], k[n]);
                     }
                     if (pad) {
-                        drop_padding<NP>(h[c], n0, a.N);
-                        drop_padding<NP>(k, n0, a.N);
+                        drop(h[c]);
+                        drop(k);
                     }
 #pragma unroll
-                    for (int j = 0; j < NP / 2; ++j) {
-                        sum = fma2(h[c][j], Cv[j], sum);
-                        sum_c[j] = fma2(twice(gv[c]), h[c][j], sum_c[j]);
+                    for (int n = 0; n < NP; ++n) {
+                        sum = n == 0 ? mul2(h[c][n], Cv[n]) : fma2(h[c][n], Cv[n], sum);
+                        sum_c[n] = c == 0 ? mul2(gv[c], h[c][n]) : fma2(gv[c], h[c][n], sum_c[n]);
                     }
-                    *reinterpret_cast<float4 *>(keep + ((t - first) * CH + c) * 128 + 4 * lane) =
-                        make_float4(k[0].x, k[0].y, k[1].x, k[1].y);
-                    p[c] = sum.x + sum.y;
+#pragma unroll
+                    for (int n = 0; n < NP; n += 2)
+                        *reinterpret_cast<float4 *>(keep + (((t - first) * CP + c) * 2 + n / 2) * 128 + 4 * lane) =
+                            make_float4(k[n].x, k[n].y, k[n + 1].x, k[n + 1].y);
+                    p[2 * c] = sum.x;
+                    p[2 * c + 1] = sum.y;
                 }
 #pragma unroll
-                for (int j = 0; j < NP / 2; ++j) {
-                    gc[2 * j] = sum_c[j].x;
-                    gc[2 * j + 1] = sum_c[j].y;
-                }
+                for (int n = 0; n < NP; ++n)
+                    gc[n] = sum_c[n].x + sum_c[n].y;
                 int at;
                 bool mine;
                 if (z) {
@@ -231,66 +270,65 @@ sel_backward_kernel(const SelArgs a)
             }
             __syncwarp();
             if (z && wc > 0) {                              // the gate's gradient, before sa is used again
-#pragma unroll 1
-                for (int m0 = 0; m0 < M; m0 += H) {
-                    RawPair<T> rz[H], rx[H], rg[H];
-                    load_places<T, WC, L>(rz, m0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
-                    load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
-                    load_places<T, WC, L>(rg, m0, gy + t0 * a.sgy, a.sgy, cnt, wc, lane, pairs);
+                constexpr int E = M > 1 ? M / 2 : 1;        // places of eight tokens
+                const int m0 = M > 1 && first > 0 ? E : 0;
+                RawPair<T> rz[E], rx[E], rg[E];
+                load_places<T, WC, L>(rz, m0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
+                load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
+                load_places<T, WC, L>(rg, m0, gy + t0 * a.sgy, a.sgy, cnt, wc, lane, pairs);
 #pragma unroll
-                    for (int k = 0; k < H; ++k) {
-                        const int m = m0 + k, t = S::tok(m, lane), c = 2 * S::cp(m, lane);
-                        if (t < first || t >= stop || c >= wc)
-                            continue;
-                        const float2 zv = pair_of<T>(rz[k]), sg = sigmoid2(zv);
-                        const float2 p = fma2(D[m % KC], pair_of<T>(rx[k]), *reinterpret_cast<const float2 *>(sa + t * WC + c));
-                        const float2 rest = make_float2(1.f - sg.x, 1.f - sg.y);
-                        store_pair<T>(gz + (t0 + t) * a.sgz + c,
-                                      mul2(mul2(pair_of<T>(rg[k]), p), fma2(mul2(zv, sg), rest, sg)), pairs, c + 1 < wc);
-                    }
+                for (int k = 0; k < E; ++k) {
+                    const int t = S::tok(m0 + k, lane), c = 2 * S::cp(m0 + k, lane);
+                    if (t < first || t >= stop || c >= wc)
+                        continue;
+                    const float2 zv = pair_of<T>(rz[k]), sg = sigmoid2(zv);
+                    const float2 p = fma2(D[k % KC], pair_of<T>(rx[k]), *reinterpret_cast<const float2 *>(sa + t * WC + c));
+                    const float2 rest = make_float2(1.f - sg.x, 1.f - sg.y);
+                    store_pair<T>(gz + (t0 + t) * a.sgz + c,
+                                  mul2(mul2(pair_of<T>(rg[k]), p), fma2(mul2(zv, sg), rest, sg)), pairs, c + 1 < wc);
                 }
                 __syncwarp();
             }
 #pragma unroll 1
             for (int t = stop - 1; t >= first; --t) {
-                float st[CH], uv[CH], gv[CH], s1[CH], s2[CH], gb[NP];
-                float2 Bv[NP / 2], Cv[NP / 2], sum_b[NP / 2];
-                load_floats<CH>(st, step + t * WC + q * CH);
-                load_floats<CH>(uv, in + t * WC + q * CH);
-                load_floats<CH>(gv, gs + t * WC + q * CH);
-                load_pairs<NP>(Bv, Bs + t * NN + n0);
-                load_pairs<NP>(Cv, Cs + t * NN + n0);
+                float2 st[CP], uv[CP], gv[CP], Bv[NP], Cv[NP], sum_b[NP];
+                float s1[CH], s2[CH], gb[NP];
+                load_pairs<CH>(st, step + t * WC + q * CH);
+                load_pairs<CH>(uv, in + t * WC + q * CH);
+                load_pairs<CH>(gv, gs + t * WC + q * CH);
+                load_pairs<2 * NP>(Bv, reinterpret_cast<const float *>(Bs + t * NN + n0));
+                load_pairs<2 * NP>(Cv, reinterpret_cast<const float *>(Cs + t * NN + n0));
 #pragma unroll
-                for (int j = 0; j < NP / 2; ++j)
-                    sum_b[j] = make_float2(0.f, 0.f);
+                for (int c = 0; c < CP; ++c) {
+                    float2 k[NP], wa, wb;
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    float2 k[NP / 2], wa = make_float2(0.f, 0.f), wb = make_float2(0.f, 0.f);
-                    const float4 kv = *reinterpret_cast<const float4 *>(keep + ((t - first) * CH + c) * 128 + 4 * lane);
-                    k[0] = make_float2(kv.x, kv.y);
-                    k[1] = make_float2(kv.z, kv.w);
-#pragma unroll
-                    for (int j = 0; j < NP / 2; ++j)
-                        e[c][j] = fma2(twice(gv[c]), Cv[j], e[c][j]);
-                    if (pad)
-                        drop_padding<NP>(e[c], n0, a.N);
-#pragma unroll
-                    for (int j = 0; j < NP / 2; ++j) {
-                        const float2 v = mul2(e[c][j], k[j]);
-                        gA[c][j] = fma2(twice(st[c]), v, gA[c][j]);
-                        wa = fma2(v, A[c][j], wa);
-                        wb = fma2(e[c][j], Bv[j], wb);
-                        sum_b[j] = fma2(twice(uv[c]), e[c][j], sum_b[j]);
-                        e[c][j] = mul2(ex2_2(mul2(twice(st[c]), A[c][j])), e[c][j]);
+                    for (int n = 0; n < NP; n += 2) {
+                        const float4 v = *reinterpret_cast<const float4 *>(keep + (((t - first) * CP + c) * 2 + n / 2) * 128 + 4 * lane);
+                        k[n] = make_float2(v.x, v.y);
+                        k[n + 1] = make_float2(v.z, v.w);
                     }
-                    s1[c] = wa.x + wa.y;
-                    s2[c] = wb.x + wb.y;
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+                        e[c][n] = fma2(gv[c], Cv[n], e[c][n]);
+                    if (pad)
+                        drop(e[c]);
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) {
+                        const float2 v = mul2(e[c][n], k[n]);
+                        gA[c][n] = fma2(st[c], v, gA[c][n]);
+                        wa = n == 0 ? mul2(v, A[c][n]) : fma2(v, A[c][n], wa);
+                        wb = n == 0 ? mul2(e[c][n], Bv[n]) : fma2(e[c][n], Bv[n], wb);
+                        sum_b[n] = c == 0 ? mul2(uv[c], e[c][n]) : fma2(uv[c], e[c][n], sum_b[n]);
+                        e[c][n] = mul2(ex2_2(mul2(st[c], A[c][n])), e[c][n]);
+                    }
+                    s1[2 * c] = wa.x;
+                    s1[2 * c + 1] = wa.y;
+                    s2[2 * c] = wb.x;
+                    s2[2 * c + 1] = wb.y;
                 }
 #pragma unroll
-                for (int j = 0; j < NP / 2; ++j) {
-                    gb[2 * j] = sum_b[j].x;
-                    gb[2 * j + 1] = sum_b[j].y;
-                }
+                for (int n = 0; n < NP; ++n)
+                    gb[n] = sum_b[n].x + sum_b[n].y;
                 int at;
                 bool mine;
                 lanes_sum<CH, LN, 1>(s1, lane, at, mine);
@@ -321,7 +359,7 @@ sel_backward_kernel(const SelArgs a)
                     vb += o[i];
                     vc += o[i + Y::kSums];
                 }
-                const long long at = ((long long)(cblock % (a.cblocks / a.groups)) * a.n_tokens + t0 + t) * row_n + tile.g * a.N + n;
+                const long long at = (part_row + t0 + t) * row_n + tile.g * a.N + n;
                 a.part_B[at] = vb;
                 a.part_C[at] = vc;
             }
@@ -350,18 +388,15 @@ sel_backward_kernel(const SelArgs a)
         }
         __syncthreads();                                    // ... and read
     }
+    const bool resumed = a.resume[s.seq] != 0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int ch = tile.c0 + q * CH + c;
-        if (q * CH + c >= wc)
-            continue;
-        write_states<NP>(a.part_A + ((long long)u * a.channels + ch) * a.N, gA[c], n0, a.N, a.N % 4 == 0);
+    for (int c = 0; c < CP; ++c) {
+        write_pair(a.part_A + (long long)u * a.channels * a.N, gA[c], c, a.N % 4 == 0);
         if (s.k == 0 && a.grad_state0) {
-            const bool resumed = a.resume[s.seq] != 0;
 #pragma unroll
-            for (int j = 0; j < NP / 2; ++j)
-                e[c][j] = resumed ? e[c][j] : make_float2(0.f, 0.f);
-            write_states<NP>(a.grad_state0 + ((long long)s.seq * a.channels + ch) * a.N, e[c], n0, a.N, false);
+            for (int n = 0; n < NP; ++n)
+                e[c][n] = resumed ? e[c][n] : make_float2(0.f, 0.f);
+            write_pair(a.grad_state0 + (long long)s.seq * a.channels * a.N, e[c], c, false);
         }
     }
     // lanes that hold the same pair of channels

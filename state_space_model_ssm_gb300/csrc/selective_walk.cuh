@@ -28,8 +28,10 @@ struct WalkLayout {
     static constexpr size_t kBytes = (size_t)(kSelWarps * kWarp + 4 * kRows) * sizeof(float);
 };
 
+// Three blocks an SM, 168 registers a thread: unbounded, kFull took 238 and 1 x 4096 x 4096 channels x 16 states
+// (bf16) 180 us instead of 126.  Four states a lane, four blocks an SM: 156 us.
 template <class T, int LN, SelMode MODE>
-__global__ void __launch_bounds__(32 * kSelWarps)
+__global__ void __launch_bounds__(32 * kSelWarps, LN == 1 && sizeof(T) == 4 ? 2 : 3)
 sel_walk_kernel(const SelArgs a)
 {
     griddep_entry();
