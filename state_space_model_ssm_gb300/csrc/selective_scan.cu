@@ -113,11 +113,13 @@ SelShape sel_shape(int channels, int N, int groups, bool backward)
 
 int sel_segment(int n_seqs, int n_tokens, const SelShape &s, bool backward)
 {
-    // warps that walk whole sequences, against those that are resident at once (three blocks an SM, two backward)
+    // Warps that walk whole sequences, against those that are resident at once (three blocks an SM, two backward).
+    // With segments the forward pass takes about one round of them; the backward pass about two, since the pass that
+    // finds what segments hand on walks the same units with twice the channels a warp.
     const long long want = kSms * kSelWarps * (backward ? 2 : 3), walk = (long long)n_seqs * s.tiles;
     if (walk >= want || n_tokens < 128 || n_tokens / n_seqs < 64)
         return 0;
-    const long long units = want / s.tiles > 1 ? want / s.tiles : 1;       // about one round of them
+    const long long round = (backward ? 2 : 1) * want, units = round / s.tiles > 1 ? round / s.tiles : 1;
     const long long seg = ((n_tokens + units - 1) / units + kSelChunk - 1) / kSelChunk * kSelChunk;
     return (int)(seg < 64 ? 64 : seg);
 }

@@ -59,24 +59,61 @@ template <int LN>
 struct BackLayout {                                         // floats of a warp, then of the block
     static constexpr int WC = 32 / LN * kSelCh, NN = kBackNP * LN;
     static constexpr int kRow = kBackL * WC;
-    static constexpr int kKeep = kKeepTokens * 32 * kSelCh * kBackNP;   // k of every token: a lane's own values
-    static constexpr int kSums = kBackL * NN;               // grad_B, grad_C of the warp's channels
-    static constexpr int kWarp = kKeep + 4 * kRow + 2 * kSums;
-    // B and C last, each value twice: as the pair that multiplies two channels
-    static constexpr size_t kBytes = ((size_t)kWarp * kSelWarps + 4 * kSums) * sizeof(float);
+    static constexpr int kSlot = 128;                       // four floats of every lane
+    static constexpr int kKeep = kKeepTokens * 4 * kSlot;   // k of every token: four slots
+    static constexpr int kWarp = kKeep + kKeepTokens * kSlot + 3 * kRow + kKeepTokens * WC;
+    static constexpr int kRows = kBackL * NN;               // of B or C, last, each value twice: as the pair that multiplies two channels
+    static constexpr size_t kBytes = ((size_t)kWarp * kSelWarps + 4 * kRows) * sizeof(float);
 };
 
+// Sums over a block's channels of what its lanes have put into slot `slot` of eight tokens (four states a lane):
+// terms are the warps' lanes of one state, `kParts` threads of a warp share an output of four states.
+template <int LN>
+__device__ __forceinline__ float4 sum_slots(const float *first, int warp_stride, int token_stride, int out, int part)
+{
+    constexpr int Q = 32 / LN, kTerms = kSelWarps * Q, kParts = LN <= 16 ? 16 / LN : 1, kEach = kTerms / kParts;
+    const int t = out / LN, sub = out % LN;
+    float2 lo = make_float2(0.f, 0.f), hi = lo;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int term = part * kEach + j, w = term / Q, q = term % Q;
+        const float4 v = *reinterpret_cast<const float4 *>(first + w * warp_stride + t * token_stride + 4 * (q * LN + sub));
+        lo = add2(lo, make_float2(v.x, v.y));
+        hi = add2(hi, make_float2(v.z, v.w));
+    }
+    float r[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+    for (int off = kParts / 2; off >= 1; off /= 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            r[e] += __shfl_xor_sync(kFullMask, r[e], off);
+    return make_float4(r[0], r[1], r[2], r[3]);
+}
+
+// Sum over a channel's lanes of one slot, two channels (c even); lanes of different channels begin at different
+// ones, so that they read different banks.
+template <int LN>
+__device__ __forceinline__ float2 sum_lanes(const float *slot, int c)
+{
+    const int q = c / 4;
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < LN; ++i)
+        v = add2(v, *reinterpret_cast<const float2 *>(slot + 4 * (q * LN + ((i + q / 2) & (LN - 1))) + c % 4));
+    return v;
+}
+
 template <class T, int LN>
-__global__ void __launch_bounds__(32 * kSelWarps, 2)
+__global__ void __launch_bounds__(32 * kSelWarps, LN == 32 ? 1 : 2)
 sel_backward_kernel(const SelArgs a)
 {
     griddep_entry();
     using Y = BackLayout<LN>;
-    constexpr int CH = kSelCh, NP = kBackNP, WC = Y::WC, NN = Y::NN, L = kBackL;
+    constexpr int CH = kSelCh, NP = kBackNP, WC = Y::WC, NN = Y::NN, L = kBackL, K = kKeepTokens;
     using S = SelStage<WC, L>;
     constexpr int M = S::M, KC = S::KC, H = M > 8 ? 8 : M;  // places loaded together
-    constexpr int kLeft = NP * LN > 32 ? NP * LN / 32 : 1;  // sums over channels that a lane ends with
-    constexpr int kOwn = CH > LN ? CH / LN : 1;             // sums over states
+    constexpr int E = M > 1 ? M / 2 : 1;                    // places of eight tokens
+    constexpr int kOwn = CH > LN ? CH / LN : 1;             // sums over states that a lane ends with
     extern __shared__ __align__(16) float sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane % LN, q = lane / LN, n0 = sub * NP;
@@ -89,10 +126,12 @@ sel_backward_kernel(const SelArgs a)
     const bool pad = a.N != NN, pairs = a.pairs != 0;
     const bool vec_c = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.chunk_states) & 15) == 0;
     float *w = sm + warp * Y::kWarp;
-    // step; step x, later sum_n e B; gp; p, later sum_n e A k
-    float *keep = w, *step = keep + Y::kKeep, *in = step + Y::kRow, *gs = in + Y::kRow, *sa = gs + Y::kRow;
-    float *sB = sa + Y::kRow, *sC = sB + Y::kSums;
-    float2 *Bs = reinterpret_cast<float2 *>(sm + kSelWarps * Y::kWarp), *Cs = Bs + Y::kSums;
+    // Of eight tokens: k, in whose place a token's sums are put once it has been read (slot 0: sum_n e A k, slot 1:
+    // sum_n e B, each of a lane's states and four channels; slot 2: sum_c e step x of its channels and four states);
+    // sum_c gp h alike; p.  Of the chunk: step, step x, gp.
+    float *keep = w, *sum_C = keep + Y::kKeep, *step = sum_C + K * Y::kSlot, *in = step + Y::kRow, *gs = in + Y::kRow;
+    float *ps = gs + Y::kRow;
+    float2 *Bs = reinterpret_cast<float2 *>(sm + kSelWarps * Y::kWarp), *Cs = Bs + Y::kRows;
     // Pairs of channels here (the walks pair states): the steps and inputs of two channels lie side by
     // side in shared memory, and a sum over states needs no last addition.
     constexpr int CP = CH / 2;
@@ -197,8 +236,8 @@ sel_backward_kernel(const SelArgs a)
         rC.store_twice(Cs, a.N);
         __syncthreads();
 #pragma unroll 1
-        for (int first = cnt > kKeepTokens ? kKeepTokens : 0; first >= 0; first -= kKeepTokens) {
-            const int stop = min(cnt, first + kKeepTokens);
+        for (int first = cnt > K ? K : 0; first >= 0; first -= K) {
+            const int stop = min(cnt, first + K);
             float2 h[CP][NP];
 #pragma unroll
             for (int c = 0; c < CP; ++c)
@@ -217,10 +256,20 @@ sel_backward_kernel(const SelArgs a)
                     for (int n = 0; n < NP; ++n)
                         h[c][n] = fma2(ex2_2(mul2(st[c], A[c][n])), h[c][n], mul2(uv[c], Bv[n]));
             }
+            // what the gate's gradient and the outputs read, loaded before the walks that come first
+            const int m0 = M > 1 && first > 0 ? E : 0;
+            RawPair<T> rz[E], rx[E], rg[E], rdt[E];
+            if (wc > 0) {
+                load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
+                if (z) {
+                    load_places<T, WC, L>(rz, m0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
+                    load_places<T, WC, L>(rg, m0, gy + t0 * a.sgy, a.sgy, cnt, wc, lane, pairs);
+                }
+            }
 #pragma unroll 1
             for (int t = first; t < stop; ++t) {
                 float2 st[CP], uv[CP], gv[CP], Bv[NP], Cv[NP], sum_c[NP];
-                float p[CH], gc[NP];
+                float p[CH];
                 load_pairs<CH>(st, step + t * WC + q * CH);
                 load_pairs<CH>(uv, in + t * WC + q * CH);
                 load_pairs<CH>(gv, gs + t * WC + q * CH);
@@ -245,54 +294,44 @@ sel_backward_kernel(const SelArgs a)
                     }
 #pragma unroll
                     for (int n = 0; n < NP; n += 2)
-                        *reinterpret_cast<float4 *>(keep + (((t - first) * CP + c) * 2 + n / 2) * 128 + 4 * lane) =
+                        *reinterpret_cast<float4 *>(keep + ((t - first) * 4 + 2 * c + n / 2) * Y::kSlot + 4 * lane) =
                             make_float4(k[n].x, k[n].y, k[n + 1].x, k[n + 1].y);
                     p[2 * c] = sum.x;
                     p[2 * c + 1] = sum.y;
                 }
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    gc[n] = sum_c[n].x + sum_c[n].y;
-                int at;
-                bool mine;
+                *reinterpret_cast<float4 *>(sum_C + (t - first) * Y::kSlot + 4 * lane) =
+                    make_float4(sum_c[0].x + sum_c[0].y, sum_c[1].x + sum_c[1].y, sum_c[2].x + sum_c[2].y, sum_c[3].x + sum_c[3].y);
                 if (z) {
+                    int at;
+                    bool mine;
                     lanes_sum<CH, LN, 1>(p, lane, at, mine);
-                    if (mine)
+                    // (lanes that hold the same sum write the same value)
 #pragma unroll
-                        for (int r = 0; r < kOwn; ++r)
-                            sa[t * WC + q * CH + at + r] = p[r];
+                    for (int r = 0; r < kOwn; ++r)
+                        ps[(t - first) * WC + q * CH + at + r] = p[r];
                 }
-                lanes_sum<NP, 32 / LN, LN>(gc, lane, at, mine);
-                if (mine)
-#pragma unroll
-                    for (int r = 0; r < kLeft; ++r)
-                        sC[t * NN + n0 + at + r] = gc[r];
             }
             __syncwarp();
-            if (z && wc > 0) {                              // the gate's gradient, before sa is used again
-                constexpr int E = M > 1 ? M / 2 : 1;        // places of eight tokens
-                const int m0 = M > 1 && first > 0 ? E : 0;
-                RawPair<T> rz[E], rx[E], rg[E];
-                load_places<T, WC, L>(rz, m0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
-                load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
-                load_places<T, WC, L>(rg, m0, gy + t0 * a.sgy, a.sgy, cnt, wc, lane, pairs);
+            if (z && wc > 0) {                              // the gate's gradient
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
                     const int t = S::tok(m0 + k, lane), c = 2 * S::cp(m0 + k, lane);
                     if (t < first || t >= stop || c >= wc)
                         continue;
                     const float2 zv = pair_of<T>(rz[k]), sg = sigmoid2(zv);
-                    const float2 p = fma2(D[k % KC], pair_of<T>(rx[k]), *reinterpret_cast<const float2 *>(sa + t * WC + c));
+                    const float2 p = fma2(D[k % KC], pair_of<T>(rx[k]), *reinterpret_cast<const float2 *>(ps + (t - first) * WC + c));
                     const float2 rest = make_float2(1.f - sg.x, 1.f - sg.y);
                     store_pair<T>(gz + (t0 + t) * a.sgz + c,
                                   mul2(mul2(pair_of<T>(rg[k]), p), fma2(mul2(zv, sg), rest, sg)), pairs, c + 1 < wc);
                 }
-                __syncwarp();
             }
+            if (wc > 0)
+                load_places<T, WC, L>(rdt, m0, dt + t0 * a.sdt, a.sdt, cnt, wc, lane, pairs);
 #pragma unroll 1
             for (int t = stop - 1; t >= first; --t) {
                 float2 st[CP], uv[CP], gv[CP], Bv[NP], Cv[NP], sum_b[NP];
-                float s1[CH], s2[CH], gb[NP];
+                float2 s1[CP], s2[CP];
+                float *slots = keep + (t - first) * 4 * Y::kSlot + 4 * lane;
                 load_pairs<CH>(st, step + t * WC + q * CH);
                 load_pairs<CH>(uv, in + t * WC + q * CH);
                 load_pairs<CH>(gv, gs + t * WC + q * CH);
@@ -303,7 +342,7 @@ sel_backward_kernel(const SelArgs a)
                     float2 k[NP], wa, wb;
 #pragma unroll
                     for (int n = 0; n < NP; n += 2) {
-                        const float4 v = *reinterpret_cast<const float4 *>(keep + (((t - first) * CP + c) * 2 + n / 2) * 128 + 4 * lane);
+                        const float4 v = *reinterpret_cast<const float4 *>(slots + (2 * c + n / 2) * Y::kSlot);
                         k[n] = make_float2(v.x, v.y);
                         k[n + 1] = make_float2(v.z, v.w);
                     }
@@ -321,72 +360,52 @@ sel_backward_kernel(const SelArgs a)
                         sum_b[n] = c == 0 ? mul2(uv[c], e[c][n]) : fma2(uv[c], e[c][n], sum_b[n]);
                         e[c][n] = mul2(ex2_2(mul2(st[c], A[c][n])), e[c][n]);
                     }
-                    s1[2 * c] = wa.x;
-                    s1[2 * c + 1] = wa.y;
-                    s2[2 * c] = wb.x;
-                    s2[2 * c + 1] = wb.y;
+                    s1[c] = wa;
+                    s2[c] = wb;
                 }
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    gb[n] = sum_b[n].x + sum_b[n].y;
-                int at;
-                bool mine;
-                lanes_sum<CH, LN, 1>(s1, lane, at, mine);
-                lanes_sum<CH, LN, 1>(s2, lane, at, mine);
-                __syncwarp();                               // the inputs of this token have been read
-                if (mine)
-#pragma unroll
-                    for (int r = 0; r < kOwn; ++r) {
-                        sa[t * WC + q * CH + at + r] = s1[r];
-                        in[t * WC + q * CH + at + r] = s2[r];
-                    }
-                lanes_sum<NP, 32 / LN, LN>(gb, lane, at, mine);
-                if (mine)
-#pragma unroll
-                    for (int r = 0; r < kLeft; ++r)
-                        sB[t * NN + n0 + at + r] = gb[r];
+                *reinterpret_cast<float4 *>(slots) = make_float4(s1[0].x, s1[0].y, s1[1].x, s1[1].y);
+                *reinterpret_cast<float4 *>(slots + Y::kSlot) = make_float4(s2[0].x, s2[0].y, s2[1].x, s2[1].y);
+                *reinterpret_cast<float4 *>(slots + 2 * Y::kSlot) =
+                    make_float4(sum_b[0].x + sum_b[0].y, sum_b[1].x + sum_b[1].y, sum_b[2].x + sum_b[2].y, sum_b[3].x + sum_b[3].y);
             }
-            __syncwarp();
-        }
-        __syncthreads();                                    // every warp's sums over its channels are there
-        for (int i = tid; i < cnt * NN; i += 32 * kSelWarps) {
-            const int t = i / NN, n = i % NN;
-            if (n < a.N) {
-                float vb = 0.f, vc = 0.f;
+            __syncthreads();                                // every warp's sums are there
+            constexpr int kParts = LN <= 16 ? 16 / LN : 1;
 #pragma unroll
-                for (int k = 0; k < kSelWarps; ++k) {
-                    const float *o = sm + k * Y::kWarp + (sB - w);
-                    vb += o[i];
-                    vc += o[i + Y::kSums];
+            for (int i = tid; i < K * LN * kParts; i += 32 * kSelWarps) {
+                const int out = i / kParts, part = i % kParts, t = first + out / LN, n = out % LN * NP;
+                const float4 vb = sum_slots<LN>(sm + 2 * Y::kSlot, Y::kWarp, 4 * Y::kSlot, out, part);
+                const float4 vc = sum_slots<LN>(sm + Y::kKeep, Y::kWarp, Y::kSlot, out, part);
+                if (part == 0 && t < stop && n < a.N) {
+                    const long long at = (part_row + t0 + t) * row_n + tile.g * a.N + n;
+                    const float b4[4] = {vb.x, vb.y, vb.z, vb.w}, c4[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+                    for (int e4 = 0; e4 < 4; ++e4)
+                        if (n + e4 < a.N) {
+                            a.part_B[at + e4] = b4[e4];
+                            a.part_C[at + e4] = c4[e4];
+                        }
                 }
-                const long long at = (part_row + t0 + t) * row_n + tile.g * a.N + n;
-                a.part_B[at] = vb;
-                a.part_C[at] = vc;
             }
-        }
-        if (wc > 0) {
+            if (wc > 0) {
 #pragma unroll
-            for (int m0 = 0; m0 < M; m0 += H) {
-                RawPair<T> rdt[H], rx[H];
-                load_places<T, WC, L>(rdt, m0, dt + t0 * a.sdt, a.sdt, cnt, wc, lane, pairs);
-                load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
-#pragma unroll
-                for (int k = 0; k < H; ++k) {
-                    const int m = m0 + k, t = S::tok(m, lane), c = 2 * S::cp(m, lane), i = t * WC + c;
-                    if (t >= cnt || c >= wc)
+                for (int k = 0; k < E; ++k) {
+                    const int t = S::tok(m0 + k, lane), c = 2 * S::cp(m0 + k, lane), i = t * WC + c;
+                    if (t < first || t >= stop || c >= wc)
                         continue;
                     const float2 xv = pair_of<T>(rx[k]), gv = *reinterpret_cast<const float2 *>(gs + i);
-                    const float2 eb = *reinterpret_cast<const float2 *>(in + i), st = *reinterpret_cast<const float2 *>(step + i);
-                    const float2 g = mul2(fma2(*reinterpret_cast<const float2 *>(sa + i), twice(kLn2), mul2(xv, eb)),
-                                          sel_slope2(add2(pair_of<T>(rdt[k]), bias[m % KC]), a.softplus));
-                    store_pair<T>(gx + (t0 + t) * a.sgx + c, fma2(D[m % KC], gv, mul2(st, eb)), pairs, c + 1 < wc);
+                    const float2 st = *reinterpret_cast<const float2 *>(step + i);
+                    const float2 sa = sum_lanes<LN>(keep + (t - first) * 4 * Y::kSlot, c);
+                    const float2 eb = sum_lanes<LN>(keep + (t - first) * 4 * Y::kSlot + Y::kSlot, c);
+                    const float2 g = mul2(fma2(sa, twice(kLn2), mul2(xv, eb)),
+                                          sel_slope2(add2(pair_of<T>(rdt[k]), bias[k % KC]), a.softplus));
+                    store_pair<T>(gx + (t0 + t) * a.sgx + c, fma2(D[k % KC], gv, mul2(st, eb)), pairs, c + 1 < wc);
                     store_pair<T>(gdt + (t0 + t) * a.sgdt + c, g, pairs, c + 1 < wc);
-                    gD[m % KC] = fma2(gv, xv, gD[m % KC]);
-                    gbias[m % KC] = add2(gbias[m % KC], g);
+                    gD[k % KC] = fma2(gv, xv, gD[k % KC]);
+                    gbias[k % KC] = add2(gbias[k % KC], g);
                 }
             }
+            __syncthreads();                                // ... and read
         }
-        __syncthreads();                                    // ... and read
     }
     const bool resumed = a.resume[s.seq] != 0;
 #pragma unroll
