@@ -35,7 +35,9 @@ def scan_bounds(slots, x, dt, A, B, C, D, starts, lens, resume, z=None, dt_bias=
     T, channels = x.shape
     N = A.shape[1]
     v, step, slope = om.step_of(dt, dt_bias, softplus)
-    es = (3 * np.abs(v) + 18) * U if softplus else np.full_like(v, 2 * U)
+    # above the threshold the step is v itself; exp(-inf) is exactly 0, and so is the step
+    with np.errstate(invalid="ignore"):
+        es = np.where(v > 20, 2 * U, np.where(np.isinf(v), 0.0, (3 * np.abs(v) + 18) * U)) if softplus else np.full_like(v, 2 * U)
     Ba, Ca = np.abs(_rep(B, channels, groups)), np.abs(_rep(C, channels, groups))
     d = np.zeros(channels) if D is None else np.abs(D)
     sg = om.sigmoid(z) if z is not None else None
@@ -54,9 +56,7 @@ def scan_bounds(slots, x, dt, A, B, C, D, starts, lens, resume, z=None, dt_bias=
         gD_m, out["grad_D"] = np.zeros(channels), np.zeros(channels)
         gb_m, out["grad_dt_bias"] = np.zeros(channels), np.zeros(channels)
         out["grad_slots"] = np.zeros((len(lens),) + A.shape)
-        Z = om.sigmoid(v)
-        eslope = (3 * np.abs(v) + 8) * U if softplus else np.zeros_like(v)
-        del Z
+        eslope = np.where((v > 20) | np.isinf(v), 0.0, (3 * np.abs(v) + 8) * U) if softplus else np.zeros_like(v)
 
     def fold(m):
         return m.reshape(groups, -1, N).sum(1).ravel()

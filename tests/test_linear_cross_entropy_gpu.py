@@ -113,7 +113,7 @@ def test_several_pieces_of_the_vocabulary():
     T, V, D = 9000, 20000, 64
     c = _case(T, V, D, seed=8, ignored=0.5, equal=True)
     need = pkg.linear_cross_entropy_workspace_bytes(c["h"], c["w"], backward=True)
-    assert need > 9216 * D * 4 + (200 << 20)                # one piece of G, and grad_hidden in fp32
+    assert need < 9216 * 20224 * 2                          # less than G of the whole vocabulary (79 tiles of 256)
     loss, lse, gh, gw = _run(c)
     keep = torch.nonzero(c["t"] != -100)[:, 0]
     rows = keep[::200]
