@@ -126,9 +126,10 @@ def train(model, tokens, vocab):
     report = []
     for name in ("conv", "dt_bias", "A_log", "D", "norm", "w_dt"):
         d = torch.sign(grads[name])                           # a direction along which the loss does change
-        step = 2e-2 * float(model.p[name].abs().mean())
+        slope = float((grads[name].double() * d).sum())
+        step = 5e-3 / max(slope, 1e-2)                        # a change well above the roundings of the losses
         up, down = (float(model.loss(x, targets, meta, {**model.p, name: model.p[name] + s * step * d})) for s in (1, -1))
-        report.append((name, float((grads[name].double() * d).sum()), (up - down) / (2 * step)))
+        report.append((name, slope, (up - down) / (2 * step)))
     return float(model.loss(x, targets, meta)), report
 
 
