@@ -20,7 +20,9 @@
 // are fp32, and what is written is rounded once).  It is held relative to the largest |grad_loss|,
 // so that a mean's 1 / T is no rounding, and for fp16 2^15 times that, so that probabilities down to
 // 2^-29 keep all their bits; the sums get the factors back in fp32.
+#include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "packed.cuh"
 #include "pair_gemm.cuh"
@@ -55,10 +57,11 @@ struct LossArgs {
     float *label_logit;                       // [T]
     float2 *part;                             // [2 vocabulary tiles][T rounded up]
     void *hp, *wp, *G;
-    float *acc;                               // [T rounded up][D] fp32: grad h of the pieces so far
+    float *acc;                               // [splits][T rounded up][dp] fp32: grad h of the pieces or splits
     int t_pad, blocks;                        // T rounded up to a tile
     float factor;                             // 2^15 for fp16, else 1
     int v0, vp, first_piece, last_piece;      // a piece of the vocabulary
+    int splits;                               // most pairs that share a tile of grad h
     int fail_waits;
 };
 
@@ -236,7 +239,7 @@ loss_pack_weight_kernel(const LossArgs a)
 struct StatsEpilogue {
     const LossArgs &a;
     int rows;
-    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any, int split, float *block)
     {
         const int label = row < rows ? a.label[row] : -1;
         float m = -INFINITY, s = 0.f;
@@ -286,14 +289,14 @@ loss_stats_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, co
 {
     griddep_entry();
     const int rows = *a.kept;
-    pair::run<BF16, false, false>(pair::Shape{rows, a.V, a.D}, kGroupM, hmap, wmap, a.fail_waits, StatsEpilogue{a, rows});
+    pair::run<BF16, false, false>(pair::Shape{rows, a.V, a.D, 1}, kGroupM, hmap, wmap, a.fail_waits, StatsEpilogue{a, rows});
 }
 
 // G of a piece: rows up to a whole tile, zeros past the rows and past the vocabulary.
 template <class T>
 struct GradEpilogue {
     const LossArgs &a;
-    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any, int split, float *block)
     {
         const int label = a.label[row] - a.v0;
         const float scale = a.scale[row], lse = a.row_lse[row] * kLog2e;
@@ -323,60 +326,85 @@ loss_grad_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, con
 {
     griddep_entry();
     const int rows = *a.kept;
-    pair::run<BF16, false, false>(pair::Shape{rows, a.vp, a.D}, kGroupM, hmap, wmap, a.fail_waits, GradEpilogue<T>{a});
+    pair::run<BF16, false, false>(pair::Shape{rows, a.vp, a.D, 1}, kGroupM, hmap, wmap, a.fail_waits, GradEpilogue<T>{a});
 }
 
-// grad h: added up over the pieces in fp32, the last one writes the rows where they belong.
+// 32 columns of a warp's rows in 16 bits: `out` a lane's row (null: none), `left` how many columns exist.  Rows
+// on 16-byte boundaries are written as they lie in the lanes; others go through shared memory, so that
+// the lanes write neighbouring columns (grad w of 466 x 32003 x 1001 fp16: element by element along
+// rows 263 us, so 53).
+template <class T>
+__device__ __forceinline__ void write_rows(T *out, const float (&v)[32], int left, float back, bool aligned, float *block)
+{
+    const int lane = threadIdx.x & 31;
+    if (aligned && left >= 32) {
+        if (out)
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                Vec<T, 8> o;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    o.v[k] = from_float<T>(v[i + k] * back);
+                store_vec<T, 8>(out + i, o);
+            }
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        block[lane * 33 + i] = v[i] * back;
+    __syncwarp();
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+        T *row = reinterpret_cast<T *>(__shfl_sync(kFullMask, reinterpret_cast<unsigned long long>(out), r));
+        if (row && lane < left)
+            row[lane] = from_float<T>(block[r * 33 + lane]);
+    }
+}
+
+// Pairs that share a tile's terms (the vocabulary) where rows and width alone do not give every pair a tile.
+__host__ __device__ __forceinline__ int splits_of(int pairs, int rows, int D, int most)
+{
+    const int tiles = ((rows + pair::kTileM - 1) / pair::kTileM) * ((D + pair::kTileN - 1) / pair::kTileN);
+    const int n = tiles > 0 ? pairs / tiles : 1;
+    return n < 1 ? 1 : n > most ? most : n;
+}
+
+// grad h.  Sums that are whole go where they belong; those of a split, or of a piece that is not the last, to fp32
+// rows, in which pieces add up.
 template <class T>
 struct HiddenEpilogue {
     const LossArgs &a;
     int rows;
     float back;
-    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    bool aligned;
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any, int split, float *block)
     {
-        const bool in = row < rows;
-        float *acc = a.acc + (long long)row * a.dp + col;
-        T *out = in && a.last_piece ? static_cast<T *>(a.grad_h) + a.index[row] * a.sgh + col : nullptr;
+        const bool in = row < rows, direct = a.splits == 1 && a.last_piece;
+        float *acc = a.acc + ((long long)split * a.t_pad + row) * a.dp + col;
+        T *out = in && direct ? static_cast<T *>(a.grad_h) + a.index[row] * a.sgh + col : nullptr;
 #pragma unroll 1
         for (int j = 0; j < pair::kHalf; j += 32) {
             float v[32];
             pair::columns(v, at, j, ok, any);
-            if (!in || col + j >= a.D)
+            if (col + j >= a.D)
                 continue;
-            // rows of acc are dp long: whole groups of 8
+            if (in && (a.splits > 1 || !direct || !a.first_piece)) {    // rows of acc are dp long: whole groups of 4
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                if (col + j + i >= a.dp)
-                    break;
-                float4 *p = reinterpret_cast<float4 *>(acc + j + i);
-                if (!a.first_piece) {
-                    const float4 q = *p;
-                    v[i] += q.x; v[i + 1] += q.y; v[i + 2] += q.z; v[i + 3] += q.w;
+                for (int i = 0; i < 32; i += 4) {
+                    if (col + j + i >= a.dp)
+                        break;
+                    float4 *p = reinterpret_cast<float4 *>(acc + j + i);
+                    if (!a.first_piece) {
+                        const float4 q = *p;
+                        v[i] += q.x; v[i + 1] += q.y; v[i + 2] += q.z; v[i + 3] += q.w;
+                    }
+                    if (!direct)
+                        *p = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
-                if (!a.last_piece)
-                    *p = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
-            if (a.last_piece)
-                write_row<T>(out + j, v, a.D - col - j, back);
-        }
-    }
-    template <class U>
-    static __device__ __forceinline__ void write_row(U *out, const float (&v)[32], int left, float back)
-    {
-        if (left >= 32 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                Vec<U, 8> o;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    o.v[k] = from_float<U>(v[i + k] * back);
-                store_vec<U, 8>(out + i, o);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < left)
-                    out[i] = from_float<U>(v[i] * back);
+            if (direct)
+                write_rows<T>(out ? out + j : nullptr, v, a.D - col - j, back, aligned, block);
         }
     }
 };
@@ -387,25 +415,57 @@ loss_hidden_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, c
 {
     griddep_entry();
     const int rows = *a.kept;
-    const HiddenEpilogue<T> epi{a, rows, *a.top / a.factor};
-    pair::run<BF16, false, true>(pair::Shape{rows, a.D, min(a.vp, a.V - a.v0)}, kGroupM, gmap, wmap, a.fail_waits, epi);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(a.grad_h) | (uintptr_t)(a.sgh * 2)) & 15) == 0;
+    const HiddenEpilogue<T> epi{a, rows, *a.top / a.factor, aligned};
+    const int splits = splits_of(gridDim.x / 2, rows, a.D, a.splits);
+    pair::run<BF16, false, true>(pair::Shape{rows, a.D, min(a.vp, a.V - a.v0), splits}, kGroupM, gmap, wmap, a.fail_waits, epi);
+}
+
+// Rows of grad h from their splits' sums, where they belong: a block a row.
+template <class T>
+__global__ void __launch_bounds__(128)
+loss_hidden_join_kernel(const LossArgs a, int pairs)
+{
+    griddep_entry();
+    const int row = blockIdx.x, rows = *a.kept;
+    if (row >= rows)
+        return;
+    const int splits = splits_of(pairs, rows, a.D, a.splits);
+    const float back = *a.top / a.factor;
+    const long long next = (long long)a.t_pad * a.dp;
+    T *out = static_cast<T *>(a.grad_h) + a.index[row] * a.sgh;
+    for (int d = threadIdx.x; d < a.D; d += 128) {
+        const float *p = a.acc + (long long)row * a.dp + d;
+        float v = 0.f;
+        for (int s0 = 0; s0 < splits; s0 += 8) {
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[i] = p[min(s0 + i, splits - 1) * next];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v += s0 + i < splits ? q[i] : 0.f;
+        }
+        out[d] = from_float<T>(v * back);
+    }
 }
 
 template <class T>
 struct WeightEpilogue {
     const LossArgs &a;
     float back;
-    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any)
+    bool aligned;
+    __device__ __forceinline__ void tile(int row, int col, uint32_t at, bool ok, bool any, int split, float *block)
     {
         const int v = a.v0 + row;
         const bool in = v < a.V && row < a.vp;
-        T *out = static_cast<T *>(a.grad_w) + (in ? v * a.sgw : 0) + col;
+        T *out = in ? static_cast<T *>(a.grad_w) + v * a.sgw + col : nullptr;
 #pragma unroll 1
         for (int j = 0; j < pair::kHalf; j += 32) {
             float x[32];
             pair::columns(x, at, j, ok, any);
-            if (in && col + j < a.D)
-                HiddenEpilogue<T>::write_row(out + j, x, a.D - col - j, back);
+            if (col + j < a.D)
+                write_rows<T>(in ? out + j : nullptr, x, a.D - col - j, back, aligned, block);
         }
     }
 };
@@ -416,8 +476,9 @@ loss_weight_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, c
 {
     griddep_entry();
     const int rows = *a.kept;
-    const WeightEpilogue<T> epi{a, *a.top / a.factor};
-    pair::run<BF16, true, true>(pair::Shape{min(a.vp, a.V - a.v0), a.D, rows}, kGroupM, gmap, hmap, a.fail_waits, epi);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(a.grad_w) | (uintptr_t)(a.sgw * 2)) & 15) == 0;
+    const WeightEpilogue<T> epi{a, *a.top / a.factor, aligned};
+    pair::run<BF16, true, true>(pair::Shape{min(a.vp, a.V - a.v0), a.D, rows, 1}, kGroupM, gmap, hmap, a.fail_waits, epi);
 }
 
 // (largest logit, sum) of two disjoint sets of columns.
@@ -486,9 +547,14 @@ bool encode(CUtensorMap *map, const void *p, bool bf16, long long width, long lo
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+long long tiles_of(long long m, long long n)
+{
+    return ((m + pair::kTileM - 1) / pair::kTileM) * ((n + pair::kTileN - 1) / pair::kTileN);
+}
+
 // What lies where in the workspace.
 struct Plan {
-    int t_pad, blocks, dp, pieces, vp;
+    int t_pad, blocks, dp, pieces, vp, splits;
     bool pack_w;
     size_t counts, tops, kept, index, label, scale, row_lse, logit, part, hp, wp, G, acc, total;
 };
@@ -524,12 +590,21 @@ Plan plan(const void *w, int T, int V, int D, long long sw, bool backward)
         p.scale = take((size_t)p.t_pad * 4);
         p.row_lse = take((size_t)p.t_pad * 4);
         p.G = take((size_t)p.t_pad * p.vp * 2);
-        p.acc = p.pieces > 1 ? take((size_t)p.t_pad * p.dp * 4) : at;
+        // with one piece and few tiles, splits: up to 16, at least 16 stages each, and 64 MB of sums
+        p.splits = 1;
+        if (p.pieces == 1) {
+            const size_t sums = (size_t)p.t_pad * p.dp * 4;
+            const long long most = std::min<long long>({16, p.vp / (16 * pair::kTerms), (long long)(((size_t)64 << 20) / sums)});
+            if (most > 1 && tiles_of(T, D) * 2 <= kSms / 2)
+                p.splits = (int)most;
+        }
+        p.acc = p.pieces > 1 || p.splits > 1 ? take((size_t)p.splits * p.t_pad * p.dp * 4) : at;
         p.logit = p.part = 0;
     } else {
         p.logit = take((size_t)T * 4);
         p.part = take((size_t)(all / pair::kHalf) * p.t_pad * sizeof(float2));
         p.scale = p.row_lse = p.G = p.acc = 0;
+        p.splits = 1;
     }
     p.total = at;
     return p;
@@ -573,11 +648,6 @@ cudaError_t launch_pairs(K kernel, long long tiles, cudaStream_t st, const LossA
                       pair::Smem::kTotal, st, a, x, y);
 }
 
-long long tiles_of(long long m, long long n)
-{
-    return ((m + pair::kTileM - 1) / pair::kTileM) * ((n + pair::kTileN - 1) / pair::kTileN);
-}
-
 template <class T, bool BF16>
 cudaError_t launch_loss(LossArgs a, const Plan &p, bool backward, cudaStream_t st)
 {
@@ -617,8 +687,12 @@ cudaError_t launch_loss(LossArgs a, const Plan &p, bool backward, cudaStream_t s
         if (!encode(&wpiece, wv, BF16, a.D, rows, sw, 128) || !encode(&wpiece_n, wv, BF16, a.D, rows, sw, 64))
             return cudaErrorInvalidValue;
         e = launch_pairs(loss_grad_kernel<T, BF16>, tiles_of(a.T, a.vp), st, a, hmap, wpiece);
+        const long long tiles = a.splits > 1 ? INT_MAX : tiles_of(a.T, a.D);     // (every pair: the device knows the splits)
         if (e == cudaSuccess)
-            e = launch_pairs(loss_hidden_kernel<T, BF16>, tiles_of(a.T, a.D), st, a, gmap, wpiece_n);
+            e = launch_pairs(loss_hidden_kernel<T, BF16>, tiles, st, a, gmap, wpiece_n);
+        if (e == cudaSuccess && a.splits > 1)
+            e = launch_pdl(loss_hidden_join_kernel<T>, dim3(a.T), dim3(128), 0, st, a,
+                           resident_pairs(loss_hidden_kernel<T, BF16>));
         if (e == cudaSuccess && a.grad_w)
             e = launch_pairs(loss_weight_kernel<T, BF16>, tiles_of(rows, a.D), st, a, gmap_m, hmap_n);
         if (e != cudaSuccess)
@@ -643,7 +717,7 @@ cudaError_t launch_cross_entropy(const CrossEntropy &c, void *workspace, bool ba
     a.loss = c.loss; a.lse = c.lse; a.grad_h = c.grad_h; a.grad_w = c.grad_w;
     a.T = c.T; a.V = c.V; a.D = c.D; a.wide = c.wide; a.ignore = c.ignore;
     a.sh = c.sh; a.sw = c.sw; a.sgh = c.sgh; a.sgw = c.sgw;
-    a.dp = p.dp; a.t_pad = p.t_pad; a.blocks = p.blocks;
+    a.dp = p.dp; a.t_pad = p.t_pad; a.blocks = p.blocks; a.splits = backward ? p.splits : 1;
     a.counts = reinterpret_cast<int *>(ws + p.counts);
     a.tops = reinterpret_cast<float *>(ws + p.tops);
     a.kept = reinterpret_cast<int *>(ws + p.kept);

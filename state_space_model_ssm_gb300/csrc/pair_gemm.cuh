@@ -37,12 +37,15 @@ constexpr int kLimit = 1 << 22;               // polls before a wait gives up (s
 struct Smem {
     static constexpr int kBar = kStages * 2 * kOperand;
     static constexpr int kBars = 3 * kStages + 5;
-    static constexpr int kTotal = kBar + kBars * 8 + 16;
+    static constexpr int kBlock = kBar + (kBars * 8 + 16 + 15) / 16 * 16;   // 32 x 32 values of each epilogue warp, rows of 33
+    static constexpr int kTotal = kBlock + kEpilogueWarps * 32 * 33 * 4;
 };
+static_assert(Smem::kTotal <= 227 * 1024, "one block an SM");
 
-// Tiles of a launch: numbers that the device works out from how many rows there are.
+// Tiles of a launch: numbers that the device works out from how many rows there are.  With `splits` > 1 the
+// terms of a tile are shared by that many pairs, each of which runs the epilogue on its own sum.
 struct Shape {
-    int m, n, k;                              // rows of A, of B, terms
+    int m, n, k, splits;                      // rows of A, of B, terms
 };
 
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr)      // MN-major, 128-byte swizzle: 64 x 64 blocks of 8 KB
@@ -100,7 +103,8 @@ __device__ __forceinline__ void cluster_sync()
 }
 
 // One launch over the tiles of `shape`: groups of `group_m` row tiles, in which the row tile runs fastest.
-// Epi: setup(args), then tile(...) for each tile with a thread's half row of D.
+// epi.tile(row, first column, tensor memory address, whether the sums are there, whether there are any terms, split, the
+// warp's block of shared memory) runs for each tile with a thread's half row of D.
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtensorMap &amap, const CUtensorMap &bmap,
                                     int fail_waits, Epi epi)
@@ -111,7 +115,8 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
     const uint32_t rank = cluster_rank();
     const int pairs = gridDim.x / 2, pair_id = blockIdx.x / 2;
     const int tiles_m = (shape.m + kTileM - 1) / kTileM, tiles_n = (shape.n + kTileN - 1) / kTileN;
-    const int tiles = tiles_m * tiles_n, n_k = (shape.k + kTerms - 1) / kTerms;
+    const int stages = (shape.k + kTerms - 1) / kTerms, per_split = (stages + shape.splits - 1) / shape.splits;
+    const int places = tiles_m * tiles_n, tiles = places * shape.splits;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Smem::kBar);
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + Smem::kBars);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, peer = empty + 8 * kStages;
@@ -140,11 +145,16 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
     fence_after();
     cluster_sync();                                         // both blocks' barriers are there
     const uint32_t tmem = *slot;
-    auto place = [&](int tile, int &m, int &n) {
+    // a tile's rows, columns and range of stages
+    auto place = [&](int tile, int &m, int &n, int &k0) {
+        const int split = tile / places;
+        tile -= split * places;
+        k0 = split * per_split;
         const int per = group_m * tiles_n, g = tile / per, in = tile - g * per;
         const int gm = min(group_m, tiles_m - g * group_m);
         m = (g * group_m + in % gm) * kTileM;
         n = in / gm * kTileN;
+        return max(0, min(per_split, stages - k0));
     };
 
     if (warp == 0) {
@@ -152,11 +162,11 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
         int issued = 0;
         bool ok = true;
         for (int tile = pair_id; tile < tiles && ok; tile += pairs) {
-            int m, n;
-            place(tile, m, n);
+            int m, n, k0;
+            const int k1 = place(tile, m, n, k0) + k0;
             m += rank * kRowsB;
             n += rank * kRowsB;
-            for (int k = 0; k < n_k; ++k) {
+            for (int k = k0; k < k1; ++k) {
                 ok = __all_sync(kFullMask, mbar_poll(empty + 8 * r.s, r.phase ^ 1, cap));
                 if (!ok)
                     break;
@@ -190,8 +200,9 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
     } else if (warp == 1 && rank == 1) {
         Ring<kStages> r;
         bool ok = true;
-        for (int tile = pair_id; tile < tiles && ok; tile += pairs)
-            for (int k = 0; k < n_k; ++k) {
+        for (int tile = pair_id; tile < tiles && ok; tile += pairs) {
+            int m, n, k0;
+            for (int k = place(tile, m, n, k0); k > 0; --k) {
                 ok = __all_sync(kFullMask, mbar_poll(full + 8 * r.s, r.phase, cap));
                 if (!ok)
                     break;
@@ -200,12 +211,17 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
                 __syncwarp();
                 r.next();
             }
+        }
     } else if (warp == 1) {
         constexpr uint32_t id = idesc<BF16, A_MN, B_MN>();
         Ring<kStages> r;
         Ring<2> acc;
         bool ok = true;
-        for (int tile = pair_id; tile < tiles && ok && n_k > 0; tile += pairs) {
+        for (int tile = pair_id; tile < tiles && ok; tile += pairs) {
+            int m, n, k0;
+            const int n_k = place(tile, m, n, k0);
+            if (n_k == 0)
+                continue;
             ok = __all_sync(kFullMask, mbar_poll(accempty + 8 * acc.s, acc.phase ^ 1, cap));
             if (!ok)
                 break;
@@ -240,15 +256,16 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
         Ring<2> acc;
         bool ok = true;
         for (int tile = pair_id; tile < tiles; tile += pairs) {
-            int m, n;
-            place(tile, m, n);
+            int m, n, k0;
+            const int n_k = place(tile, m, n, k0);
             if (n_k > 0) {
                 ok = ok && mbar_poll(accfull + 8 * acc.s, acc.phase, cap);
                 ok = __all_sync(kFullMask, ok);
                 fence_after();
             }
             const uint32_t at = tmem + kTileN * acc.s + half * kHalf + ((uint32_t)(32 * quarter) << 16);
-            epi.tile(m + (int)rank * kRowsB + 32 * quarter + lane, n + half * kHalf, at, ok, n_k > 0);
+            epi.tile(m + (int)rank * kRowsB + 32 * quarter + lane, n + half * kHalf, at, ok, n_k > 0, tile / places,
+                     reinterpret_cast<float *>(sm + Smem::kBlock) + e * 32 * 33);
             if (n_k > 0) {
                 fence_before();
                 __syncwarp();

@@ -156,8 +156,9 @@ __device__ __forceinline__ float2 sel_slope2(float2 v, bool softplus)
 // How a warp stages pairs of channels of up to L tokens: place m of a lane is token tok(m), pair cp(m).
 template <int WC, int L>
 struct SelStage {
-    static constexpr int P = WC / 2, KC = P >= 32 ? P / 32 : 1, TI = P >= 32 ? 1 : 32 / P, M = L * P / 32;
-    static_assert(M >= 1 && L % TI == 0, "whole places");
+    static constexpr int P = WC / 2, KC = P >= 32 ? P / 32 : 1, TI = P >= 32 ? 1 : 32 / P;
+    static constexpr int M = L * P / 32 > 0 ? L * P / 32 : 1, kTokens = L > TI ? L : TI;   // (places past L are staged and not used)
+    static_assert(kTokens % TI == 0, "whole places");
     static __device__ __forceinline__ int tok(int m, int lane) { return P >= 32 ? m / KC : m * TI + lane / P; }
     static __device__ __forceinline__ int cp(int m, int lane) { return P >= 32 ? lane + 32 * (m % KC) : lane % P; }
 };
@@ -311,8 +312,9 @@ __device__ __forceinline__ void write_states(float *row, const float2 (&v)[NP / 
     }
 }
 
-// States past the last one are kept at zero: an infinite input would make them NaN (0 times
-// infinity), and their zeros of C would not take that out of a sum.
+// States past the last one are zero, and stay so while steps and inputs are finite.  In a chunk where one is not
+// they are set back after every token: 0 times infinity would make them NaN, and their zeros of C would not
+// take that out of a sum.
 template <int NP>
 __device__ __forceinline__ void drop_padding(float2 (&v)[NP / 2], int n0, int N)
 {

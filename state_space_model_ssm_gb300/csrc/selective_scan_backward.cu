@@ -58,7 +58,7 @@ constexpr int kBackL = kSelChunk, kBackNP = 4, kKeepTokens = 8;
 template <int LN>
 struct BackLayout {                                         // floats of a warp, then of the block
     static constexpr int WC = 32 / LN * kSelCh, NN = kBackNP * LN;
-    static constexpr int kRow = kBackL * WC;
+    static constexpr int kRow = SelStage<WC, kBackL>::kTokens * WC;
     static constexpr int kSlot = 128;                       // four floats of every lane
     static constexpr int kKeep = kKeepTokens * 4 * kSlot;   // k of every token: four slots
     static constexpr int kWarp = kKeep + kKeepTokens * kSlot + 3 * kRow + kKeepTokens * WC;
@@ -66,12 +66,16 @@ struct BackLayout {                                         // floats of a warp,
     static constexpr size_t kBytes = ((size_t)kWarp * kSelWarps + 4 * kRows) * sizeof(float);
 };
 
+// Threads that share an output of a block's sums over channels.
+template <int LN>
+constexpr int kSumParts = 32 * kSelWarps / (kKeepTokens * LN) > 1 ? 32 * kSelWarps / (kKeepTokens * LN) : 1;
+
 // Sums over a block's channels of what its lanes have put into slot `slot` of eight tokens (four states a lane):
 // terms are the warps' lanes of one state, `kParts` threads of a warp share an output of four states.
 template <int LN>
 __device__ __forceinline__ float4 sum_slots(const float *first, int warp_stride, int token_stride, int out, int part)
 {
-    constexpr int Q = 32 / LN, kTerms = kSelWarps * Q, kParts = LN <= 16 ? 16 / LN : 1, kEach = kTerms / kParts;
+    constexpr int Q = 32 / LN, kTerms = kSelWarps * Q, kParts = kSumParts<LN>, kEach = kTerms / kParts;
     const int t = out / LN, sub = out % LN;
     float2 lo = make_float2(0.f, 0.f), hi = lo;
 #pragma unroll
@@ -103,6 +107,9 @@ __device__ __forceinline__ float2 sum_lanes(const float *slot, int c)
     return v;
 }
 
+// Two blocks an SM (1 x 4096 x 4096 channels x 16 states, bf16: 488 us).  Three of 168 registers with k of four tokens
+// (546 to 590 us), two channels a lane with three blocks (594 us), a saved state every 8 tokens
+// and no second walk (538 us) were slower.
 template <class T, int LN>
 __global__ void __launch_bounds__(32 * kSelWarps, LN == 32 ? 1 : 2)
 sel_backward_kernel(const SelArgs a)
@@ -112,7 +119,7 @@ sel_backward_kernel(const SelArgs a)
     constexpr int CH = kSelCh, NP = kBackNP, WC = Y::WC, NN = Y::NN, L = kBackL, K = kKeepTokens;
     using S = SelStage<WC, L>;
     constexpr int M = S::M, KC = S::KC, H = M > 8 ? 8 : M;  // places loaded together
-    constexpr int E = M > 1 ? M / 2 : 1;                    // places of eight tokens
+    constexpr int R = L / K, E = M >= R ? M / R : 1;        // places of K tokens (all of them where a place has more)
     constexpr int kOwn = CH > LN ? CH / LN : 1;             // sums over states that a lane ends with
     extern __shared__ __align__(16) float sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -161,7 +168,7 @@ sel_backward_kernel(const SelArgs a)
                 write_states<NP>(base + (long long)(tile.c0 + c) * a.N, r, n0, a.N, vec);
         }
     };
-    auto drop = [&](float2 (&v)[NP]) {                      // padding states
+    auto drop_padding = [&](float2 (&v)[NP]) {              // (see there)
 #pragma unroll
         for (int n = 0; n < NP; ++n)
             v[n] = n0 + n < a.N ? v[n] : make_float2(0.f, 0.f);
@@ -203,6 +210,7 @@ sel_backward_kernel(const SelArgs a)
 #pragma unroll
         for (int c = 0; c < CP; ++c)
             read_pair(h0[c], cs, c, vec_c, true);
+        float2 finite = make_float2(0.f, 0.f);              // a NaN once anything is infinite or a NaN
         if (wc > 0) {
 #pragma unroll
             for (int m0 = 0; m0 < M; m0 += H) {
@@ -221,6 +229,8 @@ sel_backward_kernel(const SelArgs a)
                         const float2 zv = pair_of<T>(rz[k]);
                         g = mul2(g, mul2(zv, sigmoid2(zv)));
                     }
+                    if (pad)
+                        finite = fma2(g, twice(0.f), fma2(v, twice(0.f), fma2(st, twice(0.f), finite)));
                     // what is not there takes no part in the sums over channels
                     const bool one = t < cnt && c < wc, two = t < cnt && c + 1 < wc;
                     *reinterpret_cast<float2 *>(step + t * WC + c) = make_float2(one ? st.x : 0.f, two ? st.y : 0.f);
@@ -232,11 +242,12 @@ sel_backward_kernel(const SelArgs a)
             for (int i = lane; i < 3 * Y::kRow; i += 32)
                 step[i] = 0.f;
         }
+        const bool drop = pad && __any_sync(kFullMask, finite.x + finite.y != 0.f);
         rB.store_twice(Bs, a.N);
         rC.store_twice(Cs, a.N);
         __syncthreads();
 #pragma unroll 1
-        for (int first = cnt > K ? K : 0; first >= 0; first -= K) {
+        for (int first = (cnt - 1) / K * K; first >= 0; first -= K) {
             const int stop = min(cnt, first + K);
             float2 h[CP][NP];
 #pragma unroll
@@ -257,7 +268,7 @@ sel_backward_kernel(const SelArgs a)
                         h[c][n] = fma2(ex2_2(mul2(st[c], A[c][n])), h[c][n], mul2(uv[c], Bv[n]));
             }
             // what the gate's gradient and the outputs read, loaded before the walks that come first
-            const int m0 = M > 1 && first > 0 ? E : 0;
+            const int m0 = M >= R ? first / K * E : 0;
             RawPair<T> rz[E], rx[E], rg[E], rdt[E];
             if (wc > 0) {
                 load_places<T, WC, L>(rx, m0, x + t0 * a.sx, a.sx, cnt, wc, lane, pairs);
@@ -283,9 +294,9 @@ sel_backward_kernel(const SelArgs a)
                         k[n] = mul2(ex2_2(mul2(st[c], A[c][n])), h[c][n]);
                         h[c][n] = fma2(uv[c], Bv[n], k[n]);
                     }
-                    if (pad) {
-                        drop(h[c]);
-                        drop(k);
+                    if (drop) {
+                        drop_padding(h[c]);
+                        drop_padding(k);
                     }
 #pragma unroll
                     for (int n = 0; n < NP; ++n) {
@@ -349,8 +360,8 @@ sel_backward_kernel(const SelArgs a)
 #pragma unroll
                     for (int n = 0; n < NP; ++n)
                         e[c][n] = fma2(gv[c], Cv[n], e[c][n]);
-                    if (pad)
-                        drop(e[c]);
+                    if (drop)
+                        drop_padding(e[c]);
 #pragma unroll
                     for (int n = 0; n < NP; ++n) {
                         const float2 v = mul2(e[c][n], k[n]);
@@ -369,7 +380,7 @@ sel_backward_kernel(const SelArgs a)
                     make_float4(sum_b[0].x + sum_b[0].y, sum_b[1].x + sum_b[1].y, sum_b[2].x + sum_b[2].y, sum_b[3].x + sum_b[3].y);
             }
             __syncthreads();                                // every warp's sums are there
-            constexpr int kParts = LN <= 16 ? 16 / LN : 1;
+            constexpr int kParts = kSumParts<LN>;
 #pragma unroll
             for (int i = tid; i < K * LN * kParts; i += 32 * kSelWarps) {
                 const int out = i / kParts, part = i % kParts, t = first + out / LN, n = out % LN * NP;

@@ -29,9 +29,10 @@ struct WalkLayout {
 };
 
 // Three blocks an SM, 168 registers a thread: unbounded, kFull took 238 and 1 x 4096 x 4096 channels x 16 states
-// (bf16) 180 us instead of 126.  Four states a lane, four blocks an SM: 156 us.
+// (bf16) 180 us instead of 126.  Four states a lane, four blocks an SM: 156 us.  fp32 rows need twice the registers
+// while staged and spill at three blocks (4 x 777 x 1001 channels: 80 us instead of 54).
 template <class T, int LN, SelMode MODE>
-__global__ void __launch_bounds__(32 * kSelWarps, LN == 1 && sizeof(T) == 4 ? 2 : 3)
+__global__ void __launch_bounds__(32 * kSelWarps, sizeof(T) == 4 && (LN == 1 || MODE == kFull) ? 2 : 3)
 sel_walk_kernel(const SelArgs a)
 {
     griddep_entry();
@@ -112,6 +113,7 @@ sel_walk_kernel(const SelArgs a)
                 if (q * CH + c < wc)
                     write_states<NP>(cs + (long long)(tile.c0 + q * CH + c) * a.N, h[c], n0, a.N, vec_c);
         }
+        float2 finite = make_float2(0.f, 0.f);              // a NaN once anything is infinite or a NaN
         if (wc > 0) {
 #pragma unroll
             for (int m = 0; m < M; ++m) {
@@ -122,11 +124,12 @@ sel_walk_kernel(const SelArgs a)
                     const float2 g = pair_of<T>(rz[m]);
                     xv = mul2(xv, mul2(g, sigmoid2(g)));
                 }
-                if (MODE == kCarry)
-                    *reinterpret_cast<float2 *>(in + at) = xv;
-                else
-                    *reinterpret_cast<float2 *>(in + at) = mul2(st, xv);
+                if (MODE != kCarry)
+                    xv = mul2(st, xv);
+                *reinterpret_cast<float2 *>(in + at) = xv;
                 *reinterpret_cast<float2 *>(step + at) = st;
+                if (pad)
+                    finite = fma2(xv, twice(0.f), fma2(st, twice(0.f), finite));
                 if (MODE == kFull)
                     xk[m] = rx[m];
                 else if (S::tok(m, lane) < cnt)
@@ -135,6 +138,7 @@ sel_walk_kernel(const SelArgs a)
             if (MODE == kFull && z)
                 load_places<T, WC, L>(rz, 0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
         }
+        const bool drop = pad && __any_sync(kFullMask, finite.x + finite.y != 0.f);
         rB.store(Bs, a.N);
         if (MODE == kFull)
             rC.store(Cs, a.N);
@@ -164,7 +168,7 @@ sel_walk_kernel(const SelArgs a)
                     else
                         h[c][j] = fma2(decay, h[c][j], mul2(twice(uv[c]), Bv[j]));
                 }
-                if (pad)
+                if (drop)
                     drop_padding<NP>(h[c], n0, a.N);
                 if (MODE == kFull) {
 #pragma unroll
