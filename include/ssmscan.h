@@ -720,7 +720,9 @@ int ssm_linear_cross_entropy(const void *hidden, const void *weight, const void 
  * taken.  The logits are recomputed in pieces of the vocabulary; G of a piece is held
  * in dtype relative to the largest |grad_loss| (fp16: times 2^15), so each of its terms is rounded
  * to half a step before the products; the sums are fp32 and rounded once.
- * grad_weight may be NULL (a frozen projection): it is not computed.
+ * grad_weight may be NULL (a frozen projection): it is not computed.  Outputs must not overlap
+ * inputs.  Where there are few rows, several pairs of SMs share the terms of grad_hidden; the
+ * order of its sum depends on the sizes and on how many rows count, not on the run.
  * workspace: as above with backward = 1: also one piece of G (256 MB, or for large calls 16 bytes an
  * element of hidden) and, where there are several, grad_hidden in fp32.
  */

@@ -108,8 +108,8 @@ __device__ __forceinline__ float2 sum_lanes(const float *slot, int c)
 }
 
 // Two blocks an SM (1 x 4096 x 4096 channels x 16 states, bf16: 488 us).  Three of 168 registers with k of four tokens
-// (546 to 590 us), two channels a lane with three blocks (594 us), a saved state every 8 tokens
-// and no second walk (538 us) were slower.
+// (546 to 590 us), k of four tokens in registers (625 us: more code, more barriers), two channels a lane with three
+// blocks (594 us), a saved state every 8 tokens and no second walk (538 us) were slower.
 template <class T, int LN>
 __global__ void __launch_bounds__(32 * kSelWarps, LN == 32 ? 1 : 2)
 sel_backward_kernel(const SelArgs a)
