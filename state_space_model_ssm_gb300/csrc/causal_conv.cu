@@ -17,6 +17,8 @@
 // span.  Backward recomputes v from the window.  Only the first span of a sequence reads its
 // slot, so it writes it too.  The sums over tokens of grad w and grad bias leave as one row a
 // span and are added in a second kernel in a fixed order.
+#include <type_traits>
+
 #include "packed.cuh"
 
 namespace ssm {
@@ -209,7 +211,7 @@ causal_conv_kernel(const ConvArgs a)
             ch.write(slot + u, K - 1, v);
         }
     }
-    for (int b = begin; b < end; b += kRun) {
+    auto run = [&](int b, auto whole) {                     // whole: every token of the run is in the span
         RawPair<T> in[kRun];
 #pragma unroll
         for (int r = 0; r < kRun; ++r)
@@ -219,10 +221,15 @@ causal_conv_kernel(const ConvArgs a)
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
             const float2 v = taps<K>(w, bias, win, pair_of<T>(in[r]));
-            if (b + r < end)
+            if (decltype(whole)::value || b + r < end)
                 ch.store(out + (long long)(b + r) * a.so, a.silu ? mul2(v, sigmoid2(v)) : v);
         }
-    }
+    };
+    int b = begin;
+    for (; b + kRun <= end; b += kRun)
+        run(b, std::true_type());
+    if (b < end)
+        run(b, std::false_type());
 }
 
 template <class T, bool PAIRS, int K>
@@ -263,7 +270,9 @@ causal_conv_backward_kernel(const ConvArgs a)
     if (begin < end)
         fetch(begin);
     first_window<T, K>(win, a.state0, x, a, ch, seq, begin);
-    for (int b = begin; b < stop; b += kRun) {
+    // whole: every token of the run is in the span, and behind its first K - 1
+    auto run = [&](int b, auto whole) {
+        constexpr bool W = decltype(whole)::value;
         RawPair<T> in[kRun], g[kRun];
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
@@ -275,7 +284,7 @@ causal_conv_backward_kernel(const ConvArgs a)
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
             const int t = b + r;
-            if (t < stop && t < len) {
+            if (W || (t < stop && t < len)) {
                 const float2 now = pair_of<T>(in[r]);
                 float2 before[K > 1 ? K - 1 : 1], gv = pair_of<T>(g[r]);
 #pragma unroll
@@ -286,7 +295,7 @@ causal_conv_backward_kernel(const ConvArgs a)
                     const float2 s = sigmoid2(v);
                     gv = mul2(gv, fma2(mul2(v, s), make_float2(1.f - s.x, 1.f - s.y), s));
                 }
-                if (t < end) {
+                if (W || t < end) {
                     gb = add2(gb, gv);
 #pragma unroll
                     for (int u = 0; u < K - 1; ++u)
@@ -298,7 +307,9 @@ causal_conv_backward_kernel(const ConvArgs a)
                     sum[u] = fma2(w[u], gv, sum[u]);
             }
             // stream entry t is complete: token t - (K - 1), or entry t of the slot
-            if (t < stop && (t >= begin + K - 1 || k == 0)) {
+            if (W) {
+                ch.store(gx + (long long)(t - (K - 1)) * a.sgx, sum[0]);
+            } else if (t < stop && (t >= begin + K - 1 || k == 0)) {
                 float2 done = sum[0];
                 if (K > 1 && t >= len && a.grad_state)
                     done = add2(done, ch.read(a.grad_state + slot + t - len, K - 1));
@@ -312,6 +323,13 @@ causal_conv_backward_kernel(const ConvArgs a)
                 sum[u] = sum[u + 1];
             sum[K - 1] = zero;
         }
+    };
+    static_assert(kRun >= K - 1, "the run behind the first is behind the window");
+    for (int b = begin; b < stop; b += kRun) {
+        if (b > begin && b + kRun <= end)
+            run(b, std::true_type());
+        else
+            run(b, std::false_type());
     }
     float *part = a.part + (long long)unit * (K + 1) * a.C;
 #pragma unroll

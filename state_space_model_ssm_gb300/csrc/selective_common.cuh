@@ -15,9 +15,10 @@
 // instruction; the exponential is the hardware's 2^x of the rounded product
 // step * (A log2(e)), within 2 ulp and 2^-24 of its argument.
 //
-// Time: a unit is a sequence, or one of its segments of `seg` tokens where sequences
-// and channels alone do not fill the device.  Then a pass before composes each
-// segment's state from zero, and a small one walks the segments.
+// Time: a unit is a sequence, or, of a sequence so long that others would have to wait for it, a
+// segment of `seg` tokens.  Of those a pass before composes each segment's state from zero, and a
+// small one walks the segments.  The lengths are on the device, so a plan made there says which
+// sequences are cut; the host says from which length on.
 #pragma once
 
 #include "packed.cuh"
@@ -38,7 +39,7 @@ struct SelArgs {
     int n_seqs, n_tokens, channels, N, groups, softplus;
     long long sx, sdt, sz, sB, sC, sy;
     float *chunk_states;
-    int seg;                              // tokens of a segment, 0: units are whole sequences
+    int seg, whole;                       // tokens of a segment (0: units are sequences); of the longest sequence left whole
     const int2 *units;                    // (sequence, segment)
     const int *first;                     // [n_seqs + 1]: a sequence's first unit; the last entry: how many there are
     float *unit_state, *unit_step;        // [units][channels][N], [units][channels]
@@ -76,7 +77,7 @@ __device__ __forceinline__ int sel_seq_len(const SelArgs &a, int seq, long long 
 struct SelUnit {
     int seq, k, begin, end, len;
     long long t0;
-    bool last;                            // of its sequence
+    bool last, cut;                       // the last of its sequence; one of several
 };
 
 __device__ __forceinline__ bool sel_unit(const SelArgs &a, int u, SelUnit &s)
@@ -91,8 +92,9 @@ __device__ __forceinline__ bool sel_unit(const SelArgs &a, int u, SelUnit &s)
         s.k = v.y;
     }
     s.len = sel_seq_len(a, s.seq, s.t0);
-    s.begin = a.seg * s.k;
-    s.end = a.seg ? min(s.len, s.begin + a.seg) : s.len;
+    s.cut = a.seg && a.first[s.seq + 1] - a.first[s.seq] > 1;
+    s.begin = s.cut ? a.seg * s.k : 0;
+    s.end = s.cut ? min(s.len, s.begin + a.seg) : s.len;
     s.last = s.end == s.len;
     return true;
 }
@@ -362,9 +364,12 @@ struct SelShape {
     int wc, cblocks, tiles;               // channels of a warp; blocks of channels; warps of channels
 };
 SelShape sel_shape(int channels, int N, int groups, bool backward);
-// Tokens of a segment (0: whole sequences) and the bound on units.
+// Tokens of a segment (0: units are sequences) and of the longest sequence that is left whole.
+struct SelCut {
+    int seg, whole;
+};
+SelCut sel_cut(int n_seqs, int n_tokens, const SelShape &s, bool backward);
 bool sel_pairs(const SelArgs &a, int dtype);
-int sel_segment(int n_seqs, int n_tokens, const SelShape &s, bool backward);
 int sel_max_units(int n_seqs, int n_tokens, int seg);
 long long sel_chunk_rows(long long n_seqs, long long n_tokens);
 cudaError_t launch_sel_plan(const SelArgs &a, int2 *units, int *first, cudaStream_t st);   // a.max_units bounds it

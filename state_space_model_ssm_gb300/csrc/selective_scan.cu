@@ -2,13 +2,15 @@
 // Formulas and the layout of a warp: selective_common.cuh.
 //
 // The walk itself: selective_walk.cuh.
+#include <algorithm>
+
 #include "selective_walk.cuh"
 
 namespace ssm {
 
 namespace {
 
-// Units of every sequence: as many segments as its tokens take, one at least.
+// Units of every sequence: one, or as many segments as its tokens take.
 __global__ void __launch_bounds__(1024)
 sel_plan_kernel(const SelArgs a, int2 *units, int *first)
 {
@@ -19,7 +21,8 @@ sel_plan_kernel(const SelArgs a, int2 *units, int *first)
     for (int s0 = 0; s0 < a.n_seqs; s0 += 1024) {
         const int seq = s0 + tid;
         long long t0;
-        const int mine = seq < a.n_seqs ? max(1, (sel_seq_len(a, seq, t0) + a.seg - 1) / a.seg) : 0;
+        const int len = seq < a.n_seqs ? sel_seq_len(a, seq, t0) : 0;
+        const int mine = seq >= a.n_seqs ? 0 : len <= a.whole ? 1 : (len + a.seg - 1) / a.seg;
         int incl = mine;
         for (int off = 1; off < 32; off *= 2) {
             const int v = __shfl_up_sync(kFullMask, incl, off);
@@ -58,6 +61,8 @@ sel_combine_kernel(const SelArgs a)
         return;
     const long long e = i - seq * width;
     const int c = (int)(e / a.N), u1 = a.first[seq + 1];
+    if (u1 - a.first[seq] <= 1)                             // a whole sequence reads its slot itself
+        return;
     const float A = a.A[e] * kLog2e;
     float h = a.resume[seq] != 0 ? a.state[i] : 0.f;
     // loads of a run of units together (one by one, each waited for the store before it)
@@ -111,17 +116,20 @@ SelShape sel_shape(int channels, int N, int groups, bool backward)
     return s;
 }
 
-int sel_segment(int n_seqs, int n_tokens, const SelShape &s, bool backward)
+SelCut sel_cut(int n_seqs, int n_tokens, const SelShape &s, bool backward)
 {
-    // Warps that walk whole sequences, against those that are resident at once (three blocks an SM, two backward).
-    // With segments the forward pass takes about one round of them; the backward pass about two, since the pass that
-    // finds what segments hand on walks the same units with twice the channels a warp.
-    const long long want = kSms * kSelWarps * (backward ? 2 : 3), walk = (long long)n_seqs * s.tiles;
-    if (walk >= want || n_tokens < 128 || n_tokens / n_seqs < 64)
-        return 0;
-    const long long round = (backward ? 2 : 1) * want, units = round / s.tiles > 1 ? round / s.tiles : 1;
+    // Warps that are resident at once (three blocks an SM; two backward), and the tokens that each would walk if
+    // all had the same to do.  A sequence of at most one and a half times that is not worth the second walk.
+    const long long warps = kSms * kSelWarps * (backward ? 2 : 3);
+    const long long even = ((long long)n_tokens * s.tiles + warps - 1) / warps, whole = even + even / 2 < 128 ? 128 : even + even / 2;
+    if (n_tokens <= whole || n_tokens == n_seqs)            // (as many tokens as sequences: a decode step)
+        return SelCut{0, 0};
+    // Segments: of one sequence, one round of warps (backward two, since the pass that finds what segments hand on has
+    // twice the channels a warp); of several, whose lengths are not known here, shorter ones, so that the last
+    // round has less to wait for (12 uneven, 7889 tokens x 4096 channels x 16 states: 362 us with one round).
+    const long long rounds = (n_seqs == 1 ? 1 : 3) * (backward ? 2 : 1), units = std::max(1LL, rounds * warps / s.tiles);
     const long long seg = ((n_tokens + units - 1) / units + kSelChunk - 1) / kSelChunk * kSelChunk;
-    return (int)(seg < 64 ? 64 : seg);
+    return SelCut{(int)std::max(64LL, seg), (int)std::max(whole, seg)};
 }
 
 // Whether two channels of each of these rows are one aligned word.
@@ -160,7 +168,7 @@ Workspace layout(int n_seqs, int channels, int N, int units)
 
 size_t sel_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, int N, int groups)
 {
-    const int seg = sel_segment(n_seqs, n_tokens, sel_shape(channels, N, groups, false), false);
+    const int seg = sel_cut(n_seqs, n_tokens, sel_shape(channels, N, groups, false), false).seg;
     return seg ? layout(n_seqs, channels, N, sel_max_units(n_seqs, n_tokens, seg)).total : 0;
 }
 
@@ -169,7 +177,9 @@ cudaError_t launch_selective_scan(SelArgs a, int dtype, void *workspace, cudaStr
     const SelShape s = sel_shape(a.channels, a.N, a.groups, false);
     a.cblocks = s.cblocks;
     a.pairs = sel_pairs(a, dtype);
-    a.seg = sel_segment(a.n_seqs, a.n_tokens, s, false);
+    const SelCut cut = sel_cut(a.n_seqs, a.n_tokens, s, false);
+    a.seg = cut.seg;
+    a.whole = cut.whole;
     const int units = sel_max_units(a.n_seqs, a.n_tokens, a.seg);
     a.max_units = units;
     if (a.seg) {

@@ -33,6 +33,8 @@ sel_carry_combine_kernel(const SelArgs a)
         return;
     const long long e = i - seq * width;
     const int c = (int)(e / a.N), u0 = a.first[seq];
+    if (a.first[seq + 1] - u0 <= 1)                         // a whole sequence takes grad_state itself
+        return;
     const float A = a.A[e] * kLog2e;
     float g = a.grad_state ? a.grad_state[i] : 0.f;
     for (int u = a.first[seq + 1] - 1; u >= u0; u -= kCombineRun) {
@@ -176,7 +178,7 @@ sel_backward_kernel(const SelArgs a)
 #pragma unroll
     for (int c = 0; c < CP; ++c) {
         read_pair(A[c], a.A, c, false, true);
-        if (a.seg)
+        if (s.cut)
             read_pair(e[c], a.unit_state + (long long)u * a.channels * a.N, c, a.N % 4 == 0, true);
         else
             read_pair(e[c], a.grad_state + (long long)s.seq * a.channels * a.N, c, false, a.grad_state != nullptr);
@@ -229,8 +231,6 @@ sel_backward_kernel(const SelArgs a)
                         const float2 zv = pair_of<T>(rz[k]);
                         g = mul2(g, mul2(zv, sigmoid2(zv)));
                     }
-                    if (pad)
-                        finite = fma2(g, twice(0.f), fma2(v, twice(0.f), fma2(st, twice(0.f), finite)));
                     // what is not there takes no part in the sums over channels
                     const bool one = t < cnt && c < wc, two = t < cnt && c + 1 < wc;
                     *reinterpret_cast<float2 *>(step + t * WC + c) = make_float2(one ? st.x : 0.f, two ? st.y : 0.f);
@@ -238,6 +238,14 @@ sel_backward_kernel(const SelArgs a)
                     *reinterpret_cast<float2 *>(gs + t * WC + c) = make_float2(one ? g.x : 0.f, two ? g.y : 0.f);
                 }
             }
+            if (pad)                                        // (a lane's own places)
+#pragma unroll 1
+                for (int m = 0; m < M; ++m) {
+                    const float *p = step + S::tok(m, lane) * WC + 2 * S::cp(m, lane);
+#pragma unroll
+                    for (int r = 0; r < 3; ++r)
+                        finite = fma2(*reinterpret_cast<const float2 *>(p + r * Y::kRow), twice(0.f), finite);
+                }
         } else {
             for (int i = lane; i < 3 * Y::kRow; i += 32)
                 step[i] = 0.f;
@@ -570,7 +578,7 @@ Workspace layout(int n_seqs, int n_tokens, int channels, int N, int groups, int 
 size_t sel_backward_workspace_bytes(int n_seqs, int n_tokens, int channels, int N, int groups)
 {
     const SelShape s = sel_shape(channels, N, groups, true);
-    return layout(n_seqs, n_tokens, channels, N, groups, sel_segment(n_seqs, n_tokens, s, true), s.cblocks).total;
+    return layout(n_seqs, n_tokens, channels, N, groups, sel_cut(n_seqs, n_tokens, s, true).seg, s.cblocks).total;
 }
 
 cudaError_t launch_selective_scan_backward(SelArgs a, int dtype, void *workspace, cudaStream_t st)
@@ -578,7 +586,9 @@ cudaError_t launch_selective_scan_backward(SelArgs a, int dtype, void *workspace
     const SelShape s = sel_shape(a.channels, a.N, a.groups, true);
     a.cblocks = s.cblocks;
     a.pairs = sel_pairs(a, dtype);
-    a.seg = sel_segment(a.n_seqs, a.n_tokens, s, true);
+    const SelCut cut = sel_cut(a.n_seqs, a.n_tokens, s, true);
+    a.seg = cut.seg;
+    a.whole = cut.whole;
     a.max_units = sel_max_units(a.n_seqs, a.n_tokens, a.seg);
     unsigned char *w = static_cast<unsigned char *>(workspace);
     const Workspace l = layout(a.n_seqs, a.n_tokens, a.channels, a.N, a.groups, a.seg, a.cblocks);

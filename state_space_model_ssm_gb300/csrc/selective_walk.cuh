@@ -65,7 +65,7 @@ sel_walk_kernel(const SelArgs a)
             A[c][j] = mul2(A[c][j], twice(kLog2e));
         if (MODE != kFull)
             read_states<NP>(h[c], nullptr, n0, a.N, false, false);
-        else if (a.seg)
+        else if (s.cut)
             read_states<NP>(h[c], a.unit_state + ((long long)u * a.channels + ch) * a.N, n0, a.N, a.N % 4 == 0, there);
         else
             read_states<NP>(h[c], a.state + ((long long)s.seq * a.channels + ch) * a.N, n0, a.N, vec,
@@ -128,8 +128,6 @@ sel_walk_kernel(const SelArgs a)
                     xv = mul2(st, xv);
                 *reinterpret_cast<float2 *>(in + at) = xv;
                 *reinterpret_cast<float2 *>(step + at) = st;
-                if (pad)
-                    finite = fma2(xv, twice(0.f), fma2(st, twice(0.f), finite));
                 if (MODE == kFull)
                     xk[m] = rx[m];
                 else if (S::tok(m, lane) < cnt)
@@ -137,6 +135,13 @@ sel_walk_kernel(const SelArgs a)
             }
             if (MODE == kFull && z)
                 load_places<T, WC, L>(rz, 0, z + t0 * a.sz, a.sz, cnt, wc, lane, pairs);
+            if (pad)                                        // (a lane's own places)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const int at = S::tok(m, lane) * WC + 2 * S::cp(m, lane);
+                    finite = fma2(*reinterpret_cast<const float2 *>(in + at), twice(0.f),
+                                  fma2(*reinterpret_cast<const float2 *>(step + at), twice(0.f), finite));
+                }
         }
         const bool drop = pad && __any_sync(kFullMask, finite.x + finite.y != 0.f);
         rB.store(Bs, a.N);

@@ -182,9 +182,7 @@ def test_many_segments_and_long_sequences():
     _check(c, y, slots, _backward(c, ch))
 
 
-def test_whole_walks_without_segments():
-    """So many sequences that none is cut."""
-    assert pkg.selective_scan_workspace_bytes(400, 400 * 70, 320, 16) == 0
+def test_many_sequences_none_of_them_cut():
     c = _case(320, 16, [70] * 400, seed=13)
     y, slots, ch = _forward(c, train=True)
     grads = _backward(c, ch)
@@ -197,6 +195,14 @@ def test_whole_walks_without_segments():
         part = {n: v[rows] for n, v in grads.items() if n in ("grad_x", "grad_dt", "grad_z", "grad_B", "grad_C")}
         part["grad_slots"] = grads["grad_slots"][k:k + 1]
         _check(s, y[rows], slots[k:k + 1], part)
+
+
+def test_a_long_sequence_among_single_tokens():
+    """Most sequences are left whole, one is cut."""
+    lens = [1] * 120 + [900] + [1] * 80 + [0, 130]
+    c = _case(48, 16, lens, seed=17, dtype=torch.bfloat16)
+    y, slots, ch = _forward(c, train=True)
+    _check(c, y, slots, _backward(c, ch))
 
 
 def test_step_by_step_equals_one_call():
