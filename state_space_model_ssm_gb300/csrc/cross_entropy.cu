@@ -287,9 +287,10 @@ template <bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_stats_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, const __grid_constant__ CUtensorMap wmap)
 {
-    griddep_entry();
-    const int rows = *a.kept;
-    pair::run<BF16, false, false>(pair::Shape{rows, a.V, a.D, 1}, kGroupM, hmap, wmap, a.fail_waits, StatsEpilogue{a, rows});
+    pair::run<BF16, false, false>(kGroupM, hmap, wmap, a.fail_waits, [&] {
+        const int rows = *a.kept;
+        return pair::Work<StatsEpilogue>{{rows, a.V, a.D, 1}, {a, rows}};
+    });
 }
 
 // G of a piece: rows up to a whole tile, zeros past the rows and past the vocabulary.
@@ -324,9 +325,8 @@ template <class T, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_grad_kernel(const LossArgs a, const __grid_constant__ CUtensorMap hmap, const __grid_constant__ CUtensorMap wmap)
 {
-    griddep_entry();
-    const int rows = *a.kept;
-    pair::run<BF16, false, false>(pair::Shape{rows, a.vp, a.D, 1}, kGroupM, hmap, wmap, a.fail_waits, GradEpilogue<T>{a});
+    pair::run<BF16, false, false>(kGroupM, hmap, wmap, a.fail_waits,
+                                  [&] { return pair::Work<GradEpilogue<T>>{{*a.kept, a.vp, a.D, 1}, {a}}; });
 }
 
 // 32 columns of a warp's rows in 16 bits: `out` a lane's row (null: none), `left` how many columns exist.  Rows
@@ -413,12 +413,11 @@ template <class T, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_hidden_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap wmap)
 {
-    griddep_entry();
-    const int rows = *a.kept;
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.grad_h) | (uintptr_t)(a.sgh * 2)) & 15) == 0;
-    const HiddenEpilogue<T> epi{a, rows, *a.top / a.factor, aligned};
-    const int splits = splits_of(gridDim.x / 2, rows, a.D, a.splits);
-    pair::run<BF16, false, true>(pair::Shape{rows, a.D, min(a.vp, a.V - a.v0), splits}, kGroupM, gmap, wmap, a.fail_waits, epi);
+    pair::run<BF16, false, true>(kGroupM, gmap, wmap, a.fail_waits, [&] {
+        const int rows = *a.kept, splits = splits_of(gridDim.x / 2, rows, a.D, a.splits);
+        return pair::Work<HiddenEpilogue<T>>{{rows, a.D, min(a.vp, a.V - a.v0), splits}, {a, rows, *a.top / a.factor, aligned}};
+    });
 }
 
 // Rows of grad h from their splits' sums, where they belong: a block a row.
@@ -474,11 +473,10 @@ template <class T, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 loss_weight_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap hmap)
 {
-    griddep_entry();
-    const int rows = *a.kept;
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.grad_w) | (uintptr_t)(a.sgw * 2)) & 15) == 0;
-    const WeightEpilogue<T> epi{a, *a.top / a.factor, aligned};
-    pair::run<BF16, true, true>(pair::Shape{min(a.vp, a.V - a.v0), a.D, rows, 1}, kGroupM, gmap, hmap, a.fail_waits, epi);
+    pair::run<BF16, true, true>(kGroupM, gmap, hmap, a.fail_waits, [&] {
+        return pair::Work<WeightEpilogue<T>>{{min(a.vp, a.V - a.v0), a.D, *a.kept, 1}, {a, *a.top / a.factor, aligned}};
+    });
 }
 
 // (largest logit, sum) of two disjoint sets of columns.

@@ -102,21 +102,26 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
 }
 
-// One launch over the tiles of `shape`: groups of `group_m` row tiles, in which the row tile runs fastest.
+// What a launch does: its tiles, and the epilogue of each.
+template <class Epi>
+struct Work {
+    Shape shape;
+    Epi epi;
+};
+
+// One launch: groups of `group_m` row tiles, in which the row tile runs fastest.  make() says what there is to do; it
+// and everything else that reads memory comes after the kernel before has finished, barriers and tensor
+// memory are set up while it still runs.
 // epi.tile(row, first column, tensor memory address, whether the sums are there, whether there are any terms, split, the
 // warp's block of shared memory) runs for each tile with a thread's half row of D.
-template <bool BF16, bool A_MN, bool B_MN, class Epi>
-__device__ __forceinline__ void run(const Shape shape, int group_m, const CUtensorMap &amap, const CUtensorMap &bmap,
-                                    int fail_waits, Epi epi)
+template <bool BF16, bool A_MN, bool B_MN, class Make>
+__device__ __forceinline__ void run(int group_m, const CUtensorMap &amap, const CUtensorMap &bmap, int fail_waits, Make make)
 {
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pairs = gridDim.x / 2, pair_id = blockIdx.x / 2;
-    const int tiles_m = (shape.m + kTileM - 1) / kTileM, tiles_n = (shape.n + kTileN - 1) / kTileN;
-    const int stages = (shape.k + kTerms - 1) / kTerms, per_split = (stages + shape.splits - 1) / shape.splits;
-    const int places = tiles_m * tiles_n, tiles = places * shape.splits;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Smem::kBar);
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + Smem::kBars);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, peer = empty + 8 * kStages;
@@ -145,6 +150,13 @@ __device__ __forceinline__ void run(const Shape shape, int group_m, const CUtens
     fence_after();
     cluster_sync();                                         // both blocks' barriers are there
     const uint32_t tmem = *slot;
+    griddep_entry();
+    auto work = make();
+    const Shape shape = work.shape;
+    auto &epi = work.epi;
+    const int tiles_m = (shape.m + kTileM - 1) / kTileM, tiles_n = (shape.n + kTileN - 1) / kTileN;
+    const int stages = (shape.k + kTerms - 1) / kTerms, per_split = (stages + shape.splits - 1) / shape.splits;
+    const int places = tiles_m * tiles_n, tiles = places * shape.splits;
     // a tile's rows, columns and range of stages
     auto place = [&](int tile, int &m, int &n, int &k0) {
         const int split = tile / places;

@@ -7,9 +7,9 @@
 //
 // Every state has its own decay, so there is no matrix form: the work is one
 // exponential and about five multiplications an element (token, channel, state).
-// A warp owns a tile of channels with all their states: LN lanes share four channels
-// and each holds NP of their states, so a lane has 4 x NP independent recurrences
-// in registers.  What a lane reads from shared memory for a token (four steps and inputs,
+// A warp owns a tile of channels with all their states: LN lanes share CH channels
+// and each holds NP of their states, so a lane has CH x NP independent recurrences
+// in registers.  What a lane reads from shared memory for a token (CH steps and inputs,
 // NP values of B and of C) serves all of them: with single channels a lane
 // the reads of B and C cost more than the arithmetic.  Two states go into one packed fp32
 // instruction; the exponential is the hardware's 2^x of the rounded product
@@ -26,7 +26,7 @@
 namespace ssm {
 
 constexpr int kSelChunk = 16;             // tokens for each of which training saves a state
-constexpr int kSelCh = 4;                 // channels of a lane
+constexpr int kSelCh = 4;                 // channels of a lane (two in the walks of small calls)
 constexpr int kSelWarps = 4;              // warps of a block: neighbouring channel tiles of one unit
 constexpr int kSelMaxState = 128;
 constexpr int kCombineRun = 8;            // units whose loads the combining kernels issue together

@@ -107,8 +107,8 @@ long long sel_chunk_rows(long long n_seqs, long long n_tokens) { return n_seqs +
 
 SelShape sel_shape(int channels, int N, int groups, bool backward)
 {
-    // eight states a lane in the walks, four in the backward kernel
-    const int lanes = (N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : N <= 64 ? 8 : 16) * (backward ? 2 : 1);
+    // lanes of a channel: eight states each in the walks, four in the backward kernel
+    const int lanes = (N <= 16 ? 2 : N <= 32 ? 4 : N <= 64 ? 8 : 16) * (backward ? 2 : 1);
     SelShape s;
     s.wc = 32 / lanes * kSelCh;
     s.cblocks = groups * sel_group_blocks(channels, groups, s.wc);

@@ -536,7 +536,8 @@ cudaError_t launch_type(const SelArgs &a, cudaStream_t st)
         if (e != cudaSuccess)
             return e;
     }
-    e = a.N <= 8 ? launch_shape<T, 2>(a, st) : a.N <= 16 ? launch_shape<T, 4>(a, st) : a.N <= 32 ? launch_shape<T, 8>(a, st)
+    // (up to 8 states as for 16: with two lanes a channel a block needs 139 KB and spills, and was half as fast)
+    e = a.N <= 16 ? launch_shape<T, 4>(a, st) : a.N <= 32 ? launch_shape<T, 8>(a, st)
         : a.N <= 64 ? launch_shape<T, 16>(a, st) : launch_shape<T, 32>(a, st);
     if (e != cudaSuccess)
         return e;

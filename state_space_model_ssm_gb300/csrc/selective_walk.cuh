@@ -18,12 +18,13 @@ namespace ssm {
 
 enum SelMode { kFull, kState, kCarry };
 
-constexpr int kWalkL = 8, kWalkNP = 8;
+constexpr int kWalkL = 8;
 
-template <int LN>
+template <int CH, int NP, int LN>
 struct WalkLayout {
-    static constexpr int WC = 32 / LN * kSelCh, NN = kWalkNP * LN;
-    static constexpr int kWarp = 2 * kWalkL * WC;           // floats: steps, inputs
+    static constexpr int WC = 32 / LN * CH, NN = NP * LN;
+    static constexpr int kStage = SelStage<WC, kWalkL>::kTokens * WC;
+    static constexpr int kWarp = 2 * kStage;                // floats: steps, inputs
     static constexpr int kRows = kWalkL * NN;               // of B or C
     static constexpr size_t kBytes = (size_t)(kSelWarps * kWarp + 4 * kRows) * sizeof(float);
 };
@@ -31,13 +32,13 @@ struct WalkLayout {
 // Three blocks an SM, 168 registers a thread: unbounded, kFull took 238 and 1 x 4096 x 4096 channels x 16 states
 // (bf16) 180 us instead of 126.  Four states a lane, four blocks an SM: 156 us.  fp32 rows need twice the registers
 // while staged and spill at three blocks (4 x 777 x 1001 channels: 80 us instead of 54).
-template <class T, int LN, SelMode MODE>
-__global__ void __launch_bounds__(32 * kSelWarps, sizeof(T) == 4 && (LN == 1 || MODE == kFull) ? 2 : 3)
+template <class T, int CH, int NP, int LN, SelMode MODE>
+__global__ void __launch_bounds__(32 * kSelWarps, CH * NP == 8 ? 5 : sizeof(T) == 4 && MODE == kFull ? 2 : 3)
 sel_walk_kernel(const SelArgs a)
 {
     griddep_entry();
-    using Y = WalkLayout<LN>;
-    constexpr int CH = kSelCh, NP = kWalkNP, WC = Y::WC, NN = Y::NN, L = kWalkL;
+    using Y = WalkLayout<CH, NP, LN>;
+    constexpr int WC = Y::WC, NN = Y::NN, L = kWalkL;
     using S = SelStage<WC, L>;
     constexpr int M = S::M, KC = S::KC;
     extern __shared__ __align__(16) float sm[];
@@ -52,7 +53,7 @@ sel_walk_kernel(const SelArgs a)
     const bool vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;
     const bool vec_c = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.chunk_states) & 15) == 0;
     const bool pad = a.N != NN, pairs = a.pairs != 0;
-    float *step = sm + warp * Y::kWarp, *in = step + L * WC, *rows = sm + kSelWarps * Y::kWarp;
+    float *step = sm + warp * Y::kWarp, *in = step + Y::kStage, *rows = sm + kSelWarps * Y::kWarp;
 
     float2 h[CH][NP / 2], A[CH][NP / 2];
 #pragma unroll
@@ -237,11 +238,11 @@ sel_walk_kernel(const SelArgs a)
     }
 }
 
-template <class T, int LN, SelMode MODE>
+template <class T, int CH, int NP, int LN, SelMode MODE>
 cudaError_t launch_walk(const SelArgs &a, int units, cudaStream_t st)
 {
-    using Y = WalkLayout<LN>;
-    const auto kernel = sel_walk_kernel<T, LN, MODE>;
+    using Y = WalkLayout<CH, NP, LN>;
+    const auto kernel = sel_walk_kernel<T, CH, NP, LN, MODE>;
     const cudaError_t e = set_dynamic_smem(reinterpret_cast<const void *>(kernel), Y::kBytes);
     if (e != cudaSuccess)
         return e;
@@ -249,15 +250,28 @@ cudaError_t launch_walk(const SelArgs &a, int units, cudaStream_t st)
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(32 * kSelWarps), Y::kBytes, st, a);
 }
 
-// By the states' number: 8 of them a lane.
+// By the states' number: 8 of them (4) and four channels a lane.  Where that leaves the device without work (fewer
+// warps than kNarrow), a warp alone on its scheduler waits for its own instructions, so four states and two channels a
+// lane, a quarter of the work and four times the warps, take less time.
+constexpr long long kNarrow = 6 * kSms;
+
 template <class T, SelMode MODE>
 cudaError_t launch_walk_states(const SelArgs &a, int units, cudaStream_t st)
 {
-    if (a.N <= 8) return launch_walk<T, 1, MODE>(a, units, st);
-    if (a.N <= 16) return launch_walk<T, 2, MODE>(a, units, st);
-    if (a.N <= 32) return launch_walk<T, 4, MODE>(a, units, st);
-    if (a.N <= 64) return launch_walk<T, 8, MODE>(a, units, st);
-    return launch_walk<T, 16, MODE>(a, units, st);
+    if constexpr (MODE != kCarry) {
+        if (units * (long long)sel_shape(a.channels, a.N, a.groups, false).tiles < kNarrow) {
+            if (a.N <= 8) return launch_walk<T, 2, 4, 2, MODE>(a, units, st);
+            if (a.N <= 16) return launch_walk<T, 2, 4, 4, MODE>(a, units, st);
+            if (a.N <= 32) return launch_walk<T, 2, 4, 8, MODE>(a, units, st);
+            if (a.N <= 64) return launch_walk<T, 2, 4, 16, MODE>(a, units, st);
+            return launch_walk<T, 2, 4, 32, MODE>(a, units, st);
+        }
+    }
+    if (a.N <= 8) return launch_walk<T, 4, 4, 2, MODE>(a, units, st);
+    if (a.N <= 16) return launch_walk<T, 4, 8, 2, MODE>(a, units, st);
+    if (a.N <= 32) return launch_walk<T, 4, 8, 4, MODE>(a, units, st);
+    if (a.N <= 64) return launch_walk<T, 4, 8, 8, MODE>(a, units, st);
+    return launch_walk<T, 4, 8, 16, MODE>(a, units, st);
 }
 
 }  // namespace ssm
