@@ -177,7 +177,7 @@ sel_backward_kernel(const SelArgs a)
     };
 #pragma unroll
     for (int c = 0; c < CP; ++c) {
-        read_pair(A[c], a.A, c, false, true);
+        read_pair(A[c], a.A, c, a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.A) & 15) == 0, true);
         if (s.cut)
             read_pair(e[c], a.unit_state + (long long)u * a.channels * a.N, c, a.N % 4 == 0, true);
         else
@@ -294,18 +294,23 @@ sel_backward_kernel(const SelArgs a)
                 load_pairs<CH>(gv, gs + t * WC + q * CH);
                 load_pairs<2 * NP>(Bv, reinterpret_cast<const float *>(Bs + t * NN + n0));
                 load_pairs<2 * NP>(Cv, reinterpret_cast<const float *>(Cs + t * NN + n0));
+                float2 k[CP][NP];
 #pragma unroll
-                for (int c = 0; c < CP; ++c) {
-                    float2 sum = make_float2(0.f, 0.f), k[NP];
+                for (int c = 0; c < CP; ++c)
 #pragma unroll
                     for (int n = 0; n < NP; ++n) {
-                        k[n] = mul2(ex2_2(mul2(st[c], A[c][n])), h[c][n]);
-                        h[c][n] = fma2(uv[c], Bv[n], k[n]);
+                        k[c][n] = mul2(ex2_2(mul2(st[c], A[c][n])), h[c][n]);
+                        h[c][n] = fma2(uv[c], Bv[n], k[c][n]);
                     }
-                    if (drop) {
+                if (drop)                                   // (one branch a token: it is not known to be uniform)
+#pragma unroll
+                    for (int c = 0; c < CP; ++c) {
                         drop_padding(h[c]);
-                        drop_padding(k);
+                        drop_padding(k[c]);
                     }
+#pragma unroll
+                for (int c = 0; c < CP; ++c) {
+                    float2 sum;
 #pragma unroll
                     for (int n = 0; n < NP; ++n) {
                         sum = n == 0 ? mul2(h[c][n], Cv[n]) : fma2(h[c][n], Cv[n], sum);
@@ -314,7 +319,7 @@ sel_backward_kernel(const SelArgs a)
 #pragma unroll
                     for (int n = 0; n < NP; n += 2)
                         *reinterpret_cast<float4 *>(keep + ((t - first) * 4 + 2 * c + n / 2) * Y::kSlot + 4 * lane) =
-                            make_float4(k[n].x, k[n].y, k[n + 1].x, k[n + 1].y);
+                            make_float4(k[c][n].x, k[c][n].y, k[c][n + 1].x, k[c][n + 1].y);
                     p[2 * c] = sum.x;
                     p[2 * c + 1] = sum.y;
                 }
@@ -356,23 +361,29 @@ sel_backward_kernel(const SelArgs a)
                 load_pairs<CH>(gv, gs + t * WC + q * CH);
                 load_pairs<2 * NP>(Bv, reinterpret_cast<const float *>(Bs + t * NN + n0));
                 load_pairs<2 * NP>(Cv, reinterpret_cast<const float *>(Cs + t * NN + n0));
+                float2 k[CP][NP];
 #pragma unroll
                 for (int c = 0; c < CP; ++c) {
-                    float2 k[NP], wa, wb;
 #pragma unroll
                     for (int n = 0; n < NP; n += 2) {
                         const float4 v = *reinterpret_cast<const float4 *>(slots + (2 * c + n / 2) * Y::kSlot);
-                        k[n] = make_float2(v.x, v.y);
-                        k[n + 1] = make_float2(v.z, v.w);
+                        k[c][n] = make_float2(v.x, v.y);
+                        k[c][n + 1] = make_float2(v.z, v.w);
                     }
 #pragma unroll
                     for (int n = 0; n < NP; ++n)
                         e[c][n] = fma2(gv[c], Cv[n], e[c][n]);
-                    if (drop)
+                }
+                if (drop)
+#pragma unroll
+                    for (int c = 0; c < CP; ++c)
                         drop_padding(e[c]);
 #pragma unroll
+                for (int c = 0; c < CP; ++c) {
+                    float2 wa, wb;
+#pragma unroll
                     for (int n = 0; n < NP; ++n) {
-                        const float2 v = mul2(e[c][n], k[n]);
+                        const float2 v = mul2(e[c][n], k[c][n]);
                         gA[c][n] = fma2(st[c], v, gA[c][n]);
                         wa = n == 0 ? mul2(v, A[c][n]) : fma2(v, A[c][n], wa);
                         wb = n == 0 ? mul2(e[c][n], Bv[n]) : fma2(e[c][n], Bv[n], wb);

@@ -52,6 +52,7 @@ sel_walk_kernel(const SelArgs a)
     const int wc = tile.c1 - tile.c0;                       // channels of this warp that exist; 0: it only helps with B and C
     const bool vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;
     const bool vec_c = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.chunk_states) & 15) == 0;
+    const bool vec_a = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.A) & 15) == 0;
     const bool pad = a.N != NN, pairs = a.pairs != 0;
     float *step = sm + warp * Y::kWarp, *in = step + Y::kStage, *rows = sm + kSelWarps * Y::kWarp;
 
@@ -60,7 +61,7 @@ sel_walk_kernel(const SelArgs a)
     for (int c = 0; c < CH; ++c) {
         const int ch = tile.c0 + q * CH + c;
         const bool there = q * CH + c < wc;
-        read_states<NP>(A[c], a.A + (long long)ch * a.N, n0, a.N, false, there);
+        read_states<NP>(A[c], a.A + (long long)ch * a.N, n0, a.N, vec_a, there);
 #pragma unroll
         for (int j = 0; j < NP / 2; ++j)
             A[c][j] = mul2(A[c][j], twice(kLog2e));
@@ -164,8 +165,7 @@ sel_walk_kernel(const SelArgs a)
             if (MODE == kFull)
                 load_pairs<NP>(Cv, Cs + t * NN + n0);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                float2 sum = make_float2(0.f, 0.f);
+            for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int j = 0; j < NP / 2; ++j) {
                     const float2 decay = ex2_2(mul2(twice(st[c]), A[c][j]));
@@ -174,15 +174,19 @@ sel_walk_kernel(const SelArgs a)
                     else
                         h[c][j] = fma2(decay, h[c][j], mul2(twice(uv[c]), Bv[j]));
                 }
-                if (drop)
-                    drop_padding<NP>(h[c], n0, a.N);
-                if (MODE == kFull) {
+            if (drop)                                       // (one branch a token: it is not known to be uniform)
 #pragma unroll
-                    for (int j = 0; j < NP / 2; ++j)
+                for (int c = 0; c < CH; ++c)
+                    drop_padding<NP>(h[c], n0, a.N);
+            if (MODE == kFull)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    float2 sum = mul2(h[c][0], Cv[0]);
+#pragma unroll
+                    for (int j = 1; j < NP / 2; ++j)
                         sum = fma2(h[c][j], Cv[j], sum);
                     p[c] = sum.x + sum.y;
                 }
-            }
             if (MODE == kFull) {
                 int at;
                 bool mine;
@@ -250,16 +254,22 @@ cudaError_t launch_walk(const SelArgs &a, int units, cudaStream_t st)
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(32 * kSelWarps), Y::kBytes, st, a);
 }
 
-// By the states' number: 8 of them (4) and four channels a lane.  Where that leaves the device without work (fewer
-// warps than kNarrow), a warp alone on its scheduler waits for its own instructions, so four states and two channels a
-// lane, a quarter of the work and four times the warps, take less time.
-constexpr long long kNarrow = 6 * kSms;
+// By the states' number: 8 of them (4) and four channels a lane.  Where that leaves the device without work, or has
+// little to do but loads, four states and two channels a lane, a quarter of the work and four times the warps, take less
+// time: a warp alone on its scheduler waits for its own instructions.  4096 channels x 16 states, bf16, one token a
+// sequence, wide / narrow: 16 sequences 9.3 / 6.9 us, 32 14.9 / 10.3, 64 23.8 / 21.6, 256 75.8 / 76.8; 1 x 4096 tokens 209 / 259.
+template <SelMode MODE>
+bool narrow_walk(const SelArgs &a, int units)
+{
+    const long long warps = units * (long long)sel_shape(a.channels, a.N, a.groups, false).tiles;
+    return MODE != kCarry && warps < (a.n_tokens <= 8LL * a.n_seqs ? 48 : 6) * (long long)kSms;
+}
 
 template <class T, SelMode MODE>
 cudaError_t launch_walk_states(const SelArgs &a, int units, cudaStream_t st)
 {
     if constexpr (MODE != kCarry) {
-        if (units * (long long)sel_shape(a.channels, a.N, a.groups, false).tiles < kNarrow) {
+        if (narrow_walk<MODE>(a, units)) {
             if (a.N <= 8) return launch_walk<T, 2, 4, 2, MODE>(a, units, st);
             if (a.N <= 16) return launch_walk<T, 2, 4, 4, MODE>(a, units, st);
             if (a.N <= 32) return launch_walk<T, 2, 4, 8, MODE>(a, units, st);
