@@ -30,6 +30,7 @@ constexpr int kSelCh = 4;                 // channels of a lane (two in the walk
 constexpr int kSelWarps = 4;              // warps of a block: neighbouring channel tiles of one unit
 constexpr int kSelMaxState = 128;
 constexpr int kCombineRun = 8;            // units whose loads the combining kernels issue together
+
 struct SelArgs {
     float *state;
     const void *x, *dt, *z, *B, *C;
@@ -370,6 +371,7 @@ struct SelCut {
 };
 SelCut sel_cut(int n_seqs, int n_tokens, const SelShape &s, bool backward);
 bool sel_pairs(const SelArgs &a, int dtype);
+dim3 sel_combine_grid(const SelArgs &a);
 int sel_max_units(int n_seqs, int n_tokens, int seg);
 long long sel_chunk_rows(long long n_seqs, long long n_tokens);
 cudaError_t launch_sel_plan(const SelArgs &a, int2 *units, int *first, cudaStream_t st);   // a.max_units bounds it

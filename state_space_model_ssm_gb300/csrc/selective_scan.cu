@@ -50,36 +50,38 @@ sel_plan_kernel(const SelArgs a, int2 *units, int *first)
         first[a.n_seqs] = min(base, a.max_units);
 }
 
-// The state entering each unit, in place of the unit's state from zero.
+// The state entering each unit, in place of the unit's state from zero.  grid: (channels and states, shares of the
+// sequences); a whole sequence reads its slot itself.
 __global__ void __launch_bounds__(256)
 sel_combine_kernel(const SelArgs a)
 {
     griddep_entry();
-    const long long width = (long long)a.channels * a.N, i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int seq = (int)(i / width);
-    if (seq >= a.n_seqs)
+    const long long width = (long long)a.channels * a.N, e = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (e >= width)
         return;
-    const long long e = i - seq * width;
-    const int c = (int)(e / a.N), u1 = a.first[seq + 1];
-    if (u1 - a.first[seq] <= 1)                             // a whole sequence reads its slot itself
-        return;
+    const int c = (int)(e / a.N);
     const float A = a.A[e] * kLog2e;
-    float h = a.resume[seq] != 0 ? a.state[i] : 0.f;
-    // loads of a run of units together (one by one, each waited for the store before it)
-    for (int u = a.first[seq]; u < u1; u += kCombineRun) {
-        float own[kCombineRun], step[kCombineRun];
+    for (int seq = blockIdx.y; seq < a.n_seqs; seq += gridDim.y) {
+        const int u0 = a.first[seq], u1 = a.first[seq + 1];
+        if (u1 - u0 <= 1)
+            continue;
+        float h = a.resume[seq] != 0 ? a.state[seq * width + e] : 0.f;
+        // loads of a run of units together (one by one, each waited for the store before it)
+        for (int u = u0; u < u1; u += kCombineRun) {
+            float own[kCombineRun], step[kCombineRun];
 #pragma unroll
-        for (int k = 0; k < kCombineRun; ++k) {
-            const long long v = min(u + k, u1 - 1);
-            own[k] = a.unit_state[v * width + e];
-            step[k] = a.unit_step[v * a.channels + c];
-        }
+            for (int k = 0; k < kCombineRun; ++k) {
+                const long long v = min(u + k, u1 - 1);
+                own[k] = a.unit_state[v * width + e];
+                step[k] = a.unit_step[v * a.channels + c];
+            }
 #pragma unroll
-        for (int k = 0; k < kCombineRun; ++k) {
-            if (u + k >= u1)
-                break;
-            a.unit_state[(u + k) * width + e] = h;
-            h = fmaf(ex2(step[k] * A), h, own[k]);          // (the last unit's values are not there, and not used)
+            for (int k = 0; k < kCombineRun; ++k) {
+                if (u + k >= u1)
+                    break;
+                a.unit_state[(u + k) * width + e] = h;
+                h = fmaf(ex2(step[k] * A), h, own[k]);      // (the last unit's values are not there, and not used)
+            }
         }
     }
 }
@@ -91,8 +93,7 @@ cudaError_t launch_type(const SelArgs &a, int units, cudaStream_t st)
         cudaError_t e = launch_walk_states<T, kState>(a, units, st);
         if (e != cudaSuccess)
             return e;
-        const long long n = (long long)a.n_seqs * a.channels * a.N;
-        e = launch_pdl(sel_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+        e = launch_pdl(sel_combine_kernel, sel_combine_grid(a), dim3(256), 0, st, a);
         if (e != cudaSuccess)
             return e;
     }
@@ -124,10 +125,9 @@ SelCut sel_cut(int n_seqs, int n_tokens, const SelShape &s, bool backward)
     const long long even = ((long long)n_tokens * s.tiles + warps - 1) / warps, whole = even + even / 2 < 128 ? 128 : even + even / 2;
     if (n_tokens <= whole || n_tokens == n_seqs)            // (as many tokens as sequences: a decode step)
         return SelCut{0, 0};
-    // Segments: of one sequence, one round of warps (backward two, since the pass that finds what segments hand on has
-    // twice the channels a warp); of several, whose lengths are not known here, shorter ones, so that the last
-    // round has less to wait for (12 uneven, 7889 tokens x 4096 channels x 16 states: 362 us with one round).
-    const long long rounds = (n_seqs == 1 ? 1 : 3) * (backward ? 2 : 1), units = std::max(1LL, rounds * warps / s.tiles);
+    // One round of warps, backward two, since the pass that finds what segments hand on has twice the channels a warp.
+    // (Shorter segments gain nothing: 12 uneven sequences of 7889 tokens x 4096 channels x 16 states, one round 365 us, three 377.)
+    const long long units = std::max(1LL, (backward ? 2 : 1) * warps / s.tiles);
     const long long seg = ((n_tokens + units - 1) / units + kSelChunk - 1) / kSelChunk * kSelChunk;
     return SelCut{(int)std::max(64LL, seg), (int)std::max(whole, seg)};
 }
@@ -141,6 +141,13 @@ bool sel_pairs(const SelArgs &a, int dtype)
     };
     return a.channels / a.groups % 2 == 0 && even(a.x, a.sx) && even(a.dt, a.sdt) && even(a.z, a.sz) && even(a.y, a.sy) &&
            even(a.grad_y, a.sgy) && even(a.grad_x, a.sgx) && even(a.grad_dt, a.sgdt) && even(a.grad_z, a.sgz);
+}
+
+// Of the combining kernels: at most as many shares of the sequences as can have been cut.
+dim3 sel_combine_grid(const SelArgs &a)
+{
+    const long long width = (long long)a.channels * a.N, cut = a.n_tokens / (a.whole + 1LL) + 1;
+    return dim3((unsigned)((width + 255) / 256), (unsigned)std::min<long long>({cut, a.n_seqs, 65535}));
 }
 
 int sel_max_units(int n_seqs, int n_tokens, int seg) { return seg ? n_seqs + n_tokens / seg : n_seqs; }

@@ -10,9 +10,10 @@
 // Per chunk of 16 tokens, from the state the forward pass saved, eight tokens at a time: the
 // states are computed again with k kept in shared memory (one exponential more an element
 // than keeping the decays too, half the memory), and with them the sums that need h; then the
-// tokens are walked backwards.  Sums over states cross the LN lanes of a channel, sums over channels the
-// lanes, then the block's warps in shared memory, then channel blocks in a second
-// kernel: always in the same order.
+// tokens are walked backwards.  A lane's share of a sum over states or channels goes to shared memory (exchanged
+// between lanes for every token, the sums took a quarter of the instructions) and other threads add the
+// shares up, over the block's warps too; sums over channel blocks and units are left to two small kernels.  Always
+// in the same order.
 //
 // Units of time as in the forward pass: with segments, a pass before finds what each segment
 // hands to the one in front of it.
@@ -22,35 +23,37 @@ namespace ssm {
 
 namespace {
 
-// The gradient that reaches each unit from behind, in place of what the unit hands on.
+// The gradient that reaches each unit from behind, in place of what the unit hands on.  grid: (channels and states,
+// shares of the sequences); a whole sequence takes grad_state itself.
 __global__ void __launch_bounds__(256)
 sel_carry_combine_kernel(const SelArgs a)
 {
     griddep_entry();
-    const long long width = (long long)a.channels * a.N, i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int seq = (int)(i / width);
-    if (seq >= a.n_seqs)
+    const long long width = (long long)a.channels * a.N, e = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (e >= width)
         return;
-    const long long e = i - seq * width;
-    const int c = (int)(e / a.N), u0 = a.first[seq];
-    if (a.first[seq + 1] - u0 <= 1)                         // a whole sequence takes grad_state itself
-        return;
+    const int c = (int)(e / a.N);
     const float A = a.A[e] * kLog2e;
-    float g = a.grad_state ? a.grad_state[i] : 0.f;
-    for (int u = a.first[seq + 1] - 1; u >= u0; u -= kCombineRun) {
-        float own[kCombineRun], step[kCombineRun];
+    for (int seq = blockIdx.y; seq < a.n_seqs; seq += gridDim.y) {
+        const int u0 = a.first[seq], u1 = a.first[seq + 1];
+        if (u1 - u0 <= 1)
+            continue;
+        float g = a.grad_state ? a.grad_state[seq * width + e] : 0.f;
+        for (int u = u1 - 1; u >= u0; u -= kCombineRun) {
+            float own[kCombineRun], step[kCombineRun];
 #pragma unroll
-        for (int k = 0; k < kCombineRun; ++k) {
-            const long long v = max(u - k, u0);
-            own[k] = a.unit_state[v * width + e];
-            step[k] = a.unit_step[v * a.channels + c];
-        }
+            for (int k = 0; k < kCombineRun; ++k) {
+                const long long v = max(u - k, u0);
+                own[k] = a.unit_state[v * width + e];
+                step[k] = a.unit_step[v * a.channels + c];
+            }
 #pragma unroll
-        for (int k = 0; k < kCombineRun; ++k) {
-            if (u - k < u0)
-                break;
-            a.unit_state[(u - k) * width + e] = g;
-            g = fmaf(ex2(step[k] * A), g, own[k]);          // (the first unit's values are not there, and not used)
+            for (int k = 0; k < kCombineRun; ++k) {
+                if (u - k < u0)
+                    break;
+                a.unit_state[(u - k) * width + e] = g;
+                g = fmaf(ex2(step[k] * A), g, own[k]);      // (the first unit's values are not there, and not used)
+            }
         }
     }
 }
@@ -542,8 +545,7 @@ cudaError_t launch_type(const SelArgs &a, cudaStream_t st)
         e = launch_walk_states<T, kCarry>(a, a.max_units, st);
         if (e != cudaSuccess)
             return e;
-        const long long n = (long long)a.n_seqs * a.channels * a.N;
-        e = launch_pdl(sel_carry_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+        e = launch_pdl(sel_carry_combine_kernel, sel_combine_grid(a), dim3(256), 0, st, a);
         if (e != cudaSuccess)
             return e;
     }
