@@ -64,25 +64,35 @@ __device__ __forceinline__ bool find_span(const ConvArgs &a, int u, int &seq, in
     if (a.units == a.n_seqs)                                // no sequence is longer than a span
         return u < a.n_seqs;
     const int lane = threadIdx.x & 31;
+    constexpr int kEach = 4;                                // groups of 32 sequences whose lengths are loaded together
     int base = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-        long long t0;
-        const int mine = s0 + lane < a.n_seqs ? max(1, (seq_len(a, s0 + lane, t0) + a.span - 1) / a.span) : 0;
-        int incl = mine;
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 32 * kEach) {
+        int spans[kEach];
 #pragma unroll
-        for (int off = 1; off < 32; off *= 2) {
-            const int v = __shfl_up_sync(kFullMask, incl, off);
-            if (lane >= off)
-                incl += v;
+        for (int j = 0; j < kEach; ++j) {
+            const int s = s0 + 32 * j + lane;
+            long long t0;
+            spans[j] = s < a.n_seqs ? max(1, (seq_len(a, s, t0) + a.span - 1) / a.span) : 0;
         }
-        const unsigned m = __ballot_sync(kFullMask, u < base + incl);
-        if (m) {
-            const int l = __ffs(m) - 1;
-            seq = s0 + l;
-            k = u - base - __shfl_sync(kFullMask, incl - mine, l);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int all = __reduce_add_sync(kFullMask, spans[j]);
+            if (u >= base + all) {
+                base += all;
+                continue;
+            }
+            int incl = spans[j];
+#pragma unroll
+            for (int off = 1; off < 32; off *= 2) {
+                const int v = __shfl_up_sync(kFullMask, incl, off);
+                if (lane >= off)
+                    incl += v;
+            }
+            const int l = __ffs(__ballot_sync(kFullMask, u < base + incl)) - 1;
+            seq = s0 + 32 * j + l;
+            k = u - base - __shfl_sync(kFullMask, incl - spans[j], l);
             return true;
         }
-        base += __shfl_sync(kFullMask, incl, 31);
     }
     return false;
 }
