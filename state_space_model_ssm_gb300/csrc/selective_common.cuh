@@ -53,7 +53,7 @@ struct SelArgs {
     float *part_A, *part_D, *part_bias;   // [units][channels][N], [units][channels] twice
     float *part_B, *part_C;               // [channel blocks][n_tokens][groups N]
     int max_units, cblocks;
-    int pairs;                            // two channels of every row are one aligned word
+    int pairs, narrow;                    // two channels of every row are one aligned word; tiles of the walks
 };
 
 // Row of chunk_states for chunk j of a sequence that starts at token t0: the first chunk's by
@@ -369,7 +369,8 @@ SelShape sel_shape(int channels, int N, int groups, bool backward);
 struct SelCut {
     int seg, whole;
 };
-SelCut sel_cut(int n_seqs, int n_tokens, const SelShape &s, bool backward);
+SelCut sel_cut(int n_seqs, int n_tokens, int channels, int N, int groups, bool backward);
+bool sel_narrow(int n_seqs, int n_tokens, int units, int tiles);
 bool sel_pairs(const SelArgs &a, int dtype);
 dim3 sel_combine_grid(const SelArgs &a);
 int sel_max_units(int n_seqs, int n_tokens, int seg);

@@ -117,19 +117,58 @@ SelShape sel_shape(int channels, int N, int groups, bool backward)
     return s;
 }
 
-SelCut sel_cut(int n_seqs, int n_tokens, const SelShape &s, bool backward)
+// The walks' blocks of channels with narrow tiles.
+int sel_narrow_blocks(int channels, int N, int groups)
+{
+    const int lanes = N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32;
+    return groups * sel_group_blocks(channels, groups, 32 / lanes * 2);
+}
+
+// Tokens of a segment for which rounds of `resident` blocks, `cblocks` of them a unit, take the least time: r rounds of
+// segments that are just short enough for r, if the sequences were alike.  Forward and backward, tokens / warps for a
+// segment (backward, twice that) / this: 4 x 777 tokens x 1001 channels x 13 states, fp32, 234 / 212 us; 6763 tokens
+// of five sequences, one of them 6508, x 320 x 16, bf16, 252 / 220; 1 x 4096 x 4096 x 16 is cut the same.  Forward, 12
+// uneven sequences of 7889 tokens x 4096 x 16: 370 / 367.
+long long sel_segment(int n_seqs, int n_tokens, long long cblocks, long long resident)
+{
+    const long long each = (n_tokens + n_seqs - 1) / n_seqs;
+    long long best = 0, least = 0;
+    for (int r = 1; r <= 4; ++r) {
+        const long long units = std::max(1LL, r * resident / cblocks / n_seqs);     // of a sequence
+        const long long seg = std::max(64LL, ((each + units - 1) / units + kSelChunk - 1) / kSelChunk * kSelChunk);
+        const long long blocks = n_seqs * ((each + seg - 1) / seg) * cblocks;
+        const long long time = (blocks + resident - 1) / resident * seg;
+        if (r == 1 || time < least) {
+            best = seg;
+            least = time;
+        }
+    }
+    return best;
+}
+
+SelCut sel_cut(int n_seqs, int n_tokens, int channels, int N, int groups, bool backward)
 {
     // Warps that are resident at once (three blocks an SM; two backward), and the tokens that each would walk if
     // all had the same to do.  A sequence of at most one and a half times that is not worth the second walk.
-    const long long warps = kSms * kSelWarps * (backward ? 2 : 3);
+    const SelShape s = sel_shape(channels, N, groups, backward);
+    const long long blocks = kSms * (backward ? 2 : 3), warps = kSelWarps * blocks;
     const long long even = ((long long)n_tokens * s.tiles + warps - 1) / warps, whole = even + even / 2 < 128 ? 128 : even + even / 2;
     if (n_tokens <= whole || n_tokens == n_seqs)            // (as many tokens as sequences: a decode step)
         return SelCut{0, 0};
-    // One round of warps, backward two, since the pass that finds what segments hand on has twice the channels a warp.
-    // (Shorter segments gain nothing: 12 uneven sequences of 7889 tokens x 4096 channels x 16 states, one round 365 us, three 377.)
-    const long long units = std::max(1LL, (backward ? 2 : 1) * warps / s.tiles);
-    const long long seg = ((n_tokens + units - 1) / units + kSelChunk - 1) / kSelChunk * kSelChunk;
-    return SelCut{(int)std::max(64LL, seg), (int)std::max(whole, seg)};
+    long long seg = sel_segment(n_seqs, n_tokens, s.cblocks, blocks);
+    if (!backward && sel_narrow(n_seqs, n_tokens, sel_max_units(n_seqs, n_tokens, (int)seg), s.tiles))
+        seg = sel_segment(n_seqs, n_tokens, sel_narrow_blocks(channels, N, groups), 5 * kSms);
+    return SelCut{(int)seg, (int)std::max(whole, seg)};
+}
+
+// Whether the walks take narrow tiles.  Wide ones have four channels and eight states (four, up to 8 states) a
+// lane.  Where that leaves the device without work, or has little to do but loads, four states and two channels a lane,
+// a quarter of the work and four times the warps, take less time: a warp alone on its scheduler waits for its own
+// instructions.  4096 channels x 16 states, bf16, one token a sequence, wide / narrow: 16 sequences 9.3 / 6.9 us,
+// 32 14.9 / 10.3, 64 23.8 / 21.6, 256 75.8 / 76.8; 1 x 4096 tokens 209 / 259.
+bool sel_narrow(int n_seqs, int n_tokens, int units, int tiles)
+{
+    return (long long)units * tiles < (n_tokens <= 8LL * n_seqs ? 48 : 6) * (long long)kSms;
 }
 
 // Whether two channels of each of these rows are one aligned word.
@@ -175,7 +214,7 @@ Workspace layout(int n_seqs, int channels, int N, int units)
 
 size_t sel_scan_workspace_bytes(int n_seqs, int n_tokens, int channels, int N, int groups)
 {
-    const int seg = sel_cut(n_seqs, n_tokens, sel_shape(channels, N, groups, false), false).seg;
+    const int seg = sel_cut(n_seqs, n_tokens, channels, N, groups, false).seg;
     return seg ? layout(n_seqs, channels, N, sel_max_units(n_seqs, n_tokens, seg)).total : 0;
 }
 
@@ -184,10 +223,11 @@ cudaError_t launch_selective_scan(SelArgs a, int dtype, void *workspace, cudaStr
     const SelShape s = sel_shape(a.channels, a.N, a.groups, false);
     a.cblocks = s.cblocks;
     a.pairs = sel_pairs(a, dtype);
-    const SelCut cut = sel_cut(a.n_seqs, a.n_tokens, s, false);
+    const SelCut cut = sel_cut(a.n_seqs, a.n_tokens, a.channels, a.N, a.groups, false);
     a.seg = cut.seg;
     a.whole = cut.whole;
     const int units = sel_max_units(a.n_seqs, a.n_tokens, a.seg);
+    a.narrow = sel_narrow(a.n_seqs, a.n_tokens, units, s.tiles);
     a.max_units = units;
     if (a.seg) {
         unsigned char *w = static_cast<unsigned char *>(workspace);

@@ -592,7 +592,7 @@ Workspace layout(int n_seqs, int n_tokens, int channels, int N, int groups, int 
 size_t sel_backward_workspace_bytes(int n_seqs, int n_tokens, int channels, int N, int groups)
 {
     const SelShape s = sel_shape(channels, N, groups, true);
-    return layout(n_seqs, n_tokens, channels, N, groups, sel_cut(n_seqs, n_tokens, s, true).seg, s.cblocks).total;
+    return layout(n_seqs, n_tokens, channels, N, groups, sel_cut(n_seqs, n_tokens, channels, N, groups, true).seg, s.cblocks).total;
 }
 
 cudaError_t launch_selective_scan_backward(SelArgs a, int dtype, void *workspace, cudaStream_t st)
@@ -600,7 +600,7 @@ cudaError_t launch_selective_scan_backward(SelArgs a, int dtype, void *workspace
     const SelShape s = sel_shape(a.channels, a.N, a.groups, true);
     a.cblocks = s.cblocks;
     a.pairs = sel_pairs(a, dtype);
-    const SelCut cut = sel_cut(a.n_seqs, a.n_tokens, s, true);
+    const SelCut cut = sel_cut(a.n_seqs, a.n_tokens, a.channels, a.N, a.groups, true);
     a.seg = cut.seg;
     a.whole = cut.whole;
     a.max_units = sel_max_units(a.n_seqs, a.n_tokens, a.seg);

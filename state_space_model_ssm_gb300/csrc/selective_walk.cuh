@@ -254,22 +254,12 @@ cudaError_t launch_walk(const SelArgs &a, int units, cudaStream_t st)
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(32 * kSelWarps), Y::kBytes, st, a);
 }
 
-// By the states' number: 8 of them (4) and four channels a lane.  Where that leaves the device without work, or has
-// little to do but loads, four states and two channels a lane, a quarter of the work and four times the warps, take less
-// time: a warp alone on its scheduler waits for its own instructions.  4096 channels x 16 states, bf16, one token a
-// sequence, wide / narrow: 16 sequences 9.3 / 6.9 us, 32 14.9 / 10.3, 64 23.8 / 21.6, 256 75.8 / 76.8; 1 x 4096 tokens 209 / 259.
-template <SelMode MODE>
-bool narrow_walk(const SelArgs &a, int units)
-{
-    const long long warps = units * (long long)sel_shape(a.channels, a.N, a.groups, false).tiles;
-    return MODE != kCarry && warps < (a.n_tokens <= 8LL * a.n_seqs ? 48 : 6) * (long long)kSms;
-}
-
+// By the states' number, with wide or narrow tiles (sel_narrow).
 template <class T, SelMode MODE>
 cudaError_t launch_walk_states(const SelArgs &a, int units, cudaStream_t st)
 {
     if constexpr (MODE != kCarry) {
-        if (narrow_walk<MODE>(a, units)) {
+        if (a.narrow) {
             if (a.N <= 8) return launch_walk<T, 2, 4, 2, MODE>(a, units, st);
             if (a.N <= 16) return launch_walk<T, 2, 4, 4, MODE>(a, units, st);
             if (a.N <= 32) return launch_walk<T, 2, 4, 8, MODE>(a, units, st);
