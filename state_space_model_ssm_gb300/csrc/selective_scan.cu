@@ -124,14 +124,23 @@ int sel_narrow_blocks(int channels, int N, int groups)
     return groups * sel_group_blocks(channels, groups, 32 / lanes * 2);
 }
 
-// Tokens of a segment for which rounds of `resident` blocks, `cblocks` of them a unit, take the least time: r rounds of
-// segments that are just short enough for r, if the sequences were alike.  Forward and backward, tokens / warps for a
-// segment (backward, twice that) / this: 4 x 777 tokens x 1001 channels x 13 states, fp32, 234 / 212 us; 6763 tokens
-// of five sequences, one of them 6508, x 320 x 16, bf16, 252 / 220; 1 x 4096 x 4096 x 16 is cut the same.  Forward, 12
-// uneven sequences of 7889 tokens x 4096 x 16: 370 / 367.
-long long sel_segment(int n_seqs, int n_tokens, long long cblocks, long long resident)
+// Tokens of a segment, for `resident` blocks at once and `cblocks` of them a unit.
+// Up to 8 sequences: the one for which rounds of blocks take the least time, r rounds of segments that are just short
+// enough for r, if the sequences were alike.  More of them are rarely alike and the longest, cut too coarsely, ends last:
+// `rounds` of all tokens.  That also bounds how many units there are beside the sequences.  Both, in us, bf16, 16 states:
+//   4 x 777 tokens x 1001 channels x 13, fp32, forward and backward     alike 210   rounds 234
+//   6508 and four short sequences x 320 channels, the same              alike 220   rounds 251
+//   20 x 300 and one of 3000 tokens x 4096 channels                     alike 335, forward and backward 1647   rounds 326, 1520
+//   60 x 200 and one of 1000                                            alike 505, 2767                        rounds 459, 2686
+//   16 x 512 and one of 4096                                            alike 466, 2518                        rounds 470, 2072
+// One round of all tokens takes 932 forward where 100 sequences of 128 and one of 4096 take 562 with four.
+long long sel_segment(int n_seqs, int n_tokens, long long cblocks, long long resident, int rounds)
 {
     const long long each = (n_tokens + n_seqs - 1) / n_seqs;
+    if (n_seqs > 8) {
+        const long long even = (n_tokens * cblocks + rounds * resident - 1) / (rounds * resident);
+        return std::max(64LL, (even + kSelChunk - 1) / kSelChunk * kSelChunk);
+    }
     long long best = 0, least = 0;
     for (int r = 1; r <= 4; ++r) {
         const long long units = std::max(1LL, r * resident / cblocks / n_seqs);     // of a sequence
@@ -155,9 +164,9 @@ SelCut sel_cut(int n_seqs, int n_tokens, int channels, int N, int groups, bool b
     const long long even = ((long long)n_tokens * s.tiles + warps - 1) / warps, whole = even + even / 2 < 128 ? 128 : even + even / 2;
     if (n_tokens <= whole || n_tokens == n_seqs)            // (as many tokens as sequences: a decode step)
         return SelCut{0, 0};
-    long long seg = sel_segment(n_seqs, n_tokens, s.cblocks, blocks);
+    long long seg = sel_segment(n_seqs, n_tokens, s.cblocks, blocks, backward ? 8 : 4);
     if (!backward && sel_narrow(n_seqs, n_tokens, sel_max_units(n_seqs, n_tokens, (int)seg), s.tiles))
-        seg = sel_segment(n_seqs, n_tokens, sel_narrow_blocks(channels, N, groups), 5 * kSms);
+        seg = sel_segment(n_seqs, n_tokens, sel_narrow_blocks(channels, N, groups), 5 * kSms, 4);
     return SelCut{(int)seg, (int)std::max(whole, seg)};
 }
 
