@@ -289,8 +289,10 @@ int ssm_causal_conv_backward(const void *grad_out, const float *grad_state, cons
     c.x = x; c.w = weight; c.bias = bias; c.starts = seq_starts; c.lens = seq_lens; c.resume = resume_flags;
     c.n_seqs = n_seqs; c.n_tokens = n_tokens; c.channels = channels; c.K = kernel_size; c.silu = silu != 0; c.dtype = dtype;
     c.sx = x_stride; c.sgo = grad_out_stride; c.sgx = grad_x_stride;
-    c.grad_out = grad_out; c.state0 = initial_state; c.grad_state = grad_state;
-    c.grad_x = grad_x; c.grad_w = grad_weight; c.grad_bias = grad_bias; c.grad_state0 = grad_initial_state;
+    c.grad_out = grad_out; c.grad_x = grad_x; c.grad_w = grad_weight; c.grad_bias = grad_bias;
+    if (kernel_size > 1) {                                  // one tap has no slots, whatever pointers stand for them (and no flags)
+        c.state0 = initial_state; c.grad_state = grad_state; c.grad_state0 = grad_initial_state;
+    }
     c.part = static_cast<float *>(workspace);
     return status_of(ssm::launch_causal_conv(c, true, stream));
 }

@@ -266,7 +266,7 @@ causal_conv_backward_kernel(const ConvArgs a)
     const T *x = static_cast<const T *>(a.x) + t0 * a.sx, *go = static_cast<const T *>(a.grad_out) + t0 * a.sgo;
     T *gx = static_cast<T *>(a.grad_x) + t0 * a.sgx;
     const long long slot = (long long)seq * a.C * (K - 1);
-    const bool resumed = a.grad_state0 && a.resume[seq] != 0;
+    const bool resumed = K > 1 && a.grad_state0 && a.resume[seq] != 0;
     const int stop = end + K - 1;                           // the last entries need the tokens behind the span
     RawPair<T> next_x[kRun], next_g[kRun];
     auto fetch = [&](int b) {

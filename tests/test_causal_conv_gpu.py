@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import state_space_model_ssm_gb300 as pkg
+from state_space_model_ssm_gb300 import binding as bd
 from oracle import model as om
 from tests.model_helpers import DTYPES, close, conv_bounds, np64
 
@@ -140,3 +141,19 @@ def test_streams_graph_and_bits():
     torch.cuda.synchronize()
     for o, s, gr in ((og, sg, gg), (o2, s2, g2)):
         assert torch.equal(o, out) and torch.equal(s, slots) and all(torch.equal(gr[k], g[k]) for k in g)
+
+
+def test_one_tap_reads_no_flags():
+    """A C caller may leave resume_flags out for one tap, also where it has pointers for the (empty) slots."""
+    c = _case(66, 1, [40, 7], seed=9)
+    out, slots, g = _run(c)
+    T, C = c["x"].shape
+    spare = torch.full((2, C), 7.0, device="cuda")         # stands for slots of no values: neither read nor written
+    gx, gw, gb = torch.empty_like(out), torch.empty_like(c["weight"]), torch.empty_like(c["bias"])
+    ws = torch.empty(pkg.causal_conv_backward_workspace_bytes(2, T, C, 1), dtype=torch.uint8, device="cuda")
+    p = torch.Tensor.data_ptr
+    rc = bd.load().ssm_causal_conv_backward(p(c["grad_out"]), p(spare), p(c["x"]), p(c["weight"]), p(c["bias"]), p(spare),
+                                            p(c["starts"]), p(c["lens"]), None, 2, T, C, 1, 1, 0, C, c["x"].stride(0), p(gx),
+                                            p(gw), p(gb), p(spare), C, p(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == bd.SSM_OK and (spare == 7.0).all()
+    assert torch.equal(gx, g["x"]) and torch.equal(gw, g["weight"]) and torch.equal(gb, g["bias"])
