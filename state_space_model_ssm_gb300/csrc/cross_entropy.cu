@@ -269,14 +269,14 @@ struct StatsEpilogue {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     s = v[i] != v[i] ? v[i] : s;
-                continue;
-            }
-            float sum = 0.f;
+            } else {
+                float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                sum += ex2(fmaf(v[i], kLog2e, -top));
-            s = fmaf(s, ex2(m - top), sum);
-            m = top;
+                for (int i = 0; i < 32; ++i)
+                    sum += ex2(fmaf(v[i], kLog2e, -top));
+                s = fmaf(s, ex2(m - top), sum);
+                m = top;
+            }
         }
         if (row < rows)
             a.part[(long long)(col / pair::kHalf) * a.t_pad + row] = make_float2(ok ? m : __int_as_float(0x7fc00000), s);

@@ -291,14 +291,17 @@ __device__ __forceinline__ void run(int group_m, const CUtensorMap &amap, const 
     __syncwarp();
     cluster_sync();
     if (warp == 2) {
+        __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
     }
 }
 
-// 32 columns of a thread's half row, or NaN where a wait gave up, or zeros where there are no terms.
+// 32 columns of a thread's half row, or NaN where a wait gave up, or zeros where there are no terms.  For a whole
+// warp: its lanes meet first, whatever branches an epilogue took for single rows (the load needs them together).
 __device__ __forceinline__ void columns(float (&v)[32], uint32_t at, int j, bool ok, bool any)
 {
+    __syncwarp();
     if (any) {
         uint32_t r[32];
         tmem_ld32u(r, at + j);

@@ -221,3 +221,38 @@ def test_waits_that_give_up(monkeypatch):
     assert r.returncode == 0 and "gave up" in r.stdout, r.stdout + r.stderr
     c = _case(600, 700, 64, seed=14)
     _check(c, *_run(c))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_rows_of_a_warp_that_part(dtype):
+    """Odd rows have logits of -inf in every other run of 32 columns (a product that overflows), even rows have none; some
+    rows are NaN.  A warp's rows then take different ways between two loads of its columns."""
+    big, factor = (2.0 ** 100, -2.0 ** 60) if dtype == "bf16" else (float("inf"), -2.0)
+    c = _case(150, 600, 64, TYPES[dtype], seed=15)
+    gone = (torch.arange(600, device="cuda") // 32) % 2 == 1
+    part = torch.arange(150, device="cuda") % 2 == 1
+    c["h"][:, 0] = 0.0
+    c["w"][:, 0] = -2.0 if dtype == "fp16" else 0.0         # (inf times 0 is a NaN: fp16 rows of inf are all -inf)
+    c["w"][gone, 0] = factor
+    c["t"] %= 32                                            # targets in columns that stay
+    clean = dict(c, h=c["h"].clone())
+    c["h"][part, 0] = big
+    c["h"][40:44] = float("nan")
+    loss, lse, gh, gw = _run(c)
+    assert torch.isnan(loss[40:44]).all() and torch.isnan(lse[40:44]).all() and torch.isnan(gh[40:44]).all()
+    fine = torch.ones(150, dtype=torch.bool, device="cuda")
+    fine[40:44] = False
+    if dtype == "fp16":                                     # rows without a finite logit: lse -inf, the loss no number
+        assert (lse[part & fine] == float("-inf")).all() and torch.isnan(loss[part & fine]).all()
+        fine &= ~part
+    for rows, cols in ((fine & ~part, slice(None)), (fine & part, ~gone)):
+        if not rows.any():
+            continue
+        h, w = np64(clean["h"][rows]), np64(c["w"][cols])
+        h[:, 0] = w[:, 0] = 0.0
+        t = c["t"][rows].cpu().numpy()                      # (the first 32 columns are the first of either choice)
+        gl = np64(c["gl"][rows])
+        b = loss_bounds(h, w, t, -100, TYPES[dtype], gl)
+        rl, re = om.linear_cross_entropy(h, w, t, -100)
+        close(loss[rows], rl, b["loss"])
+        close(lse[rows], re, b["lse"])
