@@ -718,8 +718,9 @@ int ssm_linear_cross_entropy(const void *hidden, const void *weight, const void 
  *     grad_hidden = G weight (zeros for ignored rows),   grad_weight = G^T hidden
  * both in dtype.  lse as the forward call wrote it; its own gradient is not
  * taken.  The logits are recomputed in pieces of the vocabulary; G of a piece is held
- * in dtype relative to the largest |grad_loss| (fp16: times 2^15), so each of its terms is rounded
- * to half a step before the products; the sums are fp32 and rounded once.
+ * in dtype relative to the largest finite |grad_loss| (fp16: times 2^15), so each of its terms is rounded
+ * to half a step before the products; the sums are fp32 and rounded once.  A grad_loss that is infinite or
+ * NaN reaches its own row of grad_hidden, and grad_weight.
  * grad_weight may be NULL (a frozen projection): it is not computed.  Outputs must not overlap
  * inputs.  Where there are few rows, several pairs of SMs share the terms of grad_hidden; the
  * order of its sum depends on the sizes and on how many rows count, not on the run.

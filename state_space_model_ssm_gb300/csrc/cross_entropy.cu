@@ -17,7 +17,7 @@
 // forward, 2 T V D again and 4 T V D backward.
 //
 // Roundings: G is rounded to 16 bits for its products (half a step of each term; the sums
-// are fp32, and what is written is rounded once).  It is held relative to the largest |grad_loss|,
+// are fp32, and what is written is rounded once).  It is held relative to the largest finite |grad_loss|,
 // so that a mean's 1 / T is no rounding, and for fp16 2^15 times that, so that probabilities down to
 // 2^-29 keep all their bits; the sums get the factors back in fp32.
 #include <algorithm>
@@ -47,9 +47,9 @@ struct LossArgs {
     int dp;                                   // packed row length
     // workspace
     int *counts;                              // [blocks] kept rows of each kCountRows
-    float *tops;                              // [blocks] largest |grad_loss| of them
+    float *tops;                              // [blocks] largest finite |grad_loss| of them
     int *kept;                                // rows that are kept
-    float *top;                               // largest |grad_loss| of them
+    float *top;                               // largest finite |grad_loss| of them, 1 if that is 0
     int *index;                               // [T] row of each kept one
     int *label;                               // [T rounded up to a tile] its target, -1 past the end
     float *scale;                             // its grad_loss relative to the largest, times the type's factor
@@ -100,8 +100,8 @@ __device__ __forceinline__ Counted block_sum(int n, float m)
     return c;
 }
 
-// Kept ones of rows [t0, t1), and the largest |grad_loss| of them (a NaN counts as none: its row is NaN by
-// itself).
+// Kept ones of rows [t0, t1), and the largest finite |grad_loss| of them (a NaN's or an infinity's row is no number
+// by itself; as what the others are relative to, it would take them along).
 __device__ __forceinline__ Counted count_rows(const LossArgs &a, int t0, int t1, bool tops)
 {
     int n = 0;
@@ -110,8 +110,10 @@ __device__ __forceinline__ Counted count_rows(const LossArgs &a, int t0, int t1,
     for (int t = t0 + threadIdx.x; t < t1; t += 256) {
         const bool keep = target_of(a, t) != a.ignore;
         n += keep ? 1 : 0;
-        if (tops)
-            m = fmaxf(m, keep ? fabsf(a.grad_loss[t]) : 0.f);
+        if (tops) {
+            const float g = keep ? fabsf(a.grad_loss[t]) : 0.f;
+            m = fmaxf(m, g < INFINITY ? g : 0.f);
+        }
     }
     return block_sum(n, m);
 }
@@ -158,6 +160,8 @@ loss_pack_kernel(const LossArgs a)
         before = block_sum(n, 0.f).n + count_rows(a, whole * kCountRows, min(r0, a.T), false).n;
         all = block_sum(every, m);
     }
+    if (all.m == 0.f)                                       // (rows that are no number stay so)
+        all.m = 1.f;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *a.kept = all.n;
         *a.top = all.m;

@@ -256,3 +256,19 @@ def test_rows_of_a_warp_that_part(dtype):
         rl, re = om.linear_cross_entropy(h, w, t, -100)
         close(loss[rows], rl, b["loss"])
         close(lse[rows], re, b["lse"])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,V,D", [(60, 300, 64), (200, 5000, 200)])
+def test_infinite_gradients_stay_in_their_rows(T, V, D, dtype):
+    """Rows whose grad_loss is infinite or no number leave the other rows' gradients as they are."""
+    c = _case(T, V, D, TYPES[dtype], seed=16)
+    c["gl"][5], c["gl"][17], c["gl"][30] = float("inf"), float("nan"), float("-inf")
+    fine = torch.isfinite(c["gl"])
+    loss, lse, gh, gw = _run(c)
+    assert not torch.isfinite(gh[~fine]).any() and not torch.isfinite(gw).any()
+    sub = dict(c, h=c["h"][fine], t=c["t"][fine], gl=c["gl"][fine])
+    _check(sub, loss[fine], lse[fine], gh[fine])
+    c["gl"][fine] = 0.0                                     # nothing finite to be relative to
+    _, _, gh, gw = _run(c)
+    assert (gh[fine] == 0).all() and not torch.isfinite(gh[~fine]).any()
