@@ -269,10 +269,12 @@ struct StatsEpilogue {
             for (int i = 1; i < 32; ++i)
                 top = fmaxf(top, v[i]);
             top = fmaxf(m, top * kLog2e);
-            if (top == -INFINITY) {                         // columns past the last, logits of -inf, or NaN alone
-#pragma unroll
+            if (fabsf(top) == INFINITY) {                   // an infinite logit: sum 1; or columns past the last, logits of
+#pragma unroll                                              // -inf, NaN alone: no terms
                 for (int i = 0; i < 32; ++i)
                     s = v[i] != v[i] ? v[i] : s;
+                s = top > 0.f && s == s ? 1.f : s;
+                m = top;
             } else {
                 float sum = 0.f;
 #pragma unroll
@@ -483,14 +485,15 @@ loss_weight_kernel(const LossArgs a, const __grid_constant__ CUtensorMap gmap, c
     });
 }
 
-// (largest logit, sum) of two disjoint sets of columns.
+// (largest logit, sum) of two disjoint sets of columns.  Under an infinite maximum a finite part has no share, but for
+// its NaN.
 __device__ __forceinline__ float2 join(float2 p, float2 q)
 {
     const float top = fmaxf(p.x, q.x);
     if (p.x != p.x || q.x != q.x)                           // a wait gave up
         return make_float2(__int_as_float(0x7fc00000), 0.f);
-    if (top == -INFINITY)
-        return make_float2(top, p.y + q.y);
+    if (fabsf(top) == INFINITY)
+        return make_float2(top, (p.x == top ? p.y : 0.f * p.y) + (q.x == top ? q.y : 0.f * q.y));
     return make_float2(top, p.y * ex2(p.x - top) + q.y * ex2(q.x - top));
 }
 

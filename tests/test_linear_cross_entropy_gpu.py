@@ -272,3 +272,27 @@ def test_infinite_gradients_stay_in_their_rows(T, V, D, dtype):
     c["gl"][fine] = 0.0                                     # nothing finite to be relative to
     _, _, gh, gw = _run(c)
     assert (gh[fine] == 0).all() and not torch.isfinite(gh[~fine]).any()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_infinite_logits(dtype):
+    """A logit that overflows makes its row's lse and loss infinite, wherever among the columns it stands; NaN stays NaN."""
+    c = _case(70, 900, 64, TYPES[dtype], seed=17)
+    big, one = (2.0 ** 100, 2.0 ** 60) if dtype == "bf16" else (float("inf"), 1.0)
+    c["h"][:, 0] = 0.0
+    c["w"][:, 0] = 0.0 if dtype == "bf16" else -1.0
+    up = torch.tensor([0, 40, 41, 300, 899], device="cuda")
+    c["t"] = torch.where(torch.isin(c["t"], up), c["t"] + 1, c["t"]) % 899
+    c["t"][c["t"] == 41] = 42
+    c["t"][c["t"] == 0] = 1
+    clean = dict(c, w=c["w"].clone())
+    c["w"][up, 0] = one
+    c["h"][::3, 0] = big
+    c["h"][3, 5] = float("nan")
+    loss, lse, gh, gw = _run(c)
+    inf = torch.arange(70, device="cuda") % 3 == 0
+    inf[3] = False
+    assert (lse[inf] == float("inf")).all() and (loss[inf] == float("inf")).all()
+    assert torch.isnan(lse[3]) and torch.isnan(loss[3])
+    rest = torch.arange(70, device="cuda") % 3 != 0
+    _check(dict(clean, h=c["h"][rest], t=c["t"][rest], gl=c["gl"][rest]), loss[rest], lse[rest])
