@@ -600,6 +600,7 @@ size_t ssm_int8_matmul_workspace_bytes(const int8_t *x, const int8_t *w, int row
  *   x, dt, y     [n_tokens][channels] of dtype;  z the same, or NULL: y = p
  *   B, C         [n_tokens][n_groups][d_state] of dtype (contiguous within a token)
  *   A            [channels][d_state] fp32, finite;  D, dt_bias [channels] fp32 or NULL (zeros)
+ *                (either sign: a decay may grow; one token's exp(step A) is fp32, infinite above step A = 88)
  *   chunk_states NULL, or (training) fp32 [ssm_selective_scan_chunks(...)][channels][d_state],
  *                out: the state entering every 16 tokens, which the backward pass reads
  * d_state 1 .. 128 (SSM_ERR_UNSUPPORTED above).  Where sequences and channels alone

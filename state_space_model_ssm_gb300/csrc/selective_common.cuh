@@ -156,6 +156,18 @@ __device__ __forceinline__ float2 sel_slope2(float2 v, bool softplus)
     return make_float2(v.x > 20.f ? 1.f : s.x, v.y > 20.f ? 1.f : s.y);
 }
 
+// A state h behind a whole segment: 2^x h + own, x the sum of its tokens' exponents.  2^x alone can overflow where the
+// product does not, and where h is 0 (decays that grow: A above 0, or negative steps), so it goes in parts
+// that fp32 holds; between -126 and 126 the first is all of it.  A zero stays zero, an infinity infinite, as token by
+// token.
+__device__ __forceinline__ float sel_passed(float h, float x, float own)
+{
+    const float first = fminf(fmaxf(x, -126.f), 126.f), second = fminf(fmaxf(x - first, -126.f), 126.f);
+    float third = x - first - second;                       // (NaN where x is)
+    third = third < -126.f ? -126.f : third;
+    return h == 0.f ? own : fmaf(h * ex2(third) * ex2(second), ex2(first), own);
+}
+
 // How a warp stages pairs of channels of up to L tokens: place m of a lane is token tok(m), pair cp(m).
 template <int WC, int L>
 struct SelStage {

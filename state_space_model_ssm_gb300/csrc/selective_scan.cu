@@ -80,7 +80,7 @@ sel_combine_kernel(const SelArgs a)
                 if (u + k >= u1)
                     break;
                 a.unit_state[(u + k) * width + e] = h;
-                h = fmaf(ex2(step[k] * A), h, own[k]);      // (the last unit's values are not there, and not used)
+                h = sel_passed(h, step[k] * A, own[k]);     // (the last unit's values are not there, and not used)
             }
         }
     }

@@ -52,7 +52,7 @@ sel_carry_combine_kernel(const SelArgs a)
                 if (u - k < u0)
                     break;
                 a.unit_state[(u - k) * width + e] = g;
-                g = fmaf(ex2(step[k] * A), g, own[k]);      // (the first unit's values are not there, and not used)
+                g = sel_passed(g, step[k] * A, own[k]);     // (the first unit's values are not there, and not used)
             }
         }
     }

@@ -292,3 +292,30 @@ def test_captured_and_replayed_beside_eager_calls():
         torch.cuda.synchronize()
         assert torch.equal(yg, y) and torch.equal(slots_g, slots) and torch.equal(held["grad_x"], eager["grad_x"])
         assert all(torch.equal(again[k], eager[k]) for k in NAMES)
+
+
+@pytest.mark.parametrize("N", [13, 16])
+@pytest.mark.parametrize("left", [0.0, 1e-35])
+def test_segments_whose_decay_overflows(left, N):
+    """Decays that grow (A above 0): over a segment of 64 tokens by 2^130, which fp32 does not hold, on states of `left`.
+    Token by token everything is finite; so it is in segments.  Sequences: growth on small states, ordinary tokens, growth
+    behind the last gradient."""
+    lens = [256, 320]
+    c = _case(12, N, lens, resume=[1, 1], seed=18, softplus=False, bias=False, gate=False)
+    assert pkg.selective_scan_workspace_bytes(2, 576, 12, N) > 0
+    g = torch.Generator().manual_seed(19)
+    c["A"] = (0.7 + 0.01 * torch.rand(12, N, generator=g)).cuda()
+    c["dt"] = torch.full((576, 12), -0.3, device="cuda")
+    c["x"] = c["x"] * 1e-8
+    c["grad_y"] *= 1e-8
+    c["slots"], c["grad_state"] = c["slots"].clone(), c["grad_state"] * left
+    c["slots"][:] = left * torch.randn(2, 12, N, generator=g).cuda()
+    for start, n in zip((0, 256), lens):
+        for part in (slice(start, start + 64), slice(start + n - 64, start + n)):
+            c["dt"][part] = 130 * 0.6931471805599453 / 64 / 0.7     # 130 / 64 of an exponent of 2 a token at least
+            c["x"][part] = 0.0
+            c["grad_y"][part] = 0.0
+    y, slots, ch = _forward(c, train=True)
+    grads = _backward(c, ch)
+    assert torch.isfinite(slots).all() and all(torch.isfinite(v).all() for v in grads.values() if v is not None)
+    _check(c, y, slots, grads)
