@@ -11,7 +11,7 @@ rounding move the argument by 2|w|u, so exp is within (2|w| + 4)u.
    rounding is at most one u a token relative: n X u more, n the sequence's length.
  * states and their gradients follow their recurrences with 4u a step; sums over N states or n tokens add a u a
    term (in whatever order), sums over channels 24u (four channels in a lane, five exchanges, four warps, up to
-   eleven blocks).
+   eleven blocks; `blocks` says if there are more).
 The tensor cores add products in fp32 with truncation: 2u of the sum of magnitudes a term.
 """
 import numpy as np
@@ -30,7 +30,7 @@ def _rep(rows, channels, groups):
 
 
 def scan_bounds(slots, x, dt, A, B, C, D, starts, lens, resume, z=None, dt_bias=None, softplus=False, groups=1,
-                grad_y=None, grad_state=None):
+                grad_y=None, grad_state=None, blocks=11):
     """Bounds (float64 arrays by name) of y and the slots, and with grad_y of the gradients."""
     T, channels = x.shape
     N = A.shape[1]
@@ -42,6 +42,7 @@ def scan_bounds(slots, x, dt, A, B, C, D, starts, lens, resume, z=None, dt_bias=
     d = np.zeros(channels) if D is None else np.abs(D)
     sg = om.sigmoid(z) if z is not None else None
     gate = np.abs(z * sg) if z is not None else np.ones_like(x)
+    over = (15 + blocks) * U                                  # a sum over channels
     eg = sig_err(z) + 4 * U if z is not None else np.zeros_like(x)
     u, ax = np.abs(step * x), np.abs(x)
     out = {"y": np.zeros_like(x), "slots": np.zeros((len(lens),) + A.shape)}
@@ -107,8 +108,8 @@ def scan_bounds(slots, x, dt, A, B, C, D, starts, lens, resume, z=None, dt_bias=
             out["grad_dt_bias"] += out["grad_dt"][t]
             gb_m += slope[t] * gsM
             ue = u[t][:, None] * eM
-            out["grad_B"][t] = fold(u[t][:, None] * eE + ue * (es[t][:, None] + 26 * U))
-            out["grad_C"][t] = fold(gp[t][:, None] * hE + gp[t][:, None] * hM * (eg[t][:, None] + 26 * U))
+            out["grad_B"][t] = fold(u[t][:, None] * eE + ue * (es[t][:, None] + over))
+            out["grad_C"][t] = fold(gp[t][:, None] * hE + gp[t][:, None] * hM * (eg[t][:, None] + over))
             eE = a * eE + a * eM * (ea + 2 * U)
             eM = a * eM
         out["grad_slots"][k] = eE if resume[k] else 0.0

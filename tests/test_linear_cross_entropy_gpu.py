@@ -259,7 +259,7 @@ def test_rows_of_a_warp_that_part(dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("T,V,D", [(60, 300, 64), (200, 5000, 200)])
+@pytest.mark.parametrize("T,V,D", [(60, 300, 64), (200, 5000, 200), (9000, 64, 16)])
 def test_infinite_gradients_stay_in_their_rows(T, V, D, dtype):
     """Rows whose grad_loss is infinite or no number leave the other rows' gradients as they are."""
     c = _case(T, V, D, TYPES[dtype], seed=16)
@@ -296,3 +296,13 @@ def test_infinite_logits(dtype):
     assert torch.isnan(lse[3]) and torch.isnan(loss[3])
     rest = torch.arange(70, device="cuda") % 3 != 0
     _check(dict(clean, h=c["h"][rest], t=c["t"][rest], gl=c["gl"][rest]), loss[rest], lse[rest])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,V,D,ignored", [(100, 9000, 1000, 0.0), (300, 20000, 1024, 0.5), (64, 8000, 4096, 0.2),
+                                           (513, 5000, 2048, 0.1), (40, 40000, 300, 0.3), (256, 17000, 200, 0.97)])
+def test_terms_shared_by_several_pairs(T, V, D, ignored, dtype):
+    """Few tiles of grad hidden: 3 to 16 pairs share each one's terms (fewer where ignored rows leave whole tiles out), at
+    widths of real models and with a grad_loss of every size."""
+    c = _case(T, V, D, TYPES[dtype], ignored=ignored, seed=18)
+    _check(c, *_run(c))

@@ -75,11 +75,11 @@ def _ref(c):
         z=a["z"], dt_bias=a["dt_bias"], softplus=c["softplus"], groups=c["groups"])
 
 
-def _check(c, y, slots, grads=None):
+def _check(c, y, slots, grads=None, blocks=11):
     args, kw = _ref(c)
     y_ref, s_ref, _ = om.selective_scan(*args, **kw)
     gy, gs = (np64(c["grad_y"]), np64(c["grad_state"])) if grads is not None else (None, None)
-    b = scan_bounds(*args, **kw, grad_y=gy, grad_state=gs)
+    b = scan_bounds(*args, **kw, grad_y=gy, grad_state=gs, blocks=blocks)
     own = ~np.isnan(y_ref[:, 0])
     rows, dtype = torch.from_numpy(own), c["x"].dtype
     # Without softplus a step may be negative and a state grow without bound.  What passes through a state or a state's
