@@ -157,15 +157,14 @@ __device__ __forceinline__ float2 sel_slope2(float2 v, bool softplus)
 }
 
 // A state h behind a whole segment: 2^x h + own, x the sum of its tokens' exponents.  2^x alone can overflow where the
-// product does not, and where h is 0 (decays that grow: A above 0, or negative steps), so it goes in parts
-// that fp32 holds; between -126 and 126 the first is all of it.  A zero stays zero, an infinity infinite, as token by
-// token.
+// product does not, and where h is 0 (decays that grow: A above 0, or negative steps), so it goes in two
+// factors that are never infinite; between -126 and 127 the second is 1.  From 2^254 on the product overflows for
+// every normal h, below 2^-252 it is nothing beside own.  A zero stays zero, an infinity infinite, as token by
+// token; a step that is no number is in own already.
 __device__ __forceinline__ float sel_passed(float h, float x, float own)
 {
-    const float first = fminf(fmaxf(x, -126.f), 126.f), second = fminf(fmaxf(x - first, -126.f), 126.f);
-    float third = x - first - second;                       // (NaN where x is)
-    third = third < -126.f ? -126.f : third;
-    return h == 0.f ? own : fmaf(h * ex2(third) * ex2(second), ex2(first), own);
+    const float first = fminf(fmaxf(x, -126.f), 127.f), second = fminf(fmaxf(x - first, -126.f), 127.f);
+    return fmaf(h * ex2(second), ex2(first), own);
 }
 
 // How a warp stages pairs of channels of up to L tokens: place m of a lane is token tok(m), pair cp(m).
