@@ -662,8 +662,8 @@ size_t ssm_selective_scan_backward_workspace_bytes(int n_seqs, int n_tokens, int
  *   bias        [channels] fp32 or NULL
  *   conv_state  [n_seqs][channels][kernel_size-1] fp32, in/out (NULL allowed for kernel_size 1)
  *   kernel_size 1 .. 8 (SSM_ERR_UNSUPPORTED above)
- * out must not overlap an input.  Fastest with rows and slots of whole 8-byte (16-bit types) or
- * 16-byte words and channels a multiple of 4.
+ * out must not overlap an input.  Fastest with an even number of channels and rows on whole words of two
+ * channels (4 bytes for 16-bit types, 8 for fp32).
  */
 int ssm_causal_conv(const void *x, const float *weight, const float *bias, float *conv_state, void *out,
                     const int32_t *seq_starts, const int32_t *seq_lens, const int32_t *resume_flags, int n_seqs,
@@ -702,7 +702,8 @@ size_t ssm_causal_conv_backward_workspace_bytes(int n_seqs, int n_tokens, int ch
  *   hidden [rows][width], weight [vocab][width] of dtype: SSM_BF16 or SSM_F16
  *          (SSM_ERR_UNSUPPORTED for SSM_F32, and for width above 65536)
  *   targets [rows] int32, or int64 with targets_64;  loss, lse [rows] fp32
- * Sums are fp32.  workspace: 256-byte aligned,
+ * Sums are fp32; the tensor cores' truncate (lse of 4096 products of order one a logit: 9e-6 rms, where fp32
+ * products rounded to nearest have 4e-7).  workspace: 256-byte aligned,
  * ssm_linear_cross_entropy_workspace_bytes(weight, ..., 0): the rows that count, back to
  * back, the parts of the sums, and the weights if their rows are not 16-byte
  * aligned; scratch, not shared by calls that overlap on the GPU.
@@ -720,7 +721,8 @@ int ssm_linear_cross_entropy(const void *hidden, const void *weight, const void 
  * both in dtype.  lse as the forward call wrote it; its own gradient is not
  * taken.  The logits are recomputed in pieces of the vocabulary; G of a piece is held
  * in dtype relative to the largest finite |grad_loss| (fp16: times 2^15), so each of its terms is rounded
- * to half a step before the products; the sums are fp32 and rounded once.  A grad_loss that is infinite or
+ * to half a step before the products (fp16: terms below 2^-29 of the largest |grad_loss| to 2^-40 of it, which is all of a
+ * row whose grad_loss is that much smaller); the sums are fp32 and rounded once.  A grad_loss that is infinite or
  * NaN reaches its own row of grad_hidden, and grad_weight.
  * grad_weight may be NULL (a frozen projection): it is not computed.  Outputs must not overlap
  * inputs.  Where there are few rows, several pairs of SMs share the terms of grad_hidden; the

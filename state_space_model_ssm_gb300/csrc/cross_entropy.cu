@@ -19,7 +19,8 @@
 // Roundings: G is rounded to 16 bits for its products (half a step of each term; the sums
 // are fp32, and what is written is rounded once).  It is held relative to the largest finite |grad_loss|,
 // so that a mean's 1 / T is no rounding, and for fp16 2^15 times that, so that probabilities down to
-// 2^-29 keep all their bits; the sums get the factors back in fp32.
+// 2^-29 keep all their bits; the sums get the factors back in fp32.  The tensor cores truncate as they add: at a width of
+// 4096 the lse is off by 9e-6 (rms, logits of order one), 20 times what an fp32 product rounded to nearest is.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -33,7 +34,9 @@ namespace {
 
 constexpr int kCountRows = 1024;              // rows of a block of the counting kernel
 constexpr int kPackRows = 8;                  // rows of a block of the packing kernel, a warp each
-constexpr int kCountAlone = 8192;             // rows that every packing block counts by itself, without that kernel
+// Rows that every packing block counts by itself, without that kernel: up to here its launch costs as much (256 x 64,
+// forward: 8192 rows counted by the blocks 16.6 us, 8200 by the kernel 16.2; 1024 by the blocks 11.2).
+constexpr int kCountAlone = 8192;
 constexpr int kJoinLanes = 32;                // threads that join a row's parts
 constexpr int kGroupM = 16;                   // row tiles that share the vocabulary's rows in L2
 

@@ -53,7 +53,8 @@ __device__ __forceinline__ float rcp(float v)
 
 __device__ __forceinline__ float2 rcp2(float2 v) { return make_float2(rcp(v.x), rcp(v.y)); }
 
-// sigmoid(v); v times it is 0 times v where exp(-v) overflows (v below -88).
+// sigmoid(v), within (2|v| + 8) 2^-24 of it: the rounded argument of 2^x, and the two approximations.  v times it is 0 times
+// v where exp(-v) overflows (v below -88).
 __device__ __forceinline__ float2 sigmoid2(float2 v)
 {
     return rcp2(make_float2(1.f + ex2(-v.x * kLog2e), 1.f + ex2(-v.y * kLog2e)));

@@ -129,7 +129,7 @@ __device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x),
 // The discretised step of two values.  softplus(v) = max(v, 0) + log1p(e) with e = exp(-|v|), and
 // log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3: the series 2 s (1 + s^2/3 + s^4/5 + ...) to s^14
 // leaves (1/9)^8 / 17 < 2^-29 of it, and keeps the relative accuracy of small e, which a
-// logarithm of 1 + e would lose.
+// logarithm of 1 + e would lose.  All together within (3|v| + 18) 2^-24 of the step.
 __device__ __forceinline__ float2 sel_step2(float2 v, bool softplus)
 {
     if (!softplus)
